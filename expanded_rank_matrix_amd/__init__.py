@@ -86,6 +86,13 @@ def load():
         lib.externd_apply_factors.argtypes = [vp, vp, vp, i64, i64, i64, vp, i64, vp, vp]
         lib.externd_apply_factors_static.restype = ci
         lib.externd_apply_factors_static.argtypes = [vp, vp, vp, i64, i64, i64, vp, i64, vp, vp]
+        lib.externd_quantize_rows.restype = ci
+        lib.externd_quantize_rows.argtypes = [vp, ci, i64, i64, i64, vp, i64, vp, vp]
+        lib.externd_apply_quantized.restype = ci
+        lib.externd_apply_quantized.argtypes = [vp, vp, i64, i64, i64, vp, ci, vp, i64, i64, vp, ci,
+                                                i64, vp, vp]
+        lib.externd_apply_quantized_workspace.restype = i64
+        lib.externd_apply_quantized_workspace.argtypes = [ci, i64, i64]
         lib.externd_status_string.restype = ctypes.c_char_p
         lib.externd_status_string.argtypes = [ci]
         lib.externd_last_error.restype = ctypes.c_char_p
@@ -279,6 +286,159 @@ def apply_factors_static(B, C, D, m: int, n: int, X, stream=None, out=None):
                                              X2.shape[0], _dev_ptr(Y), _stream_ptr(stream))
     _check(rc)
     return Y[0] if single else Y.reshape(X2.shape[0], m)
+
+
+class _Run:
+    """Where one call runs: the device of its tensors made current, the stream, and outputs and
+    workspace allocated on that stream, so that their memory is reused in its order.  Inputs that
+    belong to another stream are recorded on this one."""
+
+    def __init__(self, device, stream, inputs):
+        import torch
+
+        self.guard = None
+        if device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(device)
+            self.guard.__enter__()
+        try:
+            cur = torch.cuda.current_stream(device)
+            self.stream = cur if stream is None else stream
+            self.on = None
+            if self.stream != cur:
+                if self.stream.device != device:
+                    raise ValueError(f"stream is on {self.stream.device}, the tensors are on {device}")
+                for t in inputs:
+                    if t is not None:
+                        t.record_stream(self.stream)
+                self.on = torch.cuda.stream(self.stream)
+                self.on.__enter__()
+        except BaseException:
+            if self.guard is not None:
+                self.guard.__exit__(None, None, None)
+            raise
+        self.ptr = self.stream.cuda_stream
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        if self.on is not None:
+            self.on.__exit__(*exc)
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        return False
+
+
+_TYPE = None
+
+
+def _types():
+    """torch dtype -> the C ABI's number of the type."""
+    global _TYPE
+    if _TYPE is None:
+        import torch
+
+        _TYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.int8: 3}
+    return _TYPE
+
+
+def _rows(t, types, name, shape=None, device=None):
+    """t as rows of the C ABI: a CUDA matrix of one of ``types`` whose rows are contiguous and do
+    not overlap, on ``device`` and of exactly ``shape`` when given.  Returns its row distance."""
+    if not (t.is_cuda and t.dtype in types and t.dim() == 2):
+        raise ValueError(f"{name} must be a CUDA matrix of {' or '.join(map(str, types))}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    rows, n = t.shape
+    if n > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if rows <= 1:
+        return max(n, 1)
+    if t.stride(0) < n:
+        raise ValueError(f"{name} must have rows that do not overlap")
+    return t.stride(0)
+
+
+def quantize_rows(X, stream=None, out=None):
+    """Rows of X (rows x n, fp32, fp16 or bf16, device; rows may be strided) to 8-bit integers with
+    one scale a row: scale = max |x| / 127 and Q the whole numbers nearest to 127 x / max |x|, ties
+    to even.  Returns (Q int8 rows x n, scale fp32 rows); ``out`` may supply that pair (Q's rows may
+    be strided).  A row of zeros gets scale 0, one with a NaN or an infinity scale NaN; both get
+    zeros.  Quantises the weights of ``apply_quantized`` (rows are output channels) and tokens that
+    several products share.  Enqueued on the stream without waiting."""
+    import torch
+
+    types = _types()
+    ldx = _rows(X, _float_types(), "X")
+    rows, n = X.shape
+    dev = X.device
+    with _Run(dev, stream, (X,) if out is None else (X, *out)) as run:
+        if out is None:
+            out = (torch.empty((rows, n), dtype=torch.int8, device=dev),
+                   torch.empty(rows, dtype=torch.float32, device=dev))
+        Q, scale = out
+        ldq = _rows(Q, (torch.int8,), "out[0]", shape=(rows, n), device=dev)
+        _require(scale, torch.float32, "out[1]", shape=(rows,), device=dev)
+        _check(load().externd_quantize_rows(X.data_ptr(), types[X.dtype], rows, n, ldx, Q.data_ptr(), ldq,
+                                            scale.data_ptr(), run.ptr))
+    return Q, scale
+
+
+def _float_types():
+    import torch
+
+    return (torch.float32, torch.float16, torch.bfloat16)
+
+
+def apply_quantized(W, w_scale, X, x_scale=None, out_dtype=None, stream=None, out=None):
+    """Y[t][o] = x_scale[t] w_scale[o] sum_j X[t][j] W[o][j]: a layer in 8-bit integers, beside
+    ``apply_factors`` for the layers that stay unfactored.  W (m x n int8) and w_scale (m fp32) are
+    as ``quantize_rows`` gives them.  X (n or tokens x n) is int8 with x_scale (tokens fp32), or
+    fp32, fp16 or bf16 without it: its tokens are then quantised on the way as ``quantize_rows``
+    does.  W, X and ``out`` may have strided rows.  Returns Y (m or tokens x m) of ``out_dtype``
+    (fp32, fp16 or bf16; by default X's type, fp32 for int8 tokens).  The integer sum is exact; Y is
+    rounded once.  Enqueued on the stream without waiting."""
+    import torch
+
+    types = _types()
+    ldw = _rows(W, (torch.int8,), "W")
+    m, n = W.shape
+    dev = W.device
+    _require(w_scale, torch.float32, "w_scale", shape=(m,), device=dev)
+    single = X.dim() == 1
+    X2 = X.unsqueeze(0) if single else X
+    ldx = _rows(X2, tuple(types), "X", device=dev)
+    tokens = X2.shape[0]
+    if X2.shape[1] != n:
+        raise ValueError(f"X must be n or tokens x n with n = {n}")
+    if (X.dtype == torch.int8) != (x_scale is not None):
+        raise ValueError("x_scale is given with int8 tokens and only then")
+    if x_scale is not None:
+        _require(x_scale, torch.float32, "x_scale", shape=(tokens,), device=dev)
+    if out is not None:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError("out must be of out_dtype")
+        out_dtype = out.dtype
+    elif out_dtype is None:
+        out_dtype = torch.float32 if X.dtype == torch.int8 else X.dtype
+    if out_dtype not in _float_types():
+        raise ValueError("out_dtype must be torch.float32, torch.float16 or torch.bfloat16")
+    lib = load()
+    with _Run(dev, stream, (W, w_scale, X, x_scale, out)) as run:
+        if out is None:
+            Y = torch.empty((tokens, m), dtype=out_dtype, device=dev)
+        else:
+            Y = out.unsqueeze(0) if single and out.dim() == 1 else out
+        ldy = _rows(Y, _float_types(), "out", shape=(tokens, m), device=dev)
+        size = lib.externd_apply_quantized_workspace(types[X.dtype], tokens, n)
+        ws = torch.empty(size, dtype=torch.uint8, device=dev) if size > 0 else None
+        _check(lib.externd_apply_quantized(
+            W.data_ptr(), w_scale.data_ptr(), m, n, ldw, X2.data_ptr(), types[X.dtype],
+            None if x_scale is None else x_scale.data_ptr(), tokens, ldx, Y.data_ptr(), types[out_dtype], ldy,
+            None if ws is None else ws.data_ptr(), run.ptr))
+    return Y[0] if single else Y
 
 
 def unpack(packed, length: int) -> np.ndarray:

@@ -478,4 +478,56 @@ int externd_matvec(const float* R, int64_t m, int64_t n, const int8_t* t, const 
   return EXTERND_OK;
 }
 
+// ---- layers in 8-bit integers: enqueue only, the caller's workspace
+
+static bool float_type(int t) { return t == EXTERND_F32 || t == EXTERND_F16 || t == EXTERND_BF16; }
+
+constexpr int64_t kMaxCount = 2147483647;  // rows, tokens, channels
+constexpr int64_t kMaxProductLen = 131071; // 128 128 n < 2^31: the sum of products of int8 fits int32
+constexpr int64_t kMaxLd = (int64_t)1 << 40;
+
+int externd_quantize_rows(const void* X, int x_type, int64_t rows, int64_t n, int64_t ldx, int8_t* Q, int64_t ldq,
+                          float* scale, void* stream) {
+  g_last_error.clear();
+  if (!float_type(x_type)) return fail(EXTERND_EINVAL, "x_type must be EXTERND_F32, EXTERND_F16 or EXTERND_BF16");
+  if (rows < 0 || rows > kMaxCount) return fail(EXTERND_EINVAL, "need 0 <= rows < 2^31");
+  if (n < 1 || n > kMaxCount - 4096) return fail(EXTERND_EINVAL, "need 1 <= n < 2^31 - 4096");
+  if (ldx < n || ldx > kMaxLd || ldq < n || ldq > kMaxLd)
+    return fail(EXTERND_EINVAL, "ldx and ldq must be at least n (and at most 2^40)");
+  if (rows == 0) return EXTERND_OK;
+  if (!X || !Q || !scale) return fail(EXTERND_EINVAL, "null pointer argument");
+  HIP_OR_FAIL(quantize_run(X, x_type, rows, (int)n, ldx, Q, ldq, (int)n, scale, reinterpret_cast<hipStream_t>(stream)));
+  return EXTERND_OK;
+}
+
+int64_t externd_apply_quantized_workspace(int x_type, int64_t tokens, int64_t n) {
+  if (!(float_type(x_type) || x_type == EXTERND_I8) || tokens < 0 || tokens > kMaxCount || n < 1 || n > kMaxProductLen)
+    return -1;
+  return (int64_t)product_workspace_bytes(x_type, tokens, (int)n);
+}
+
+int externd_apply_quantized(const int8_t* W, const float* w_scale, int64_t m, int64_t n, int64_t ldw, const void* X,
+                            int x_type, const float* x_scale, int64_t tokens, int64_t ldx, void* Y, int y_type,
+                            int64_t ldy, void* workspace, void* stream) {
+  g_last_error.clear();
+  if (!float_type(x_type) && x_type != EXTERND_I8)
+    return fail(EXTERND_EINVAL, "x_type must be EXTERND_F32, EXTERND_F16, EXTERND_BF16 or EXTERND_I8");
+  if (!float_type(y_type)) return fail(EXTERND_EINVAL, "y_type must be EXTERND_F32, EXTERND_F16 or EXTERND_BF16");
+  if (tokens < 0 || tokens > kMaxCount || m < 1 || m > kMaxCount)
+    return fail(EXTERND_EINVAL, "need 0 <= tokens < 2^31 and 1 <= m < 2^31");
+  if (n < 1 || n > kMaxProductLen)
+    return fail(EXTERND_EINVAL, "need 1 <= n <= %lld (the sum of products must fit int32)", (long long)kMaxProductLen);
+  if (ldw < n || ldw > kMaxLd || ldx < n || ldx > kMaxLd || ldy < m || ldy > kMaxLd)
+    return fail(EXTERND_EINVAL, "ldw and ldx must be at least n and ldy at least m (and at most 2^40)");
+  if (tokens == 0) return EXTERND_OK;
+  if (!W || !w_scale || !X || !Y) return fail(EXTERND_EINVAL, "null pointer argument");
+  if ((x_type == EXTERND_I8) != (x_scale != nullptr))
+    return fail(EXTERND_EINVAL, "x_scale is given with x_type EXTERND_I8 and only then");
+  if (product_workspace_bytes(x_type, tokens, (int)n) > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15)))
+    return fail(EXTERND_EINVAL, "workspace of externd_apply_quantized_workspace() bytes, 16-byte aligned, is needed");
+  HIP_OR_FAIL(product_run(W, w_scale, (int)m, (int)n, ldw, X, x_type, x_scale, (int)tokens, ldx, Y, y_type, ldy,
+                          workspace, reinterpret_cast<hipStream_t>(stream)));
+  return EXTERND_OK;
+}
+
 }  // extern "C"

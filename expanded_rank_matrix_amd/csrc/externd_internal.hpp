@@ -92,4 +92,13 @@ hipError_t infer_static_scratch(void** ptr);
 hipError_t infer_run(const uint32_t* B, const uint32_t* C, const float* D, int k, int m, int n, const float* X,
                      int batch, float* Y, void* ws, hipStream_t st);
 
+// 8-bit rows and products (quant.hip).  Types as in the C ABI: 0 fp32, 1 fp16, 2 bf16, 3 int8.
+// np bytes of each row of Q are written, zeros behind the first n.
+hipError_t quantize_run(const void* X, int type, long long rows, int n, long long ldx, int8_t* Q, long long ldq, int np,
+                        float* scale, hipStream_t st);
+size_t product_workspace_bytes(int x_type, long long tokens, int n);
+hipError_t product_run(const int8_t* W, const float* sw, int m, int n, long long ldw, const void* X, int x_type,
+                       const float* sx, int tokens, long long ldx, void* Y, int y_type, long long ldy, void* ws,
+                       hipStream_t st);
+
 }  // namespace externd

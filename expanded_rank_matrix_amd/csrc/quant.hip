@@ -1,0 +1,399 @@
+// Products in 8-bit integers with a scale for each token and each output channel, and the
+// quantisation of rows that makes their operands.
+//
+//   quantise:  a_t = max_j |x_tj|,  s_t = fl32(a_t / 127),  q_tj = the whole number nearest to the
+//              exact quotient 127 x_tj / a_t, ties to even
+//   product:   y_to = s_t w_o sum_j q_tj W_oj
+//
+// The sum is exact in int32 (n <= 131071), so it does not depend on how it is split; it is converted
+// to fp32 and multiplied by the two scales (three fp32 roundings), then rounded once to Y's type.
+#include "common.hpp"
+#include "externd_internal.hpp"
+#include "types.hpp"
+
+namespace externd {
+
+// ---- quantisation of rows ---------------------------------------------------------------------
+// q = rint(127 x / a) of the exact quotient.  The fp32 estimate x fl(127 / a) is off by less than
+// 127 2^-22.9 < 2^-15: only an estimate that close to a border between two whole numbers can round
+// to the wrong side, and those few are redone in fp64, whose rounded quotient is never on the wrong
+// side: 254 x and (2 q + 1) a are 32-bit integers times a power of two, so a quotient that is no
+// tie is at least 2^-25 from one.
+__device__ __forceinline__ int quant1(float x, float inv, float a) {
+  const float r = x * inv;
+  float q = rintf(r);
+  if (fabsf(r - q) > 0.5f - 0x1p-14f) q = (float)rint(127.0 * (double)x / (double)a);
+  return (int)q;
+}
+// rows whose largest value is so small that 127 / a overflows (or nears it) take fp64 throughout
+__device__ __forceinline__ int quant1_small(float x, float a) { return (int)rint(127.0 * (double)x / (double)a); }
+
+__device__ __forceinline__ unsigned pack4(int a, int b, int c, int d) {
+  return (unsigned)(a & 255) | (unsigned)(b & 255) << 8 | (unsigned)(c & 255) << 16 | (unsigned)d << 24;
+}
+
+// One row per TPR threads (64: a wave; 256: the workgroup), 8 elements per thread and step; the
+// first CH steps of a row stay in registers between the search for its maximum and its rounding, a
+// longer row's rest is read again.  np bytes of each Q row are written, zeros behind the first n.
+// A row with a NaN or an infinity gets scale NaN and q = 0.
+template <typename T, int TPR, int CH>
+__global__ void __launch_bounds__(256) quantize_kernel(const T* __restrict__ X, long long rows, int n, long long ldx,
+                                                       int8_t* __restrict__ Q, long long ldq, int np,
+                                                       float* __restrict__ scale) {
+  constexpr int RPW = 256 / TPR;
+  __shared__ unsigned wmx[4];
+  const int tid = threadIdx.x % TPR;
+  const long long row = (long long)blockIdx.x * RPW + threadIdx.x / TPR;
+  const long long rr = row < rows ? row : rows - 1;
+  const T* x = X + rr * ldx;
+  float v[CH][8];
+  unsigned mx = 0u;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int j = (c * TPR + tid) * 8;
+    if (j + 8 <= n) load8(x + j, v[c]);
+    else load8_tail(x + j, (long long)n - j, v[c]);
+  }
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const unsigned b = __float_as_uint(v[c][e]) & 0x7FFFFFFFu;
+      mx = b > mx ? b : mx;
+    }
+  for (long long j = (long long)(CH * TPR + tid) * 8; j < n; j += TPR * 8) {
+    float w[8];
+    if (j + 8 <= n) load8(x + j, w);
+    else load8_tail(x + j, n - j, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const unsigned b = __float_as_uint(w[e]) & 0x7FFFFFFFu;
+      mx = b > mx ? b : mx;
+    }
+  }
+  mx = wave_max_u32(mx);
+  if (TPR == 256) {
+    if ((threadIdx.x & 63) == 0) wmx[threadIdx.x >> 6] = mx;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 4; ++w) mx = wmx[w] > mx ? wmx[w] : mx;
+  }
+  if (row >= rows) return;
+  const bool bad = mx >= 0x7F800000u;
+  const float a = __uint_as_float(mx);
+  const bool tiny = mx < 0x0D000000u;  // a < 2^-101
+  const float inv = bad || mx == 0u ? 0.0f : 127.0f / a;
+  if (tid == 0) scale[row] = bad ? __uint_as_float(0x7FC00000u) : a / 127.0f;
+  int8_t* q = Q + row * ldq;
+  auto emit = [&](long long j, const float (&w)[8]) {
+    int k[8];
+    if (bad || mx == 0u) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) k[e] = 0;
+    } else if (tiny) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) k[e] = quant1_small(w[e], a);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) k[e] = quant1(w[e], inv, a);
+    }
+    if (j + 8 <= np) {
+      iv2_any o;
+      o[0] = (int)pack4(k[0], k[1], k[2], k[3]);
+      o[1] = (int)pack4(k[4], k[5], k[6], k[7]);
+      *reinterpret_cast<iv2_any*>(q + j) = o;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (j + e < np) q[j + e] = (int8_t)k[e];
+    }
+  };
+#pragma unroll
+  for (int c = 0; c < CH; ++c) emit((long long)(c * TPR + tid) * 8, v[c]);
+  for (long long j = (long long)(CH * TPR + tid) * 8; j < np; j += TPR * 8) {
+    float w[8];
+    if (j + 8 <= n) load8(x + j, w);
+    else load8_tail(x + j, n - j, w);
+    emit(j, w);
+  }
+}
+
+template <typename T>
+static hipError_t quantize_typed(const T* X, long long rows, int n, long long ldx, int8_t* Q, long long ldq, int np,
+                                 float* scale, hipStream_t st) {
+  if (n <= 64 * 8 * 2) {
+    hipLaunchKernelGGL((quantize_kernel<T, 64, 2>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, st, X, rows, n, ldx,
+                       Q, ldq, np, scale);
+  } else {
+    hipLaunchKernelGGL((quantize_kernel<T, 256, 5>), dim3((unsigned)rows), dim3(256), 0, st, X, rows, n, ldx, Q, ldq,
+                       np, scale);
+  }
+  return hipGetLastError();
+}
+
+hipError_t quantize_run(const void* X, int type, long long rows, int n, long long ldx, int8_t* Q, long long ldq, int np,
+                        float* scale, hipStream_t st) {
+  switch (type) {
+    case 0: return quantize_typed(static_cast<const float*>(X), rows, n, ldx, Q, ldq, np, scale, st);
+    case 1: return quantize_typed(static_cast<const _Float16*>(X), rows, n, ldx, Q, ldq, np, scale, st);
+    case 2: return quantize_typed(static_cast<const __bf16*>(X), rows, n, ldx, Q, ldq, np, scale, st);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+// ---- operand loads ----------------------------------------------------------------------------
+// 16 bytes of a row at k, zeros from the row's end on
+__device__ __forceinline__ iv4 row16(const int8_t* __restrict__ row, int k, int n) {
+  if (k + 16 <= n) return *reinterpret_cast<const iv4_any*>(row + k);
+  iv4 v = {0, 0, 0, 0};
+#pragma unroll
+  for (int e = 0; e < 16; ++e)
+    if (k + e < n) v[e >> 2] |= (int)((unsigned)(unsigned char)row[k + e] << (8 * (e & 3)));
+  return v;
+}
+
+template <typename T>
+__device__ __forceinline__ void store_y(T* p, float v) {
+  *p = (T)v;
+}
+
+// ---- few tokens -------------------------------------------------------------------------------
+// Workgroup: 16 output channels, all tokens (at most 16 NT), the row length split over eight waves
+// in steps of 64 bytes.  MFMA D(16 x 16) += A(16 x 64) B(64 x 16): A row = channel, B column =
+// token, lane l holding the 16 bytes at 16 (l / 16) of row (column) l % 16 of the step.  The waves'
+// partial tiles add in LDS.
+constexpr int kFewWaves = 8;
+template <int NT, typename YT>
+__global__ void __launch_bounds__(64 * kFewWaves) few_kernel(const int8_t* __restrict__ W, long long ldw, int m, int n,
+                                                             const float* __restrict__ sw,
+                                                             const int8_t* __restrict__ Xq, long long ldx, int tokens,
+                                                             const float* __restrict__ sx, YT* __restrict__ Y,
+                                                             long long ldy) {
+  __shared__ int red[kFewWaves][NT * 256];
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, lr = lane & 15, gg = lane >> 4;
+  const int r0 = blockIdx.x * 16;
+  const int r = r0 + lr < m ? r0 + lr : m - 1;
+  const int8_t* wr = W + (long long)r * ldw;
+  const int8_t* xr[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int c = 16 * t + lr < tokens ? 16 * t + lr : tokens - 1;
+    xr[t] = Xq + (long long)c * ldx;
+  }
+  iv4 acc[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) acc[t] = iv4{0, 0, 0, 0};
+  const int full = n / 64;
+  int s = wv;
+  constexpr int U = 4;
+  for (; s + (U - 1) * kFewWaves < full; s += U * kFewWaves) {
+    iv4 a[U], b[U][NT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = 64 * (s + u * kFewWaves) + 16 * gg;
+      a[u] = *reinterpret_cast<const iv4_any*>(wr + k);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) b[u][t] = *reinterpret_cast<const iv4_any*>(xr[t] + k);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[u], b[u][t], acc[t], 0, 0, 0);
+  }
+  for (; 64 * s < n; s += kFewWaves) {
+    const int k = 64 * s + 16 * gg;
+    const iv4 a = row16(wr, k, n);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, row16(xr[t], k, n), acc[t], 0, 0, 0);
+  }
+  // acc[t][q] = D(channel 4 gg + q, token lr): stored token-major
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) red[wv][t * 256 + lr * 16 + 4 * gg + q] = acc[t][q];
+  __syncthreads();
+  for (int x = tid; x < NT * 256; x += 64 * kFewWaves) {
+    const int tok = x >> 4, o = r0 + (x & 15);
+    if (tok < tokens && o < m) {
+      int sum = 0;
+#pragma unroll
+      for (int w = 0; w < kFewWaves; ++w) sum += red[w][x];
+      store_y(Y + (long long)tok * ldy + o, (float)sum * sx[tok] * sw[o]);
+    }
+  }
+}
+
+// ---- many tokens ------------------------------------------------------------------------------
+// Workgroup: a BM x BN tile of Y (tokens x channels), WR x WC waves, each with FM x FN accumulators
+// of v_mfma_i32_32x32x32_i8 (A row = token l % 32, B column = channel l % 32, both with the 16 bytes
+// at 16 (l / 32) of the step; accumulator element i of lane l is row 8 (i / 4) + 4 (l / 32) + i % 4,
+// column l % 32).  The tiles' rows pass through LDS 128 bytes at a time, double buffered: the loads
+// of the next 128 bytes go out before the products of these, and are stored to the other buffer
+// after them.  The 16-byte piece c of row r sits at c ^ (r / 2 % 8), so that 16 consecutive rows'
+// pieces of one column lie in different banks.
+template <int BM, int BN, int WR, int WC, typename EPI>
+__global__ void __launch_bounds__(64 * WR * WC) tile_kernel(const int8_t* __restrict__ A, long long lda, int M,
+                                                            const int8_t* __restrict__ B, long long ldb, int N, int K,
+                                                            int ntm, int ntn, EPI epi) {
+  constexpr int NTHR = 64 * WR * WC, PA = BM * 8 / NTHR, PB = BN * 8 / NTHR;
+  constexpr int FM = BM / WR / 32, FN = BN / WC / 32;
+  __shared__ __attribute__((aligned(16))) int8_t la[2][BM * 128];
+  __shared__ __attribute__((aligned(16))) int8_t lb[2][BN * 128];
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  const int wr = wv / WC, wc = wv % WC;
+  // workgroups go round the eight XCDs: each XCD gets a run of neighbouring tiles, so that its L2
+  // holds the rows that they share
+  const int total = ntm * ntn, per = (total + 7) / 8, rem = total % 8;
+  const int xcd = blockIdx.x % 8, at = blockIdx.x / 8;
+  const int tile = rem == 0 || xcd < rem ? xcd * per + at : rem * per + (xcd - rem) * (per - 1) + at;
+  const int tm = tile % ntm, tn = tile / ntm;
+  const long long m0 = (long long)tm * BM, n0 = (long long)tn * BN;
+  const int8_t* ap[PA];
+  const int8_t* bp[PB];
+  int ao[PA], bo[PB];
+#pragma unroll
+  for (int p = 0; p < PA; ++p) {
+    const int x = tid + NTHR * p, r = x >> 3, c = x & 7;
+    const long long row = m0 + r < M ? m0 + r : M - 1;
+    ap[p] = A + row * lda;
+    ao[p] = r * 128 + ((c ^ ((r >> 1) & 7)) << 4);
+  }
+#pragma unroll
+  for (int p = 0; p < PB; ++p) {
+    const int x = tid + NTHR * p, r = x >> 3, c = x & 7;
+    const long long row = n0 + r < N ? n0 + r : N - 1;
+    bp[p] = B + row * ldb;
+    bo[p] = r * 128 + ((c ^ ((r >> 1) & 7)) << 4);
+  }
+  const int kc = (tid & 7) * 16;  // this thread's piece within each 128 bytes
+  iv4 sa[PA], sb[PB];
+  auto fetch = [&](int k0) {
+    if (k0 + 128 <= K) {
+#pragma unroll
+      for (int p = 0; p < PA; ++p) sa[p] = *reinterpret_cast<const iv4_any*>(ap[p] + k0 + kc);
+#pragma unroll
+      for (int p = 0; p < PB; ++p) sb[p] = *reinterpret_cast<const iv4_any*>(bp[p] + k0 + kc);
+    } else {
+#pragma unroll
+      for (int p = 0; p < PA; ++p) sa[p] = row16(ap[p], k0 + kc, K);
+#pragma unroll
+      for (int p = 0; p < PB; ++p) sb[p] = row16(bp[p], k0 + kc, K);
+    }
+  };
+  auto put = [&](int buf) {
+#pragma unroll
+    for (int p = 0; p < PA; ++p) *reinterpret_cast<iv4*>(la[buf] + ao[p]) = sa[p];
+#pragma unroll
+    for (int p = 0; p < PB; ++p) *reinterpret_cast<iv4*>(lb[buf] + bo[p]) = sb[p];
+  };
+  iv16 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
+  const int nk = (K + 127) / 128;
+  const int lr = lane & 31, lg = lane >> 5;
+  const int ra = wr * (BM / WR) + lr, rb = wc * (BN / WC) + lr;  // rows r + 32 f share r / 2 % 8
+  const int za = (ra >> 1) & 7, zb = (rb >> 1) & 7;
+  fetch(0);
+  put(0);
+  __syncthreads();
+  for (int t = 0; t < nk; ++t) {
+    const int buf = t & 1;
+    if (t + 1 < nk) fetch(128 * (t + 1));
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      iv4 fa[FM], fb[FN];
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+        fa[i] = *reinterpret_cast<const iv4*>(la[buf] + (ra + 32 * i) * 128 + (((2 * ks + lg) ^ za) << 4));
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        fb[j] = *reinterpret_cast<const iv4*>(lb[buf] + (rb + 32 * j) * 128 + (((2 * ks + lg) ^ zb) << 4));
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[i], fb[j], acc[i][j], 0, 0, 0);
+    }
+    if (t + 1 < nk) put(buf ^ 1);
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+      epi(m0 + wr * (BM / WR) + 32 * i + 4 * lg, n0 + wc * (BN / WC) + 32 * j + lr, M, N, acc[i][j]);
+}
+
+// y = sum s_t w_o: the lane holds rows row + 8 (i / 4) + i % 4 of column col
+template <typename YT>
+struct ScaledY {
+  const float* sx;
+  const float* sw;
+  YT* Y;
+  long long ldy;
+  __device__ __forceinline__ void operator()(long long row, long long col, int M, int N, const iv16& acc) const {
+    if (col >= N) return;
+    const float w = sw[col];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const long long r = row + 8 * (e >> 2) + (e & 3);
+      if (r < M) store_y(Y + r * ldy + col, (float)acc[e] * sx[r] * w);
+    }
+  }
+};
+
+template <typename YT>
+static hipError_t product_typed(const int8_t* W, const float* sw, int m, int n, long long ldw, const int8_t* Xq,
+                                const float* sx, int tokens, long long ldx, YT* Y, long long ldy, hipStream_t st) {
+  const unsigned few = (unsigned)((m + 15) / 16);
+  if (tokens <= 16) {
+    hipLaunchKernelGGL((few_kernel<1, YT>), dim3(few), dim3(64 * kFewWaves), 0, st, W, ldw, m, n, sw, Xq, ldx, tokens,
+                       sx, Y, ldy);
+  } else if (tokens <= 32) {
+    hipLaunchKernelGGL((few_kernel<2, YT>), dim3(few), dim3(64 * kFewWaves), 0, st, W, ldw, m, n, sw, Xq, ldx, tokens,
+                       sx, Y, ldy);
+  } else {
+    const ScaledY<YT> epi{sx, sw, Y, ldy};
+    const long long ntm = (tokens + 127) / 128, ntn = (m + 127ll) / 128;
+    if (ntm * ntn > 2147483647ll) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((tile_kernel<128, 128, 2, 2, ScaledY<YT>>), dim3((unsigned)(ntm * ntn)), dim3(256), 0, st, Xq,
+                       ldx, tokens, W, ldw, m, n, (int)ntm, (int)ntn, epi);
+  }
+  return hipGetLastError();
+}
+
+// Workspace of a product whose tokens come as floating-point rows: their scales and their
+// quantised rows, padded to a multiple of 16 bytes.
+static size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
+static long long pad16(long long n) { return (n + 15) & ~15ll; }
+size_t product_workspace_bytes(int x_type, long long tokens, int n) {
+  return x_type == 3 ? 0 : al256((size_t)tokens * 4) + al256((size_t)tokens * pad16(n));
+}
+
+hipError_t product_run(const int8_t* W, const float* sw, int m, int n, long long ldw, const void* X, int x_type,
+                       const float* sx, int tokens, long long ldx, void* Y, int y_type, long long ldy, void* ws,
+                       hipStream_t st) {
+  const int8_t* Xq = static_cast<const int8_t*>(X);
+  if (x_type != 3) {
+    float* scale = static_cast<float*>(ws);
+    int8_t* q = static_cast<int8_t*>(ws) + al256((size_t)tokens * 4);
+    const long long np = pad16(n);
+    const hipError_t e = quantize_run(X, x_type, tokens, n, ldx, q, np, (int)np, scale, st);
+    if (e != hipSuccess) return e;
+    Xq = q;
+    sx = scale;
+    ldx = np;
+  }
+  switch (y_type) {
+    case 0: return product_typed(W, sw, m, n, ldw, Xq, sx, tokens, ldx, static_cast<float*>(Y), ldy, st);
+    case 1: return product_typed(W, sw, m, n, ldw, Xq, sx, tokens, ldx, static_cast<_Float16*>(Y), ldy, st);
+    case 2: return product_typed(W, sw, m, n, ldw, Xq, sx, tokens, ldx, static_cast<__bf16*>(Y), ldy, st);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace externd

@@ -1,0 +1,63 @@
+// Element types of the entry points that take more than fp32, and unaligned 16-byte access.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace externd {
+
+typedef int iv4 __attribute__((ext_vector_type(4)));
+typedef int iv16 __attribute__((ext_vector_type(16)));
+typedef float fv4 __attribute__((ext_vector_type(4)));
+// The same vectors at any byte address: gfx950 loads and stores them with one instruction at every
+// alignment, so rows of odd length need no path of their own.
+typedef int iv4_any __attribute__((ext_vector_type(4), aligned(1)));
+typedef int iv2_any __attribute__((ext_vector_type(2), aligned(1)));
+
+// Element types by their number in the C ABI (EXTERND_F32, EXTERND_F16, EXTERND_BF16).
+template <int TYPE>
+struct Elem;
+template <>
+struct Elem<0> {
+  typedef float type;
+};
+template <>
+struct Elem<1> {
+  typedef _Float16 type;
+};
+template <>
+struct Elem<2> {
+  typedef __bf16 type;
+};
+
+// 8 consecutive elements as fp32
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const iv4 a = *reinterpret_cast<const iv4_any*>(p), b = *reinterpret_cast<const iv4_any*>(p + 4);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    v[e] = __int_as_float(a[e]);
+    v[4 + e] = __int_as_float(b[e]);
+  }
+}
+__device__ __forceinline__ void load8(const _Float16* p, float (&v)[8]) {
+  typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+  const h8 h = __builtin_bit_cast(h8, (iv4)*reinterpret_cast<const iv4_any*>(p));
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = (float)h[e];
+}
+__device__ __forceinline__ void load8(const __bf16* p, float (&v)[8]) {
+  const iv4 a = *reinterpret_cast<const iv4_any*>(p);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    v[2 * e] = __int_as_float(a[e] << 16);
+    v[2 * e + 1] = __int_as_float(a[e] & (int)0xFFFF0000);
+  }
+}
+
+// the first `count` of 8 consecutive elements, zeros behind them
+template <typename T>
+__device__ __forceinline__ void load8_tail(const T* p, long long count, float (&v)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = e < count ? (float)p[e] : 0.0f;
+}
+
+}  // namespace externd

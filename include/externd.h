@@ -15,7 +15,8 @@
  *  - Array pointers are HIP device pointers on the current device unless marked (host).
  *  - Matrices are dense row-major fp32 with leading dimension equal to their column count.
  *  - The caller owns and allocates every argument buffer; inputs must not alias outputs.
- *  - Calls are synchronous: they return after all work issued on `stream` has completed.
+ *  - Calls are synchronous: they return after all work issued on `stream` has completed, except
+ *    the inference, quantisation, distillation and gradient entries, which only enqueue.
  *  - On a nonzero status the output contents are unspecified; externd_last_error() returns a
  *    thread-local message describing the failure.  No C++ exception crosses the ABI.
  *  - Packed ternary vectors: element t sits in bits 2(t%16)..2(t%16)+1 of 32-bit word t/16;
@@ -200,6 +201,54 @@ int externd_apply_factors(const uint32_t* B_packed, const uint32_t* C_packed, co
  * EXTERND_EDEVICE for HIP errors. */
 int externd_apply_factors_static(const uint32_t* B_packed, const uint32_t* C_packed, const float* D, int64_t k,
                                  int64_t m, int64_t n, const float* X, int64_t batch, float* Y, void* stream);
+
+/* ---- Layers kept in 8-bit integers --------------------------------------------------------
+ * The entries from here to externd_status_string serve and repair a model beside its factored
+ * layers.  They only enqueue kernels on `stream` and return without waiting, allocate nothing,
+ * keep nothing between calls, may be captured into a HIP graph, and may run at once on different
+ * streams as long as the calls' workspaces differ.  Rows may be strided: an ld argument is the
+ * distance between the starts of two rows in elements, at least the row's length.  No alignment
+ * beyond the element type's own is asked for.  A count of 0 rows (tokens, vectors) is valid and
+ * leaves nothing to do.  Statuses as for externd_apply_factors. */
+
+/* Element types of the arguments marked x_type, y_type, ... */
+#define EXTERND_F32 0
+#define EXTERND_F16 1
+#define EXTERND_BF16 2
+#define EXTERND_I8 3
+
+/* Rows to 8-bit integers, one scale a row (tokens of an activation, output channels of a weight
+ * matrix):  a = max_j |X[r][j]|,  scale[r] = a / 127 rounded once to fp32,  Q[r][j] = the whole
+ * number nearest to the exact quotient 127 X[r][j] / a, ties to even (-127 .. 127).  A row of
+ * zeros gets scale 0 and zeros; a row with a NaN or an infinity gets scale NaN and zeros.
+ *   X      rows x n of x_type (EXTERND_F32, _F16 or _BF16), row distance ldx
+ *   Q      rows x n int8, row distance ldq
+ *   scale  rows fp32
+ * 0 <= rows < 2^31, 1 <= n < 2^31 - 4096. */
+int externd_quantize_rows(const void* X, int x_type, int64_t rows, int64_t n, int64_t ldx, int8_t* Q, int64_t ldq,
+                          float* scale, void* stream);
+
+/* Inference through a layer in 8-bit integers, a scale for each token and each output channel:
+ *   Y[t][o] = x_scale[t] w_scale[o] sum_j Xq[t][j] W[o][j]
+ * The sum is exact (int32), so the result does not depend on the launch shape; it is converted to
+ * fp32 and multiplied by the two scales in fp32, and rounded once to y_type.
+ *   W        m x n int8 (device), row distance ldw: one row per output channel
+ *   w_scale  m fp32
+ *   X        tokens x n, row distance ldx, of x_type: EXTERND_I8 with x_scale (tokens fp32) given,
+ *            or EXTERND_F32, _F16, _BF16 with x_scale NULL: the tokens are then quantised on the
+ *            way exactly as externd_quantize_rows does (a token with a NaN or an infinity gives a
+ *            row of NaN)
+ *   Y        tokens x m of y_type (EXTERND_F32, _F16 or _BF16), row distance ldy
+ *   workspace  externd_apply_quantized_workspace(x_type, tokens, n) bytes, 16-byte aligned (NULL
+ *            where that is 0), used by this call alone until it has run
+ * 0 <= tokens < 2^31, 1 <= m < 2^31, 1 <= n <= 131071 (the largest n whose sum of products of
+ * 8-bit integers fits int32). */
+int externd_apply_quantized(const int8_t* W, const float* w_scale, int64_t m, int64_t n, int64_t ldw, const void* X,
+                            int x_type, const float* x_scale, int64_t tokens, int64_t ldx, void* Y, int y_type,
+                            int64_t ldy, void* workspace, void* stream);
+
+/* Bytes of workspace externd_apply_quantized needs; -1 for sizes or a type it refuses. */
+int64_t externd_apply_quantized_workspace(int x_type, int64_t tokens, int64_t n);
 
 /* Human-readable name of a status code (static string). */
 const char* externd_status_string(int status);
