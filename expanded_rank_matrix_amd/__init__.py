@@ -93,6 +93,14 @@ def load():
                                                 i64, vp, vp]
         lib.externd_apply_quantized_workspace.restype = i64
         lib.externd_apply_quantized_workspace.argtypes = [ci, i64, i64]
+        lib.externd_distill_loss.restype = ci
+        lib.externd_distill_loss.argtypes = [vp, ci, i64, i64, i64, vp, ci, vp, ci, i64, f32, vp, vp, vp,
+                                             vp, i64, vp, vp]
+        lib.externd_distill_workspace.restype = i64
+        lib.externd_distill_workspace.argtypes = [i64, i64]
+        lib.externd_distill_grad.restype = ci
+        lib.externd_distill_grad.argtypes = [vp, ci, i64, i64, i64, vp, vp, ci, vp, ci, i64, f32, vp, vp,
+                                             i64, vp]
         lib.externd_status_string.restype = ctypes.c_char_p
         lib.externd_status_string.argtypes = [ci]
         lib.externd_last_error.restype = ctypes.c_char_p
@@ -439,6 +447,81 @@ def apply_quantized(W, w_scale, X, x_scale=None, out_dtype=None, stream=None, ou
             None if x_scale is None else x_scale.data_ptr(), tokens, ldx, Y.data_ptr(), types[out_dtype], ldy,
             None if ws is None else ws.data_ptr(), run.ptr))
     return Y[0] if single else Y
+
+
+def _distill_args(logits, teacher, index, weight, name, out):
+    """Validated (ldz, ldd, index_bytes) of the distillation entry points."""
+    import torch
+
+    ldz = _rows(logits, _float_types(), "logits")
+    rows, vocab = logits.shape
+    dev = logits.device
+    _require(teacher, _float_types(), "teacher", device=dev)
+    if teacher.dim() != 2 or teacher.shape[0] != rows:
+        raise ValueError(f"teacher must be rows x top with rows = {rows}")
+    _require(index, (torch.int32, torch.int64), "index", shape=teacher.shape, device=dev)
+    _require(weight, torch.float32, name, shape=(rows,), device=dev)
+    ldd = vocab
+    if out is not None:
+        ldd = _rows(out, (logits.dtype,), "out", shape=(rows, vocab), device=dev)
+    return ldz, ldd, index.element_size()
+
+
+def distill_loss(logits, teacher, index, temperature: float = 1.0, weight=None, grad: bool = False,
+                 stream=None, out=None):
+    """Distillation of a student from a teacher's top logits: for each row (token)
+    loss = weight T^2 sum_k p_k (log p_k - log q[index_k]), p the softmax of the row's valid
+    teacher logits / T, q the softmax of all its logits / T.
+
+    logits (rows x vocab, fp32, fp16 or bf16; rows may be strided), teacher (rows x top, any of
+    these types) and index (rows x top, int32 or int64; an entry outside the vocabulary, such as -1,
+    or with a teacher logit of -inf does not count), weight (rows fp32; rows of weight 0 are not
+    read).  Returns (loss fp32 rows, stats fp32 rows x 2); with ``grad`` or ``out`` also dlogits, the
+    gradient of the losses' sum, formed in the same call (``out`` may be a preallocated tensor, or
+    logits itself).  ``stats`` feeds ``distill_grad``.  Enqueued on the stream without waiting."""
+    import torch
+
+    types = _types()
+    ldz, ldd, ib = _distill_args(logits, teacher, index, weight, "weight", out)
+    rows, vocab = logits.shape
+    dev = logits.device
+    lib = load()
+    with _Run(dev, stream, (logits, teacher, index, weight, out)) as run:
+        loss = torch.empty(rows, dtype=torch.float32, device=dev)
+        stats = torch.empty((rows, 2), dtype=torch.float32, device=dev)
+        if out is None and grad:
+            out = torch.empty((rows, vocab), dtype=logits.dtype, device=dev)
+        size = lib.externd_distill_workspace(rows, vocab)
+        ws = torch.empty(size, dtype=torch.uint8, device=dev) if size > 0 else None
+        _check(lib.externd_distill_loss(
+            logits.data_ptr(), types[logits.dtype], rows, vocab, ldz, teacher.data_ptr(), types[teacher.dtype],
+            index.data_ptr(), ib, teacher.shape[1], temperature, None if weight is None else weight.data_ptr(),
+            loss.data_ptr(), stats.data_ptr(), None if out is None else out.data_ptr(), ldd,
+            None if ws is None else ws.data_ptr(), run.ptr))
+    return (loss, stats) if out is None else (loss, stats, out)
+
+
+def distill_grad(logits, stats, teacher, index, temperature: float = 1.0, grad_loss=None, stream=None,
+                 out=None):
+    """The gradient of ``distill_loss`` from its ``stats`` on the same logits:
+    dlogits[r][v] = grad_loss[r] T (q[v] - sum of p_k with index_k = v), of logits' type; grad_loss
+    (rows fp32, 1 where None) takes the weight's place, and a row where it is 0 is not read.  ``out``
+    may be a preallocated tensor, or logits itself.  Enqueued on the stream without waiting."""
+    import torch
+
+    types = _types()
+    ldz, ldd, ib = _distill_args(logits, teacher, index, grad_loss, "grad_loss", out)
+    rows, vocab = logits.shape
+    dev = logits.device
+    _require(stats, torch.float32, "stats", shape=(rows, 2), device=dev)
+    with _Run(dev, stream, (logits, stats, teacher, index, grad_loss, out)) as run:
+        if out is None:
+            out = torch.empty((rows, vocab), dtype=logits.dtype, device=dev)
+        _check(load().externd_distill_grad(
+            logits.data_ptr(), types[logits.dtype], rows, vocab, ldz, stats.data_ptr(), teacher.data_ptr(),
+            types[teacher.dtype], index.data_ptr(), ib, teacher.shape[1], temperature,
+            None if grad_loss is None else grad_loss.data_ptr(), out.data_ptr(), ldd, run.ptr))
+    return out
 
 
 def unpack(packed, length: int) -> np.ndarray:

@@ -530,4 +530,66 @@ int externd_apply_quantized(const int8_t* W, const float* w_scale, int64_t m, in
   return EXTERND_OK;
 }
 
+// ---- distillation on a teacher's top logits
+
+constexpr int64_t kMaxVocab = (int64_t)1 << 30;
+constexpr int64_t kMaxTop = 1024;
+
+int64_t externd_distill_workspace(int64_t rows, int64_t vocab) {
+  if (rows < 0 || rows > kMaxCount || vocab < 1 || vocab > kMaxVocab) return -1;
+  return (int64_t)distill_workspace_bytes(rows, (int)vocab);
+}
+
+// what both directions check; 1 where there is nothing to do
+static int distill_checks(const void* logits, int z_type, int64_t rows, int64_t vocab, int64_t ldz, const void* teacher,
+                          int t_type, const void* index, int index_bytes, int64_t top, float temperature) {
+  if (!float_type(z_type) || !float_type(t_type))
+    return fail(EXTERND_EINVAL, "z_type and t_type must be EXTERND_F32, EXTERND_F16 or EXTERND_BF16");
+  if (index_bytes != 4 && index_bytes != 8) return fail(EXTERND_EINVAL, "index_bytes must be 4 or 8");
+  if (rows < 0 || rows > kMaxCount) return fail(EXTERND_EINVAL, "need 0 <= rows < 2^31");
+  if (vocab < 1 || vocab > kMaxVocab) return fail(EXTERND_EINVAL, "need 1 <= vocab <= 2^30");
+  if (top < 1 || top > kMaxTop) return fail(EXTERND_EINVAL, "need 1 <= top <= %lld", (long long)kMaxTop);
+  if (ldz < vocab || ldz > kMaxLd) return fail(EXTERND_EINVAL, "ldz must be at least vocab (and at most 2^40)");
+  if (!std::isfinite(temperature) || temperature < 1e-3f || temperature > 1e3f)
+    return fail(EXTERND_EINVAL, "temperature must be in [1e-3, 1e3]");
+  if (rows == 0) return 1;
+  if (!logits || !teacher || !index) return fail(EXTERND_EINVAL, "null pointer argument");
+  return EXTERND_OK;
+}
+
+int externd_distill_loss(const void* logits, int z_type, int64_t rows, int64_t vocab, int64_t ldz, const void* teacher,
+                         int t_type, const void* index, int index_bytes, int64_t top, float temperature,
+                         const float* weight, float* loss, float* stats, void* dlogits, int64_t ldd, void* workspace,
+                         void* stream) {
+  g_last_error.clear();
+  const int rc = distill_checks(logits, z_type, rows, vocab, ldz, teacher, t_type, index, index_bytes, top, temperature);
+  if (rc < 0) return rc;
+  if (dlogits && (ldd < vocab || ldd > kMaxLd)) return fail(EXTERND_EINVAL, "ldd must be at least vocab (and at most 2^40)");
+  if (rc == 1) return EXTERND_OK;
+  if (!loss || !stats) return fail(EXTERND_EINVAL, "null pointer argument");
+  if (dlogits == logits && ldd != ldz) return fail(EXTERND_EINVAL, "a gradient in the logits' place needs ldd = ldz");
+  if (distill_workspace_bytes(rows, (int)vocab) > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15)))
+    return fail(EXTERND_EINVAL, "workspace of externd_distill_workspace() bytes, 16-byte aligned, is needed");
+  const DistillLaunch L{logits, teacher, index, weight, loss, stats, dlogits, workspace, rows, ldz, ldd,
+                        (int)vocab, (int)top, z_type, t_type, index_bytes, temperature};
+  HIP_OR_FAIL(distill_run(L, reinterpret_cast<hipStream_t>(stream)));
+  return EXTERND_OK;
+}
+
+int externd_distill_grad(const void* logits, int z_type, int64_t rows, int64_t vocab, int64_t ldz, const float* stats,
+                         const void* teacher, int t_type, const void* index, int index_bytes, int64_t top,
+                         float temperature, const float* grad_loss, void* dlogits, int64_t ldd, void* stream) {
+  g_last_error.clear();
+  const int rc = distill_checks(logits, z_type, rows, vocab, ldz, teacher, t_type, index, index_bytes, top, temperature);
+  if (rc < 0) return rc;
+  if (ldd < vocab || ldd > kMaxLd) return fail(EXTERND_EINVAL, "ldd must be at least vocab (and at most 2^40)");
+  if (rc == 1) return EXTERND_OK;
+  if (!stats || !dlogits) return fail(EXTERND_EINVAL, "null pointer argument");
+  if (dlogits == logits && ldd != ldz) return fail(EXTERND_EINVAL, "a gradient in the logits' place needs ldd = ldz");
+  const DistillLaunch L{logits, teacher, index, grad_loss, nullptr, const_cast<float*>(stats), dlogits, nullptr, rows, ldz,
+                        ldd, (int)vocab, (int)top, z_type, t_type, index_bytes, temperature};
+  HIP_OR_FAIL(distill_run(L, reinterpret_cast<hipStream_t>(stream)));
+  return EXTERND_OK;
+}
+
 }  // extern "C"

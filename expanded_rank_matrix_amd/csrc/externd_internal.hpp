@@ -101,4 +101,22 @@ hipError_t product_run(const int8_t* W, const float* sw, int m, int n, long long
                        const float* sx, int tokens, long long ldx, void* Y, int y_type, long long ldy, void* ws,
                        hipStream_t st);
 
+// Distillation on a teacher's top logits (distill.hip).  loss null: the gradient from given stats
+// (weight is then the loss's gradient); else loss and stats, and the gradient where dlogits is given.
+struct DistillLaunch {
+  const void* logits;
+  const void* teacher;
+  const void* index;
+  const float* weight;
+  float* loss;
+  float* stats;
+  void* dlogits;
+  void* ws;
+  long long rows, ldz, ldd;
+  int vocab, top, z_type, t_type, index_bytes;
+  float temperature;
+};
+size_t distill_workspace_bytes(long long rows, int V);
+hipError_t distill_run(const DistillLaunch& L, hipStream_t st);
+
 }  // namespace externd

@@ -250,6 +250,49 @@ int externd_apply_quantized(const int8_t* W, const float* w_scale, int64_t m, in
 /* Bytes of workspace externd_apply_quantized needs; -1 for sizes or a type it refuses. */
 int64_t externd_apply_quantized_workspace(int x_type, int64_t tokens, int64_t n);
 
+/* ---- Distillation on a teacher's top logits -----------------------------------------------
+ * The loss that repairs a factored model's outputs: for each row (token) the divergence of the
+ * student's distribution q over the whole vocabulary from the teacher's p over its top entries,
+ *   p = softmax of teacher[k] / T over the row's valid entries k,   q = softmax of logits / T,
+ *   loss = weight T^2 sum_k p_k (log p_k - log q[index[k]]).
+ * An entry is valid if 0 <= index < vocab and its teacher logit is above -inf; the others (shorter
+ * lists: index -1) do not count.  One index may come several times in a row.  A row without a
+ * valid entry has loss 0 and gradient 0.  A row of weight 0 is not read: its loss, statistics and
+ * gradient are 0.  Logits of -inf have q = 0 (a valid entry of p > 0 there gives loss +inf); a row
+ * whose logits hold NaN or +inf, or are all -inf, gives NaN, and so do a NaN or +inf among its
+ * valid teacher logits.
+ *   logits       rows x vocab of z_type (EXTERND_F32, _F16, _BF16), row distance ldz
+ *   teacher      rows x top of t_type (one of the same), dense
+ *   index        rows x top int32 (index_bytes 4) or int64 (8), dense
+ *   temperature  T in [1e-3, 1e3]
+ *   weight       rows fp32, or NULL for 1
+ *   loss         rows fp32
+ *   stats        rows x 2 fp32: the row's largest logit and the sum of exp((z - largest) / T) over
+ *                the vocabulary, for externd_distill_grad
+ *   dlogits      NULL, or rows x vocab of z_type, row distance ldd: the gradient of the losses' sum,
+ *                  weight T (q[v] - sum of p_k with index[k] = v),  0 in rows without valid entry.
+ *                It may be logits itself (with ldd = ldz), and must not overlap it otherwise.
+ *   workspace    externd_distill_workspace(rows, vocab) bytes, 16-byte aligned (NULL where that is
+ *                0), used by this call alone until it has run
+ * Statistics, sums and losses are kept in fp32 and fp64 as the row is read once; the gradient is
+ * rounded once to z_type; exp((z - largest) / T) below 2^-126 counts as 0.  Deterministic.  0 <= rows < 2^31, 1 <= vocab <= 2^30, 1 <= top <= 1024. */
+int externd_distill_loss(const void* logits, int z_type, int64_t rows, int64_t vocab, int64_t ldz, const void* teacher,
+                         int t_type, const void* index, int index_bytes, int64_t top, float temperature,
+                         const float* weight, float* loss, float* stats, void* dlogits, int64_t ldd, void* workspace,
+                         void* stream);
+
+/* Bytes of workspace externd_distill_loss needs; -1 for sizes it refuses. */
+int64_t externd_distill_workspace(int64_t rows, int64_t vocab);
+
+/* The gradient alone, from the stats of externd_distill_loss on the same logits:
+ *   dlogits[r][v] = grad_loss[r] T (q[v] - sum of p_k with index[k] = v)
+ * grad_loss (rows fp32, NULL for 1) takes the weights' place: a row where it is 0 is not read and
+ * gets 0.  Rows whose forward weight was 0 have no stats and must have grad_loss 0.  Arguments as
+ * for externd_distill_loss; dlogits may be logits itself (with ldd = ldz). */
+int externd_distill_grad(const void* logits, int z_type, int64_t rows, int64_t vocab, int64_t ldz, const float* stats,
+                         const void* teacher, int t_type, const void* index, int index_bytes, int64_t top,
+                         float temperature, const float* grad_loss, void* dlogits, int64_t ldd, void* stream);
+
 /* Human-readable name of a status code (static string). */
 const char* externd_status_string(int status);
 
