@@ -101,6 +101,10 @@ def load():
         lib.externd_distill_grad.restype = ci
         lib.externd_distill_grad.argtypes = [vp, ci, i64, i64, i64, vp, vp, ci, vp, ci, i64, f32, vp, vp,
                                              i64, vp]
+        lib.externd_apply_factors_grad.restype = ci
+        lib.externd_apply_factors_grad.argtypes = [vp, vp, vp, i64, i64, i64, vp, vp, i64, vp, vp, vp, vp]
+        lib.externd_apply_factors_grad_workspace.restype = i64
+        lib.externd_apply_factors_grad_workspace.argtypes = [i64, i64, i64, i64]
         lib.externd_status_string.restype = ctypes.c_char_p
         lib.externd_status_string.argtypes = [ci]
         lib.externd_last_error.restype = ctypes.c_char_p
@@ -294,6 +298,54 @@ def apply_factors_static(B, C, D, m: int, n: int, X, stream=None, out=None):
                                              X2.shape[0], _dev_ptr(Y), _stream_ptr(stream))
     _check(rc)
     return Y[0] if single else Y.reshape(X2.shape[0], m)
+
+
+def apply_factors_grad(B, C, D, m: int, n: int, X, dY, need_dX: bool = True, need_dD: bool = True,
+                       stream=None, out=None):
+    """Gradient of ``apply_factors`` at X (n or batch x n, fp32) for dY (m or batch x m, fp32): the
+    ternary factors are fixed, X and the scales have gradients,
+    dX = (C^T diag(D) B^T dY^T)^T and dD_i = sum over the batch of (C x)_i (B^T dy)_i.
+
+    Returns (dX, dD) (fp32; dX of X's shape), None for one that is not needed (X may be None where
+    dD is not needed).  ``out`` may supply the pair.  Enqueued on the stream without waiting."""
+    import torch
+
+    _require(D, torch.float32, "D")
+    if D.dim() != 1:
+        raise ValueError("D must be a vector of k scales")
+    k, dev = D.shape[0], D.device
+    words32 = (torch.int32, torch.uint32)
+    _require(B, words32, "B", shape=(k, packed_words(m)), device=dev)
+    _require(C, words32, "C", shape=(k, packed_words(n)), device=dev)
+    if not (need_dX or need_dD):
+        raise ValueError("need_dX or need_dD must be set")
+    _require(dY, torch.float32, "dY", device=dev)
+    single = dY.dim() == 1
+    if dY.dim() not in (1, 2) or dY.shape[-1] != m:
+        raise ValueError("dY must be m or batch x m")
+    batch = 1 if single else dY.shape[0]
+    lead = () if single else (batch,)
+    if X is None and need_dD:
+        raise ValueError("X is needed for dD")
+    _require(X, torch.float32, "X", shape=(*lead, n), device=dev)
+    lib = load()
+    with _Run(dev, stream, (B, C, D, X, dY, *(out or ()))) as run:
+        if out is None:
+            dX = torch.empty((*lead, n), dtype=torch.float32, device=dev) if need_dX else None
+            dD = torch.empty(k, dtype=torch.float32, device=dev) if need_dD else None
+        else:
+            dX, dD = (t if need else None for t, need in zip(out, (need_dX, need_dD)))
+            if (dX is None) == need_dX or (dD is None) == need_dD:
+                raise ValueError("out must hold dX and dD where they are needed")
+            _require(dX, torch.float32, "out[0]", shape=(*lead, n), device=dev)
+            _require(dD, torch.float32, "out[1]", shape=(k,), device=dev)
+        size = lib.externd_apply_factors_grad_workspace(k, m, n, batch)
+        ws = torch.empty(size, dtype=torch.uint8, device=dev) if size > 0 else None
+        _check(lib.externd_apply_factors_grad(
+            B.data_ptr(), C.data_ptr(), D.data_ptr(), k, m, n, None if X is None else X.data_ptr(), dY.data_ptr(),
+            batch, None if dX is None else dX.data_ptr(), None if dD is None else dD.data_ptr(),
+            None if ws is None else ws.data_ptr(), run.ptr))
+    return dX, dD
 
 
 class _Run:

@@ -592,4 +592,35 @@ int externd_distill_grad(const void* logits, int z_type, int64_t rows, int64_t v
   return EXTERND_OK;
 }
 
+// ---- gradient of the factored layer
+
+constexpr int64_t kMaxFactorLen = (int64_t)1 << 23;  // 128 len < 2^31: a digit's sum fits int32
+
+int64_t externd_apply_factors_grad_workspace(int64_t k, int64_t m, int64_t n, int64_t batch) {
+  if (k < 1 || m < 1 || n < 1 || k > kMaxFactorLen || m > kMaxFactorLen || n > kMaxFactorLen || batch < 0 ||
+      batch > kMaxCount)
+    return -1;
+  return (int64_t)grad_workspace_bytes((int)k, (int)m, (int)n, batch);
+}
+
+int externd_apply_factors_grad(const uint32_t* B_packed, const uint32_t* C_packed, const float* D, int64_t k, int64_t m,
+                               int64_t n, const float* X, const float* dY, int64_t batch, float* dX, float* dD,
+                               void* workspace, void* stream) {
+  g_last_error.clear();
+  if (k < 1 || m < 1 || n < 1 || k > kMaxFactorLen || m > kMaxFactorLen || n > kMaxFactorLen)
+    return fail(EXTERND_EINVAL, "need 1 <= k, m, n <= %lld", (long long)kMaxFactorLen);
+  if (batch < 0 || batch > kMaxCount) return fail(EXTERND_EINVAL, "need 0 <= batch < 2^31");
+  if (!dX && !dD) {
+    if (batch == 0) return EXTERND_OK;
+    return fail(EXTERND_EINVAL, "dX or dD must be given");
+  }
+  if (!B_packed || !C_packed || !D) return fail(EXTERND_EINVAL, "null pointer argument");
+  if (batch > 0 && (!dY || (dD && !X))) return fail(EXTERND_EINVAL, "null pointer argument");
+  if (batch > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15)))
+    return fail(EXTERND_EINVAL, "workspace of externd_apply_factors_grad_workspace() bytes, 16-byte aligned, is needed");
+  HIP_OR_FAIL(grad_run(B_packed, C_packed, D, (int)k, (int)m, (int)n, X, dY, batch, dX, dD, workspace,
+                       reinterpret_cast<hipStream_t>(stream)));
+  return EXTERND_OK;
+}
+
 }  // extern "C"

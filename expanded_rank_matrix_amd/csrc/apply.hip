@@ -107,11 +107,14 @@ __device__ __forceinline__ void fx_digits7(const unsigned long long (&b)[4], uns
 // (the 16 lanes of a group still read the word's 256 contiguous bytes; the builders' stores of one
 // column for 16 words fall in distinct banks).
 // smax[b gridDim.x + blockIdx.x] receives the workgroup's max |s_b| (high word of the fp64 bits).
+// RAW (the layer's gradient): t itself goes to Traw, and s only where S is given.
+template <bool RAW>
 __global__ void __launch_bounds__(kTThreads) infer_t_kernel(const uint32_t* __restrict__ C, int wn, int n,
                                                       const float* __restrict__ D, int k, const float* __restrict__ X,
                                                       int batch, int x_vec4, int c_vec4, double* __restrict__ S,
                                                       unsigned* __restrict__ smax, long long* __restrict__ Yacc,
-                                                      long long nY, unsigned* __restrict__ cnt, int ncnt) {
+                                                      long long nY, unsigned* __restrict__ cnt, int ncnt,
+                                                      double* __restrict__ Traw) {
   // every argument fetched at once (else the compiler waits for them one after another)
   asm volatile("" ::"s"(C), "s"(wn), "s"(n), "s"(D), "s"(k), "s"(X), "s"(batch), "s"(x_vec4), "s"(c_vec4), "s"(S),
                "s"(smax), "s"(Yacc), "s"(nY), "s"(cnt), "s"(ncnt));
@@ -134,7 +137,7 @@ __global__ void __launch_bounds__(kTThreads) infer_t_kernel(const uint32_t* __re
   const int wnp = (wn + 15) & ~15;
   // threads 0..63 finish (tile tid >> 5, row (tid >> 1) & 15, vector tid & 1): their scale, early
   const int fi = blockIdx.x * kTComp + 16 * ((tid >> 5) & 1) + ((tid >> 1) & 15);
-  const float dfin = D[fi < k ? fi : 0];  // an unconditional load: nothing waits for it until the end
+  const float dfin = RAW && !S ? 1.0f : D[fi < k ? fi : 0];  // an unconditional load: nothing waits for it until the end
   int e0 = 0, e1 = 0;
   long long T = 0;  // threads 0..63: (tile tid >> 5, row (tid >> 1) & 15, vector tid & 1)
   for (int cw0 = 0; cw0 < wnp; cw0 += kTWords) {
@@ -308,10 +311,13 @@ __global__ void __launch_bounds__(kTThreads) infer_t_kernel(const uint32_t* __re
     const int b = b0 + v;
     unsigned hb = 0u;
     if (i < k && b < batch) {
-      const double s = (double)dfin * ldexp((double)T, -(v ? e1 : e0));
-      S[(size_t)b * k + i] = s;
+      const double t = ldexp((double)T, -(v ? e1 : e0));
+      const double s = (double)dfin * t;
+      if (RAW) Traw[(size_t)b * k + i] = t;
+      if (!RAW || S) S[(size_t)b * k + i] = s;
       hb = hi_abs(s);
     }
+    if (RAW && !S) return;
     const unsigned h0 = wave_max_u32(v == 0 ? hb : 0u), h1 = wave_max_u32(v == 1 ? hb : 0u);
     if (tid == 0) {
       smax[(size_t)b0 * gridDim.x + blockIdx.x] = h0;
@@ -545,10 +551,61 @@ hipError_t infer_run(const uint32_t* B, const uint32_t* C, const float* D, int k
   const int gb = (batch + 1) / 2;
   const long long nwg = infer_groups(m), nch = (k + kYComp - 1) / kYComp;
   if (nwg * nch > 2147483647ll || nwg * gb > 2147483647ll) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(infer_t_kernel, dim3(gxt, gb), dim3(kTThreads), 0, st, C, wn, n, D, k, X, batch, x_vec4, c_vec4, S,
-                     smax, Yacc, nY, cnt, (int)(nwg * gb));
+  hipLaunchKernelGGL((infer_t_kernel<false>), dim3(gxt, gb), dim3(kTThreads), 0, st, C, wn, n, D, k, X, batch, x_vec4,
+                     c_vec4, S, smax, Yacc, nY, cnt, (int)(nwg * gb), nullptr);
   hipLaunchKernelGGL(infer_y_kernel, dim3((unsigned)(nwg * nch), gb), dim3(kYThreads), 0, st, B, wm, m, k, S, batch, smax,
                      gxt, (int)nwg, b_vec4, Yacc, cnt, Y);
+  return hipGetLastError();
+}
+
+// ---- gradient of few vectors ------------------------------------------------------------------
+// y = B diag(D) C x:  u = B^T dy,  dx = C^T (D u) is inference with the factors exchanged, and
+// dD_i = sum_b t_bi u_bi with t = C x needs one t pass more.
+__global__ void __launch_bounds__(256) grad_d_kernel(const double* __restrict__ Tr, const double* __restrict__ U, int k,
+                                                     int batch, float* __restrict__ dD) {
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= k) return;
+  double s = 0.0;
+  for (int b = 0; b < batch; ++b) s += Tr[(size_t)b * k + i] * U[(size_t)b * k + i];
+  dD[i] = (float)s;
+}
+
+size_t infer_grad_workspace_bytes(int k, int n, int batch) {
+  return infer_workspace_bytes(k, n, batch) + 2 * al256((size_t)batch * k * 8);
+}
+
+hipError_t infer_grad_run(const uint32_t* B, const uint32_t* C, const float* D, int k, int m, int n, const float* X,
+                          const float* dY, int batch, float* dX, float* dD, void* ws, hipStream_t st) {
+  const int wm = (m + 15) / 16, wn = (n + 15) / 16, gxt = infer_gxt(k);
+  char* base = static_cast<char*>(ws);
+  double* S = reinterpret_cast<double*>(base);
+  base += al256((size_t)batch * k * 8);
+  double* U = reinterpret_cast<double*>(base);
+  base += al256((size_t)batch * k * 8);
+  double* Tr = reinterpret_cast<double*>(base);
+  base += al256((size_t)batch * k * 8);
+  long long* acc = reinterpret_cast<long long*>(base);
+  base += al256((size_t)batch * n * 8);
+  unsigned* smax = reinterpret_cast<unsigned*>(base);
+  base += al256((size_t)batch * gxt * 4);
+  unsigned* cnt = reinterpret_cast<unsigned*>(base);
+  auto vec4 = [](long long words, const void* p) {
+    return (words % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) ? 1 : 0;
+  };
+  const int gb = (batch + 1) / 2;
+  const long long nwg = infer_groups(n), nch = (k + kYComp - 1) / kYComp;
+  if (nwg * nch > 2147483647ll || nwg * gb > 2147483647ll) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((infer_t_kernel<true>), dim3(gxt, gb), dim3(kTThreads), 0, st, B, wm, m, D, k, dY, batch,
+                     vec4(m, dY), vec4(wm, B), dX ? S : nullptr, smax, acc, dX ? (long long)batch * n : 0ll, cnt,
+                     dX ? (int)(nwg * gb) : 0, U);
+  if (dD) {
+    hipLaunchKernelGGL((infer_t_kernel<true>), dim3(gxt, gb), dim3(kTThreads), 0, st, C, wn, n, D, k, X, batch,
+                       vec4(n, X), vec4(wn, C), static_cast<double*>(nullptr), smax, acc, 0ll, cnt, 0, Tr);
+    hipLaunchKernelGGL(grad_d_kernel, dim3((k + 255) / 256), dim3(256), 0, st, Tr, U, k, batch, dD);
+  }
+  if (dX)
+    hipLaunchKernelGGL(infer_y_kernel, dim3((unsigned)(nwg * nch), gb), dim3(kYThreads), 0, st, C, wn, n, k, S, batch,
+                       smax, gxt, (int)nwg, vec4(wn, C), acc, cnt, dX);
   return hipGetLastError();
 }
 

@@ -119,4 +119,13 @@ struct DistillLaunch {
 size_t distill_workspace_bytes(long long rows, int V);
 hipError_t distill_run(const DistillLaunch& L, hipStream_t st);
 
+// Gradient of the factored layer: few vectors (apply.hip), any batch (grad.hip).  dX or dD may be
+// null (X too where dD is).
+size_t infer_grad_workspace_bytes(int k, int n, int batch);
+hipError_t infer_grad_run(const uint32_t* B, const uint32_t* C, const float* D, int k, int m, int n, const float* X,
+                          const float* dY, int batch, float* dX, float* dD, void* ws, hipStream_t st);
+size_t grad_workspace_bytes(int k, int m, int n, long long batch);
+hipError_t grad_run(const uint32_t* B, const uint32_t* C, const float* D, int k, int m, int n, const float* X,
+                    const float* dY, long long batch, float* dX, float* dD, void* ws, hipStream_t st);
+
 }  // namespace externd

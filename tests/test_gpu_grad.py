@@ -1,0 +1,222 @@
+"""The factored layer's gradient against its formula in 64 bits, and a compressed layer's whole run.
+
+Tolerances, from the arithmetic: a vector's image is within ux = 2^-31 2^E of it per element (|x| < 2^E),
+u, t, D u and the outputs round to fp32 once each (eps = 2^-24), dD's sum is fp64:
+  |du_i| <= nnz(B_i) uy + eps |u_i|        |dt_i| <= nnz(C_i) ux + eps |t_i|
+  |d dD_i| <= sum_b (|t| |du| + |u| |dt| + |du| |dt|) + eps |dD_i|
+  |d dx_j| <= sum_i |C_ij| (|D_i| |du_i| + eps |D_i u_i| + us) + eps |dx_j|
+A rounding to fp32 below the smallest normal number is off by up to half the smallest subnormal,
+2^-150, whatever the value: each eps |v| above is eps |v| + 2^-150."""
+
+import numpy as np
+import pytest
+import torch
+
+import expanded_rank_matrix_amd as erm
+from tests.test_oracle_apply import pack, random_factors
+
+pytestmark = pytest.mark.gpu
+EPS, SUB = 2.0**-24, 2.0**-150
+
+
+def device(Bt, Ct, D):
+    put = lambda p: torch.from_numpy(np.ascontiguousarray(p).view(np.int32)).cuda()
+    return put(pack(Bt)), put(pack(Ct)), torch.from_numpy(np.ascontiguousarray(D, dtype=np.float32)).cuda()
+
+
+def unit(v):
+    """Half a unit of each row's image."""
+    mx = np.max(np.abs(v), axis=1, initial=0.0)
+    return np.ldexp(1.0, np.where(mx > 0, np.frexp(mx)[1], 0) - 31)[:, None]
+
+
+def check(Bt, Ct, D, X, dY, dX, dD):
+    B, C, d = Bt.astype(np.float64), Ct.astype(np.float64), D.astype(np.float64)
+    x, y = X.astype(np.float64), dY.astype(np.float64)
+    u, t = y @ B.T, x @ C.T
+    du = np.count_nonzero(Bt, axis=1)[None] * unit(y) + EPS * np.abs(u) + SUB
+    dt = np.count_nonzero(Ct, axis=1)[None] * unit(x) + EPS * np.abs(t) + SUB
+    if dD is not None:
+        want = (t * u).sum(0)
+        tol = (np.abs(t) * du + np.abs(u) * dt + du * dt).sum(0) * (1 + 1e-9) + EPS * np.abs(want) + SUB
+        off = np.abs(dD.cpu().numpy() - want)
+        assert np.all(off <= tol), f"dD off by {np.max(off / tol):.3g} of the tolerance"
+    if dX is not None:
+        s = u * d
+        want = s @ C
+        us = 2 * unit(s)  # one binade of slack: the largest |s| may round up over a power of two
+        tol = (np.abs(d) * du + EPS * np.abs(s) + SUB + us) @ np.abs(C) * (1 + 1e-6) + EPS * np.abs(want) + SUB
+        off = np.abs(dX.cpu().numpy() - want)
+        assert np.all(off <= tol), f"dX off by {np.max(off / tol):.3g} of the tolerance"
+
+
+def run(k, m, n, batch, seed=0, scale=1.0):
+    rng = np.random.default_rng(seed + k + m + n + batch)
+    Bt, Ct, D = random_factors(rng, k, m, n)
+    X = (rng.standard_normal((batch, n)) * scale).astype(np.float32)
+    X[:, rng.integers(0, n)] *= 20
+    dY = rng.standard_normal((batch, m)).astype(np.float32)
+    Bp, Cp, Dd = device(Bt, Ct, D)
+    Xc, Yc = torch.from_numpy(X).cuda(), torch.from_numpy(dY).cuda()
+    dX, dD = erm.apply_factors_grad(Bp, Cp, Dd, m, n, Xc, Yc)
+    assert tuple(dX.shape) == (batch, n) and tuple(dD.shape) == (k,)
+    check(Bt, Ct, D, X, dY, dX, dD)
+    one, none = erm.apply_factors_grad(Bp, Cp, Dd, m, n, None, Yc, need_dD=False)
+    assert none is None and torch.equal(one, dX)
+    none, one = erm.apply_factors_grad(Bp, Cp, Dd, m, n, Xc, Yc, need_dX=False)
+    assert none is None and torch.equal(one, dD)
+    return Bt, Ct, D, X, dY, dX, dD
+
+
+@pytest.mark.parametrize("batch", [1, 2, 3, 15, 16, 17, 32, 33, 65, 130])
+@pytest.mark.parametrize("k,m,n", [(1, 1, 1), (5, 7, 9), (16, 16, 16), (64, 17, 33), (300, 389, 103), (37, 1100, 17),
+                                   (1003, 16, 2000)])
+def test_gradient_matches_formula(k, m, n, batch):
+    run(k, m, n, batch)
+
+
+@pytest.mark.parametrize("k,m,n,batch", [(7680, 2560, 2560, 1), (7680, 2560, 2560, 40), (1536, 1024, 1024, 300),
+                                         (64, 48, 50, 4096), (64, 48, 50, 8200), (600, 5000, 7000, 5), (600, 5000, 7000, 18)])
+def test_gradient_larger_sizes(k, m, n, batch):
+    run(k, m, n, batch)
+
+
+@pytest.mark.parametrize("scale", [1e-38, 1e-42, 1e30])
+@pytest.mark.parametrize("batch", [2, 20])
+def test_gradient_extreme_scales(batch, scale):
+    run(50, 40, 60, batch, scale=scale)
+
+
+@pytest.mark.parametrize("batch", [4, 50])
+def test_zero_parts(batch):
+    Bt, Ct, D, X, dY, _, _ = run(40, 50, 60, batch)
+    Z = np.zeros_like(Bt)
+    Xc, Yc = torch.from_numpy(X).cuda(), torch.from_numpy(dY).cuda()
+    dX, dD = erm.apply_factors_grad(*device(Z, Ct, D), 50, 60, Xc, Yc)
+    assert not dX.any() and not dD.any()
+    dX, dD = erm.apply_factors_grad(*device(Bt, Ct, np.zeros_like(D)), 50, 60, Xc, Yc)
+    assert not dX.any() and dD.any()
+    check(Bt, Ct, np.zeros_like(D), X, dY, dX, dD)
+    dX, dD = erm.apply_factors_grad(*device(Bt, Ct, D), 50, 60, Xc, torch.zeros_like(Yc))
+    assert not dX.any() and not dD.any()
+
+
+def test_empty_and_single_vector():
+    rng = np.random.default_rng(1)
+    Bt, Ct, D = random_factors(rng, 30, 20, 25)
+    f = device(Bt, Ct, D)
+    dX, dD = erm.apply_factors_grad(*f, 20, 25, torch.zeros((0, 25), device="cuda"), torch.zeros((0, 20), device="cuda"))
+    assert dX.shape == (0, 25) and dD.shape == (30,) and not dD.any()
+    x, y = torch.randn(25, device="cuda"), torch.randn(20, device="cuda")
+    one = erm.apply_factors_grad(*f, 20, 25, x, y)
+    row = erm.apply_factors_grad(*f, 20, 25, x[None], y[None])
+    assert one[0].shape == (25,) and torch.equal(one[0], row[0][0]) and torch.equal(one[1], row[1])
+
+
+@pytest.mark.parametrize("batch", [3, 60])
+def test_gradient_against_the_forward_pass(batch):
+    """The layer is linear in X and in D: <dX, v> = <dY, layer(v)> and <dD, w> = <dY, layer with w>."""
+    Bt, Ct, D, X, dY, dX, dD = run(200, 90, 110, batch, seed=3)
+    B, C, Dd = device(Bt, Ct, D)
+    rng = np.random.default_rng(8)
+    v = torch.from_numpy(rng.standard_normal((batch, 110)).astype(np.float32)).cuda()
+    w = torch.from_numpy(rng.standard_normal(200).astype(np.float32)).cuda()
+    y = torch.from_numpy(dY).cuda().double()
+    Yv = erm.apply_factors(B, C, Dd, 90, 110, v).double()
+    Yw = erm.apply_factors(B, C, w, 90, 110, torch.from_numpy(X).cuda()).double()
+    # every element is good to about 2^-22 of its terms' magnitudes; 2^-16 of the sums' leaves room
+    for a, b in (((dX.double() * v).sum(), (y * Yv).sum()), ((dD.double() * w).sum(), (y * Yw).sum())):
+        size = (dX.double() * v).abs().sum() + (y * Yv).abs().sum() + (dD.double() * w).abs().sum()
+        assert abs(float(a - b)) <= 2.0**-16 * float(size)
+
+
+def test_misaligned_inputs_out_streams_and_graph():
+    for batch in (5, 70):
+        Bt, Ct, D, X, dY, dX, dD = run(130, 75, 93, batch, seed=5)
+        f = device(Bt, Ct, D)
+        put = lambda a: torch.cat([torch.zeros(1), torch.from_numpy(a).reshape(-1)]).cuda()[1:].reshape(a.shape)
+        Xc, Yc = put(X), put(dY)
+        got = erm.apply_factors_grad(*f, 75, 93, Xc, Yc)
+        assert torch.equal(got[0], dX) and torch.equal(got[1], dD)
+        out = (torch.empty_like(dX), torch.empty_like(dD))
+        assert erm.apply_factors_grad(*f, 75, 93, Xc, Yc, out=out)[0] is out[0]
+        assert torch.equal(out[0], dX) and torch.equal(out[1], dD)
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+        many = [erm.apply_factors_grad(*f, 75, 93, Xc, Yc, stream=s) for _ in range(3) for s in streams]
+        torch.cuda.synchronize()
+        for g in many:
+            assert torch.equal(g[0], dX) and torch.equal(g[1], dD)
+        static = Xc.clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            g = erm.apply_factors_grad(*f, 75, 93, static, Yc)
+        for r in range(4):
+            static.copy_(Xc * (r + 1))
+            graph.replay()
+            torch.cuda.synchronize()
+            want = erm.apply_factors_grad(*f, 75, 93, static, Yc)
+            assert torch.equal(g[0], want[0]) and torch.equal(g[1], want[1]), r
+
+
+def test_binding_refusals():
+    rng = np.random.default_rng(1)
+    B, C, D = device(*random_factors(rng, 30, 20, 25))
+    x, y = torch.zeros((4, 25), device="cuda"), torch.zeros((4, 20), device="cuda")
+    g = erm.apply_factors_grad
+    bad = [lambda: g(B[:29], C, D, 20, 25, x, y), lambda: g(B, C.long(), D, 20, 25, x, y),
+           lambda: g(B, C, D[None], 20, 25, x, y), lambda: g(B, C, D.double(), 20, 25, x, y),
+           lambda: g(B, C, D, 20, 25, x[:3], y), lambda: g(B, C, D, 20, 25, x, y[:, :19].contiguous()),
+           lambda: g(B, C, D, 20, 25, x.half(), y), lambda: g(B, C, D, 20, 25, x, y.half()),
+           lambda: g(B, C, D, 20, 25, None, y), lambda: g(B, C, D, 20, 25, x, y, False, False),
+           lambda: g(B, C, D, 20, 25, x.cpu(), y), lambda: g(B, C, D, 20, 25, x, y, out=(x, None)),
+           lambda: g(B, C, D, 20, 25, x, y, out=(y, D)), lambda: g(B, C, D, 20, 25, x[0], y),
+           lambda: g(B, C, D, 20, 25, x, y[None])]
+    for i, call in enumerate(bad):
+        with pytest.raises(ValueError):
+            call()
+            pytest.fail(f"call {i} was not refused")
+
+
+def test_repairing_a_factored_head():
+    """A head's matrix is decomposed; its 8-bit form teaches the factored one: teacher logits by
+    apply_quantized, the student's by apply_factors, their distillation, and the gradient of D and of
+    the inputs, against the same chain in 64 bits and against differences."""
+    rng = np.random.default_rng(12)
+    V, n, tokens, top, T = 500, 96, 40, 24, 2.0
+    A = (rng.standard_normal((V, n)) * 0.3).astype(np.float32)
+    r = erm.decompose(torch.from_numpy(A).cuda(), 1.5, block=16)
+    k = r["k"]
+    X = torch.from_numpy(rng.standard_normal((tokens, n)).astype(np.float32)).cuda()
+    Wq, sw = erm.quantize_rows(torch.from_numpy(A).cuda())
+    teacher, index = torch.topk(erm.apply_quantized(Wq, sw, X), top, dim=1)
+    w = torch.full((tokens,), 1.0 / tokens, device="cuda")
+    w[5] = 0
+    Z = erm.apply_factors(r["B"], r["C"], r["D"], V, n, X)
+    loss, stats, dZ = erm.distill_loss(Z, teacher, index, T, w, grad=True)
+    dX, dD = erm.apply_factors_grad(r["B"], r["C"], r["D"], V, n, X, dZ)
+
+    B = torch.from_numpy(erm.unpack(r["B"], V).astype(np.float64))
+    C = torch.from_numpy(erm.unpack(r["C"], n).astype(np.float64))
+    x, a, i, wt = X.cpu().double(), teacher.cpu().double(), index.cpu(), w.cpu().double()
+
+    def total(d, xx):
+        z = (xx @ C.t() * d) @ B
+        logq = torch.log_softmax(z / T, 1).gather(1, i)
+        p = torch.softmax(a / T, 1)
+        return (wt * T * T * (p * (p.log() - logq)).sum(1)).sum()
+
+    d = r["D"].cpu().double().requires_grad_()
+    xx = x.clone().requires_grad_()
+    f = total(d, xx)
+    f.backward()
+    # each step is good to a few 2^-24 of its terms; the chain's logits reach some tens
+    assert abs(float(loss.double().sum().cpu() - f)) <= 1e-4 * float(f)
+    for got, want in ((dD.cpu().double(), d.grad), (dX.cpu().double(), xx.grad)):
+        assert (got - want).norm() <= 1e-4 * want.norm()
+    assert not dX[5].any()
+    h, v = 1e-4, torch.from_numpy(rng.standard_normal(k))
+    with torch.no_grad():
+        slope = (total(d + h * v, x) - total(d - h * v, x)) / (2 * h)
+    # the central difference's own error is h^2 times a third derivative
+    assert abs(float(slope - (dD.cpu().double() * v).sum())) <= 1e-3 * float((dD.cpu().double() * v).abs().sum())
