@@ -146,19 +146,27 @@ struct JoinDigits {
   const int* ex;
   float* out;
   long long ld;
-  __device__ __forceinline__ void operator()(long long row, long long col, int M, int N, const iv16& acc) const {
-    if (col >= N) return;
+  struct Row {
+    int e[4];
+  };
+  struct Col {};
+  __device__ __forceinline__ Row row(long long r, int M) const {
+    Row o;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const long long r = row + 8 * i;
-      if (r < M) {
-        const long long b = r >> 2;
+    for (int i = 0; i < 4; ++i) o.e[i] = ex[(r + 8 * i < M ? r + 8 * i : M - 1) >> 2];
+    return o;
+  }
+  __device__ __forceinline__ Col col(long long) const { return {}; }
+  template <bool WHOLE>
+  __device__ __forceinline__ void put(long long r, long long c, int M, int N, const Row& s, Col, const iv16& acc) const {
+    float* o = out + (r >> 2) * ld + c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (WHOLE || (r + 8 * i < M && c < N)) {
         const long long v = (long long)acc[4 * i] + ((long long)acc[4 * i + 1] << 8) +
                             ((long long)acc[4 * i + 2] << 16) + ((long long)acc[4 * i + 3] << 24);
-        const int e = ex[b];
-        out[b * ld + col] = e == kGBad ? __builtin_nanf("") : (float)ldexp((double)v, e);
+        o[2 * i * ld] = s.e[i] == kGBad ? __builtin_nanf("") : (float)ldexp((double)v, s.e[i]);
       }
-    }
   }
 };
 
@@ -218,11 +226,7 @@ size_t grad_workspace_bytes(int k, int m, int n, long long batch) {
 
 static hipError_t join_product(const int8_t* A, long long K, int M, const int8_t* B, int N, const int* ex, float* out,
                                long long ld, hipStream_t st) {
-  const long long ntm = (M + 127) / 128, ntn = (N + 127ll) / 128;
-  if (ntm * ntn > 2147483647ll) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((tile_kernel<128, 128, 2, 2, JoinDigits>), dim3((unsigned)(ntm * ntn)), dim3(256), 0, st, A, K, M,
-                     B, K, N, (int)K, (int)ntm, (int)ntn, JoinDigits{ex, out, ld});
-  return hipGetLastError();
+  return tile_product(A, K, M, B, K, N, (int)K, JoinDigits{ex, out, ld}, st);
 }
 
 hipError_t grad_run(const uint32_t* B, const uint32_t* C, const float* D, int k, int m, int n, const float* X,

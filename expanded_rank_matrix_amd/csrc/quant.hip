@@ -148,7 +148,7 @@ __device__ __forceinline__ void store_y(T* p, float v) {
 }
 
 // ---- few tokens -------------------------------------------------------------------------------
-// Workgroup: 16 output channels, all tokens (at most 16 NT), the row length split over eight waves
+// Workgroup: 16 output channels and 16 NT tokens, the row length split over eight waves
 // in steps of 64 bytes.  MFMA D(16 x 16) += A(16 x 64) B(64 x 16): A row = channel, B column =
 // token, lane l holding the 16 bytes at 16 (l / 16) of row (column) l % 16 of the step.  The waves'
 // partial tiles add in LDS.
@@ -162,13 +162,14 @@ __global__ void __launch_bounds__(64 * kFewWaves) few_kernel(const int8_t* __res
   __shared__ int red[kFewWaves][NT * 256];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, lr = lane & 15, gg = lane >> 4;
   const int r0 = blockIdx.x * 16;
+  const long long t0 = blockIdx.y * (16ll * NT);
   const int r = r0 + lr < m ? r0 + lr : m - 1;
   const int8_t* wr = W + (long long)r * ldw;
   const int8_t* xr[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const int c = 16 * t + lr < tokens ? 16 * t + lr : tokens - 1;
-    xr[t] = Xq + (long long)c * ldx;
+    const long long c = t0 + 16 * t + lr < tokens ? t0 + 16 * t + lr : tokens - 1;
+    xr[t] = Xq + c * ldx;
   }
   iv4 acc[NT];
 #pragma unroll
@@ -190,11 +191,19 @@ __global__ void __launch_bounds__(64 * kFewWaves) few_kernel(const int8_t* __res
 #pragma unroll
       for (int t = 0; t < NT; ++t) acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[u], b[u][t], acc[t], 0, 0, 0);
   }
-  for (; 64 * s < n; s += kFewWaves) {
-    const int k = 64 * s + 16 * gg;
-    const iv4 a = row16(wr, k, n);
+  if (n >= 16) {
+    for (; 64 * s < n; s += kFewWaves) {
+      const int k = 64 * s + 16 * gg;
+      const iv4 a = row16(wr, k, n);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, row16(xr[t], k, n), acc[t], 0, 0, 0);
+      for (int t = 0; t < NT; ++t)
+        acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, row16(xr[t], k, n), acc[t], 0, 0, 0);
+    }
+  } else if (s == 0) {
+    const iv4 a = row16_short(wr, 16 * gg, n);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+      acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, row16_short(xr[t], 16 * gg, n), acc[t], 0, 0, 0);
   }
   // acc[t][q] = D(channel 4 gg + q, token lr): stored token-major
 #pragma unroll
@@ -203,12 +212,13 @@ __global__ void __launch_bounds__(64 * kFewWaves) few_kernel(const int8_t* __res
     for (int q = 0; q < 4; ++q) red[wv][t * 256 + lr * 16 + 4 * gg + q] = acc[t][q];
   __syncthreads();
   for (int x = tid; x < NT * 256; x += 64 * kFewWaves) {
-    const int tok = x >> 4, o = r0 + (x & 15);
+    const long long tok = t0 + (x >> 4);
+    const int o = r0 + (x & 15);
     if (tok < tokens && o < m) {
       int sum = 0;
 #pragma unroll
       for (int w = 0; w < kFewWaves; ++w) sum += red[w][x];
-      store_y(Y + (long long)tok * ldy + o, (float)sum * sx[tok] * sw[o]);
+      store_y(Y + tok * ldy + o, (float)sum * sx[tok] * sw[o]);
     }
   }
 }
@@ -221,13 +231,28 @@ struct ScaledY {
   const float* sw;
   YT* Y;
   long long ldy;
-  __device__ __forceinline__ void operator()(long long row, long long col, int M, int N, const iv16& acc) const {
-    if (col >= N) return;
-    const float w = sw[col];
+  struct Row {
+    float s[16];
+  };
+  typedef float Col;
+  __device__ __forceinline__ Row row(long long r, int M) const {
+    Row o;
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      const long long r = row + 8 * (e >> 2) + (e & 3);
-      if (r < M) store_y(Y + r * ldy + col, (float)acc[e] * sx[r] * w);
+      const long long x = r + 8 * (e >> 2) + (e & 3);
+      o.s[e] = sx[x < M ? x : M - 1];
+    }
+    return o;
+  }
+  __device__ __forceinline__ Col col(long long c) const { return sw[c]; }
+  template <bool WHOLE>
+  __device__ __forceinline__ void put(long long r, long long c, int M, int N, const Row& s, Col w,
+                                      const iv16& acc) const {
+    YT* y = Y + r * ldy + c;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int d = 8 * (e >> 2) + (e & 3);
+      if (WHOLE || (r + d < M && c < N)) store_y(y + d * ldy, (float)acc[e] * s.s[e] * w);
     }
   }
 };
@@ -235,19 +260,20 @@ struct ScaledY {
 template <typename YT>
 static hipError_t product_typed(const int8_t* W, const float* sw, int m, int n, long long ldw, const int8_t* Xq,
                                 const float* sx, int tokens, long long ldx, YT* Y, long long ldy, hipStream_t st) {
-  const unsigned few = (unsigned)((m + 15) / 16);
+  const unsigned few = (unsigned)((m + 15ll) / 16);
   if (tokens <= 16) {
     hipLaunchKernelGGL((few_kernel<1, YT>), dim3(few), dim3(64 * kFewWaves), 0, st, W, ldw, m, n, sw, Xq, ldx, tokens,
                        sx, Y, ldy);
-  } else if (tokens <= 32) {
-    hipLaunchKernelGGL((few_kernel<2, YT>), dim3(few), dim3(64 * kFewWaves), 0, st, W, ldw, m, n, sw, Xq, ldx, tokens,
-                       sx, Y, ldy);
+  } else if (tokens <= 32 || n < 16) {  // rows too short for the tiles' loads come here whatever their number
+    const long long groups = (tokens + 31ll) / 32;
+    for (long long g = 0; g < groups; g += 65535) {  // the grid's limit; one launch below 2 million tokens
+      const unsigned gy = (unsigned)(groups - g < 65535 ? groups - g : 65535);
+      const long long t0 = 32 * g;
+      hipLaunchKernelGGL((few_kernel<2, YT>), dim3(few, gy), dim3(64 * kFewWaves), 0, st, W, ldw, m, n, sw,
+                         Xq + t0 * ldx, ldx, (int)(tokens - t0), sx + t0, Y + t0 * ldy, ldy);
+    }
   } else {
-    const ScaledY<YT> epi{sx, sw, Y, ldy};
-    const long long ntm = (tokens + 127) / 128, ntn = (m + 127ll) / 128;
-    if (ntm * ntn > 2147483647ll) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((tile_kernel<128, 128, 2, 2, ScaledY<YT>>), dim3((unsigned)(ntm * ntn)), dim3(256), 0, st, Xq,
-                       ldx, tokens, W, ldw, m, n, (int)ntm, (int)ntn, epi);
+    return tile_product(Xq, ldx, tokens, W, ldw, m, n, ScaledY<YT>{sx, sw, Y, ldy}, st);
   }
   return hipGetLastError();
 }
