@@ -92,7 +92,7 @@ def load():
         lib.externd_apply_quantized.argtypes = [vp, vp, i64, i64, i64, vp, ci, vp, i64, i64, vp, ci,
                                                 i64, vp, vp]
         lib.externd_apply_quantized_workspace.restype = i64
-        lib.externd_apply_quantized_workspace.argtypes = [ci, i64, i64]
+        lib.externd_apply_quantized_workspace.argtypes = [ci, i64, i64, i64]
         lib.externd_distill_loss.restype = ci
         lib.externd_distill_loss.argtypes = [vp, ci, i64, i64, i64, vp, ci, vp, ci, i64, f32, vp, vp, vp,
                                              vp, i64, vp, vp]
@@ -353,30 +353,30 @@ class _Run:
     workspace allocated on that stream, so that their memory is reused in its order.  Inputs that
     belong to another stream are recorded on this one."""
 
+    __slots__ = ("ptr", "guard", "on")
+
     def __init__(self, device, stream, inputs):
         import torch
 
-        self.guard = None
-        if device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(device)
+        self.guard = self.on = None
+        index = device.index
+        if index != torch._C._cuda_getDevice():
+            self.guard = torch.cuda.device(index)
             self.guard.__enter__()
-        try:
-            cur = torch.cuda.current_stream(device)
-            self.stream = cur if stream is None else stream
-            self.on = None
-            if self.stream != cur:
-                if self.stream.device != device:
-                    raise ValueError(f"stream is on {self.stream.device}, the tensors are on {device}")
+        self.ptr = torch._C._cuda_getCurrentRawStream(index)
+        if stream is not None and stream.cuda_stream != self.ptr:
+            try:
+                if stream.device != device:
+                    raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
                 for t in inputs:
                     if t is not None:
-                        t.record_stream(self.stream)
-                self.on = torch.cuda.stream(self.stream)
+                        t.record_stream(stream)
+                self.on = torch.cuda.stream(stream)
                 self.on.__enter__()
-        except BaseException:
-            if self.guard is not None:
-                self.guard.__exit__(None, None, None)
-            raise
-        self.ptr = self.stream.cuda_stream
+                self.ptr = stream.cuda_stream
+            except BaseException:
+                self.__exit__(None, None, None)
+                raise
 
     def __enter__(self):
         return self
@@ -492,7 +492,7 @@ def apply_quantized(W, w_scale, X, x_scale=None, out_dtype=None, stream=None, ou
         else:
             Y = out.unsqueeze(0) if single and out.dim() == 1 else out
         ldy = _rows(Y, _float_types(), "out", shape=(tokens, m), device=dev)
-        size = lib.externd_apply_quantized_workspace(types[X.dtype], tokens, n)
+        size = lib.externd_apply_quantized_workspace(types[X.dtype], tokens, n, m)
         ws = torch.empty(size, dtype=torch.uint8, device=dev) if size > 0 else None
         _check(lib.externd_apply_quantized(
             W.data_ptr(), w_scale.data_ptr(), m, n, ldw, X2.data_ptr(), types[X.dtype],

@@ -484,6 +484,7 @@ static bool float_type(int t) { return t == EXTERND_F32 || t == EXTERND_F16 || t
 
 constexpr int64_t kMaxCount = 2147483647;  // rows, tokens, channels
 constexpr int64_t kMaxProductLen = 131071; // 128 128 n < 2^31: the sum of products of int8 fits int32
+constexpr int64_t kMaxChannels = (int64_t)1 << 26;
 constexpr int64_t kMaxLd = (int64_t)1 << 40;
 
 int externd_quantize_rows(const void* X, int x_type, int64_t rows, int64_t n, int64_t ldx, int8_t* Q, int64_t ldq,
@@ -500,10 +501,11 @@ int externd_quantize_rows(const void* X, int x_type, int64_t rows, int64_t n, in
   return EXTERND_OK;
 }
 
-int64_t externd_apply_quantized_workspace(int x_type, int64_t tokens, int64_t n) {
-  if (!(float_type(x_type) || x_type == EXTERND_I8) || tokens < 0 || tokens > kMaxCount || n < 1 || n > kMaxProductLen)
+int64_t externd_apply_quantized_workspace(int x_type, int64_t tokens, int64_t n, int64_t m) {
+  if (!(float_type(x_type) || x_type == EXTERND_I8) || tokens < 0 || tokens > kMaxCount || n < 1 ||
+      n > kMaxProductLen || m < 1 || m > kMaxChannels)
     return -1;
-  return (int64_t)product_workspace_bytes(x_type, tokens, (int)n);
+  return (int64_t)product_workspace_bytes(x_type, tokens, (int)n, (int)m);
 }
 
 int externd_apply_quantized(const int8_t* W, const float* w_scale, int64_t m, int64_t n, int64_t ldw, const void* X,
@@ -513,8 +515,8 @@ int externd_apply_quantized(const int8_t* W, const float* w_scale, int64_t m, in
   if (!float_type(x_type) && x_type != EXTERND_I8)
     return fail(EXTERND_EINVAL, "x_type must be EXTERND_F32, EXTERND_F16, EXTERND_BF16 or EXTERND_I8");
   if (!float_type(y_type)) return fail(EXTERND_EINVAL, "y_type must be EXTERND_F32, EXTERND_F16 or EXTERND_BF16");
-  if (tokens < 0 || tokens > kMaxCount || m < 1 || m > kMaxCount)
-    return fail(EXTERND_EINVAL, "need 0 <= tokens < 2^31 and 1 <= m < 2^31");
+  if (tokens < 0 || tokens > kMaxCount || m < 1 || m > kMaxChannels)
+    return fail(EXTERND_EINVAL, "need 0 <= tokens < 2^31 and 1 <= m <= 2^26");
   if (n < 1 || n > kMaxProductLen)
     return fail(EXTERND_EINVAL, "need 1 <= n <= %lld (the sum of products must fit int32)", (long long)kMaxProductLen);
   if (ldw < n || ldw > kMaxLd || ldx < n || ldx > kMaxLd || ldy < m || ldy > kMaxLd)
@@ -523,7 +525,7 @@ int externd_apply_quantized(const int8_t* W, const float* w_scale, int64_t m, in
   if (!W || !w_scale || !X || !Y) return fail(EXTERND_EINVAL, "null pointer argument");
   if ((x_type == EXTERND_I8) != (x_scale != nullptr))
     return fail(EXTERND_EINVAL, "x_scale is given with x_type EXTERND_I8 and only then");
-  if (product_workspace_bytes(x_type, tokens, (int)n) > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15)))
+  if (product_workspace_bytes(x_type, tokens, (int)n, (int)m) > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15)))
     return fail(EXTERND_EINVAL, "workspace of externd_apply_quantized_workspace() bytes, 16-byte aligned, is needed");
   HIP_OR_FAIL(product_run(W, w_scale, (int)m, (int)n, ldw, X, x_type, x_scale, (int)tokens, ldx, Y, y_type, ldy,
                           workspace, reinterpret_cast<hipStream_t>(stream)));

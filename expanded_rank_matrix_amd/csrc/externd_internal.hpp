@@ -96,7 +96,7 @@ hipError_t infer_run(const uint32_t* B, const uint32_t* C, const float* D, int k
 // np bytes of each row of Q are written, zeros behind the first n.
 hipError_t quantize_run(const void* X, int type, long long rows, int n, long long ldx, int8_t* Q, long long ldq, int np,
                         float* scale, hipStream_t st);
-size_t product_workspace_bytes(int x_type, long long tokens, int n);
+size_t product_workspace_bytes(int x_type, long long tokens, int n, int m);
 hipError_t product_run(const int8_t* W, const float* sw, int m, int n, long long ldw, const void* X, int x_type,
                        const float* sx, int tokens, long long ldx, void* Y, int y_type, long long ldy, void* ws,
                        hipStream_t st);

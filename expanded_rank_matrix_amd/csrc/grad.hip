@@ -8,6 +8,8 @@
 // digit's sum is exact in int32 (lengths below 2^24), the four are joined in int64, scaled and
 // rounded once to fp32: the image's rounding, 2^-31 of the vector's largest power of two, is the
 // only error of a product besides.  t u and its sum over the batch are fp64, in a fixed order.
+#include <algorithm>
+
 #include "common.hpp"
 #include "externd_internal.hpp"
 #include "igemm.hpp"
@@ -146,27 +148,38 @@ struct JoinDigits {
   const int* ex;
   float* out;
   long long ld;
+  static constexpr bool kLds = false;
   struct Row {
     int e[4];
   };
-  struct Col {};
-  __device__ __forceinline__ Row row(long long r, int M) const {
+  __device__ __forceinline__ void at(long long m0, long long n0) {
+    ex += m0 >> 2;
+    out += (m0 >> 2) * ld + n0;
+  }
+  __device__ __forceinline__ Row row(int r, int mr) const {
     Row o;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o.e[i] = ex[(r + 8 * i < M ? r + 8 * i : M - 1) >> 2];
+    for (int i = 0; i < 4; ++i) o.e[i] = ex[(r + 8 * i < mr ? r + 8 * i : mr - 1) >> 2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(o.e[i]));  // not loaded one by one inside the guarded stores
     return o;
   }
-  __device__ __forceinline__ Col col(long long) const { return {}; }
-  template <bool WHOLE>
-  __device__ __forceinline__ void put(long long r, long long c, int M, int N, const Row& s, Col, const iv16& acc) const {
+  static __device__ __forceinline__ float join(int a, int b, int c, int d, int e) {
+    const long long v = (long long)a + ((long long)b << 8) + ((long long)c << 16) + ((long long)d << 24);
+    return e == kGBad ? __builtin_nanf("") : (float)ldexp((double)v, e);
+  }
+  __device__ __forceinline__ void put(int r, int c, int mr, const Row& s, const iv16& acc) const {
     float* o = out + (r >> 2) * ld + c;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (WHOLE || (r + 8 * i < M && c < N)) {
-        const long long v = (long long)acc[4 * i] + ((long long)acc[4 * i + 1] << 8) +
-                            ((long long)acc[4 * i + 2] << 16) + ((long long)acc[4 * i + 3] << 24);
-        o[2 * i * ld] = s.e[i] == kGBad ? __builtin_nanf("") : (float)ldexp((double)v, s.e[i]);
-      }
+      if (r + 8 * i < mr) o[2 * i * ld] = join(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3], s.e[i]);
+  }
+  template <int FM, int FN>
+  __device__ __forceinline__ void finish(const iv16 (&acc)[FM][FN], int r0, int c0, int mr, int nr, float*) const {
+    finish_direct<FM, FN>(*this, acc, r0, c0, mr, nr);
+  }
+  __device__ __forceinline__ void put4(long long r, int c, int M, const iv4& s) const {
+    out[(r >> 2) * ld + c] = join(s[0], s[1], s[2], s[3], ex[r >> 2]);
   }
 };
 
@@ -192,7 +205,7 @@ __global__ void __launch_bounds__(256) dfin_kernel(const double* __restrict__ pa
 }
 
 struct GradSpace {
-  size_t be, ce, ct, xd, yd, sd, u, t, ex, part, bytes;
+  size_t be, ce, ct, xd, yd, sd, u, t, ex, part, split, bytes;
 };
 static GradSpace grad_space(int k, int m, int n, long long batch) {
   const size_t c = (size_t)(batch < kGChunk ? batch : kGChunk);
@@ -214,6 +227,16 @@ static GradSpace grad_space(int k, int m, int n, long long batch) {
   s.t = take(4 * c * k);
   s.ex = take(3 * c * 4);
   s.part = take((size_t)kGParts * k * 8);
+  // the parts of a split product, one product at a time; a last pass of fewer vectors may split where
+  // the others do not
+  size_t split = 0;
+  for (long long b = batch < kGChunk ? batch : batch % kGChunk, once = 0; once < 2; b = (long long)c, ++once)
+    if (b > 0) {
+      split = std::max(split, tile_plan(4 * b, k, (int)mp).bytes);
+      split = std::max(split, tile_plan(4 * b, k, (int)np).bytes);
+      split = std::max(split, tile_plan(4 * b, n, (int)kp).bytes);
+    }
+  s.split = take(split);
   s.bytes = off;
   return s;
 }
@@ -225,8 +248,8 @@ size_t grad_workspace_bytes(int k, int m, int n, long long batch) {
 }
 
 static hipError_t join_product(const int8_t* A, long long K, int M, const int8_t* B, int N, const int* ex, float* out,
-                               long long ld, hipStream_t st) {
-  return tile_product(A, K, M, B, K, N, (int)K, JoinDigits{ex, out, ld}, st);
+                               long long ld, void* split, hipStream_t st) {
+  return tile_product(A, K, M, B, K, N, (int)K, JoinDigits{ex, out, ld}, split, st);
 }
 
 hipError_t grad_run(const uint32_t* B, const uint32_t* C, const float* D, int k, int m, int n, const float* X,
@@ -259,17 +282,17 @@ hipError_t grad_run(const uint32_t* B, const uint32_t* C, const float* D, int k,
     const int c = (int)(batch - b0 < kGChunk ? batch - b0 : kGChunk);
     hipError_t e;
     hipLaunchKernelGGL(digits_kernel, dim3(c), dim3(256), 0, st, dY + b0 * m, (long long)m, nullptr, yd, mp, ex);
-    e = join_product(yd, mp, 4 * c, be, k, ex, u, k, st);
+    e = join_product(yd, mp, 4 * c, be, k, ex, u, k, base + s.split, st);
     if (e != hipSuccess) return e;
     if (dD) {
       hipLaunchKernelGGL(digits_kernel, dim3(c), dim3(256), 0, st, X + b0 * n, (long long)n, nullptr, xd, np, ex + c);
-      e = join_product(xd, np, 4 * c, ce, k, ex + c, t, k, st);
+      e = join_product(xd, np, 4 * c, ce, k, ex + c, t, k, base + s.split, st);
       if (e != hipSuccess) return e;
       hipLaunchKernelGGL(dsum_kernel, dim3((k + 255) / 256, kGParts), dim3(256), 0, st, t, u, k, c, b0 == 0, part);
     }
     if (dX) {
       hipLaunchKernelGGL(digits_kernel, dim3(c), dim3(256), 0, st, u, (long long)k, D, sd, kp, ex + 2 * c);
-      e = join_product(sd, kp, 4 * c, ct, n, ex + 2 * c, dX + b0 * n, n, st);
+      e = join_product(sd, kp, 4 * c, ct, n, ex + 2 * c, dX + b0 * n, n, base + s.split, st);
       if (e != hipSuccess) return e;
     }
   }

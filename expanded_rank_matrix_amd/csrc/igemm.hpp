@@ -8,16 +8,19 @@ namespace externd {
 // ---- operand loads ----------------------------------------------------------------------------
 // 16 bytes of a row of n >= 16 at k, zeros from the row's end on.  A piece that crosses the end is
 // read from 16 bytes before it and shifted down, so that every load is inside the row and
-// unconditional.
-__device__ __forceinline__ iv4 row16(const int8_t* __restrict__ row, int k, int n) {
-  const int at = k < n - 16 ? k : n - 16, drop = k - at;  // bytes to shift out; 16 or more: none left
-  const iv4 v = *reinterpret_cast<const iv4_any*>(row + at);
+// unconditional; row_end shifts what row_load read.
+__device__ __forceinline__ iv4 row_load(const int8_t* __restrict__ row, int k, int n) {
+  return *reinterpret_cast<const iv4_any*>(row + (k < n - 16 ? k : n - 16));
+}
+__device__ __forceinline__ iv4 row_end(iv4 v, int k, int n) {
+  asm volatile("" : "+v"(v));  // else the load moves into a branch of its own, with its own wait
+  const int drop = k < n - 16 ? 0 : k - (n - 16);  // bytes to shift out; 16 or more: none left
   unsigned __int128 x = __builtin_bit_cast(unsigned __int128, v);
   x = drop < 16 ? x >> (8 * (drop & 15)) : (unsigned __int128)0;
   return __builtin_bit_cast(iv4, x);
 }
 // the same for a row of n < 16
-__device__ __forceinline__ iv4 row16_short(const int8_t* __restrict__ row, int k, int n) {
+__device__ __forceinline__ iv4 row_short(const int8_t* __restrict__ row, int k, int n) {
   iv4 v = {0, 0, 0, 0};
 #pragma unroll
   for (int e = 0; e < 15; ++e)
@@ -54,7 +57,7 @@ static __device__ const int kZeros[4] = {0, 0, 0, 0};  // what a direct load rea
 template <int BM, int BN, int WR, int WC, bool DMA, typename EPI>
 __global__ void __launch_bounds__(64 * WR * WC, 1) tile_kernel(const int8_t* __restrict__ A, long long lda, int M,
                                                                const int8_t* __restrict__ B, long long ldb, int N,
-                                                               int K, int ntm, int ntn, EPI epi) {
+                                                               int Kall, int kper, int ntm, int ntn, EPI epi) {
   typedef const __attribute__((address_space(1))) void gptr;
   typedef __attribute__((address_space(3))) void lptr;
   constexpr int NW = WR * WC, PA = BM / 8 / NW, PB = BN / 8 / NW;
@@ -70,8 +73,9 @@ __global__ void __launch_bounds__(64 * WR * WC, 1) tile_kernel(const int8_t* __r
   const int grp = tile / (kGroup * ntn), g0 = grp * kGroup, gs = ntm - g0 < kGroup ? ntm - g0 : kGroup;
   const int in = tile - g0 * ntn;
   const long long m0 = (long long)(g0 + in % gs) * BM, n0 = (long long)(in / gs) * BN;
-  const int8_t* ab = A + m0 * lda;
-  const int8_t* bb = B + n0 * ldb;
+  const int kbeg = blockIdx.y * kper, K = Kall - kbeg < kper ? Kall - kbeg : kper;
+  const int8_t* ab = A + m0 * lda + kbeg;
+  const int8_t* bb = B + n0 * ldb + kbeg;
   // this lane's piece of each of the wave's loads: row (p NW + wv) 8 + lane / 8, rows behind the last
   // repeat it
   const int lrow = lane >> 3;
@@ -95,55 +99,62 @@ __global__ void __launch_bounds__(64 * WR * WC, 1) tile_kernel(const int8_t* __r
     if (DMA) bo[p] = (unsigned)row * (unsigned)ldb + cb[p];
     else bp[p] = bb + row * ldb;
   }
-  const int nk = (K + 127) / 128;
+  // Stage 0 is the rows' last 128 bytes or what is left of them, stage t > 0 bytes 128 (t - 1) on: what
+  // a row's end needs is in one place before the loop.
+  const int nk = (K + 127) / 128, kl = 128 * (nk - 1);
   iv4 sa[PA], sb[PB];
-  auto load = [&](int t) {  // a stage into registers
-    const int k0 = 128 * t;
-    if (k0 + 128 <= K) {
+  auto load = [&](int t) {  // stage t > 0 into registers
+    const int k0 = 128 * (t - 1);
 #pragma unroll
-      for (int p = 0; p < PA; ++p) sa[p] = *reinterpret_cast<const iv4_any*>(ap[p] + k0 + ca[p]);
+    for (int p = 0; p < PA; ++p) sa[p] = *reinterpret_cast<const iv4_any*>(ap[p] + k0 + ca[p]);
 #pragma unroll
-      for (int p = 0; p < PB; ++p) sb[p] = *reinterpret_cast<const iv4_any*>(bp[p] + k0 + cb[p]);
-    } else {
-#pragma unroll
-      for (int p = 0; p < PA; ++p) sa[p] = row16(ap[p], k0 + ca[p], K);
-#pragma unroll
-      for (int p = 0; p < PB; ++p) sb[p] = row16(bp[p], k0 + cb[p], K);
-    }
+    for (int p = 0; p < PB; ++p) sb[p] = *reinterpret_cast<const iv4_any*>(bp[p] + k0 + cb[p]);
   };
-  // stage t into l; every direct load issued is waited for by a barrier before the kernel's end
+  auto put = [&](int8_t* l, const iv4 (&va)[PA], const iv4 (&vb)[PB]) {  // registers to LDS
+#pragma unroll
+    for (int p = 0; p < PA; ++p) *reinterpret_cast<iv4*>(l + (p * NW + wv) * 1024 + lane * 16) = va[p];
+#pragma unroll
+    for (int p = 0; p < PB; ++p) *reinterpret_cast<iv4*>(l + BM * 128 + (p * NW + wv) * 1024 + lane * 16) = vb[p];
+  };
+  auto direct = [&](int8_t* l, int p, const int8_t* s) {
+    __builtin_amdgcn_global_load_lds((gptr*)s, (lptr*)(l + (p * NW + wv) * 1024), 16, 0, 0);
+  };
+  // stage t > 0 into l (and stage t + 1 into registers); every direct load issued is waited for by a
+  // barrier before the kernel's end
   auto fetch = [&](int8_t* l, int t) {
     if (DMA) {
-      const int k0 = 128 * t;
-      if (k0 + 128 <= K) {
+      const int k0 = 128 * (t - 1);
 #pragma unroll
-        for (int p = 0; p < PA; ++p)
-          __builtin_amdgcn_global_load_lds((gptr*)(ab + k0 + ao[p]), (lptr*)(l + (p * NW + wv) * 1024), 16, 0, 0);
+      for (int p = 0; p < PA; ++p) direct(l, p, ab + k0 + ao[p]);
 #pragma unroll
-        for (int p = 0; p < PB; ++p)
-          __builtin_amdgcn_global_load_lds((gptr*)(bb + k0 + bo[p]), (lptr*)(l + BM * 128 + (p * NW + wv) * 1024), 16,
-                                           0, 0);
-      } else {
-        // pieces behind the rows' end: zeros for A, so that B's may be anything (its row's first piece)
-#pragma unroll
-        for (int p = 0; p < PA; ++p) {
-          const int8_t* s = k0 + ca[p] < K ? ab + k0 + ao[p] : reinterpret_cast<const int8_t*>(kZeros);
-          __builtin_amdgcn_global_load_lds((gptr*)s, (lptr*)(l + (p * NW + wv) * 1024), 16, 0, 0);
-        }
-#pragma unroll
-        for (int p = 0; p < PB; ++p) {
-          const int8_t* s = k0 + cb[p] < K ? bb + k0 + bo[p] : bb + (bo[p] - cb[p]);
-          __builtin_amdgcn_global_load_lds((gptr*)s, (lptr*)(l + BM * 128 + (p * NW + wv) * 1024), 16, 0, 0);
-        }
-      }
+      for (int p = 0; p < PB; ++p) direct(l + BM * 128, p, bb + k0 + bo[p]);
     } else {
-#pragma unroll
-      for (int p = 0; p < PA; ++p) *reinterpret_cast<iv4*>(l + (p * NW + wv) * 1024 + lane * 16) = sa[p];
-#pragma unroll
-      for (int p = 0; p < PB; ++p) *reinterpret_cast<iv4*>(l + BM * 128 + (p * NW + wv) * 1024 + lane * 16) = sb[p];
+      put(l, sa, sb);
       if (t + 1 < nk) load(t + 1);
     }
   };
+  if (DMA) {
+    // pieces behind the rows' end: zeros for A, so that B's may be anything (its row's first piece)
+#pragma unroll
+    for (int p = 0; p < PA; ++p)
+      direct(l0, p, kl + ca[p] < K ? ab + kl + ao[p] : reinterpret_cast<const int8_t*>(kZeros));
+#pragma unroll
+    for (int p = 0; p < PB; ++p) direct(l0 + BM * 128, p, bb + (kl + cb[p] < K ? kl + bo[p] : bo[p] - cb[p]));
+  } else {
+    iv4 ta[PA], tb[PB];  // stages 0 and 1 on their way together
+#pragma unroll
+    for (int p = 0; p < PA; ++p) ta[p] = row_load(ap[p], kl + ca[p], K);
+#pragma unroll
+    for (int p = 0; p < PB; ++p) tb[p] = row_load(bp[p], kl + cb[p], K);
+    if (nk > 1) load(1);
+    if (kl + 128 > K) {
+#pragma unroll
+      for (int p = 0; p < PA; ++p) ta[p] = row_end(ta[p], kl + ca[p], K);
+#pragma unroll
+      for (int p = 0; p < PB; ++p) tb[p] = row_end(tb[p], kl + cb[p], K);
+    }
+    put(l0, ta, tb);
+  }
   iv16 acc[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
@@ -182,8 +193,6 @@ __global__ void __launch_bounds__(64 * WR * WC, 1) tile_kernel(const int8_t* __r
     if (FM * FN > each * reads) __builtin_amdgcn_sched_group_barrier(0x008, FM * FN - each * reads, 0);
     __builtin_amdgcn_sched_barrier(0);
   };
-  if (!DMA) load(0);
-  fetch(l0, 0);
   __syncthreads();
   if (nk > 1) fetch(l1, 1);
   read(0, l0, 0);
@@ -216,26 +225,70 @@ __global__ void __launch_bounds__(64 * WR * WC, 1) tile_kernel(const int8_t* __r
     step(0, l1, 3);
   }
   mul(1);
-  // the epilogue's own operands first, all in flight together (clamped indexes, no branches), then
-  // the stores; a tile inside the matrix needs no guards
-  typename EPI::Row er[FM];
-  typename EPI::Col ec[FN];
-  const long long r0 = m0 + wr * (BM / WR) + 4 * lg, c0 = n0 + wc * (BN / WC) + lr;
+  // the wave's share of D: rows wr BM / WR on, columns wc BN / WC on of the tile; mr x nr of the tile
+  // lie in the matrix
+  epi.at(m0, n0);
+  const int mr = M - m0 < BM ? (int)(M - m0) : BM, nr = N - n0 < BN ? (int)(N - n0) : BN;
+  if (EPI::kLds) __syncthreads();  // the stages are read: LDS is free
+  constexpr int kBytes = EPI::kLds ? 32 * (32 * FN + 8) * 4 : 0;  // of one wave
+  static_assert(kBytes * ((NW + 1) / 2) <= (BM + BN) * 128, "epilogue in LDS");
+  epi.template finish<FM, FN>(acc, wr * (BM / WR), wc * (BN / WC), mr, nr,
+                              reinterpret_cast<float*>((wv & 1 ? l1 : l0) + (wv >> 1) * kBytes));
+}
+
+// An epilogue that stores from the accumulators: put() gets the first row and the column of 16 values.
+template <int FM, int FN, typename EPI>
+__device__ __forceinline__ void finish_direct(const EPI& epi, const iv16 (&acc)[FM][FN], int r0, int c0, int mr, int nr) {
+  const int lane = threadIdx.x & 63, r = r0 + 4 * (lane >> 5), c = c0 + (lane & 31);
 #pragma unroll
-  for (int i = 0; i < FM; ++i) er[i] = epi.row(r0 + 32 * i, M);
+  for (int i = 0; i < FM; ++i)
+    if (r0 + 32 * i < mr) {  // the same for the wave
+      const typename EPI::Row er = epi.row(r + 32 * i, mr);
 #pragma unroll
-  for (int j = 0; j < FN; ++j) ec[j] = epi.col(c0 + 32 * j < N ? c0 + 32 * j : N - 1);
-  if (m0 + BM <= M && n0 + BN <= N) {
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-      for (int j = 0; j < FN; ++j) epi.template put<true>(r0 + 32 * i, c0 + 32 * j, M, N, er[i], ec[j], acc[i][j]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-      for (int j = 0; j < FN; ++j) epi.template put<false>(r0 + 32 * i, c0 + 32 * j, M, N, er[i], ec[j], acc[i][j]);
+      for (int j = 0; j < FN; ++j)
+        if (c + 32 * j < nr) epi.put(r + 32 * i, c + 32 * j, mr, er, acc[i][j]);
+    }
+}
+
+// ---- split row lengths --------------------------------------------------------------------------
+// Where there are few tiles, the row length is split over blockIdx.y: each part writes its int32 tile,
+// and a second launch adds the parts (exact, in any order) and applies the epilogue.
+struct PartTile {
+  int* part;  // [parts][rows of 4][N][4]: the four consecutive rows of an accumulator lie together
+  long long N, stride;
+  int* p;
+  static constexpr bool kLds = false;
+  struct Row {};
+  __device__ __forceinline__ void at(long long m0, long long n0) {
+    p = part + blockIdx.y * stride + ((m0 >> 2) * N + n0) * 4;
   }
+  __device__ __forceinline__ Row row(int, int) const { return {}; }
+  __device__ __forceinline__ void put(int r, int c, int mr, Row, const iv16& acc) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (r + 8 * i < mr) {  // a last group of fewer than four rows is whole in the workspace
+        iv4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = acc[4 * i + e];
+        *reinterpret_cast<iv4*>(p + ((long long)((r >> 2) + 2 * i) * N + c) * 4) = v;
+      }
+  }
+  template <int FM, int FN>
+  __device__ __forceinline__ void finish(const iv16 (&acc)[FM][FN], int r0, int c0, int mr, int nr, float*) const {
+    finish_direct<FM, FN>(*this, acc, r0, c0, mr, nr);
+  }
+};
+
+template <typename EPI>
+__global__ void __launch_bounds__(256) join_kernel(const int* __restrict__ part, int parts, long long stride, int M,
+                                                   int N, EPI epi) {
+  const long long groups = (M + 3ll) / 4, x = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (x >= groups * N) return;
+  const long long g = x / N;
+  const int c = (int)(x - g * N);
+  iv4 s = {0, 0, 0, 0};
+  for (int z = 0; z < parts; ++z) s += *reinterpret_cast<const iv4*>(part + z * stride + x * 4);
+  epi.put4(4 * g, c, M, s);
 }
 
 // Whether rows can go to LDS directly.
@@ -245,31 +298,74 @@ static inline bool tile_dma(const void* p, long long ld, int K) {
 
 template <int BM, int BN, int WR, int WC, typename EPI>
 static hipError_t tile_launch(const int8_t* A, long long lda, int M, const int8_t* B, long long ldb, int N, int K,
-                              const EPI& epi, hipStream_t st) {
+                              int parts, const EPI& epi, hipStream_t st) {
   const long long ntm = (M + BM - 1ll) / BM, ntn = (N + BN - 1ll) / BN;
-  if (ntm * ntn > 2147483647ll) return hipErrorInvalidValue;
+  if (ntm * ntn > (1ll << 22)) return hipErrorInvalidValue;
+  const int kper = parts == 1 ? K : ((K + 127) / 128 + parts - 1) / parts * 128;
+  const dim3 grid((unsigned)(ntm * ntn), (unsigned)parts);
   if (tile_dma(A, lda, K) && tile_dma(B, ldb, K))
-    hipLaunchKernelGGL((tile_kernel<BM, BN, WR, WC, true, EPI>), dim3((unsigned)(ntm * ntn)), dim3(64 * WR * WC), 0, st,
-                       A, lda, M, B, ldb, N, K, (int)ntm, (int)ntn, epi);
+    hipLaunchKernelGGL((tile_kernel<BM, BN, WR, WC, true, EPI>), grid, dim3(64 * WR * WC), 0, st, A, lda, M, B, ldb, N,
+                       K, kper, (int)ntm, (int)ntn, epi);
   else
-    hipLaunchKernelGGL((tile_kernel<BM, BN, WR, WC, false, EPI>), dim3((unsigned)(ntm * ntn)), dim3(64 * WR * WC), 0, st,
-                       A, lda, M, B, ldb, N, K, (int)ntm, (int)ntn, epi);
+    hipLaunchKernelGGL((tile_kernel<BM, BN, WR, WC, false, EPI>), grid, dim3(64 * WR * WC), 0, st, A, lda, M, B, ldb, N,
+                       K, kper, (int)ntm, (int)ntn, epi);
   return hipGetLastError();
+}
+
+// Parts of the row length for few tiles.  A stage of a tile takes about 0.6 us however few
+// workgroups run (the latency of its loads; 128 x 128 and 64 x 128), so a long row length on a card
+// that is not full costs more than joining parts does: about 4 us and 8 bytes an element and part.
+// At least three stages and sixteen bytes are left to every part.
+struct TilePlan {
+  bool small;  // 64 x 128 tiles
+  int parts;
+  size_t bytes;  // of the parts
+};
+static inline TilePlan tile_plan(long long M, long long N, int K) {
+  TilePlan p{M <= 64, 1, 0};
+  const long long tiles = p.small ? (N + 127) / 128 : (M + 127) / 128 * ((N + 127) / 128);
+  const int nk = (K + 127) / 128;
+  const double bytes = 16.0 * (double)((M + 3) / 4) * (double)N;
+  double best = 0.6 * nk;
+  for (int s = 2; s <= 16 && tiles * s <= 512 && nk >= 3 * s; ++s) {
+    const int per = (nk + s - 1) / s;
+    if ((nk + per - 1) / per != s || K - (s - 1) * per * 128 < 16) continue;
+    const double t = 0.6 * per + 4.0 + 2.0 * s * bytes / 4e6;
+    if (t < best) {
+      best = t;
+      p.parts = s;
+    }
+  }
+  if (p.parts > 1) p.bytes = (size_t)p.parts * (size_t)((M + 3) / 4) * (size_t)N * 16;
+  return p;
 }
 
 // The tile shape by what its rounds over 256 CUs would cost: a tile's time at K = 2560 is about 36 us
 // (256 x 256), 29.5 us (256 x 192) and, for 128 x 128, 15 us alone on its CU and 25 us for two (its two
-// stages take 64 KB of LDS, so two workgroups share a CU).
+// stages take 64 KB of LDS, so two workgroups share a CU).  ws: tile_plan(M, N, K).bytes.
 template <typename EPI>
 static hipError_t tile_product(const int8_t* A, long long lda, int M, const int8_t* B, long long ldb, int N, int K,
-                               const EPI& epi, hipStream_t st) {
+                               const EPI& epi, void* ws, hipStream_t st) {
+  const TilePlan p = tile_plan(M, N, K);
+  if (p.parts > 1) {
+    const long long groups = (M + 3ll) / 4, stride = groups * N * 4;
+    int* part = static_cast<int*>(ws);
+    const PartTile t{part, N, stride, nullptr};
+    const hipError_t e = p.small ? tile_launch<64, 128, 2, 2>(A, lda, M, B, ldb, N, K, p.parts, t, st)
+                                 : tile_launch<128, 128, 2, 2>(A, lda, M, B, ldb, N, K, p.parts, t, st);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((join_kernel<EPI>), dim3((unsigned)((groups * N + 255) / 256)), dim3(256), 0, st, part, p.parts,
+                       stride, M, N, epi);
+    return hipGetLastError();
+  }
+  if (p.small) return tile_launch<64, 128, 2, 2>(A, lda, M, B, ldb, N, K, 1, epi, st);
   auto tiles = [&](int bm, int bn) { return ((M + bm - 1ll) / bm) * ((N + bn - 1ll) / bn); };
   const long long t1 = tiles(256, 256), t2 = tiles(256, 192), t3 = tiles(128, 128);
   const double c1 = 36.0 * ((t1 + 255) / 256), c2 = 29.5 * ((t2 + 255) / 256);
   const double c3 = t3 <= 256 ? 15.0 : 25.0 * ((t3 + 511) / 512);
-  if (c3 <= c1 && c3 <= c2) return tile_launch<128, 128, 2, 2>(A, lda, M, B, ldb, N, K, epi, st);
-  if (c2 <= c1) return tile_launch<256, 192, 4, 2>(A, lda, M, B, ldb, N, K, epi, st);
-  return tile_launch<256, 256, 2, 4>(A, lda, M, B, ldb, N, K, epi, st);
+  if (c3 <= c1 && c3 <= c2) return tile_launch<128, 128, 2, 2>(A, lda, M, B, ldb, N, K, 1, epi, st);
+  if (c2 <= c1) return tile_launch<256, 192, 4, 2>(A, lda, M, B, ldb, N, K, 1, epi, st);
+  return tile_launch<256, 256, 2, 4>(A, lda, M, B, ldb, N, K, 1, epi, st);
 }
 
 }  // namespace externd

@@ -3,7 +3,7 @@
 //
 //   quantise:  a_t = max_j |x_tj|,  s_t = fl32(a_t / 127),  q_tj = the whole number nearest to the
 //              exact quotient 127 x_tj / a_t, ties to even
-//   product:   y_to = s_t w_o sum_j q_tj W_oj
+//   product:   y_to = (sum_j q_tj W_oj) w_o s_t
 //
 // The sum is exact in int32 (n <= 131071), so it does not depend on how it is split; it is converted
 // to fp32 and multiplied by the two scales (three fp32 roundings), then rounded once to Y's type.
@@ -32,6 +32,31 @@ __device__ __forceinline__ int quant1_small(float x, float a) { return (int)rint
 __device__ __forceinline__ unsigned pack4(int a, int b, int c, int d) {
   return (unsigned)(a & 255) | (unsigned)(b & 255) << 8 | (unsigned)(c & 255) << 16 | (unsigned)d << 24;
 }
+
+// a row's scale and rounding, from the fp32 bits of its largest |x|
+struct RowScale {
+  float a, inv;
+  bool bad, tiny;
+  __device__ __forceinline__ explicit RowScale(unsigned mx) {
+    bad = mx >= 0x7F800000u;
+    tiny = mx < 0x0D000000u;  // a < 2^-101
+    a = __uint_as_float(mx);
+    inv = bad || mx == 0u ? 0.0f : 127.0f / a;
+  }
+  __device__ __forceinline__ float scale() const { return bad ? __uint_as_float(0x7FC00000u) : a / 127.0f; }
+  __device__ __forceinline__ void quantize(const float (&v)[8], int (&k)[8]) const {
+    if (bad || a == 0.0f) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) k[e] = 0;
+    } else if (tiny) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) k[e] = quant1_small(v[e], a);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) k[e] = quant1(v[e], inv, a);
+    }
+  }
+};
 
 // One row per TPR threads (64: a wave; 256: the workgroup), 8 elements per thread and step; the
 // first CH steps of a row stay in registers between the search for its maximum and its rounding, a
@@ -80,24 +105,12 @@ __global__ void __launch_bounds__(256) quantize_kernel(const T* __restrict__ X, 
     for (int w = 0; w < 4; ++w) mx = wmx[w] > mx ? wmx[w] : mx;
   }
   if (row >= rows) return;
-  const bool bad = mx >= 0x7F800000u;
-  const float a = __uint_as_float(mx);
-  const bool tiny = mx < 0x0D000000u;  // a < 2^-101
-  const float inv = bad || mx == 0u ? 0.0f : 127.0f / a;
-  if (tid == 0) scale[row] = bad ? __uint_as_float(0x7FC00000u) : a / 127.0f;
+  const RowScale rs(mx);
+  if (tid == 0) scale[row] = rs.scale();
   int8_t* q = Q + row * ldq;
   auto emit = [&](long long j, const float (&w)[8]) {
     int k[8];
-    if (bad || mx == 0u) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) k[e] = 0;
-    } else if (tiny) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) k[e] = quant1_small(w[e], a);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) k[e] = quant1(w[e], inv, a);
-    }
+    rs.quantize(w, k);
     if (j + 8 <= np) {
       iv2_any o;
       o[0] = (int)pack4(k[0], k[1], k[2], k[3]);
@@ -122,12 +135,15 @@ __global__ void __launch_bounds__(256) quantize_kernel(const T* __restrict__ X, 
 template <typename T>
 static hipError_t quantize_typed(const T* X, long long rows, int n, long long ldx, int8_t* Q, long long ldq, int np,
                                  float* scale, hipStream_t st) {
-  if (n <= 64 * 8 * 2) {
-    hipLaunchKernelGGL((quantize_kernel<T, 64, 2>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, st, X, rows, n, ldx,
-                       Q, ldq, np, scale);
-  } else {
-    hipLaunchKernelGGL((quantize_kernel<T, 256, 5>), dim3((unsigned)rows), dim3(256), 0, st, X, rows, n, ldx, Q, ldq,
-                       np, scale);
+  // runs of 2^23 rows: a launch holds below 2^32 threads
+  for (long long r = 0; r < rows; r += 1ll << 23) {
+    const long long c = rows - r < (1ll << 23) ? rows - r : 1ll << 23;
+    if (n <= 64 * 8 * 2)
+      hipLaunchKernelGGL((quantize_kernel<T, 64, 2>), dim3((unsigned)((c + 3) / 4)), dim3(256), 0, st, X + r * ldx, c, n,
+                         ldx, Q + r * ldq, ldq, np, scale + r);
+    else
+      hipLaunchKernelGGL((quantize_kernel<T, 256, 5>), dim3((unsigned)c), dim3(256), 0, st, X + r * ldx, c, n, ldx,
+                         Q + r * ldq, ldq, np, scale + r);
   }
   return hipGetLastError();
 }
@@ -148,147 +164,342 @@ __device__ __forceinline__ void store_y(T* p, float v) {
 }
 
 // ---- few tokens -------------------------------------------------------------------------------
-// Workgroup: 16 output channels and 16 NT tokens, the row length split over eight waves
-// in steps of 64 bytes.  MFMA D(16 x 16) += A(16 x 64) B(64 x 16): A row = channel, B column =
-// token, lane l holding the 16 bytes at 16 (l / 16) of row (column) l % 16 of the step.  The waves'
-// partial tiles add in LDS.
+// Workgroup: 16 MT output channels and 16 NT tokens; the row length goes round eight waves in chunks
+// of 128 bytes, so that each wave reads whole cache lines of W and two chunks' loads are in flight.
+// MFMA D(16 x 16) += A(16 x 64) B(64 x 16): A row = channel, B column = token, lane l holding the
+// 16 bytes at 16 (l / 16) of row (column) l % 16 of the step.  The waves' partial tiles add in LDS.
+//
+// XT int8_t: the tokens are 8-bit rows.  Else they are quantised here first, by every workgroup for
+// itself into LDS while the first loads of W are on their way.
 constexpr int kFewWaves = 8;
-template <int NT, typename YT>
+constexpr int kFewTokens = 16;
+constexpr int kFewFused = 4;           // tokens quantised on the way
+constexpr int kFewLds = 48 * 1024;    // bytes of their rows
+
+// distance of the quantised rows in LDS: 16 rows' pieces of one column in different banks
+__host__ __device__ constexpr int few_pitch(int n) { return (n + 127) / 128 * 128 % 256 == 0 ? (n + 127) / 128 * 128 + 16
+                                                                                           : (n + 127) / 128 * 128 + 144; }
+
+// The tokens' rows quantised into LDS by the workgroup's eight waves, G = 8, 4 or 2 of them to a
+// token (tokens <= 4), and their scales; ends with a barrier.
+template <typename T>
+__device__ __forceinline__ void few_quantize(const T* __restrict__ X, long long ldx, int tokens, int n,
+                                             int8_t* __restrict__ q, float* srow, unsigned* wmx) {
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int G = tokens == 1 ? 8 : tokens == 2 ? 4 : 2, t = wv / G, first = ((wv % G) * 64 + lane) * 8, step = 512 * G;
+  const bool mine = t < tokens;
+  const T* x = X + (mine ? t : 0) * ldx;
+  constexpr int H = 2;  // steps kept in registers; a longer row's rest is read again
+  float v[H][8];
+  unsigned mx = 0u;
+  auto get = [&](int j, float (&w)[8]) {
+    if (j + 8 <= n) load8(x + j, w);
+    else load8_tail(x + j, (long long)n - j, w);
+  };
+  auto top = [&](const float (&w)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const unsigned b = __float_as_uint(w[e]) & 0x7FFFFFFFu;
+      mx = b > mx ? b : mx;
+    }
+  };
+#pragma unroll
+  for (int h = 0; h < H; ++h) get(first + h * step, v[h]);
+#pragma unroll
+  for (int h = 0; h < H; ++h) top(v[h]);
+  for (int j = first + H * step; j < n; j += step) {
+    float w[8];
+    get(j, w);
+    top(w);
+  }
+  mx = wave_max_u32(mx);
+  if (lane == 0) wmx[wv] = mx;
+  __syncthreads();
+  if (mine) {
+    for (int g = 0; g < G; ++g) {
+      const unsigned o = wmx[t * G + g];
+      mx = o > mx ? o : mx;
+    }
+    const RowScale rs(mx);
+    if (wv % G == 0 && lane == 0) srow[t] = rs.scale();
+    const int np = (n + 127) / 128 * 128;
+    int8_t* o = q + t * few_pitch(n);
+    auto emit = [&](int j, const float (&w)[8]) {
+      int k[8];
+      rs.quantize(w, k);
+      if (j < np) {
+        *reinterpret_cast<unsigned*>(o + j) = pack4(k[0], k[1], k[2], k[3]);
+        *reinterpret_cast<unsigned*>(o + j + 4) = pack4(k[4], k[5], k[6], k[7]);
+      }
+    };
+#pragma unroll
+    for (int h = 0; h < H; ++h) emit(first + h * step, v[h]);
+    for (int j = first + H * step; j < np; j += step) {
+      float w[8];
+      get(j, w);
+      emit(j, w);
+    }
+  }
+  __syncthreads();
+}
+
+template <int MT, int NT, typename XT, typename YT>
 __global__ void __launch_bounds__(64 * kFewWaves) few_kernel(const int8_t* __restrict__ W, long long ldw, int m, int n,
-                                                             const float* __restrict__ sw,
-                                                             const int8_t* __restrict__ Xq, long long ldx, int tokens,
-                                                             const float* __restrict__ sx, YT* __restrict__ Y,
-                                                             long long ldy) {
-  __shared__ int red[kFewWaves][NT * 256];
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, lr = lane & 15, gg = lane >> 4;
-  const int r0 = blockIdx.x * 16;
+                                                             const float* __restrict__ sw, const XT* __restrict__ X,
+                                                             long long ldx, int tokens, const float* __restrict__ sx,
+                                                             YT* __restrict__ Y, long long ldy) {
+  constexpr bool FUSED = !__is_same(XT, int8_t);
+  static_assert(!FUSED || (NT == 1 && kFewFused <= 16), "quantised on the way: one column tile");
+  extern __shared__ __attribute__((aligned(16))) int8_t rows[];
+  __shared__ int red[kFewWaves][MT * NT * 256];
+  __shared__ float srow[16];
+  __shared__ unsigned wmx[kFewWaves];
+  // the wave's number in a scalar register: the branches on it must be jumps, since MFMA runs whatever
+  // the lane mask
+  const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = lane & 15, gg = lane >> 4;
+  const int r0 = blockIdx.x * (16 * MT);
   const long long t0 = blockIdx.y * (16ll * NT);
-  const int r = r0 + lr < m ? r0 + lr : m - 1;
-  const int8_t* wr = W + (long long)r * ldw;
+  const int8_t* wr[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) wr[i] = W + (long long)(r0 + 16 * i + lr < m ? r0 + 16 * i + lr : m - 1) * ldw;
   const int8_t* xr[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     const long long c = t0 + 16 * t + lr < tokens ? t0 + 16 * t + lr : tokens - 1;
-    xr[t] = Xq + c * ldx;
+    xr[t] = FUSED ? rows + c * few_pitch(n) : reinterpret_cast<const int8_t*>(X + c * ldx);
   }
-  iv4 acc[NT];
+  iv4 acc[MT][NT];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) acc[t] = iv4{0, 0, 0, 0};
-  const int full = n / 64;
-  int s = wv;
-  constexpr int U = 4;
-  for (; s + (U - 1) * kFewWaves < full; s += U * kFewWaves) {
-    iv4 a[U], b[U][NT];
+  for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k = 64 * (s + u * kFewWaves) + 16 * gg;
-      a[u] = *reinterpret_cast<const iv4_any*>(wr + k);
+    for (int t = 0; t < NT; ++t) acc[i][t] = iv4{0, 0, 0, 0};
+  const int full = n / 128;
+  iv4 a[4][MT], b[4][NT];
+  auto load_w = [&](int c, int u) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t) b[u][t] = *reinterpret_cast<const iv4_any*>(xr[t] + k);
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        a[2 * u + h][i] = *reinterpret_cast<const iv4_any*>(wr[i] + 128 * c + 64 * h + 16 * gg);
+  };
+  auto load_x = [&](int c, int u) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int8_t* p = xr[t] + 128 * c + 64 * h + 16 * gg;
+        b[2 * u + h][t] = FUSED ? *reinterpret_cast<const iv4*>(p) : (iv4)*reinterpret_cast<const iv4_any*>(p);
+      }
+  };
+  auto mul = [&](int u) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          acc[i][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[2 * u + h][i], b[2 * u + h][t], acc[i][t], 0, 0, 0);
+  };
+  int c = wv;
+  const bool two = c + kFewWaves < full;
+  if constexpr (FUSED) {
+    if (c < full) load_w(c, 0);
+    if (two) load_w(c + kFewWaves, 1);
+    few_quantize(X, ldx, tokens, n, rows, srow, wmx);
+    if (c < full) {
+      load_x(c, 0);
+      if (two) load_x(c + kFewWaves, 1);
+      mul(0);
+      if (two) mul(1);
+      c += two ? 2 * kFewWaves : kFewWaves;
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int t = 0; t < NT; ++t) acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[u], b[u][t], acc[t], 0, 0, 0);
   }
-  if (n >= 16) {
-    for (; 64 * s < n; s += kFewWaves) {
-      const int k = 64 * s + 16 * gg;
-      const iv4 a = row16(wr, k, n);
+  for (; c + kFewWaves < full; c += 2 * kFewWaves) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      load_w(c + u * kFewWaves, u);
+      load_x(c + u * kFewWaves, u);
+    }
+    mul(0);
+    mul(1);
+  }
+  if (c < full) {
+    load_w(c, 0);
+    load_x(c, 0);
+    mul(0);
+    c += kFewWaves;
+  }
+  if (c == full && n % 128 != 0) {  // the rows' end: one wave
+    const int k = 128 * full + 16 * gg;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) a[h][i] = n >= 16 ? row_load(wr[i], k + 64 * h, n) : row_short(wr[i], k + 64 * h, n);
 #pragma unroll
       for (int t = 0; t < NT; ++t)
-        acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, row16(xr[t], k, n), acc[t], 0, 0, 0);
+        b[h][t] = FUSED ? *reinterpret_cast<const iv4*>(xr[t] + k + 64 * h)  // zeros behind the row there
+                        : n >= 16 ? row_load(xr[t], k + 64 * h, n) : row_short(xr[t], k + 64 * h, n);
     }
-  } else if (s == 0) {
-    const iv4 a = row16_short(wr, 16 * gg, n);
+    if (n >= 16) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) a[h][i] = row_end(a[h][i], k + 64 * h, n);
+        if (!FUSED) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t) b[h][t] = row_end(b[h][t], k + 64 * h, n);
+        }
+      }
+    }
+    mul(0);
+  }
+  // acc[q] = D(channel 4 gg + q, token lr): stored token-major
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int t = 0; t < NT; ++t)
-      acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, row16_short(xr[t], 16 * gg, n), acc[t], 0, 0, 0);
-  }
-  // acc[t][q] = D(channel 4 gg + q, token lr): stored token-major
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) red[wv][t * 256 + lr * 16 + 4 * gg + q] = acc[t][q];
+      *reinterpret_cast<iv4*>(&red[wv][(t * 16 + lr) * (16 * MT) + 16 * i + 4 * gg]) = acc[i][t];
   __syncthreads();
-  for (int x = tid; x < NT * 256; x += 64 * kFewWaves) {
-    const long long tok = t0 + (x >> 4);
-    const int o = r0 + (x & 15);
+  for (int x = tid; x < MT * NT * 256; x += 64 * kFewWaves) {
+    const long long tok = t0 + x / (16 * MT);
+    const int o = r0 + x % (16 * MT);
     if (tok < tokens && o < m) {
       int sum = 0;
 #pragma unroll
       for (int w = 0; w < kFewWaves; ++w) sum += red[w][x];
-      store_y(Y + tok * ldy + o, (float)sum * sx[tok] * sw[o]);
+      store_y(Y + tok * ldy + o, (float)sum * sw[o] * (FUSED ? srow[tok & 15] : sx[tok]));
     }
   }
 }
 
 // ---- many tokens: the tiles of igemm.hpp ----------------------------------------------------
-// y = sum s_t w_o: the lane holds rows row + 8 (i / 4) + i % 4 of column col
+// y = sum w_o s_t.  The accumulators times w_o pass through LDS, 32 rows of the wave's columns at a
+// time, so that each lane stores 16 bytes of a row: four or eight times fewer stores than from the
+// accumulators, whole cache lines, and one guard each.  (Code run once costs too: its instructions
+// come from memory.)  The rows' distance in LDS, 32 FN + 8 words, puts the two rows that a wave
+// writes at once in different banks.
 template <typename YT>
 struct ScaledY {
   const float* sx;
   const float* sw;
   YT* Y;
   long long ldy;
-  struct Row {
-    float s[16];
-  };
-  typedef float Col;
-  __device__ __forceinline__ Row row(long long r, int M) const {
-    Row o;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const long long x = r + 8 * (e >> 2) + (e & 3);
-      o.s[e] = sx[x < M ? x : M - 1];
-    }
-    return o;
+  static constexpr bool kLds = true;
+  __device__ __forceinline__ void at(long long m0, long long n0) {
+    sx += m0;
+    sw += n0;
+    Y += m0 * ldy + n0;
   }
-  __device__ __forceinline__ Col col(long long c) const { return sw[c]; }
-  template <bool WHOLE>
-  __device__ __forceinline__ void put(long long r, long long c, int M, int N, const Row& s, Col w,
-                                      const iv16& acc) const {
-    YT* y = Y + r * ldy + c;
+  template <int FM, int FN>
+  __device__ __forceinline__ void finish(const iv16 (&acc)[FM][FN], int r0, int c0, int mr, int nr, float* l) const {
+    constexpr int W = 32 * FN, P = W + 8, E = 16 / sizeof(YT), CH = W / E;  // columns, distance, a store's elements
+    const int lane = threadIdx.x & 63, lr = lane & 31, lg = lane >> 5;
+    float w[FN];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const int d = 8 * (e >> 2) + (e & 3);
-      if (WHOLE || (r + d < M && c < N)) store_y(y + d * ldy, (float)acc[e] * s.s[e] * w);
+    for (int j = 0; j < FN; ++j) w[j] = sw[c0 + 32 * j + lr < nr ? c0 + 32 * j + lr : nr - 1];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) l[(8 * (e >> 2) + (e & 3) + 4 * lg) * P + 32 * j + lr] = (float)acc[i][j][e] * w[j];
+#pragma unroll
+      for (int x0 = 0; x0 < 32 * CH; x0 += 64) {
+        const int x = x0 + lane, row = x / CH, ch = x % CH * E, r = r0 + 32 * i + row, c = c0 + ch;
+        const float s = sx[r < mr ? r : mr - 1];
+        float v[E];
+#pragma unroll
+        for (int q = 0; q < E; q += 4) {
+          const fv4 f = *reinterpret_cast<const fv4*>(l + row * P + ch + q);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[q + e] = f[e] * s;
+        }
+        if (r < mr) {
+          YT* y = Y + r * ldy + c;
+          if (c + E <= nr) {
+            typedef YT ev __attribute__((ext_vector_type(E)));
+            ev o;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = (YT)v[e];
+            *reinterpret_cast<iv4_any*>(y) = __builtin_bit_cast(iv4, o);
+          } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+              if (c + e < nr) y[e] = (YT)v[e];
+          }
+        }
+      }
     }
+  }
+  __device__ __forceinline__ void put4(long long r, int c, int M, const iv4& sum) const {
+    const float w = sw[c];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (r + e < M) store_y(Y + (r + e) * ldy + c, (float)sum[e] * w * sx[r + e]);
   }
 };
 
-template <typename YT>
-static hipError_t product_typed(const int8_t* W, const float* sw, int m, int n, long long ldw, const int8_t* Xq,
-                                const float* sx, int tokens, long long ldx, YT* Y, long long ldy, hipStream_t st) {
-  const unsigned few = (unsigned)((m + 15ll) / 16);
-  if (tokens <= 16) {
-    hipLaunchKernelGGL((few_kernel<1, YT>), dim3(few), dim3(64 * kFewWaves), 0, st, W, ldw, m, n, sw, Xq, ldx, tokens,
-                       sx, Y, ldy);
-  } else if (tokens <= 32 || n < 16) {  // rows too short for the tiles' loads come here whatever their number
-    const long long groups = (tokens + 31ll) / 32;
-    for (long long g = 0; g < groups; g += 65535) {  // the grid's limit; one launch below 2 million tokens
-      const unsigned gy = (unsigned)(groups - g < 65535 ? groups - g : 65535);
-      const long long t0 = 32 * g;
-      hipLaunchKernelGGL((few_kernel<2, YT>), dim3(few, gy), dim3(64 * kFewWaves), 0, st, W, ldw, m, n, sw,
-                         Xq + t0 * ldx, ldx, (int)(tokens - t0), sx + t0, Y + t0 * ldy, ldy);
-    }
-  } else {
-    return tile_product(Xq, ldx, tokens, W, ldw, m, n, ScaledY<YT>{sx, sw, Y, ldy}, st);
+// MT x NT tiles a workgroup; the grid's limits are kept by taking the tokens in runs
+template <int MT, int NT, typename YT>
+static hipError_t few_launch(const int8_t* W, const float* sw, int m, int n, long long ldw, const int8_t* Xq,
+                             const float* sx, int tokens, long long ldx, YT* Y, long long ldy, hipStream_t st) {
+  const unsigned gx = (unsigned)((m + 16ll * MT - 1) / (16 * MT));
+  const long long groups = (tokens + 16ll * NT - 1) / (16 * NT);
+  for (long long g = 0; g < groups; g += 65535) {
+    const unsigned gy = (unsigned)(groups - g < 65535 ? groups - g : 65535);
+    const long long t0 = 16ll * NT * g;
+    hipLaunchKernelGGL((few_kernel<MT, NT, int8_t, YT>), dim3(gx, gy), dim3(64 * kFewWaves), 0, st, W, ldw, m, n, sw,
+                       Xq + t0 * ldx, ldx, (int)(tokens - t0), sx + t0, Y + t0 * ldy, ldy);
   }
   return hipGetLastError();
 }
 
-// Workspace of a product whose tokens come as floating-point rows: their scales and their
-// quantised rows, padded to a multiple of 16 bytes.
-static size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
-static long long pad16(long long n) { return (n + 15) & ~15ll; }
-size_t product_workspace_bytes(int x_type, long long tokens, int n) {
-  return x_type == 3 ? 0 : al256((size_t)tokens * 4) + al256((size_t)tokens * pad16(n));
+template <typename YT>
+static hipError_t product_typed(const int8_t* W, const float* sw, int m, int n, long long ldw, const int8_t* Xq,
+                                const float* sx, int tokens, long long ldx, YT* Y, long long ldy, void* parts,
+                                hipStream_t st) {
+  if (tokens <= kFewTokens) return few_launch<1, 1>(W, sw, m, n, ldw, Xq, sx, tokens, ldx, Y, ldy, st);
+  // rows too short for the tiles' loads come here whatever their number
+  if (tokens <= 32 || n < 16) return few_launch<1, 2>(W, sw, m, n, ldw, Xq, sx, tokens, ldx, Y, ldy, st);
+  return tile_product(Xq, ldx, tokens, W, ldw, m, n, ScaledY<YT>{sx, sw, Y, ldy}, parts, st);
 }
 
-hipError_t product_run(const int8_t* W, const float* sw, int m, int n, long long ldw, const void* X, int x_type,
-                       const float* sx, int tokens, long long ldx, void* Y, int y_type, long long ldy, void* ws,
-                       hipStream_t st) {
+template <typename XT, typename YT>
+static hipError_t fused_typed(const int8_t* W, const float* sw, int m, int n, long long ldw, const XT* X, int tokens,
+                              long long ldx, YT* Y, long long ldy, hipStream_t st) {
+  hipLaunchKernelGGL((few_kernel<1, 1, XT, YT>), dim3((unsigned)((m + 15ll) / 16)), dim3(64 * kFewWaves),
+                     (size_t)tokens * few_pitch(n), st, W, ldw, m, n, sw, X, ldx, tokens, nullptr, Y, ldy);
+  return hipGetLastError();
+}
+
+// Whether the tokens are quantised within the product's own launch.
+static bool fused(int x_type, long long tokens, int n) {
+  return x_type != 3 && tokens <= kFewFused && tokens * few_pitch(n) <= kFewLds;
+}
+
+// Workspace: the scales and quantised rows (padded to a multiple of 16 bytes) of tokens that come as
+// floating-point rows, and the parts of a split product.
+static size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
+static long long pad16(long long n) { return (n + 15) & ~15ll; }
+static size_t rows_bytes(int x_type, long long tokens, int n) {
+  return x_type == 3 || fused(x_type, tokens, n) ? 0 : al256((size_t)tokens * 4) + al256((size_t)tokens * pad16(n));
+}
+size_t product_workspace_bytes(int x_type, long long tokens, int n, int m) {
+  return rows_bytes(x_type, tokens, n) + (tokens > 32 && n >= 16 ? tile_plan(tokens, m, n).bytes : 0);
+}
+
+template <typename YT>
+static hipError_t product_to(const int8_t* W, const float* sw, int m, int n, long long ldw, const void* X, int x_type,
+                             const float* sx, int tokens, long long ldx, YT* Y, long long ldy, void* ws,
+                             hipStream_t st) {
+  if (fused(x_type, tokens, n)) {
+    switch (x_type) {
+      case 0: return fused_typed(W, sw, m, n, ldw, static_cast<const float*>(X), tokens, ldx, Y, ldy, st);
+      case 1: return fused_typed(W, sw, m, n, ldw, static_cast<const _Float16*>(X), tokens, ldx, Y, ldy, st);
+      default: return fused_typed(W, sw, m, n, ldw, static_cast<const __bf16*>(X), tokens, ldx, Y, ldy, st);
+    }
+  }
   const int8_t* Xq = static_cast<const int8_t*>(X);
   if (x_type != 3) {
     float* scale = static_cast<float*>(ws);
@@ -300,10 +511,17 @@ hipError_t product_run(const int8_t* W, const float* sw, int m, int n, long long
     sx = scale;
     ldx = np;
   }
+  return product_typed(W, sw, m, n, ldw, Xq, sx, tokens, ldx, Y, ldy,
+                       static_cast<char*>(ws) + rows_bytes(x_type, tokens, n), st);
+}
+
+hipError_t product_run(const int8_t* W, const float* sw, int m, int n, long long ldw, const void* X, int x_type,
+                       const float* sx, int tokens, long long ldx, void* Y, int y_type, long long ldy, void* ws,
+                       hipStream_t st) {
   switch (y_type) {
-    case 0: return product_typed(W, sw, m, n, ldw, Xq, sx, tokens, ldx, static_cast<float*>(Y), ldy, st);
-    case 1: return product_typed(W, sw, m, n, ldw, Xq, sx, tokens, ldx, static_cast<_Float16*>(Y), ldy, st);
-    case 2: return product_typed(W, sw, m, n, ldw, Xq, sx, tokens, ldx, static_cast<__bf16*>(Y), ldy, st);
+    case 0: return product_to(W, sw, m, n, ldw, X, x_type, sx, tokens, ldx, static_cast<float*>(Y), ldy, ws, st);
+    case 1: return product_to(W, sw, m, n, ldw, X, x_type, sx, tokens, ldx, static_cast<_Float16*>(Y), ldy, ws, st);
+    case 2: return product_to(W, sw, m, n, ldw, X, x_type, sx, tokens, ldx, static_cast<__bf16*>(Y), ldy, ws, st);
     default: return hipErrorInvalidValue;
   }
 }

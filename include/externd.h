@@ -239,16 +239,16 @@ int externd_quantize_rows(const void* X, int x_type, int64_t rows, int64_t n, in
  *            way exactly as externd_quantize_rows does (a token with a NaN or an infinity gives a
  *            row of NaN)
  *   Y        tokens x m of y_type (EXTERND_F32, _F16 or _BF16), row distance ldy
- *   workspace  externd_apply_quantized_workspace(x_type, tokens, n) bytes, 16-byte aligned (NULL
+ *   workspace  externd_apply_quantized_workspace(x_type, tokens, n, m) bytes, 16-byte aligned (NULL
  *            where that is 0), used by this call alone until it has run
- * 0 <= tokens < 2^31, 1 <= m < 2^31, 1 <= n <= 131071 (the largest n whose sum of products of
+ * 0 <= tokens < 2^31, 1 <= m <= 2^26, 1 <= n <= 131071 (the largest n whose sum of products of
  * 8-bit integers fits int32). */
 int externd_apply_quantized(const int8_t* W, const float* w_scale, int64_t m, int64_t n, int64_t ldw, const void* X,
                             int x_type, const float* x_scale, int64_t tokens, int64_t ldx, void* Y, int y_type,
                             int64_t ldy, void* workspace, void* stream);
 
 /* Bytes of workspace externd_apply_quantized needs; -1 for sizes or a type it refuses. */
-int64_t externd_apply_quantized_workspace(int x_type, int64_t tokens, int64_t n);
+int64_t externd_apply_quantized_workspace(int x_type, int64_t tokens, int64_t n, int64_t m);
 
 /* ---- Distillation on a teacher's top logits -----------------------------------------------
  * The loss that repairs a factored model's outputs: for each row (token) the divergence of the

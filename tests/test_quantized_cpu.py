@@ -14,7 +14,7 @@ def quantize(X=fake, t=F32, rows=4, n=8, ldx=8, Q=fake, ldq=8, scale=fake):
     return erm.load().externd_quantize_rows(X, t, rows, n, ldx, Q, ldq, scale, None)
 
 
-def product(W=fake, sw=fake, m=4, n=8, ldw=8, X=fake, xt=I8, sx=fake, tokens=2, ldx=8, Y=fake, yt=F32, ldy=4, ws=fake):
+def product(W=fake, sw=fake, m=4, n=8, ldw=8, X=fake, xt=I8, sx=fake, tokens=9, ldx=8, Y=fake, yt=F32, ldy=4, ws=fake):
     return erm.load().externd_apply_quantized(W, sw, m, n, ldw, X, xt, sx, tokens, ldx, Y, yt, ldy, ws, None)
 
 
@@ -31,7 +31,7 @@ def test_quantize_refusals(change, word):
 @pytest.mark.parametrize("change, word", [
     (dict(W=None), "null"), (dict(sw=None), "null"), (dict(X=None), "null"), (dict(Y=None), "null"),
     (dict(xt=4), "x_type"), (dict(yt=I8), "y_type"), (dict(yt=-1), "y_type"),
-    (dict(tokens=-1), "tokens"), (dict(tokens=1 << 31), "tokens"), (dict(m=0), "m <"), (dict(m=1 << 31, ldy=1 << 31), "m <"),
+    (dict(tokens=-1), "tokens"), (dict(tokens=1 << 31), "tokens"), (dict(m=0), "m <"), (dict(m=(1 << 26) + 1, ldy=1 << 31), "m <"),
     (dict(n=0), "131071"), (dict(n=131072, ldw=131072, ldx=131072), "131071"),
     (dict(ldw=7), "ldw"), (dict(ldx=7), "ldx"), (dict(ldy=3), "ldy"),
     (dict(sx=None), "x_scale"), (dict(xt=BF16), "x_scale"),
@@ -48,12 +48,13 @@ def test_nothing_to_do():
 
 def test_workspace_sizes():
     size = erm.load().externd_apply_quantized_workspace
-    assert size(I8, 100, 100) == 0
-    assert size(BF16, 0, 100) == 0
-    for t, n in ((1, 1), (3, 17), (1000, 131071), (2**31 - 1, 131071)):
+    assert size(I8, 3, 100, 100) == 0
+    assert size(BF16, 0, 100, 100) == 0
+    for t, n in ((5, 1), (3, 17000), (1000, 131071), (2**31 - 1, 131071)):
         for ty in (F32, F16, BF16):
-            assert size(ty, t, n) >= t * 4 + t * n
-    assert size(4, 1, 1) == -1 and size(F32, -1, 1) == -1 and size(F32, 1, 0) == -1 and size(F32, 1, 131072) == -1
+            assert size(ty, t, n, 1000) >= t * 4 + t * n
+    for bad in ((4, 1, 1, 1), (F32, -1, 1, 1), (F32, 1, 0, 1), (F32, 1, 131072, 1), (F32, 1, 1, 0), (F32, 1, 1, (1 << 26) + 1)):
+        assert size(*bad) == -1
 
 
 def test_binding_refuses_host_tensors():
