@@ -8,44 +8,25 @@
 // One pass over z keeps the running maximum m and the sum S of exp((z - m) / T) (8 elements a step:
 // one rescaling of the sum per step at most), so q_v = exp((z_v - m) / T) / S.  z is handled in
 // fp32, each thread's sum too; the threads' sums, log S and the K terms of the loss are fp64, since
-// log p - log q is a difference of numbers many times its size.  The gradient is a second pass: each element
-// is read once more and written once, rounded once to z's type.  The corrections p sit in LDS lists
-// by groups of 8 elements; equal indices of one row add in 64-bit fixed point (units of 2^-60), so
-// their order does not matter.
+// log p - log q is a difference of numbers many times its size.  The gradient is a second pass: g q_v
+// for every element, rounded once to z's type, and after it, behind a barrier, the teacher's at most K
+// elements once more, with p in the difference before its rounding.  Equal indices of one row meet in
+// hashed lists in LDS; their p add in 64-bit fixed point (units of 2^-60), so the order does not
+// matter and each of them writes the same value.
 #include "common.hpp"
 #include "externd_internal.hpp"
 #include "types.hpp"
 
 namespace externd {
 
-constexpr int kDThreads = 256;
-constexpr int kDBuckets = 8192;          // lists of groups (group % kDBuckets)
+constexpr int kDThreads = 256;           // of streaming workgroups
+constexpr int kDBuckets = 2048;          // lists of the teacher's indices
 constexpr unsigned short kDNone = 0xFFFF;
 constexpr unsigned long long kDNaN = ~0ull;
-
-__device__ __forceinline__ double block_sum_f64(double v, double* red) {  // red: kDThreads / 64
-  v = wave_sum_f64(v);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  double s = 0.0;
-#pragma unroll
-  for (int w = 0; w < kDThreads / 64; ++w) s += red[w];
-  return s;
-}
 
 __device__ __forceinline__ float wave_max_f32(float v) {
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) v = fmaxf(v, __shfl_xor(v, d));
-  return v;
-}
-__device__ __forceinline__ float block_max_f32(float v, float* red) {
-  v = wave_max_f32(v);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kDThreads / 64; ++w) v = fmaxf(v, red[w]);
   return v;
 }
 
@@ -67,31 +48,36 @@ __device__ __forceinline__ int teacher_index(const Teacher& t, long long at, int
   return v >= 0 && v < V ? (int)v : -1;
 }
 
-// The row's teacher into LDS: index of every entry (-1 where there is none) and e = exp((a - max) / T)
-// (0 there).  Returns 1 / sum e, so that p = e / sum e, and sum p log p; 0 where no entry is valid.
+// What the row's teacher gives: 1 / sum e (0 without a valid entry) and sum p log p.
+struct TeacherSums {
+  double pinv, plogp;
+};
+
+// The row's teacher, by one wave, into LDS: index of every entry (-1 where there is none), e =
+// exp((a - max) / T) (0 there) and the student's logit at it (0 outside lo .. hi - 1).  p = e / sum e.
 // A NaN or +inf among the valid entries makes every e NaN.
-__device__ __forceinline__ double teacher_row(const Teacher& t, long long row, int V, double rT, int* idx, float* ex,
-                                              float* redf, double* redd, double* plogp) {
+template <typename T>
+__device__ __forceinline__ TeacherSums teacher_row(const Teacher& t, long long row, int V, double rT, const T* z, int lo,
+                                                   int hi, int* idx, float* ex, float* zk) {
+  const int lane = threadIdx.x & 63;
   const long long base = row * t.top;
   float mx = -__builtin_inff();
-  int nan = 0;
-  for (int k = threadIdx.x; k < t.top; k += kDThreads) {
+  bool nan = false;
+  for (int k = lane; k < t.top; k += 64) {
     const int i = teacher_index(t, base + k, V);
-    const float a = i >= 0 ? teacher_value(t, base + k) : -__builtin_inff();
-    idx[k] = a == -__builtin_inff() ? -1 : i;
-    ex[k] = a;
-    nan |= a != a;
-    mx = fmaxf(mx, a);
+    const float a = teacher_value(t, base + k);
+    const bool valid = i >= 0 && a != -__builtin_inff();
+    idx[k] = valid ? i : -1;
+    ex[k] = valid ? a : -__builtin_inff();
+    zk[k] = valid && i >= lo && i < hi ? (float)z[i] : 0.0f;
+    nan = nan || (valid && a != a);
+    mx = fmaxf(mx, valid ? a : -__builtin_inff());
   }
-  nan = __syncthreads_or(nan);
-  mx = block_max_f32(mx, redf);
-  if (nan) mx = __builtin_nanf("");
-  if (mx == -__builtin_inff()) {  // the same in every thread
-    *plogp = 0.0;
-    return 0.0;
-  }
+  nan = __any(nan);
+  mx = nan ? __builtin_nanf("") : wave_max_f32(mx);
+  if (mx == -__builtin_inff()) return {0.0, 0.0};
   double s = 0.0, sx = 0.0;  // sums of e^x and of x e^x, x = (a - max) / T
-  for (int k = threadIdx.x; k < t.top; k += kDThreads) {
+  for (int k = lane; k < t.top; k += 64) {
     float e = 0.0f;
     if (idx[k] >= 0) {
       const double x = ((double)ex[k] - (double)mx) * rT;
@@ -101,10 +87,9 @@ __device__ __forceinline__ double teacher_row(const Teacher& t, long long row, i
     }
     ex[k] = e;
   }
-  s = block_sum_f64(s, redd);
-  sx = block_sum_f64(sx, redd);
-  *plogp = sx / s - log(s);
-  return 1.0 / s;
+  s = wave_sum_f64(s);
+  sx = wave_sum_f64(sx);
+  return {1.0 / s, sx / s - log(s)};
 }
 
 // running maximum m and sum s of exp2((z - m) c)
@@ -120,20 +105,41 @@ __device__ __forceinline__ void stats8(const float (&z)[8], float c, float& m, f
   for (int e = 0; e < 8; ++e) s += __builtin_amdgcn_exp2f((z[e] - m) * c);
 }
 
-template <typename T>
-__device__ __forceinline__ void load8_inf(const T* p, long long count, float (&v)[8]) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = e < count ? (float)p[e] : -__builtin_inff();
+__device__ __forceinline__ void stats1(float z, float c, float& m, float& s) {
+  if (z > m) {
+    s *= __builtin_amdgcn_exp2f((m - z) * c);
+    m = z;
+  }
+  s += __builtin_amdgcn_exp2f((z - m) * c);
 }
 
-// m and S over elements lo .. hi - 1 of a row, the same in every thread.  -FLT_MAX, not -inf, stands
-// for no maximum yet, so that elements of -inf add exp2(-inf) = 0.
-template <typename T>
-__device__ __forceinline__ void slice_stats(const T* z, int lo, int hi, float c, float* redf, double* redd, float& M,
-                                            double& S) {
-  float m = -__FLT_MAX__, s = 0.0f;
+// The waves' (m, s) joined, in two steps around the caller's barrier; the result is the same in every
+// thread.  A wave without elements, or with -inf alone, has s = 0 and m = -FLT_MAX (which, unlike
+// -inf, lets elements of -inf add exp2(-inf) = 0).
+__device__ __forceinline__ void stats_put(float m, float s, float c, float* wm, double* ws) {
+  const float M = wave_max_f32(m);
+  const double S = wave_sum_f64(s == 0.0f ? 0.0 : (double)s * (double)__builtin_amdgcn_exp2f((m - M) * c));
+  if ((threadIdx.x & 63) == 0) {
+    wm[threadIdx.x >> 6] = M;
+    ws[threadIdx.x >> 6] = S;
+  }
+}
+template <int TH>
+__device__ __forceinline__ void stats_get(float c, const float* wm, const double* ws, float& M, double& S) {
+  const int lane = threadIdx.x & 63;
+  const float m = lane < TH / 64 ? wm[lane] : -__FLT_MAX__;
+  const double s = lane < TH / 64 ? ws[lane] : 0.0;
+  M = wave_max_f32(m);
+  S = wave_sum_f64(s == 0.0 ? 0.0 : s * (double)__builtin_amdgcn_exp2f((m - M) * c));
+}
+
+// running (m, s) of this thread over elements lo .. hi - 1
+template <typename T, int TH>
+__device__ __forceinline__ void slice_stats(const T* z, int lo, int hi, float c, float& m, float& s) {
+  m = -__FLT_MAX__;
+  s = 0.0f;
   int j = lo + 8 * (int)threadIdx.x;
-  constexpr int step = 8 * kDThreads, U = 4;
+  constexpr int step = 8 * TH, U = 4;
   for (; (long long)j + (U - 1) * step + 8 <= hi; j += U * step) {
     float v[U][8];
 #pragma unroll
@@ -141,15 +147,13 @@ __device__ __forceinline__ void slice_stats(const T* z, int lo, int hi, float c,
 #pragma unroll
     for (int u = 0; u < U; ++u) stats8(v[u], c, m, s);
   }
-  for (; j < hi; j += step) {
+  for (; (long long)j + 8 <= hi; j += step) {
     float v[8];
-    if (hi - j >= 8) load8(z + j, v);
-    else load8_inf(z + j, hi - j, v);
+    load8(z + j, v);
     stats8(v, c, m, s);
   }
-  M = block_max_f32(m, redf);
-  // a thread without elements, or with -inf alone, has s = 0
-  S = block_sum_f64(s == 0.0f ? 0.0 : (double)s * (double)__builtin_amdgcn_exp2f((m - M) * c), redd);
+  const int rest = hi & 7;  // the last, fewer than 8: one a thread
+  if ((int)threadIdx.x < rest && hi > lo) stats1((float)z[hi - rest + (int)threadIdx.x], c, m, s);
 }
 
 template <typename T>
@@ -171,13 +175,36 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   *reinterpret_cast<iv4_any*>(p + 4) = b;
 }
 
-// The lists of the gradient's corrections, by group of 8 elements.
-__device__ __forceinline__ void lists_build(const int* idx, int top, unsigned* heads32, unsigned short* next) {
-  for (int x = threadIdx.x; x < kDBuckets / 2; x += kDThreads) heads32[x] = 0xFFFFFFFFu;
-  __syncthreads();
-  for (int k = threadIdx.x; k < top; k += kDThreads)
+// 8 elements of T as fp32 out of the 16-byte words that hold them
+template <typename T>
+__device__ __forceinline__ void unpack8(const iv4 (&h)[sizeof(T) == 4 ? 2 : 1], float (&v)[8]) {
+  typedef T v8 __attribute__((ext_vector_type(16 / sizeof(T))));
+#pragma unroll
+  for (int q = 0; q < (sizeof(T) == 4 ? 2 : 1); ++q) {
+    const v8 x = __builtin_bit_cast(v8, h[q]);
+#pragma unroll
+    for (int e = 0; e < (int)(16 / sizeof(T)); ++e) v[q * 4 + e] = (float)x[e];
+  }
+}
+template <typename T>
+__device__ __forceinline__ iv4 inf_words() {  // -inf throughout
+  const int x = sizeof(T) == 4 ? (int)0xFF800000 : __is_same(T, _Float16) ? (int)0xFC00FC00 : (int)0xFF80FF80;
+  return iv4{x, x, x, x};
+}
+
+// Lists of the teacher's entries by a hash of their index; the caller's barrier lies between clearing
+// and linking, another after linking.
+__device__ __forceinline__ int bucket(int index) { return (int)((unsigned)index * 2654435769u >> 21); }
+static_assert(kDBuckets == 1 << 11, "bucket()");
+template <int TH>
+__device__ __forceinline__ void lists_clear(unsigned* heads32) {
+  for (int x = threadIdx.x; x < kDBuckets / 2; x += TH) heads32[x] = 0xFFFFFFFFu;
+}
+template <int TH>
+__device__ __forceinline__ void lists_link(const int* idx, int top, unsigned* heads32, unsigned short* next) {
+  for (int k = threadIdx.x; k < top; k += TH)
     if (idx[k] >= 0) {
-      const int b = (idx[k] >> 3) & (kDBuckets - 1), sh = 16 * (b & 1);
+      const int b = bucket(idx[k]), sh = 16 * (b & 1);
       unsigned old = heads32[b >> 1], seen;
       do {  // exchange of one half word
         seen = old;
@@ -185,97 +212,160 @@ __device__ __forceinline__ void lists_build(const int* idx, int top, unsigned* h
       } while (old != seen);
       next[k] = (unsigned short)(seen >> sh);
     }
-  __syncthreads();
 }
 
-// dz of elements lo .. hi - 1 (lo a multiple of 8): g (exp2((z - m) c) / S - p), p = e pinv
-template <typename T>
-__device__ __forceinline__ void slice_grad(const T* z, T* d, int lo, int hi, float c, float m, float inv, float g,
-                                           const int* idx, const float* ex, double pinv, const unsigned* heads32,
-                                           const unsigned short* next) {
-  const unsigned short* heads = reinterpret_cast<const unsigned short*>(heads32);
-  const float gi = g * inv;
-  for (int j = lo + 8 * (int)threadIdx.x; j < hi; j += 8 * kDThreads) {
+// g q of 8 elements
+__device__ __forceinline__ void grad8(const float (&v)[8], float m, float c, float gi, float (&o)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) o[e] = __builtin_amdgcn_exp2f((v[e] - m) * c) * gi;
+}
+
+// g q of elements lo .. hi - 1 (lo a multiple of 8)
+template <typename T, int TH>
+__device__ __forceinline__ void slice_grad(const T* z, T* d, int lo, int hi, float m, float c, float gi) {
+  int j = lo + 8 * (int)threadIdx.x;
+  constexpr int step = 8 * TH, U = 2;
+  for (; (long long)j + (U - 1) * step + 8 <= hi; j += U * step) {
+    float v[U][8], o[8];
+#pragma unroll
+    for (int u = 0; u < U; ++u) load8(z + j + u * step, v[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      grad8(v[u], m, c, gi, o);
+      store8(d + j + u * step, o);
+    }
+  }
+  if ((long long)j + 8 <= hi) {
     float v[8], o[8];
-    const bool whole = hi - j >= 8;
-    if (whole) load8(z + j, v);
-    else load8_inf(z + j, hi - j, v);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = __builtin_amdgcn_exp2f((v[e] - m) * c) * gi;
-    unsigned k = heads[(j >> 3) & (kDBuckets - 1)];
-    if (k != kDNone) {
-      unsigned long long sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      for (; k != kDNone; k = next[k])
-        if ((idx[k] >> 3) == (j >> 3)) {
-          const double q = (double)ex[k] * pinv;  // all of a row's are NaN or none
-          const unsigned long long u = q == q ? (unsigned long long)(q * 0x1p60) : kDNaN;
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if ((idx[k] & 7) == e) sum[e] = u == kDNaN ? kDNaN : sum[e] + u;
-        }
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (sum[e]) o[e] -= sum[e] == kDNaN ? __builtin_nanf("") : g * (float)((double)sum[e] * 0x1p-60);
-    }
-    if (whole) {
-      store8(d + j, o);
-    } else {
-      for (int e = 0; e < hi - j; ++e) d[j + e] = (T)o[e];
-    }
+    load8(z + j, v);
+    grad8(v, m, c, gi, o);
+    store8(d + j, o);
+  }
+  const int rest = hi & 7;
+  if ((int)threadIdx.x < rest && hi > lo) {
+    const int x = hi - rest + (int)threadIdx.x;
+    d[x] = (T)(__builtin_amdgcn_exp2f(((float)z[x] - m) * c) * gi);
   }
 }
 
-template <typename T>
+// the teacher's elements of lo .. hi - 1: g (q - p), p = the sum of e pinv over equal indices
+template <typename T, int TH>
+__device__ __forceinline__ void teacher_grad(T* d, int lo, int hi, float m, float c, float g, float gi, double pinv,
+                                             int top, const int* idx, const float* ex, const float* zk,
+                                             const unsigned short* heads, const unsigned short* next) {
+  for (int k = threadIdx.x; k < top; k += TH) {
+    const int i = idx[k];
+    if (i < lo || i >= hi) continue;
+    unsigned long long sum = 0;
+    for (unsigned x = heads[bucket(i)]; x != kDNone; x = next[x])
+      if (idx[x] == i) {
+        const double q = (double)ex[x] * pinv;  // all of a row's are NaN or none
+        sum = q == q ? sum + (unsigned long long)(q * 0x1p60) : kDNaN;
+      }
+    const float p = sum == kDNaN ? __builtin_nanf("") : (float)((double)sum * 0x1p-60);
+    d[i] = (T)(__builtin_amdgcn_exp2f((zk[k] - m) * c) * gi - g * p);
+  }
+}
+
+template <typename T, int TH>
 __device__ __forceinline__ void slice_zero(T* d, int lo, int hi) {
   const float o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  for (int j = lo + 8 * (int)threadIdx.x; j < hi; j += 8 * kDThreads) {
-    if (hi - j >= 8) store8(d + j, o);
-    else
-      for (int e = 0; e < hi - j; ++e) d[j + e] = (T)0.0f;
-  }
+  for (int j = lo + 8 * (int)threadIdx.x; (long long)j + 8 <= hi; j += 8 * TH) store8(d + j, o);
+  const int rest = hi & 7;
+  if ((int)threadIdx.x < rest && hi > lo) d[hi - rest + (int)threadIdx.x] = (T)0.0f;
 }
 
-// sums over the teacher's entries in lo .. hi - 1 of e and of e (z - m): this thread's part.  Taken
-// from m, since z itself may be near the type's lowest value throughout a row.
-template <typename T>
-__device__ __forceinline__ void cross_part(const T* z, int lo, int hi, const int* idx, const float* ex, int top,
+// sums over the teacher's entries in lo .. hi - 1 of e and of e (z - m), by one wave.  Taken from m,
+// since z itself may be near the type's lowest value throughout a row.
+__device__ __forceinline__ void cross_sums(int lo, int hi, const int* idx, const float* ex, const float* zk, int top,
                                            float m, double& mass, double& cross) {
   mass = cross = 0.0;
-  for (int k = threadIdx.x; k < top; k += kDThreads)
+  for (int k = threadIdx.x & 63; k < top; k += 64)
     if (idx[k] >= lo && idx[k] < hi && ex[k] != 0.0f) {
       mass += (double)ex[k];
-      cross += (double)ex[k] * ((double)(float)z[idx[k]] - (double)m);
+      cross += (double)ex[k] * ((double)zk[k] - (double)m);
     }
+  mass = wave_sum_f64(mass);
+  cross = wave_sum_f64(cross);
 }
 
 // a slice's share of a split row, in the workspace
 struct Part {
   double s;      // sum of exp2((z - m) c)
-  double mass;   // sums of e and of e (z - m) over the teacher's entries
+  double mass;   // sums of e and of e (z - m) over the slice's teacher entries
   double cross;
+  TeacherSums t;
   float m;
   float unused;
 };
+
+__device__ __forceinline__ void write_loss(long long row, float w, float Tmp, const TeacherSums& t, double cross, float m,
+                                           double S, float* loss, float* stats) {
+  const double rT = 1.0 / (double)Tmp, kl = t.plogp - cross * t.pinv * rT + log(S);
+  loss[row] = t.pinv != 0.0 ? (float)((double)w * (double)Tmp * (double)Tmp * kl) : 0.0f;
+  stats[2 * row] = S == 0.0 ? -__builtin_inff() : m;
+  stats[2 * row + 1] = (float)S;
+}
+
+// the parts of a row joined, the same in every lane of a wave
+__device__ __forceinline__ void join_parts(const Part* q, int slices, float c, float& m, double& S, double& cross) {
+  const int lane = threadIdx.x & 63;
+  m = -__FLT_MAX__;
+  for (int i = lane; i < slices; i += 64) m = fmaxf(m, q[i].m);
+  m = wave_max_f32(m);
+  S = cross = 0.0;
+  for (int i = lane; i < slices; i += 64) {
+    if (q[i].s != 0.0) S += q[i].s * (double)__builtin_amdgcn_exp2f((q[i].m - m) * c);
+    if (q[i].mass != 0.0) cross += q[i].cross + q[i].mass * ((double)q[i].m - (double)m);
+  }
+  S = wave_sum_f64(S);
+  cross = wave_sum_f64(cross);
+}
+
+// Split rows without a gradient: one wave joins a row's parts.
+__global__ void __launch_bounds__(64) distill_join_kernel(const Part* __restrict__ parts, int slices, float Tmp,
+                                                          const float* __restrict__ weight, float* __restrict__ loss,
+                                                          float* __restrict__ stats) {
+  const long long row = blockIdx.x;
+  const float w = weight ? weight[row] : 1.0f;
+  if (w == 0.0f) {
+    if (threadIdx.x == 0) {
+      loss[row] = 0.0f;
+      stats[2 * row] = 0.0f;
+      stats[2 * row + 1] = 0.0f;
+    }
+    return;
+  }
+  float m;
+  double S, cross;
+  join_parts(parts + row * slices, slices, (float)(1.4426950408889634 / (double)Tmp), m, S, cross);
+  if (threadIdx.x == 0) write_loss(row, w, Tmp, parts[row * slices].t, cross, m, S, loss, stats);
+}
 
 // MODE 0: statistics and loss of whole rows, and their gradient where D is given
 // MODE 1: a slice's share of them (split rows, first launch)
 // MODE 2: the shares joined: the first slice of a row writes statistics and loss, each its gradient
 // MODE 3: gradient of a slice from given statistics
+// CH > 0 (MODE 0 with a gradient): the row, at most 8 TH CH elements, stays in registers between the two
+// passes; all its loads are in flight at once.  Wave 0 sees to the teacher meanwhile.
 // Every thread of a workgroup takes the same branches around the barriers.
-template <typename T, int MODE>
-__global__ void __launch_bounds__(kDThreads) distill_kernel(const T* Z, int V, long long ldz, Teacher teach, float Tmp,
-                                                            const float* __restrict__ weight, float* __restrict__ loss,
-                                                            float* __restrict__ stats, T* D, long long ldd, int slices,
-                                                            int slice, int gslices, Part* __restrict__ parts) {
+template <typename T, int MODE, int TH, int CH>
+__global__ void __launch_bounds__(TH) distill_kernel(const T* Z, int V, long long ldz, Teacher teach, float Tmp,
+                                                     const float* __restrict__ weight, float* __restrict__ loss,
+                                                     float* __restrict__ stats, T* D, long long ldd, int slices,
+                                                     int slice, Part* __restrict__ parts) {
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
-  __shared__ double redd[kDThreads / 64];
-  __shared__ float redf[kDThreads / 64];
+  __shared__ double ws[TH / 64];
+  __shared__ float wm[TH / 64];
+  __shared__ TeacherSums ts;
   int* idx = reinterpret_cast<int*>(lds);
   float* ex = reinterpret_cast<float*>(idx + teach.top);
-  unsigned* heads = reinterpret_cast<unsigned*>(ex + teach.top);
+  float* zk = ex + teach.top;
+  unsigned* heads = reinterpret_cast<unsigned*>(zk + teach.top);
   unsigned short* next = reinterpret_cast<unsigned short*>(heads + kDBuckets / 2);
-  const long long row = blockIdx.x / gslices;
-  const int sl = (int)(blockIdx.x % gslices);
+  const bool wave0 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) == 0;
+  const long long row = blockIdx.x / slices;
+  const int sl = (int)(blockIdx.x % slices);
   const long long lo64 = (long long)sl * slice;
   const int lo = lo64 < V ? (int)lo64 : V, hi = lo64 + slice < V ? (int)(lo64 + slice) : V;
   const T* z = Z + row * ldz;
@@ -288,57 +378,94 @@ __global__ void __launch_bounds__(kDThreads) distill_kernel(const T* Z, int V, l
       stats[2 * row] = 0.0f;
       stats[2 * row + 1] = 0.0f;
     }
-    if (D) slice_zero(d, lo, hi);
+    if (D) slice_zero<T, TH>(d, lo, hi);
     return;
   }
   const float c = (float)(1.4426950408889634 / (double)Tmp);
   const double rT = 1.0 / (double)Tmp;
-  double plogp;
-  const double pinv = teacher_row(teach, row, V, rT, idx, ex, redf, redd, &plogp);
-  __syncthreads();
+  constexpr int W = sizeof(T) == 4 ? 2 : 1;  // 16-byte words of 8 elements
+  iv4 held[CH > 0 ? CH : 1][W];
+  const int rest = V & 7;  // the row's last elements, fewer than 8: one a thread
+  float last = -__builtin_inff();
+  if (CH > 0) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int j = 8 * (i * TH + (int)threadIdx.x);
+#pragma unroll
+      for (int q = 0; q < W; ++q) held[i][q] = j + 8 <= V ? (iv4)*reinterpret_cast<const iv4_any*>(
+                                                                reinterpret_cast<const char*>(z + j) + 16 * q)
+                                                          : inf_words<T>();
+    }
+    if ((int)threadIdx.x < rest) last = (float)z[V - rest + (int)threadIdx.x];
+  }
+  if (D) lists_clear<TH>(heads);
+  if (wave0) {
+    const TeacherSums t = teacher_row(teach, row, V, rT, z, lo, hi, idx, ex, zk);
+    if (threadIdx.x == 0) ts = t;
+  }
   float m;
   double S, mass, cross = 0.0;
   if (MODE == 0 || MODE == 1) {
-    slice_stats(z, lo, hi, c, redf, redd, m, S);
-    cross_part(z, lo, hi, idx, ex, teach.top, m, mass, cross);
-    cross = block_sum_f64(cross, redd);
-    if (MODE == 1) mass = block_sum_f64(mass, redd);
-  } else if (MODE == 2) {
-    const Part* q = parts + row * slices;
-    m = -__FLT_MAX__;
-    for (int i = 0; i < slices; ++i) m = fmaxf(m, q[i].m);
-    S = 0.0;
-    for (int i = 0; i < slices; ++i) {
-      if (q[i].s != 0.0) S += q[i].s * (double)__builtin_amdgcn_exp2f((q[i].m - m) * c);
-      if (q[i].mass != 0.0) cross += q[i].cross + q[i].mass * ((double)q[i].m - (double)m);
+    float tm = -__FLT_MAX__, tsum = 0.0f;
+    if (CH > 0) {
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        // one chunk after the other, and unpacked anew in the second pass: with several chunks as fp32
+        // at a time the row would take twice the registers, and half the waves
+        asm volatile("" : "+v"(tm), "+v"(tsum));
+#pragma unroll
+        for (int q = 0; q < W; ++q) asm volatile("" : "+v"(held[i][q]));
+        float v[8];
+        unpack8<T>(held[i], v);
+        stats8(v, c, tm, tsum);
+      }
+      stats1(last, c, tm, tsum);
+    } else {
+      slice_stats<T, TH>(z, lo, hi, c, tm, tsum);
     }
+    stats_put(tm, tsum, c, wm, ws);
+  }
+  __syncthreads();  // the waves' statistics, the teacher, the cleared lists
+  const TeacherSums t = ts;
+  if (MODE == 0 || MODE == 1) {
+    stats_get<TH>(c, wm, ws, m, S);
+    if (wave0) cross_sums(lo, hi, idx, ex, zk, teach.top, m, mass, cross);
+  } else if (MODE == 2) {
+    join_parts(parts + row * slices, slices, c, m, S, cross);
   } else {
     m = stats[2 * row];
     S = (double)stats[2 * row + 1];
   }
   if (MODE == 1) {
-    if (threadIdx.x == 0) {
-      Part* o = parts + row * slices + sl;
-      o->m = m;
-      o->s = S;
-      o->mass = mass;
-      o->cross = cross;
-    }
+    if (threadIdx.x == 0) parts[row * slices + sl] = Part{S, mass, cross, t, m, 0.0f};
     return;
   }
-  if (MODE != 3 && sl == 0 && threadIdx.x == 0) {
-    const double kl = plogp - cross * pinv * rT + log(S);
-    loss[row] = pinv != 0.0 ? (float)((double)w * (double)Tmp * (double)Tmp * kl) : 0.0f;
-    stats[2 * row] = S == 0.0 ? -__builtin_inff() : m;
-    stats[2 * row + 1] = (float)S;
-  }
+  if (MODE != 3 && sl == 0 && threadIdx.x == 0) write_loss(row, w, Tmp, t, cross, m, S, loss, stats);
   if (!D) return;
-  if (pinv == 0.0) {  // no teacher, no gradient
-    slice_zero(d, lo, hi);
+  if (t.pinv == 0.0) {  // no teacher, no gradient
+    slice_zero<T, TH>(d, lo, hi);
     return;
   }
-  lists_build(idx, teach.top, heads, next);
-  slice_grad(z, d, lo, hi, c, m, (float)(1.0 / S), w * Tmp, idx, ex, pinv, heads, next);
+  lists_link<TH>(idx, teach.top, heads, next);
+  const float g = w * Tmp, gi = g * (float)(1.0 / S);
+  if (CH > 0) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int j = 8 * (i * TH + (int)threadIdx.x);
+#pragma unroll
+      for (int q = 0; q < W; ++q) asm volatile("" : "+v"(held[i][q]));
+      float v[8], o[8];
+      unpack8<T>(held[i], v);
+      grad8(v, m, c, gi, o);
+      if (j + 8 <= V) store8(d + j, o);
+    }
+    if ((int)threadIdx.x < rest) d[V - rest + (int)threadIdx.x] = (T)(__builtin_amdgcn_exp2f((last - m) * c) * gi);
+  } else {
+    slice_grad<T, TH>(z, d, lo, hi, m, c, gi);
+  }
+  __syncthreads();  // the lists are linked, and the stores above come before those below
+  teacher_grad<T, TH>(d, lo, hi, m, c, g, gi, t.pinv, teach.top, idx, ex, zk,
+                      reinterpret_cast<const unsigned short*>(heads), next);
 }
 
 // Slices of a row, so that few rows fill the card: about four workgroups a CU, none with less than
@@ -360,29 +487,58 @@ size_t distill_workspace_bytes(long long rows, int V) {
   return slices > 1 ? (size_t)rows * slices * sizeof(Part) : 0;
 }
 
-template <typename T>
-static hipError_t distill_typed(const DistillLaunch& L, hipStream_t st) {
+template <typename T, int MODE, int TH, int CH>
+static void distill_launch(const DistillLaunch& L, bool lists, int slices, int slice, hipStream_t st) {
   const Teacher t{L.teacher, L.index, L.t_type, L.index_bytes, L.top};
-  const T* Z = static_cast<const T*>(L.logits);
-  T* D = static_cast<T*>(L.dlogits);
-  Part* parts = static_cast<Part*>(L.ws);
+  const size_t smem = (size_t)L.top * 12 + (lists ? kDBuckets * 2 + (size_t)L.top * 2 : 0);
+  hipLaunchKernelGGL((distill_kernel<T, MODE, TH, CH>), dim3((unsigned)(L.rows * slices)), dim3(TH), smem, st,
+                     static_cast<const T*>(L.logits), L.vocab, L.ldz, t, L.temperature, L.weight, L.loss, L.stats,
+                     static_cast<T*>(L.dlogits), L.ldd, slices, slice, static_cast<Part*>(L.ws));
+}
+
+template <typename T>
+static hipError_t distill_typed(const DistillLaunch& all, hipStream_t st) {
   int slices, slice;
-  split(L.rows, L.vocab, &slices, &slice);
-  const size_t small = (size_t)L.top * 8, big = small + kDBuckets * 2 + (size_t)L.top * 2;
-  const unsigned whole = (unsigned)L.rows, parted = (unsigned)(L.rows * slices);
-#define EXTERND_DISTILL(MODE, GRID, GS, SMEM, LEN)                                                                     \
-  hipLaunchKernelGGL((distill_kernel<T, MODE>), dim3(GRID), dim3(kDThreads), SMEM, st, Z, L.vocab, L.ldz, t,           \
-                     L.temperature, L.weight, L.loss, L.stats, D, L.ldd, slices, LEN, GS, parts)
-  if (!L.loss) {
-    EXTERND_DISTILL(3, parted, slices, big, slice);
-  } else if (slices == 1) {
-    EXTERND_DISTILL(0, whole, 1, D ? big : small, slice);
-  } else {
-    EXTERND_DISTILL(1, parted, slices, small, slice);
-    if (D) EXTERND_DISTILL(2, parted, slices, big, slice);
-    else EXTERND_DISTILL(2, whole, 1, small, slice);
+  split(all.rows, all.vocab, &slices, &slice);
+  DistillLaunch L = all;
+  // runs of 2^21 rows: a launch holds below 2^32 threads (split rows are fewer than 1024)
+  for (long long r0 = 0; r0 < all.rows; r0 += 1ll << 21) {
+    L.rows = all.rows - r0 < (1ll << 21) ? all.rows - r0 : 1ll << 21;
+    L.logits = static_cast<const T*>(all.logits) + r0 * L.ldz;
+    L.teacher = static_cast<const char*>(all.teacher) + r0 * L.top * (L.t_type == 0 ? 4 : 2);
+    L.index = static_cast<const char*>(all.index) + r0 * L.top * L.index_bytes;
+    L.weight = all.weight ? all.weight + r0 : nullptr;
+    L.loss = all.loss ? all.loss + r0 : nullptr;
+    L.stats = all.stats + 2 * r0;
+    L.dlogits = all.dlogits ? static_cast<T*>(all.dlogits) + r0 * L.ldd : nullptr;
+    if (!L.loss) {
+      distill_launch<T, 3, kDThreads, 0>(L, true, slices, slice, st);
+    } else if (slices > 1) {
+      L.dlogits = nullptr;
+      distill_launch<T, 1, kDThreads, 0>(L, false, slices, slice, st);
+      L.dlogits = all.dlogits;
+      if (L.dlogits)
+        distill_launch<T, 2, kDThreads, 0>(L, true, slices, slice, st);
+      else
+        hipLaunchKernelGGL(distill_join_kernel, dim3((unsigned)L.rows), dim3(64), 0, st, static_cast<const Part*>(L.ws),
+                           slices, L.temperature, L.weight, L.loss, L.stats);
+    } else if (!L.dlogits) {
+      distill_launch<T, 0, kDThreads, 0>(L, false, 1, slice, st);
+    } else {
+      // The shape by the row's length: held where a thread has 8 or 16 chunks, with as few threads as
+      // hold it (several rows share a CU, one's stores under another's loads).  Measured, 2048 rows of
+      // bf16, step in us, held / 256 threads streaming / 1024 streaming: 8192: 19.5 / 18.7 / 29.5;
+      // 32768: 52.7 / 64.5 / 62.2; 65536: 115 / 163 / 137; 131072: 233 / 334 / 267.
+      constexpr bool f32 = sizeof(T) == 4;
+      if (L.vocab <= 8 * 256 * 4) distill_launch<T, 0, kDThreads, 0>(L, true, 1, slice, st);
+      else if (L.vocab <= 8 * 256 * 8) distill_launch<T, 0, 256, 8>(L, true, 1, slice, st);
+      else if (L.vocab <= 8 * 512 * 8) distill_launch<T, 0, 512, 8>(L, true, 1, slice, st);
+      else if (!f32 && L.vocab <= 8 * 512 * 16) distill_launch<T, 0, 512, f32 ? 8 : 16>(L, true, 1, slice, st);
+      else if (f32 && L.vocab <= 8 * 1024 * 8) distill_launch<T, 0, 1024, 8>(L, true, 1, slice, st);
+      else if (!f32 && L.vocab <= 8 * 1024 * 16) distill_launch<T, 0, 1024, f32 ? 8 : 16>(L, true, 1, slice, st);
+      else distill_launch<T, 0, 1024, 0>(L, true, 1, slice, st);
+    }
   }
-#undef EXTERND_DISTILL
   return hipGetLastError();
 }
 

@@ -94,7 +94,8 @@ def run(z, a, i, T=1.0, w=None, grad=True):
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("rows,vocab,top", [(1, 1, 1), (3, 7, 3), (2, 8, 8), (5, 9, 20), (4, 255, 16), (1100, 100, 7),
                                             (3, 2048, 64), (2, 2049, 1), (6, 8192, 128), (3, 40001, 256), (1, 131072, 64),
-                                            (1030, 4099, 33), (2, 70000, 1024)])
+                                            (1030, 4099, 33), (2, 70000, 1024), (1025, 8201, 9), (1024, 16385, 5),
+                                            (1024, 32769, 70), (1024, 65543, 3)])
 def test_loss_and_gradient(rows, vocab, top, dtype):
     z, a, i = make(rows, vocab, top, TYPES[dtype], rows + vocab + top)
     run(z, a, i)
