@@ -596,11 +596,12 @@ int externd_distill_grad(const void* logits, int z_type, int64_t rows, int64_t v
 
 // ---- gradient of the factored layer
 
+constexpr int64_t kMaxFactorSize = (int64_t)1 << 33;  // elements of a factor: a launch's threads
 constexpr int64_t kMaxFactorLen = (int64_t)1 << 23;  // 128 len < 2^31: a digit's sum fits int32
 
 int64_t externd_apply_factors_grad_workspace(int64_t k, int64_t m, int64_t n, int64_t batch) {
   if (k < 1 || m < 1 || n < 1 || k > kMaxFactorLen || m > kMaxFactorLen || n > kMaxFactorLen || batch < 0 ||
-      batch > kMaxCount)
+      batch > kMaxCount || k * m > kMaxFactorSize || k * n > kMaxFactorSize)
     return -1;
   return (int64_t)grad_workspace_bytes((int)k, (int)m, (int)n, batch);
 }
@@ -611,6 +612,8 @@ int externd_apply_factors_grad(const uint32_t* B_packed, const uint32_t* C_packe
   g_last_error.clear();
   if (k < 1 || m < 1 || n < 1 || k > kMaxFactorLen || m > kMaxFactorLen || n > kMaxFactorLen)
     return fail(EXTERND_EINVAL, "need 1 <= k, m, n <= %lld", (long long)kMaxFactorLen);
+  if (k * m > kMaxFactorSize || k * n > kMaxFactorSize)
+    return fail(EXTERND_EINVAL, "need k m and k n <= 2^33");
   if (batch < 0 || batch > kMaxCount) return fail(EXTERND_EINVAL, "need 0 <= batch < 2^31");
   if (!dX && !dD) {
     if (batch == 0) return EXTERND_OK;

@@ -109,12 +109,11 @@ __device__ __forceinline__ void fx_digits7(const unsigned long long (&b)[4], uns
 // smax[b gridDim.x + blockIdx.x] receives the workgroup's max |s_b| (high word of the fp64 bits).
 // RAW (the layer's gradient): t itself goes to Traw, and s only where S is given.
 template <bool RAW>
-__global__ void __launch_bounds__(kTThreads) infer_t_kernel(const uint32_t* __restrict__ C, int wn, int n,
-                                                      const float* __restrict__ D, int k, const float* __restrict__ X,
-                                                      int batch, int x_vec4, int c_vec4, double* __restrict__ S,
-                                                      unsigned* __restrict__ smax, long long* __restrict__ Yacc,
-                                                      long long nY, unsigned* __restrict__ cnt, int ncnt,
-                                                      double* __restrict__ Traw) {
+__device__ __forceinline__ void t_pass(const uint32_t* __restrict__ C, int wn, int n, const float* __restrict__ D, int k,
+                                       const float* __restrict__ X, int batch, int x_vec4, int c_vec4,
+                                       double* __restrict__ S, unsigned* __restrict__ smax,
+                                       long long* __restrict__ Yacc, long long nY, unsigned* __restrict__ cnt, int ncnt,
+                                       double* __restrict__ Traw) {
   // every argument fetched at once (else the compiler waits for them one after another)
   asm volatile("" ::"s"(C), "s"(wn), "s"(n), "s"(D), "s"(k), "s"(X), "s"(batch), "s"(x_vec4), "s"(c_vec4), "s"(S),
                "s"(smax), "s"(Yacc), "s"(nY), "s"(cnt), "s"(ncnt));
@@ -326,6 +325,14 @@ __global__ void __launch_bounds__(kTThreads) infer_t_kernel(const uint32_t* __re
   }
 }
 
+__global__ void __launch_bounds__(kTThreads) infer_t_kernel(const uint32_t* __restrict__ C, int wn, int n,
+                                                      const float* __restrict__ D, int k, const float* __restrict__ X,
+                                                      int batch, int x_vec4, int c_vec4, double* __restrict__ S,
+                                                      unsigned* __restrict__ smax, long long* __restrict__ Yacc,
+                                                      long long nY, unsigned* __restrict__ cnt, int ncnt) {
+  t_pass<false>(C, wn, n, D, k, X, batch, x_vec4, c_vec4, S, smax, Yacc, nY, cnt, ncnt, nullptr);
+}
+
 // this thread's part of max |s_b| over the t pass's per-workgroup maxima (high words of the bits)
 __device__ __forceinline__ unsigned infer_smax_part(const unsigned* smax, int gxt, int b) {
   unsigned h = 0u;
@@ -368,11 +375,10 @@ __device__ __forceinline__ void infer_s_scales(unsigned h0, unsigned h1, int k, 
 // itself, and the last one reads the sums back with atomic adds of zero, at the same place the
 // adds were made.
 // Every global load of the workgroup is issued before the first is used.
-__global__ void __launch_bounds__(kYThreads) infer_y_kernel(const uint32_t* __restrict__ B, int wm, int m, int k,
-                                                      const double* __restrict__ S, int batch,
-                                                      const unsigned* __restrict__ smax, int gxt, int nwg,
-                                                      int b_vec4, long long* __restrict__ Yacc,
-                                                      unsigned* __restrict__ cnt, float* __restrict__ Y) {
+__device__ __forceinline__ void y_pass(const uint32_t* __restrict__ B, int wm, int m, int k,
+                                       const double* __restrict__ S, int batch, const unsigned* __restrict__ smax,
+                                       int gxt, int nwg, int b_vec4, long long* __restrict__ Yacc,
+                                       unsigned* __restrict__ cnt, float* __restrict__ Y) {
   asm volatile("" ::"s"(B), "s"(wm), "s"(m), "s"(k), "s"(S), "s"(batch), "s"(smax), "s"(gxt), "s"(nwg), "s"(b_vec4),
                "s"(Yacc), "s"(cnt), "s"(Y));
   __shared__ int last;
@@ -521,6 +527,14 @@ __global__ void __launch_bounds__(kYThreads) infer_y_kernel(const uint32_t* __re
   }
 }
 
+__global__ void __launch_bounds__(kYThreads) infer_y_kernel(const uint32_t* __restrict__ B, int wm, int m, int k,
+                                                      const double* __restrict__ S, int batch,
+                                                      const unsigned* __restrict__ smax, int gxt, int nwg,
+                                                      int b_vec4, long long* __restrict__ Yacc,
+                                                      unsigned* __restrict__ cnt, float* __restrict__ Y) {
+  y_pass(B, wm, m, k, S, batch, smax, gxt, nwg, b_vec4, Yacc, cnt, Y);
+}
+
 static int infer_gxt(int k) { return (k + kTComp - 1) / kTComp; }
 
 static int infer_groups(int m) { return ((m + 15) / 16 + kYWords - 1) / kYWords; }  // output groups of the y pass
@@ -551,8 +565,8 @@ hipError_t infer_run(const uint32_t* B, const uint32_t* C, const float* D, int k
   const int gb = (batch + 1) / 2;
   const long long nwg = infer_groups(m), nch = (k + kYComp - 1) / kYComp;
   if (nwg * nch > 2147483647ll || nwg * gb > 2147483647ll) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((infer_t_kernel<false>), dim3(gxt, gb), dim3(kTThreads), 0, st, C, wn, n, D, k, X, batch, x_vec4,
-                     c_vec4, S, smax, Yacc, nY, cnt, (int)(nwg * gb), nullptr);
+  hipLaunchKernelGGL(infer_t_kernel, dim3(gxt, gb), dim3(kTThreads), 0, st, C, wn, n, D, k, X, batch, x_vec4, c_vec4, S,
+                     smax, Yacc, nY, cnt, (int)(nwg * gb));
   hipLaunchKernelGGL(infer_y_kernel, dim3((unsigned)(nwg * nch), gb), dim3(kYThreads), 0, st, B, wm, m, k, S, batch, smax,
                      gxt, (int)nwg, b_vec4, Yacc, cnt, Y);
   return hipGetLastError();
@@ -560,14 +574,49 @@ hipError_t infer_run(const uint32_t* B, const uint32_t* C, const float* D, int k
 
 // ---- gradient of few vectors ------------------------------------------------------------------
 // y = B diag(D) C x:  u = B^T dy,  dx = C^T (D u) is inference with the factors exchanged, and
-// dD_i = sum_b t_bi u_bi with t = C x needs one t pass more.
-__global__ void __launch_bounds__(256) grad_d_kernel(const double* __restrict__ Tr, const double* __restrict__ U, int k,
-                                                     int batch, float* __restrict__ dD) {
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  if (i >= k) return;
+// dD_i = sum_b t_bi u_bi with t = C x needs one t pass more.  Both t passes are one launch (blockIdx.z),
+// and dD's sums are workgroups of their own beside the y pass (blockIdx.x from ny on).
+struct TPass {
+  const uint32_t* P;
+  const float* X;
+  double* S;
+  double* raw;
+  int w, n, x_vec4, p_vec4, ncnt;
+  long long nY;
+};
+__global__ void __launch_bounds__(kTThreads) infer_grad_t_kernel(TPass p0, TPass p1, const float* __restrict__ D, int k,
+                                                           int batch, unsigned* __restrict__ smax,
+                                                           long long* __restrict__ acc, unsigned* __restrict__ cnt) {
+  const TPass p = blockIdx.z == 0 ? p0 : p1;
+  t_pass<true>(p.P, p.w, p.n, D, k, p.X, batch, p.x_vec4, p.p_vec4, p.S, smax, acc, p.nY, cnt, p.ncnt, p.raw);
+}
+
+__global__ void __launch_bounds__(kYThreads) infer_grad_y_kernel(const uint32_t* __restrict__ C, int wn, int n, int k,
+                                                           const double* __restrict__ S, int batch,
+                                                           const unsigned* __restrict__ smax, int gxt, int nwg,
+                                                           int c_vec4, long long* __restrict__ acc,
+                                                           unsigned* __restrict__ cnt, float* __restrict__ dX, int ny,
+                                                           const double* __restrict__ Tr,
+                                                           const double* __restrict__ U, float* __restrict__ dD) {
+  if ((int)blockIdx.x < ny) {
+    y_pass(C, wn, n, k, S, batch, smax, gxt, nwg, c_vec4, acc, cnt, dX);
+    return;
+  }
+  if (blockIdx.y != 0) return;
+  // 64 components a workgroup, the batch over its eight waves, the waves' sums added in order
+  __shared__ double part[kYThreads];
+  const int wv = threadIdx.x >> 6, i = ((int)blockIdx.x - ny) * 64 + (threadIdx.x & 63);
   double s = 0.0;
-  for (int b = 0; b < batch; ++b) s += Tr[(size_t)b * k + i] * U[(size_t)b * k + i];
-  dD[i] = (float)s;
+  if (i < k) {
+#pragma unroll 4
+    for (int b = wv; b < batch; b += kYThreads / 64) s += Tr[(size_t)b * k + i] * U[(size_t)b * k + i];
+  }
+  part[threadIdx.x] = s;
+  __syncthreads();
+  if (wv == 0 && i < k) {
+    for (int w = 1; w < kYThreads / 64; ++w) s += part[64 * w + threadIdx.x];
+    dD[i] = (float)s;
+  }
 }
 
 size_t infer_grad_workspace_bytes(int k, int n, int batch) {
@@ -594,18 +643,15 @@ hipError_t infer_grad_run(const uint32_t* B, const uint32_t* C, const float* D, 
   };
   const int gb = (batch + 1) / 2;
   const long long nwg = infer_groups(n), nch = (k + kYComp - 1) / kYComp;
-  if (nwg * nch > 2147483647ll || nwg * gb > 2147483647ll) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((infer_t_kernel<true>), dim3(gxt, gb), dim3(kTThreads), 0, st, B, wm, m, D, k, dY, batch,
-                     vec4(m, dY), vec4(wm, B), dX ? S : nullptr, smax, acc, dX ? (long long)batch * n : 0ll, cnt,
-                     dX ? (int)(nwg * gb) : 0, U);
-  if (dD) {
-    hipLaunchKernelGGL((infer_t_kernel<true>), dim3(gxt, gb), dim3(kTThreads), 0, st, C, wn, n, D, k, X, batch,
-                       vec4(n, X), vec4(wn, C), static_cast<double*>(nullptr), smax, acc, 0ll, cnt, 0, Tr);
-    hipLaunchKernelGGL(grad_d_kernel, dim3((k + 255) / 256), dim3(256), 0, st, Tr, U, k, batch, dD);
-  }
-  if (dX)
-    hipLaunchKernelGGL(infer_y_kernel, dim3((unsigned)(nwg * nch), gb), dim3(kYThreads), 0, st, C, wn, n, k, S, batch,
-                       smax, gxt, (int)nwg, vec4(wn, C), acc, cnt, dX);
+  if (nwg * nch > (1ll << 22) || nwg * gb > 2147483647ll) return hipErrorInvalidValue;
+  const TPass back{B, dY, dX ? S : nullptr, U, wm, m, vec4(m, dY), vec4(wm, B), dX ? (int)(nwg * gb) : 0,
+                   dX ? (long long)batch * n : 0ll};
+  const TPass fwd{C, X, nullptr, Tr, wn, n, vec4(n, X), vec4(wn, C), 0, 0ll};
+  hipLaunchKernelGGL(infer_grad_t_kernel, dim3(gxt, gb, dD ? 2 : 1), dim3(kTThreads), 0, st, back, fwd, D, k, batch, smax,
+                     acc, cnt);
+  const long long ny = dX ? nwg * nch : 0;
+  hipLaunchKernelGGL(infer_grad_y_kernel, dim3((unsigned)(ny + (dD ? (k + 63) / 64 : 0)), gb), dim3(kYThreads), 0, st, C,
+                     wn, n, k, S, batch, smax, gxt, (int)nwg, vec4(wn, C), acc, cnt, dX, (int)ny, Tr, U, dD);
   return hipGetLastError();
 }
 

@@ -1,13 +1,19 @@
 // Gradient of a layer held as packed ternary factors, y = B diag(D) C x, over a batch:
 //   u_b = B^T dy_b,   t_b = C x_b,   dD_i = sum_b t_bi u_bi,   dx_b = C^T (D u_b)
 //
-// Few vectors go through the inference kernels (apply.hip).  A larger batch is three products of
+// Little work goes through the inference kernels (apply.hip).  A larger batch is three products of
 // 8-bit integers (igemm.hpp): each vector enters as four rows of signed 8-bit digits of a
 // fixed-point image with its own power-of-two scale, N = rint(x 2^(30 - E)), |x| < 2^E for the
 // whole vector, N = d0 + 2^8 d1 + 2^16 d2 + 2^24 d3; the factors' codes are widened to bytes.  A
 // digit's sum is exact in int32 (lengths below 2^24), the four are joined in int64, scaled and
 // rounded once to fp32: the image's rounding, 2^-31 of the vector's largest power of two, is the
-// only error of a product besides.  t u and its sum over the batch are fp64, in a fixed order.
+// only error of a product besides.  t u and its sum over the batch are fp64, in a fixed order: the
+// product that makes t multiplies its tile by u's and adds over the tile's vectors, so t is never
+// stored (split products, which have no whole tiles, store it).
+//
+// Bound by the products (2048 vectors, k = 7680, 2560 x 2560: 966 10^9 operations of digits in about
+// 480 of 540 us, 2.0 10^15 a second).  Three digits would take a quarter less, but their 2^-23 of the
+// vector's largest element is worse than fp32 wherever a few channels are large.
 #include <algorithm>
 
 #include "common.hpp"
@@ -18,8 +24,7 @@
 namespace externd {
 
 constexpr int kGChunk = 4096;       // vectors per pass over the factors (bounds the workspace)
-constexpr int kGFew = 16;           // batches up to this take the inference kernels
-constexpr int kGParts = 32;         // partial sums of dD
+constexpr int kGParts = 32;         // partial sums of dD where the products are split
 constexpr int kGBad = 0x7FFFFFFF;   // exponent of a vector with a NaN or an infinity
 
 static size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -33,9 +38,9 @@ __device__ __forceinline__ unsigned widen4(unsigned x) {
 }
 
 // packed rows -> bytes: out[r][16 w .. 16 w + 15] = the codes of word w
-__global__ void __launch_bounds__(256) widen_kernel(const uint32_t* __restrict__ P, long long words,
-                                                    int8_t* __restrict__ out) {
-  const long long x = (long long)blockIdx.x * 256 + threadIdx.x;
+__device__ __forceinline__ void widen(const uint32_t* __restrict__ P, long long words, long long block,
+                                      int8_t* __restrict__ out) {
+  const long long x = block * 256 + threadIdx.x;
   if (x >= words) return;
   const unsigned w = P[x];
   const iv4 v = {(int)widen4(w & 255u), (int)widen4(w >> 8 & 255u), (int)widen4(w >> 16 & 255u), (int)widen4(w >> 24)};
@@ -43,12 +48,11 @@ __global__ void __launch_bounds__(256) widen_kernel(const uint32_t* __restrict__
 }
 
 // packed rows -> bytes of the transpose: out[j][i] = code j of row i, i < kp (zeros from k on).
-// Workgroup: 256 rows x 16 words; thread: 16 rows of one word.
-__global__ void __launch_bounds__(256) widen_t_kernel(const uint32_t* __restrict__ P, int k, int words, int n,
-                                                      int8_t* __restrict__ out, long long kp) {
-  __shared__ unsigned tile[256 * 17];
+// Workgroup (bx, by): rows 256 bx on, words 16 by on; thread: 16 rows of one word.
+__device__ __forceinline__ void widen_t(const uint32_t* __restrict__ P, int k, int words, int n, long long bx,
+                                        long long by, int8_t* __restrict__ out, long long kp, unsigned* tile) {
   const int tid = threadIdx.x;
-  const long long i0 = (long long)blockIdx.x * 256, w0 = (long long)blockIdx.y * 16;
+  const long long i0 = bx * 256, w0 = by * 16;
 #pragma unroll
   for (int u = 0; u < 16; ++u) {
     const int r = (tid >> 4) + 16 * u, c = tid & 15;
@@ -92,11 +96,8 @@ __device__ __forceinline__ void digits4(const float (&x)[4], int sh, unsigned (&
 
 // One vector a workgroup: x (times D where given) -> digit rows 4 b .. 4 b + 3 of np bytes, and the
 // exponent E - 30 of its image's unit.
-__global__ void __launch_bounds__(256) digits_kernel(const float* __restrict__ X, long long n,
-                                                     const float* __restrict__ D, int8_t* __restrict__ out,
-                                                     long long np, int* __restrict__ ex) {
-  __shared__ unsigned wmx[4];
-  const long long b = blockIdx.x;
+__device__ __forceinline__ void digits(const float* __restrict__ X, long long n, const float* __restrict__ D, long long b,
+                                       int8_t* __restrict__ out, long long np, int* __restrict__ ex, unsigned* wmx) {
   const float* x = X + b * n;
   auto get = [&](long long j, float (&v)[4]) {
     if (j + 4 <= n) {
@@ -143,6 +144,47 @@ __global__ void __launch_bounds__(256) digits_kernel(const float* __restrict__ X
   }
 }
 
+__global__ void __launch_bounds__(256) digits_kernel(const float* __restrict__ X, long long n,
+                                                     const float* __restrict__ D, int8_t* __restrict__ out,
+                                                     long long np, int* __restrict__ ex) {
+  __shared__ unsigned wmx[4];
+  digits(X, n, D, blockIdx.x, out, np, ex, wmx);
+}
+
+// Everything the products need but D u, in one launch: digits of dY and X (the rows of one pass), the
+// factors' bytes (on the first pass).  Workgroups in runs: count[q] of them for part q.
+struct Prep {
+  const float* dY;
+  const float* X;
+  const uint32_t* B;
+  const uint32_t* C;
+  int8_t* yd;
+  int8_t* xd;
+  int8_t* be;
+  int8_t* ce;
+  int8_t* ct;
+  int* ex;
+  int m, n, k, batch;
+  unsigned count[5];
+};
+__global__ void __launch_bounds__(256) prep_kernel(Prep p) {
+  __shared__ unsigned lds[256 * 17];
+  const long long kp = (p.k + 15ll) & ~15ll, mp = (p.m + 15ll) & ~15ll, np = (p.n + 15ll) & ~15ll;
+  unsigned b = blockIdx.x;
+  if (b < p.count[0]) return digits(p.dY, p.m, nullptr, b, p.yd, mp, p.ex, lds);
+  b -= p.count[0];
+  if (b < p.count[1]) return digits(p.X, p.n, nullptr, b, p.xd, np, p.ex + p.batch, lds);
+  b -= p.count[1];
+  if (b < p.count[2]) {
+    const unsigned across = (unsigned)((np / 16 + 15) / 16);
+    return widen_t(p.C, p.k, (int)(np / 16), p.n, b / across, b % across, p.ct, kp, lds);
+  }
+  b -= p.count[2];
+  if (b < p.count[3]) return widen(p.B, p.k * (mp / 16), b, p.be);
+  b -= p.count[3];
+  widen(p.C, p.k * (np / 16), b, p.ce);
+}
+
 // rows 4 b .. 4 b + 3 of a product are one vector's digits: out[b][col] = 2^e sum_q 2^(8 q) row_q
 struct JoinDigits {
   const int* ex;
@@ -183,29 +225,105 @@ struct JoinDigits {
   }
 };
 
-// part[p][i] (+)= sum over the batch's rows of part p of t u
+// The product that makes t, with u at hand: part[rows / 64 (32 for a matrix of up to 64 rows)][col] =
+// the sum of t u over the vectors of those rows.
+struct DotDigits {
+  const int* ex;
+  const float* u;
+  long long ld;
+  double* part;
+  long long row0;
+  static constexpr bool kLds = false;
+  __device__ __forceinline__ void at(long long m0, long long n0) {
+    ex += m0 >> 2;
+    u += (m0 >> 2) * ld + n0;
+    part += n0;
+    row0 = m0;
+  }
+  template <int FM, int FN>
+  __device__ __forceinline__ void finish(const iv16 (&acc)[FM][FN], int r0, int c0, int mr, int nr, float*) const {
+    const int lane = threadIdx.x & 63, lg = lane >> 5, lr = lane & 31;
+    constexpr int G = FM > 1 ? 2 : 1;  // accumulators of one partial sum
+#pragma unroll
+    for (int g = 0; g < FM; g += G) {
+      if (r0 + 32 * g >= mr) break;  // the same for the wave
+      int e[G][4];
+      float uv[G][FN][4];
+#pragma unroll
+      for (int i = 0; i < G; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int r = r0 + 32 * (g + i) + 4 * lg + 8 * q, v = (r < mr ? r : mr - 1) >> 2;
+          e[i][q] = ex[v];
+#pragma unroll
+          for (int j = 0; j < FN; ++j) {
+            const int c = c0 + 32 * j + lr;
+            uv[i][j][q] = u[v * ld + (c < nr ? c : nr - 1)];
+          }
+        }
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        double s = 0.0;
+#pragma unroll
+        for (int i = 0; i < G; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const iv16& a = acc[g + i][j];
+            const long long v = (long long)a[4 * q] + ((long long)a[4 * q + 1] << 8) + ((long long)a[4 * q + 2] << 16) +
+                                ((long long)a[4 * q + 3] << 24);
+            const double t = e[i][q] == kGBad ? (double)__builtin_nanf("") : ldexp((double)v, e[i][q]);
+            if (r0 + 32 * (g + i) + 4 * lg + 8 * q < mr) s += t * (double)uv[i][j][q];
+          }
+        s += __shfl_xor(s, 32);
+        const int c = c0 + 32 * j + lr;
+        if (lg == 0 && c < nr) part[(row0 + r0 + 32 * g) / (32 * G) * ld + c] = s;
+      }
+    }
+  }
+};
+
+// part[p][i] = sum over the batch's rows of part p of t u (split products)
 __global__ void __launch_bounds__(256) dsum_kernel(const float* __restrict__ Tm, const float* __restrict__ U, int k,
-                                                   int batch, int first, double* __restrict__ part) {
+                                                   int batch, double* __restrict__ part) {
   const int i = blockIdx.x * 256 + threadIdx.x;
   if (i >= k) return;
   const int per = (batch + kGParts - 1) / kGParts;
   const int b0 = blockIdx.y * per, b1 = b0 + per < batch ? b0 + per : batch;
-  double s = first ? 0.0 : part[(size_t)blockIdx.y * k + i];
+  double s = 0.0;
+#pragma unroll 4
   for (int b = b0; b < b1; ++b) s += (double)Tm[(size_t)b * k + i] * (double)U[(size_t)b * k + i];
   part[(size_t)blockIdx.y * k + i] = s;
 }
 
-__global__ void __launch_bounds__(256) dfin_kernel(const double* __restrict__ part, int parts, int k,
-                                                   float* __restrict__ dD) {
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  if (i >= k) return;
+// the parts of one pass added in order to what earlier passes left in sum; the last pass rounds.
+// Workgroup: 64 components, the parts over its four waves.
+__global__ void __launch_bounds__(256) dfin_kernel(const double* __restrict__ part, int parts, int k, int first, int last,
+                                                   double* __restrict__ sum, float* __restrict__ dD) {
+  __shared__ double ws[256];
+  const int wv = threadIdx.x >> 6, i = blockIdx.x * 64 + (threadIdx.x & 63);
   double s = 0.0;
-  for (int p = 0; p < parts; ++p) s += part[(size_t)p * k + i];
-  dD[i] = (float)s;
+  if (i < k) {
+#pragma unroll 8
+    for (int p = wv; p < parts; p += 4) s += part[(size_t)p * k + i];
+  }
+  ws[threadIdx.x] = s;
+  __syncthreads();
+  if (wv != 0 || i >= k) return;
+  for (int w = 1; w < 4; ++w) s += ws[64 * w + threadIdx.x];
+  if (!first) s += sum[i];
+  if (last) dD[i] = (float)s;
+  else sum[i] = s;
+}
+
+// Batches whose work is small enough for the inference kernels: they take about 6 10^-8 us per vector
+// and pair of a component and an element, in two launches, against the seven launches and 40 us or
+// more of the products.
+static bool grad_few(int k, int m, int n, long long batch) {
+  return batch <= 4096 && (double)batch * k * ((double)m + 2.0 * n) <= 8.5e8;
 }
 
 struct GradSpace {
-  size_t be, ce, ct, xd, yd, sd, u, t, ex, part, split, bytes;
+  size_t be, ce, ct, xd, yd, sd, u, t, ex, part, sum, split, bytes;
 };
 static GradSpace grad_space(int k, int m, int n, long long batch) {
   const size_t c = (size_t)(batch < kGChunk ? batch : kGChunk);
@@ -224,18 +342,19 @@ static GradSpace grad_space(int k, int m, int n, long long batch) {
   s.yd = take(4 * c * mp);
   s.sd = take(4 * c * kp);
   s.u = take(4 * c * k);
-  s.t = take(4 * c * k);
   s.ex = take(3 * c * 4);
-  s.part = take((size_t)kGParts * k * 8);
-  // the parts of a split product, one product at a time; a last pass of fewer vectors may split where
-  // the others do not
-  size_t split = 0;
-  for (long long b = batch < kGChunk ? batch : batch % kGChunk, once = 0; once < 2; b = (long long)c, ++once)
+  s.part = take(std::max<size_t>(kGParts, 4 * c / 32 + 2) * k * 8);
+  s.sum = take((size_t)k * 8);
+  // t and the parts of split products, one product at a time; a last pass of fewer vectors may split
+  // where the others do not
+  size_t split = 0, t = 0;
+  for (const long long b : {(long long)c, batch % kGChunk})
     if (b > 0) {
-      split = std::max(split, tile_plan(4 * b, k, (int)mp).bytes);
-      split = std::max(split, tile_plan(4 * b, k, (int)np).bytes);
-      split = std::max(split, tile_plan(4 * b, n, (int)kp).bytes);
+      const TilePlan pt = tile_plan(4 * b, k, (int)np);
+      if (pt.parts > 1) t = std::max(t, (size_t)(4 * b * k));
+      split = std::max({split, pt.bytes, tile_plan(4 * b, k, (int)mp).bytes, tile_plan(4 * b, n, (int)kp).bytes});
     }
+  s.t = take(t);
   s.split = take(split);
   s.bytes = off;
   return s;
@@ -243,60 +362,68 @@ static GradSpace grad_space(int k, int m, int n, long long batch) {
 
 size_t grad_workspace_bytes(int k, int m, int n, long long batch) {
   if (batch == 0) return 0;
-  if (batch <= kGFew) return infer_grad_workspace_bytes(k, n, (int)batch);
+  if (grad_few(k, m, n, batch)) return infer_grad_workspace_bytes(k, n, (int)batch);
   return grad_space(k, m, n, batch).bytes;
-}
-
-static hipError_t join_product(const int8_t* A, long long K, int M, const int8_t* B, int N, const int* ex, float* out,
-                               long long ld, void* split, hipStream_t st) {
-  return tile_product(A, K, M, B, K, N, (int)K, JoinDigits{ex, out, ld}, split, st);
 }
 
 hipError_t grad_run(const uint32_t* B, const uint32_t* C, const float* D, int k, int m, int n, const float* X,
                     const float* dY, long long batch, float* dX, float* dD, void* ws, hipStream_t st) {
+  const dim3 gk((k + 63) / 64);
   if (batch == 0) {
-    if (dD) hipLaunchKernelGGL(dfin_kernel, dim3((k + 255) / 256), dim3(256), 0, st, nullptr, 0, k, dD);
+    if (dD) hipLaunchKernelGGL(dfin_kernel, gk, dim3(256), 0, st, nullptr, 0, k, 1, 1, nullptr, dD);
     return hipGetLastError();
   }
-  if (batch <= kGFew) return infer_grad_run(B, C, D, k, m, n, X, dY, (int)batch, dX, dD, ws, st);
+  if (grad_few(k, m, n, batch)) return infer_grad_run(B, C, D, k, m, n, X, dY, (int)batch, dX, dD, ws, st);
   const GradSpace s = grad_space(k, m, n, batch);
   char* base = static_cast<char*>(ws);
-  int8_t* be = reinterpret_cast<int8_t*>(base + s.be);
-  int8_t* ce = reinterpret_cast<int8_t*>(base + s.ce);
-  int8_t* ct = reinterpret_cast<int8_t*>(base + s.ct);
-  int8_t* xd = reinterpret_cast<int8_t*>(base + s.xd);
-  int8_t* yd = reinterpret_cast<int8_t*>(base + s.yd);
-  int8_t* sd = reinterpret_cast<int8_t*>(base + s.sd);
-  float* u = reinterpret_cast<float*>(base + s.u);
-  float* t = reinterpret_cast<float*>(base + s.t);
-  int* ex = reinterpret_cast<int*>(base + s.ex);
-  double* part = reinterpret_cast<double*>(base + s.part);
+  auto at = [&](size_t o) { return static_cast<void*>(base + o); };
+  float* u = static_cast<float*>(at(s.u));
+  float* t = static_cast<float*>(at(s.t));
+  double* part = static_cast<double*>(at(s.part));
+  double* sum = static_cast<double*>(at(s.sum));
+  int* ex = static_cast<int*>(at(s.ex));
+  int8_t* sd = static_cast<int8_t*>(at(s.sd));
+  void* split = at(s.split);
   const long long kp = pad16(k), mp = pad16(m), np = pad16(n);
-  const long long wb = k * (mp / 16), wc = k * (np / 16);
-  hipLaunchKernelGGL(widen_kernel, dim3((unsigned)((wb + 255) / 256)), dim3(256), 0, st, B, wb, be);
-  if (dD) hipLaunchKernelGGL(widen_kernel, dim3((unsigned)((wc + 255) / 256)), dim3(256), 0, st, C, wc, ce);
-  if (dX)
-    hipLaunchKernelGGL(widen_t_kernel, dim3((k + 255) / 256, (unsigned)((np / 16 + 15) / 16)), dim3(256), 0, st, C, k,
-                       (int)(np / 16), n, ct, kp);
+  Prep p{dY, X, B, C, static_cast<int8_t*>(at(s.yd)), static_cast<int8_t*>(at(s.xd)), static_cast<int8_t*>(at(s.be)),
+         static_cast<int8_t*>(at(s.ce)), static_cast<int8_t*>(at(s.ct)), ex, m, n, k, 0, {}};
   for (long long b0 = 0; b0 < batch; b0 += kGChunk) {
     const int c = (int)(batch - b0 < kGChunk ? batch - b0 : kGChunk);
-    hipError_t e;
-    hipLaunchKernelGGL(digits_kernel, dim3(c), dim3(256), 0, st, dY + b0 * m, (long long)m, nullptr, yd, mp, ex);
-    e = join_product(yd, mp, 4 * c, be, k, ex, u, k, base + s.split, st);
+    const bool first = b0 == 0, last = b0 + c == batch;
+    p.dY = dY + b0 * m;
+    p.X = X + b0 * n;
+    p.batch = c;
+    const long long count[5] = {c, dD ? c : 0, first && dX ? (k + 255ll) / 256 * ((np / 16 + 15) / 16) : 0,
+                                first ? (k * (mp / 16) + 255) / 256 : 0, first && dD ? (k * (np / 16) + 255) / 256 : 0};
+    long long all = 0;
+    for (int q = 0; q < 5; ++q) {
+      p.count[q] = (unsigned)count[q];
+      all += count[q];
+    }
+    if (all > (1ll << 23)) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(prep_kernel, dim3((unsigned)all), dim3(256), 0, st, p);
+    hipError_t e = tile_product(p.yd, mp, 4 * c, p.be, mp, k, (int)mp, JoinDigits{ex, u, k}, split, st);
     if (e != hipSuccess) return e;
     if (dD) {
-      hipLaunchKernelGGL(digits_kernel, dim3(c), dim3(256), 0, st, X + b0 * n, (long long)n, nullptr, xd, np, ex + c);
-      e = join_product(xd, np, 4 * c, ce, k, ex + c, t, k, base + s.split, st);
-      if (e != hipSuccess) return e;
-      hipLaunchKernelGGL(dsum_kernel, dim3((k + 255) / 256, kGParts), dim3(256), 0, st, t, u, k, c, b0 == 0, part);
+      int parts = kGParts;
+      if (tile_plan(4ll * c, k, (int)np).parts > 1) {
+        e = tile_product(p.xd, np, 4 * c, p.ce, np, k, (int)np, JoinDigits{ex + c, t, k}, split, st);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL(dsum_kernel, dim3((k + 255) / 256, kGParts), dim3(256), 0, st, t, u, k, c, part);
+      } else {
+        const int rows = 4 * c <= 64 ? 32 : 64;
+        parts = (4 * c + rows - 1) / rows;
+        e = tile_whole(p.xd, np, 4 * c, p.ce, np, k, (int)np, DotDigits{ex + c, u, k, part, 0}, st);
+        if (e != hipSuccess) return e;
+      }
+      hipLaunchKernelGGL(dfin_kernel, gk, dim3(256), 0, st, part, parts, k, (int)first, (int)last, sum, dD);
     }
     if (dX) {
       hipLaunchKernelGGL(digits_kernel, dim3(c), dim3(256), 0, st, u, (long long)k, D, sd, kp, ex + 2 * c);
-      e = join_product(sd, kp, 4 * c, ct, n, ex + 2 * c, dX + b0 * n, n, base + s.split, st);
+      e = tile_product(sd, kp, 4 * c, p.ct, kp, n, (int)kp, JoinDigits{ex + 2 * c, dX + b0 * n, n}, split, st);
       if (e != hipSuccess) return e;
     }
   }
-  if (dD) hipLaunchKernelGGL(dfin_kernel, dim3((k + 255) / 256), dim3(256), 0, st, part, kGParts, k, dD);
   return hipGetLastError();
 }
 

@@ -317,7 +317,7 @@ static hipError_t tile_launch(const int8_t* A, long long lda, int M, const int8_
 // that is not full costs more than joining parts does: about 4 us and 8 bytes an element and part.
 // At least three stages and sixteen bytes are left to every part.
 struct TilePlan {
-  bool small;  // 64 x 128 tiles
+  bool small;  // 64 x 128 tiles (M <= 64)
   int parts;
   size_t bytes;  // of the parts
 };
@@ -342,23 +342,11 @@ static inline TilePlan tile_plan(long long M, long long N, int K) {
 
 // The tile shape by what its rounds over 256 CUs would cost: a tile's time at K = 2560 is about 36 us
 // (256 x 256), 29.5 us (256 x 192) and, for 128 x 128, 15 us alone on its CU and 25 us for two (its two
-// stages take 64 KB of LDS, so two workgroups share a CU).  ws: tile_plan(M, N, K).bytes.
+// stages take 64 KB of LDS, so two workgroups share a CU).
 template <typename EPI>
-static hipError_t tile_product(const int8_t* A, long long lda, int M, const int8_t* B, long long ldb, int N, int K,
-                               const EPI& epi, void* ws, hipStream_t st) {
-  const TilePlan p = tile_plan(M, N, K);
-  if (p.parts > 1) {
-    const long long groups = (M + 3ll) / 4, stride = groups * N * 4;
-    int* part = static_cast<int*>(ws);
-    const PartTile t{part, N, stride, nullptr};
-    const hipError_t e = p.small ? tile_launch<64, 128, 2, 2>(A, lda, M, B, ldb, N, K, p.parts, t, st)
-                                 : tile_launch<128, 128, 2, 2>(A, lda, M, B, ldb, N, K, p.parts, t, st);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((join_kernel<EPI>), dim3((unsigned)((groups * N + 255) / 256)), dim3(256), 0, st, part, p.parts,
-                       stride, M, N, epi);
-    return hipGetLastError();
-  }
-  if (p.small) return tile_launch<64, 128, 2, 2>(A, lda, M, B, ldb, N, K, 1, epi, st);
+static hipError_t tile_whole(const int8_t* A, long long lda, int M, const int8_t* B, long long ldb, int N, int K,
+                             const EPI& epi, hipStream_t st) {
+  if (M <= 64) return tile_launch<64, 128, 2, 2>(A, lda, M, B, ldb, N, K, 1, epi, st);
   auto tiles = [&](int bm, int bn) { return ((M + bm - 1ll) / bm) * ((N + bn - 1ll) / bn); };
   const long long t1 = tiles(256, 256), t2 = tiles(256, 192), t3 = tiles(128, 128);
   const double c1 = 36.0 * ((t1 + 255) / 256), c2 = 29.5 * ((t2 + 255) / 256);
@@ -366,6 +354,23 @@ static hipError_t tile_product(const int8_t* A, long long lda, int M, const int8
   if (c3 <= c1 && c3 <= c2) return tile_launch<128, 128, 2, 2>(A, lda, M, B, ldb, N, K, 1, epi, st);
   if (c2 <= c1) return tile_launch<256, 192, 4, 2>(A, lda, M, B, ldb, N, K, 1, epi, st);
   return tile_launch<256, 256, 2, 4>(A, lda, M, B, ldb, N, K, 1, epi, st);
+}
+
+// The product in whole or split tiles.  ws: tile_plan(M, N, K).bytes.
+template <typename EPI>
+static hipError_t tile_product(const int8_t* A, long long lda, int M, const int8_t* B, long long ldb, int N, int K,
+                               const EPI& epi, void* ws, hipStream_t st) {
+  const TilePlan p = tile_plan(M, N, K);
+  if (p.parts == 1) return tile_whole(A, lda, M, B, ldb, N, K, epi, st);
+  const long long groups = (M + 3ll) / 4, stride = groups * N * 4;
+  int* part = static_cast<int*>(ws);
+  const PartTile t{part, N, stride, nullptr};
+  const hipError_t e = p.small ? tile_launch<64, 128, 2, 2>(A, lda, M, B, ldb, N, K, p.parts, t, st)
+                               : tile_launch<128, 128, 2, 2>(A, lda, M, B, ldb, N, K, p.parts, t, st);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((join_kernel<EPI>), dim3((unsigned)((groups * N + 255) / 256)), dim3(256), 0, st, part, p.parts,
+                     stride, M, N, epi);
+  return hipGetLastError();
 }
 
 }  // namespace externd

@@ -298,14 +298,14 @@ int externd_distill_grad(const void* logits, int z_type, int64_t rows, int64_t v
  * scales D have gradients.  With u = B^T dY[b] and t = C X[b] for each of `batch` vectors:
  *   dX[b] = C^T (D u),     dD[i] = sum over b of t_i u_i
  * The vectors enter as fixed-point images (within 2^-31 of the vector's largest power of two per
- * element), the sums over them are exact; t, u, D u and dX are rounded to fp32 once each (batches
- * of up to 16 keep t and u in fp64), dD is summed in fp64 in a fixed order.  Deterministic.
+ * element), the sums over them are exact; t, u, D u and dX are rounded to fp32 at most once each (little
+ * work keeps t, u and D u in fp64), dD is summed in fp64 in a fixed order.  Deterministic.
  *   B_packed, C_packed, D   as externd_apply_factors
  *   X   batch x n fp32 (may be NULL where dD is)      dY  batch x m fp32
  *   dX  batch x n fp32, or NULL                       dD  k fp32, or NULL (0 for batch 0)
  *   workspace  externd_apply_factors_grad_workspace(k, m, n, batch) bytes, 16-byte aligned, used
  *              by this call alone until it has run
- * 1 <= k, m, n <= 2^23, 0 <= batch < 2^31.  A non-finite X or dY gives meaningless values in
+ * 1 <= k, m, n <= 2^23, k m and k n <= 2^33, 0 <= batch < 2^31.  A non-finite X or dY gives meaningless values in
  * dD and in its vector of dX. */
 int externd_apply_factors_grad(const uint32_t* B_packed, const uint32_t* C_packed, const float* D, int64_t k, int64_t m,
                                int64_t n, const float* X, const float* dY, int64_t batch, float* dX, float* dD,

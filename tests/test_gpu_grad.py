@@ -75,19 +75,23 @@ def test_gradient_matches_formula(k, m, n, batch):
     run(k, m, n, batch)
 
 
-@pytest.mark.parametrize("k,m,n,batch", [(7680, 2560, 2560, 1), (7680, 2560, 2560, 40), (1536, 1024, 1024, 300),
-                                         (64, 48, 50, 4096), (64, 48, 50, 8200), (600, 5000, 7000, 5), (600, 5000, 7000, 18)])
+# the products: much work, or more than 4096 vectors; whole and split tiles, ragged in every size
+@pytest.mark.parametrize("k,m,n,batch", [(7680, 2560, 2560, 1), (7680, 2560, 2560, 16), (7680, 2560, 2560, 17),
+                                         (7680, 2560, 2560, 40), (3001, 2999, 2503, 37), (1003, 777, 1025, 334),
+                                         (1536, 1024, 1024, 300), (900, 640, 2100, 513), (64, 48, 50, 4096),
+                                         (64, 48, 50, 4097), (37, 110, 17, 8200), (1, 1, 1, 5000), (130, 257, 300, 9000),
+                                         (600, 5000, 7000, 5), (600, 5000, 7000, 90)])
 def test_gradient_larger_sizes(k, m, n, batch):
     run(k, m, n, batch)
 
 
 @pytest.mark.parametrize("scale", [1e-38, 1e-42, 1e30])
-@pytest.mark.parametrize("batch", [2, 20])
+@pytest.mark.parametrize("batch", [2, 20, 4100])
 def test_gradient_extreme_scales(batch, scale):
     run(50, 40, 60, batch, scale=scale)
 
 
-@pytest.mark.parametrize("batch", [4, 50])
+@pytest.mark.parametrize("batch", [4, 50, 4200])
 def test_zero_parts(batch):
     Bt, Ct, D, X, dY, _, _ = run(40, 50, 60, batch)
     Z = np.zeros_like(Bt)
@@ -113,7 +117,7 @@ def test_empty_and_single_vector():
     assert one[0].shape == (25,) and torch.equal(one[0], row[0][0]) and torch.equal(one[1], row[1])
 
 
-@pytest.mark.parametrize("batch", [3, 60])
+@pytest.mark.parametrize("batch", [3, 60, 4200])
 def test_gradient_against_the_forward_pass(batch):
     """The layer is linear in X and in D: <dX, v> = <dY, layer(v)> and <dD, w> = <dY, layer with w>."""
     Bt, Ct, D, X, dY, dX, dD = run(200, 90, 110, batch, seed=3)
@@ -131,7 +135,7 @@ def test_gradient_against_the_forward_pass(batch):
 
 
 def test_misaligned_inputs_out_streams_and_graph():
-    for batch in (5, 70):
+    for batch in (5, 70, 4300):
         Bt, Ct, D, X, dY, dX, dD = run(130, 75, 93, batch, seed=5)
         f = device(Bt, Ct, D)
         put = lambda a: torch.cat([torch.zeros(1), torch.from_numpy(a).reshape(-1)]).cuda()[1:].reshape(a.shape)

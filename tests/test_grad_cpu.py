@@ -16,7 +16,7 @@ def grad(B=fake, C=fake, D=fake, k=8, m=4, n=4, X=fake, dY=fake, batch=2, dX=fak
 @pytest.mark.parametrize("change, word", [
     (dict(B=None), "null"), (dict(C=None), "null"), (dict(D=None), "null"), (dict(dY=None), "null"), (dict(X=None), "null"),
     (dict(dX=None, dD=None), "dX or dD"), (dict(k=0), "k, m, n"), (dict(m=0), "k, m, n"), (dict(n=0), "k, m, n"),
-    (dict(k=(1 << 23) + 1), "k, m, n"), (dict(batch=-1), "batch"), (dict(batch=1 << 31), "batch"),
+    (dict(k=(1 << 23) + 1), "k, m, n"), (dict(k=1 << 20, m=(1 << 13) + 1), "2^33"), (dict(k=1 << 20, n=(1 << 13) + 1), "2^33"), (dict(batch=-1), "batch"), (dict(batch=1 << 31), "batch"),
     (dict(ws=None), "workspace"), (dict(ws=ctypes.c_void_p(8)), "workspace")])
 def test_refusals(change, word):
     assert grad(**change) == erm.EINVAL
