@@ -43,10 +43,10 @@ __device__ __forceinline__ iv4 row_short(const int8_t* __restrict__ row, int k, 
 // The fragments of the next 32 bytes are read from LDS while the products of these run, two reads
 // between four products (the scheduling groups), and the barrier that hands the stage over comes
 // before the last of a stage's four steps, whose products cover the reads behind it.
-// Measured (256 x 256, 8 waves, 8192^3): 2.36 10^15 operations a second, the matrix cores busy 62% of
-// the time at 1.8 GHz (the card's clock falls under this load; 2.4 GHz in calls of some 100 us).  A
-// tile bound by LDS reads would gain from larger tiles per wave, but four waves of 128 x 128 were
-// slower (2.30) for want of a second wave to cover the barrier.
+// Measured (256 x 256, 8 waves, 8192^3): 2.0 to 2.4 10^15 operations a second by the card's clock, which
+// falls to 1.8 GHz under this load; the matrix cores are busy 62% of the time.  Four waves of 128 x 128
+// each read less from LDS but were slower (2.2 to 2.3) for want of a second wave to cover the barrier;
+// more stages in smaller tiles, and a raised wave priority around the products, lost 2 to 5%.
 //
 // Workgroups go round the eight XCDs: each XCD gets a run of neighbouring tiles, in groups of kGroup
 // tile rows, so that the tiles it holds at one time share rows in its L2 (8192 x 7680 x 2560 in
@@ -119,19 +119,25 @@ __global__ void __launch_bounds__(64 * WR * WC, 1) tile_kernel(const int8_t* __r
   auto direct = [&](int8_t* l, int p, const int8_t* s) {
     __builtin_amdgcn_global_load_lds((gptr*)s, (lptr*)(l + (p * NW + wv) * 1024), 16, 0, 0);
   };
-  // stage t > 0 into l (and stage t + 1 into registers); every direct load issued is waited for by a
-  // barrier before the kernel's end
-  auto fetch = [&](int8_t* l, int t) {
+  // a third of stage t > 0 into l: three of the four steps between two barriers issue one each, so that
+  // the loads do not come in one burst (1 to 3% over issuing them together).  Through registers, the
+  // first does all (and loads stage t + 1).  Every direct load issued is waited for by a barrier
+  // before the kernel's end.
+  auto fetch = [&](int8_t* l, int t, int third) {
     if (DMA) {
       const int k0 = 128 * (t - 1);
+      constexpr int all = PA + PB, each = (all + 2) / 3;
 #pragma unroll
-      for (int p = 0; p < PA; ++p) direct(l, p, ab + k0 + ao[p]);
-#pragma unroll
-      for (int p = 0; p < PB; ++p) direct(l + BM * 128, p, bb + k0 + bo[p]);
-    } else {
+      for (int p = 0; p < all; ++p)
+        if (p / each == third) {
+          if (p < PA) direct(l, p, ab + k0 + ao[p < PA ? p : 0]);
+          else direct(l + BM * 128, p - PA, bb + k0 + bo[p < PA ? 0 : p - PA]);
+        }
+    } else if (third == 0) {
       put(l, sa, sb);
       if (t + 1 < nk) load(t + 1);
     }
+    __builtin_amdgcn_sched_barrier(0);
   };
   if (DMA) {
     // pieces behind the rows' end: zeros for A, so that B's may be anything (its row's first piece)
@@ -194,7 +200,11 @@ __global__ void __launch_bounds__(64 * WR * WC, 1) tile_kernel(const int8_t* __r
     __builtin_amdgcn_sched_barrier(0);
   };
   __syncthreads();
-  if (nk > 1) fetch(l1, 1);
+  if (nk > 1) {
+    fetch(l1, 1, 0);
+    fetch(l1, 1, 1);
+    fetch(l1, 1, 2);
+  }
   read(0, l0, 0);
   __builtin_amdgcn_sched_barrier(0);
   int t = 0;
@@ -203,16 +213,21 @@ __global__ void __launch_bounds__(64 * WR * WC, 1) tile_kernel(const int8_t* __r
     step(1, l0, 2);
     step(0, l0, 3);
     __syncthreads();
-    fetch(l0, t + 2);
-    __builtin_amdgcn_sched_barrier(0);
+    fetch(l0, t + 2, 0);
     step(1, l1, 0);
+    fetch(l0, t + 2, 1);
     step(0, l1, 1);
+    fetch(l0, t + 2, 2);
     step(1, l1, 2);
     step(0, l1, 3);
     __syncthreads();
-    if (t + 3 < nk) fetch(l1, t + 3);
-    __builtin_amdgcn_sched_barrier(0);
+    const bool more = t + 3 < nk;
+    if (more) fetch(l1, t + 3, 0);
     step(1, l0, 0);
+    if (more) {
+      fetch(l1, t + 3, 1);
+      fetch(l1, t + 3, 2);
+    }
   }
   step(0, l0, 1);
   step(1, l0, 2);
@@ -340,17 +355,18 @@ static inline TilePlan tile_plan(long long M, long long N, int K) {
   return p;
 }
 
-// The tile shape by what its rounds over 256 CUs would cost: a tile's time at K = 2560 is about 36 us
-// (256 x 256), 29.5 us (256 x 192) and, for 128 x 128, 15 us alone on its CU and 25 us for two (its two
-// stages take 64 KB of LDS, so two workgroups share a CU).
+// The tile shape by what its rounds over 256 CUs cost, in us at K = 2560: 38 for 256 x 256, 30 for
+// 256 x 192, 22 for 512 tiles of 128 x 128 (its stages take 64 KB of LDS: two workgroups share a CU) and
+// 13.5 for up to 256 of them.  Measured, 256 x 256 / 256 x 192 / 128 x 128: 8192 x 7680 x 2560 178 / 165 /
+// 181 us, 2048 x 9728 x 2560 66 / 57 / 58, 1024 x 9728 x 2560 34 / 29 / 36, 4096 x 2560 x 9728 111 / 98 / 120.
 template <typename EPI>
 static hipError_t tile_whole(const int8_t* A, long long lda, int M, const int8_t* B, long long ldb, int N, int K,
                              const EPI& epi, hipStream_t st) {
   if (M <= 64) return tile_launch<64, 128, 2, 2>(A, lda, M, B, ldb, N, K, 1, epi, st);
   auto tiles = [&](int bm, int bn) { return ((M + bm - 1ll) / bm) * ((N + bn - 1ll) / bn); };
   const long long t1 = tiles(256, 256), t2 = tiles(256, 192), t3 = tiles(128, 128);
-  const double c1 = 36.0 * ((t1 + 255) / 256), c2 = 29.5 * ((t2 + 255) / 256);
-  const double c3 = t3 <= 256 ? 15.0 : 25.0 * ((t3 + 511) / 512);
+  const double c1 = 38.0 * ((t1 + 255) / 256), c2 = 30.0 * ((t2 + 255) / 256);
+  const double c3 = 22.0 * (t3 / 512) + (t3 % 512 == 0 ? 0.0 : t3 % 512 <= 256 ? 13.5 : 22.0);
   if (c3 <= c1 && c3 <= c2) return tile_launch<128, 128, 2, 2>(A, lda, M, B, ldb, N, K, 1, epi, st);
   if (c2 <= c1) return tile_launch<256, 192, 4, 2>(A, lda, M, B, ldb, N, K, 1, epi, st);
   return tile_launch<256, 256, 2, 4>(A, lda, M, B, ldb, N, K, 1, epi, st);
