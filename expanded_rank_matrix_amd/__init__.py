@@ -328,23 +328,34 @@ def apply_factors_grad(B, C, D, m: int, n: int, X, dY, need_dX: bool = True, nee
     if X is None and need_dD:
         raise ValueError("X is needed for dD")
     _require(X, torch.float32, "X", shape=(*lead, n), device=dev)
-    lib = load()
+    args = (B, C, D, k, m, n, X, dY, batch, lead, need_dX, need_dD, out)
+    ptr = _here(dev, stream)
+    if ptr is not None:
+        return _apply_factors_grad(*args, ptr)
     with _Run(dev, stream, (B, C, D, X, dY, *(out or ()))) as run:
-        if out is None:
-            dX = torch.empty((*lead, n), dtype=torch.float32, device=dev) if need_dX else None
-            dD = torch.empty(k, dtype=torch.float32, device=dev) if need_dD else None
-        else:
-            dX, dD = (t if need else None for t, need in zip(out, (need_dX, need_dD)))
-            if (dX is None) == need_dX or (dD is None) == need_dD:
-                raise ValueError("out must hold dX and dD where they are needed")
-            _require(dX, torch.float32, "out[0]", shape=(*lead, n), device=dev)
-            _require(dD, torch.float32, "out[1]", shape=(k,), device=dev)
-        size = lib.externd_apply_factors_grad_workspace(k, m, n, batch)
-        ws = torch.empty(size, dtype=torch.uint8, device=dev) if size > 0 else None
-        _check(lib.externd_apply_factors_grad(
-            B.data_ptr(), C.data_ptr(), D.data_ptr(), k, m, n, None if X is None else X.data_ptr(), dY.data_ptr(),
-            batch, None if dX is None else dX.data_ptr(), None if dD is None else dD.data_ptr(),
-            None if ws is None else ws.data_ptr(), run.ptr))
+        return _apply_factors_grad(*args, run.ptr)
+
+
+def _apply_factors_grad(B, C, D, k, m, n, X, dY, batch, lead, need_dX, need_dD, out, stream):
+    import torch
+
+    dev = D.device
+    lib = load()
+    if out is None:
+        dX = torch.empty((*lead, n), dtype=torch.float32, device=dev) if need_dX else None
+        dD = torch.empty(k, dtype=torch.float32, device=dev) if need_dD else None
+    else:
+        dX, dD = (t if need else None for t, need in zip(out, (need_dX, need_dD)))
+        if (dX is None) == need_dX or (dD is None) == need_dD:
+            raise ValueError("out must hold dX and dD where they are needed")
+        _require(dX, torch.float32, "out[0]", shape=(*lead, n), device=dev)
+        _require(dD, torch.float32, "out[1]", shape=(k,), device=dev)
+    size = lib.externd_apply_factors_grad_workspace(k, m, n, batch)
+    ws = torch.empty(size, dtype=torch.uint8, device=dev) if size > 0 else None
+    _check(lib.externd_apply_factors_grad(
+        B.data_ptr(), C.data_ptr(), D.data_ptr(), k, m, n, None if X is None else X.data_ptr(), dY.data_ptr(), batch,
+        None if dX is None else dX.data_ptr(), None if dD is None else dD.data_ptr(),
+        None if ws is None else ws.data_ptr(), stream))
     return dX, dD
 
 
@@ -389,17 +400,28 @@ class _Run:
         return False
 
 
-_TYPE = None
+_TYPE = None  # torch dtype -> the C ABI's number of the type
+_FLOAT = ()   # the floating-point ones
 
 
 def _types():
-    """torch dtype -> the C ABI's number of the type."""
-    global _TYPE
+    global _TYPE, _FLOAT
     if _TYPE is None:
         import torch
 
+        _FLOAT = (torch.float32, torch.float16, torch.bfloat16)
         _TYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.int8: 3}
     return _TYPE
+
+
+def _here(device, stream):
+    """The pointer of the current stream where a call runs just there, on the current device; None
+    where it takes a _Run."""
+    import torch
+
+    if stream is None and device.index == torch._C._cuda_getDevice():
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return None
 
 
 def _rows(t, types, name, shape=None, device=None):
@@ -409,16 +431,17 @@ def _rows(t, types, name, shape=None, device=None):
         raise ValueError(f"{name} must be a CUDA matrix of {' or '.join(map(str, types))}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     rows, n = t.shape
-    if n > 1 and t.stride(1) != 1:
+    if shape is not None and (rows, n) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    ld, inner = t.stride()
+    if n > 1 and inner != 1:
         raise ValueError(f"{name} must have contiguous rows")
     if rows <= 1:
         return max(n, 1)
-    if t.stride(0) < n:
+    if ld < n:
         raise ValueError(f"{name} must have rows that do not overlap")
-    return t.stride(0)
+    return ld
 
 
 def quantize_rows(X, stream=None, out=None):
@@ -428,28 +451,30 @@ def quantize_rows(X, stream=None, out=None):
     be strided).  A row of zeros gets scale 0, one with a NaN or an infinity scale NaN; both get
     zeros.  Quantises the weights of ``apply_quantized`` (rows are output channels) and tokens that
     several products share.  Enqueued on the stream without waiting."""
+    types = _types()
+    ldx = _rows(X, _FLOAT, "X")
+    args = (X, types[X.dtype], ldx, out)
+    ptr = _here(X.device, stream)
+    if ptr is not None:
+        return _quantize_rows(*args, ptr)
+    with _Run(X.device, stream, (X,) if out is None else (X, *out)) as run:
+        return _quantize_rows(*args, run.ptr)
+
+
+def _quantize_rows(X, x_type, ldx, out, stream):
     import torch
 
-    types = _types()
-    ldx = _rows(X, _float_types(), "X")
     rows, n = X.shape
     dev = X.device
-    with _Run(dev, stream, (X,) if out is None else (X, *out)) as run:
-        if out is None:
-            out = (torch.empty((rows, n), dtype=torch.int8, device=dev),
-                   torch.empty(rows, dtype=torch.float32, device=dev))
-        Q, scale = out
-        ldq = _rows(Q, (torch.int8,), "out[0]", shape=(rows, n), device=dev)
-        _require(scale, torch.float32, "out[1]", shape=(rows,), device=dev)
-        _check(load().externd_quantize_rows(X.data_ptr(), types[X.dtype], rows, n, ldx, Q.data_ptr(), ldq,
-                                            scale.data_ptr(), run.ptr))
+    if out is None:
+        out = (torch.empty((rows, n), dtype=torch.int8, device=dev), torch.empty(rows, dtype=torch.float32, device=dev))
+        ldq = n
+    else:
+        ldq = _rows(out[0], (torch.int8,), "out[0]", shape=(rows, n), device=dev)
+        _require(out[1], torch.float32, "out[1]", shape=(rows,), device=dev)
+    Q, scale = out
+    _check(load().externd_quantize_rows(X.data_ptr(), x_type, rows, n, ldx, Q.data_ptr(), ldq, scale.data_ptr(), stream))
     return Q, scale
-
-
-def _float_types():
-    import torch
-
-    return (torch.float32, torch.float16, torch.bfloat16)
 
 
 def apply_quantized(W, w_scale, X, x_scale=None, out_dtype=None, stream=None, out=None):
@@ -460,55 +485,78 @@ def apply_quantized(W, w_scale, X, x_scale=None, out_dtype=None, stream=None, ou
     does.  W, X and ``out`` may have strided rows.  Returns Y (m or tokens x m) of ``out_dtype``
     (fp32, fp16 or bf16; by default X's type, fp32 for int8 tokens).  The integer sum is exact; Y is
     rounded once.  Enqueued on the stream without waiting."""
-    import torch
-
     types = _types()
-    ldw = _rows(W, (torch.int8,), "W")
+    x_type = types.get(X.dtype)
+    ldw = _rows(W, _INT8 or _int8(), "W")
     m, n = W.shape
     dev = W.device
-    _require(w_scale, torch.float32, "w_scale", shape=(m,), device=dev)
+    _require(w_scale, _FLOAT[0], "w_scale", shape=(m,), device=dev)
     single = X.dim() == 1
     X2 = X.unsqueeze(0) if single else X
-    ldx = _rows(X2, tuple(types), "X", device=dev)
-    tokens = X2.shape[0]
-    if X2.shape[1] != n:
+    ldx = _rows(X2, types, "X", device=dev)
+    tokens, nx = X2.shape
+    if nx != n:
         raise ValueError(f"X must be n or tokens x n with n = {n}")
-    if (X.dtype == torch.int8) != (x_scale is not None):
+    if (x_type == 3) != (x_scale is not None):
         raise ValueError("x_scale is given with int8 tokens and only then")
     if x_scale is not None:
-        _require(x_scale, torch.float32, "x_scale", shape=(tokens,), device=dev)
+        _require(x_scale, _FLOAT[0], "x_scale", shape=(tokens,), device=dev)
     if out is not None:
         if out_dtype is not None and out.dtype != out_dtype:
             raise ValueError("out must be of out_dtype")
         out_dtype = out.dtype
     elif out_dtype is None:
-        out_dtype = torch.float32 if X.dtype == torch.int8 else X.dtype
-    if out_dtype not in _float_types():
+        out_dtype = _FLOAT[0] if x_type == 3 else X.dtype
+    if out_dtype not in _FLOAT:
         raise ValueError("out_dtype must be torch.float32, torch.float16 or torch.bfloat16")
-    lib = load()
+    args = (W, w_scale, m, n, ldw, X2, x_type, x_scale, tokens, ldx, out_dtype, out, single)
+    ptr = _here(dev, stream)
+    if ptr is not None:
+        return _apply_quantized(*args, ptr)
     with _Run(dev, stream, (W, w_scale, X, x_scale, out)) as run:
-        if out is None:
-            Y = torch.empty((tokens, m), dtype=out_dtype, device=dev)
-        else:
-            Y = out.unsqueeze(0) if single and out.dim() == 1 else out
-        ldy = _rows(Y, _float_types(), "out", shape=(tokens, m), device=dev)
-        size = lib.externd_apply_quantized_workspace(types[X.dtype], tokens, n, m)
-        ws = torch.empty(size, dtype=torch.uint8, device=dev) if size > 0 else None
-        _check(lib.externd_apply_quantized(
-            W.data_ptr(), w_scale.data_ptr(), m, n, ldw, X2.data_ptr(), types[X.dtype],
-            None if x_scale is None else x_scale.data_ptr(), tokens, ldx, Y.data_ptr(), types[out_dtype], ldy,
-            None if ws is None else ws.data_ptr(), run.ptr))
+        return _apply_quantized(*args, run.ptr)
+
+
+_INT8 = ()
+
+
+def _int8():
+    global _INT8
+    import torch
+
+    _INT8 = (torch.int8,)
+    return _INT8
+
+
+def _apply_quantized(W, w_scale, m, n, ldw, X, x_type, x_scale, tokens, ldx, y_type, out, single, stream):
+    import torch
+
+    dev = W.device
+    lib = load()
+    if out is None:
+        Y = torch.empty((tokens, m), dtype=y_type, device=dev)
+        ldy = m
+    else:
+        Y = out.unsqueeze(0) if single and out.dim() == 1 else out
+        ldy = _rows(Y, _FLOAT, "out", shape=(tokens, m), device=dev)
+    size = lib.externd_apply_quantized_workspace(x_type, tokens, n, m)
+    ws = torch.empty(size, dtype=torch.uint8, device=dev) if size > 0 else None
+    _check(lib.externd_apply_quantized(
+        W.data_ptr(), w_scale.data_ptr(), m, n, ldw, X.data_ptr(), x_type,
+        None if x_scale is None else x_scale.data_ptr(), tokens, ldx, Y.data_ptr(), _TYPE[y_type], ldy,
+        None if ws is None else ws.data_ptr(), stream))
     return Y[0] if single else Y
 
 
 def _distill_args(logits, teacher, index, weight, name, out):
-    """Validated (ldz, ldd, index_bytes) of the distillation entry points."""
+    """Validated arguments of the distillation entry points: the logits', the teacher's, ldd."""
     import torch
 
-    ldz = _rows(logits, _float_types(), "logits")
+    types = _types()
+    ldz = _rows(logits, _FLOAT, "logits")
     rows, vocab = logits.shape
     dev = logits.device
-    _require(teacher, _float_types(), "teacher", device=dev)
+    _require(teacher, _FLOAT, "teacher", device=dev)
     if teacher.dim() != 2 or teacher.shape[0] != rows:
         raise ValueError(f"teacher must be rows x top with rows = {rows}")
     _require(index, (torch.int32, torch.int64), "index", shape=teacher.shape, device=dev)
@@ -516,7 +564,8 @@ def _distill_args(logits, teacher, index, weight, name, out):
     ldd = vocab
     if out is not None:
         ldd = _rows(out, (logits.dtype,), "out", shape=(rows, vocab), device=dev)
-    return ldz, ldd, index.element_size()
+    return (logits.data_ptr(), types[logits.dtype], rows, vocab, ldz), (
+        teacher.data_ptr(), types[teacher.dtype], index.data_ptr(), index.element_size(), teacher.shape[1]), ldd
 
 
 def distill_loss(logits, teacher, index, temperature: float = 1.0, weight=None, grad: bool = False,
@@ -531,25 +580,29 @@ def distill_loss(logits, teacher, index, temperature: float = 1.0, weight=None, 
     read).  Returns (loss fp32 rows, stats fp32 rows x 2); with ``grad`` or ``out`` also dlogits, the
     gradient of the losses' sum, formed in the same call (``out`` may be a preallocated tensor, or
     logits itself).  ``stats`` feeds ``distill_grad``.  Enqueued on the stream without waiting."""
+    args = (logits, *_distill_args(logits, teacher, index, weight, "weight", out), temperature, weight, grad, out)
+    ptr = _here(logits.device, stream)
+    if ptr is not None:
+        return _distill_loss(*args, ptr)
+    with _Run(logits.device, stream, (logits, teacher, index, weight, out)) as run:
+        return _distill_loss(*args, run.ptr)
+
+
+def _distill_loss(logits, z, t, ldd, temperature, weight, grad, out, stream):
     import torch
 
-    types = _types()
-    ldz, ldd, ib = _distill_args(logits, teacher, index, weight, "weight", out)
     rows, vocab = logits.shape
     dev = logits.device
     lib = load()
-    with _Run(dev, stream, (logits, teacher, index, weight, out)) as run:
-        loss = torch.empty(rows, dtype=torch.float32, device=dev)
-        stats = torch.empty((rows, 2), dtype=torch.float32, device=dev)
-        if out is None and grad:
-            out = torch.empty((rows, vocab), dtype=logits.dtype, device=dev)
-        size = lib.externd_distill_workspace(rows, vocab)
-        ws = torch.empty(size, dtype=torch.uint8, device=dev) if size > 0 else None
-        _check(lib.externd_distill_loss(
-            logits.data_ptr(), types[logits.dtype], rows, vocab, ldz, teacher.data_ptr(), types[teacher.dtype],
-            index.data_ptr(), ib, teacher.shape[1], temperature, None if weight is None else weight.data_ptr(),
-            loss.data_ptr(), stats.data_ptr(), None if out is None else out.data_ptr(), ldd,
-            None if ws is None else ws.data_ptr(), run.ptr))
+    loss = torch.empty(rows, dtype=torch.float32, device=dev)
+    stats = torch.empty((rows, 2), dtype=torch.float32, device=dev)
+    if out is None and grad:
+        out = torch.empty((rows, vocab), dtype=logits.dtype, device=dev)
+    size = lib.externd_distill_workspace(rows, vocab)
+    ws = torch.empty(size, dtype=torch.uint8, device=dev) if size > 0 else None
+    _check(lib.externd_distill_loss(*z, *t, temperature, None if weight is None else weight.data_ptr(),
+                                    loss.data_ptr(), stats.data_ptr(), None if out is None else out.data_ptr(), ldd,
+                                    None if ws is None else ws.data_ptr(), stream))
     return (loss, stats) if out is None else (loss, stats, out)
 
 
@@ -559,20 +612,23 @@ def distill_grad(logits, stats, teacher, index, temperature: float = 1.0, grad_l
     dlogits[r][v] = grad_loss[r] T (q[v] - sum of p_k with index_k = v), of logits' type; grad_loss
     (rows fp32, 1 where None) takes the weight's place, and a row where it is 0 is not read.  ``out``
     may be a preallocated tensor, or logits itself.  Enqueued on the stream without waiting."""
+    z, t, ldd = _distill_args(logits, teacher, index, grad_loss, "grad_loss", out)
+    _require(stats, _FLOAT[0], "stats", shape=(logits.shape[0], 2), device=logits.device)
+    args = (logits, z, t, ldd, stats, temperature, grad_loss, out)
+    ptr = _here(logits.device, stream)
+    if ptr is not None:
+        return _distill_grad(*args, ptr)
+    with _Run(logits.device, stream, (logits, stats, teacher, index, grad_loss, out)) as run:
+        return _distill_grad(*args, run.ptr)
+
+
+def _distill_grad(logits, z, t, ldd, stats, temperature, grad_loss, out, stream):
     import torch
 
-    types = _types()
-    ldz, ldd, ib = _distill_args(logits, teacher, index, grad_loss, "grad_loss", out)
-    rows, vocab = logits.shape
-    dev = logits.device
-    _require(stats, torch.float32, "stats", shape=(rows, 2), device=dev)
-    with _Run(dev, stream, (logits, stats, teacher, index, grad_loss, out)) as run:
-        if out is None:
-            out = torch.empty((rows, vocab), dtype=logits.dtype, device=dev)
-        _check(load().externd_distill_grad(
-            logits.data_ptr(), types[logits.dtype], rows, vocab, ldz, stats.data_ptr(), teacher.data_ptr(),
-            types[teacher.dtype], index.data_ptr(), ib, teacher.shape[1], temperature,
-            None if grad_loss is None else grad_loss.data_ptr(), out.data_ptr(), ldd, run.ptr))
+    if out is None:
+        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    _check(load().externd_distill_grad(*z, stats.data_ptr(), *t, temperature,
+                                       None if grad_loss is None else grad_loss.data_ptr(), out.data_ptr(), ldd, stream))
     return out
 
 
