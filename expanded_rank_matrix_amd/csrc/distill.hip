@@ -175,17 +175,6 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   *reinterpret_cast<iv4_any*>(p + 4) = b;
 }
 
-// 8 elements of T as fp32 out of the 16-byte words that hold them
-template <typename T>
-__device__ __forceinline__ void unpack8(const iv4 (&h)[sizeof(T) == 4 ? 2 : 1], float (&v)[8]) {
-  typedef T v8 __attribute__((ext_vector_type(16 / sizeof(T))));
-#pragma unroll
-  for (int q = 0; q < (sizeof(T) == 4 ? 2 : 1); ++q) {
-    const v8 x = __builtin_bit_cast(v8, h[q]);
-#pragma unroll
-    for (int e = 0; e < (int)(16 / sizeof(T)); ++e) v[q * 4 + e] = (float)x[e];
-  }
-}
 template <typename T>
 __device__ __forceinline__ iv4 inf_words() {  // -inf throughout
   const int x = sizeof(T) == 4 ? (int)0xFF800000 : __is_same(T, _Float16) ? (int)0xFC00FC00 : (int)0xFF80FF80;
@@ -383,7 +372,7 @@ __global__ void __launch_bounds__(TH) distill_kernel(const T* Z, int V, long lon
   }
   const float c = (float)(1.4426950408889634 / (double)Tmp);
   const double rT = 1.0 / (double)Tmp;
-  constexpr int W = sizeof(T) == 4 ? 2 : 1;  // 16-byte words of 8 elements
+  constexpr int W = words8<T>();
   iv4 held[CH > 0 ? CH : 1][W];
   const int rest = V & 7;  // the row's last elements, fewer than 8: one a thread
   float last = -__builtin_inff();
@@ -392,9 +381,7 @@ __global__ void __launch_bounds__(TH) distill_kernel(const T* Z, int V, long lon
     for (int i = 0; i < CH; ++i) {
       const int j = 8 * (i * TH + (int)threadIdx.x);
 #pragma unroll
-      for (int q = 0; q < W; ++q) held[i][q] = j + 8 <= V ? (iv4)*reinterpret_cast<const iv4_any*>(
-                                                                reinterpret_cast<const char*>(z + j) + 16 * q)
-                                                          : inf_words<T>();
+      for (int q = 0; q < W; ++q) held[i][q] = j + 8 <= V ? word8(z + j, q) : inf_words<T>();
     }
     if ((int)threadIdx.x < rest) last = (float)z[V - rest + (int)threadIdx.x];
   }

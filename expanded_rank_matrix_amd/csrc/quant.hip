@@ -58,10 +58,20 @@ struct RowScale {
   }
 };
 
+__device__ __forceinline__ unsigned max_abs8(const float (&v)[8], unsigned mx) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const unsigned b = __float_as_uint(v[e]) & 0x7FFFFFFFu;
+    mx = b > mx ? b : mx;
+  }
+  return mx;
+}
+
 // One row per TPR threads (64: a wave; 256: the workgroup), 8 elements per thread and step; the
 // first CH steps of a row stay in registers between the search for its maximum and its rounding, a
-// longer row's rest is read again.  np bytes of each Q row are written, zeros behind the first n.
-// A row with a NaN or an infinity gets scale NaN and q = 0.
+// longer row's rest is read again.  The row's last elements, fewer than 8, are one a thread.  np bytes
+// of each Q row are written, zeros behind the first n (np - n <= TPR).
+// Bound by memory (4096 x 9728 bf16: 26 us, 4.6 TB/s, a large copy's 4.8).
 template <typename T, int TPR, int CH>
 __global__ void __launch_bounds__(256) quantize_kernel(const T* __restrict__ X, long long rows, int n, long long ldx,
                                                        int8_t* __restrict__ Q, long long ldq, int np,
@@ -70,32 +80,27 @@ __global__ void __launch_bounds__(256) quantize_kernel(const T* __restrict__ X, 
   __shared__ unsigned wmx[4];
   const int tid = threadIdx.x % TPR;
   const long long row = (long long)blockIdx.x * RPW + threadIdx.x / TPR;
-  const long long rr = row < rows ? row : rows - 1;
-  const T* x = X + rr * ldx;
-  float v[CH][8];
-  unsigned mx = 0u;
+  const T* x = X + (row < rows ? row : rows - 1) * ldx;
+  const int whole = n & ~7, rest = n - whole;
+  iv4 held[CH][words8<T>()];  // all loads in flight together, those behind the row at its start
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int j = (c * TPR + tid) * 8;
-    if (j + 8 <= n) load8(x + j, v[c]);
-    else load8_tail(x + j, (long long)n - j, v[c]);
+#pragma unroll
+    for (int h = 0; h < words8<T>(); ++h) held[c][h] = whole > 0 ? word8(x + (j < whole ? j : 0), h) : iv4{0, 0, 0, 0};
   }
+  const float last = tid < rest ? (float)x[whole + tid] : 0.0f;
+  unsigned mx = __float_as_uint(last) & 0x7FFFFFFFu;
+  float v[CH][8];
 #pragma unroll
-  for (int c = 0; c < CH; ++c)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const unsigned b = __float_as_uint(v[c][e]) & 0x7FFFFFFFu;
-      mx = b > mx ? b : mx;
-    }
-  for (long long j = (long long)(CH * TPR + tid) * 8; j < n; j += TPR * 8) {
+  for (int c = 0; c < CH; ++c) {
+    unpack8<T>(held[c], v[c]);
+    mx = max_abs8(v[c], mx);  // a repeat of the row's start changes nothing
+  }
+  for (long long j = (long long)(CH * TPR + tid) * 8; j < whole; j += TPR * 8) {
     float w[8];
-    if (j + 8 <= n) load8(x + j, w);
-    else load8_tail(x + j, n - j, w);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const unsigned b = __float_as_uint(w[e]) & 0x7FFFFFFFu;
-      mx = b > mx ? b : mx;
-    }
+    load8(x + j, w);
+    mx = max_abs8(w, mx);
   }
   mx = wave_max_u32(mx);
   if (TPR == 256) {
@@ -111,25 +116,28 @@ __global__ void __launch_bounds__(256) quantize_kernel(const T* __restrict__ X, 
   auto emit = [&](long long j, const float (&w)[8]) {
     int k[8];
     rs.quantize(w, k);
-    if (j + 8 <= np) {
-      iv2_any o;
-      o[0] = (int)pack4(k[0], k[1], k[2], k[3]);
-      o[1] = (int)pack4(k[4], k[5], k[6], k[7]);
-      *reinterpret_cast<iv2_any*>(q + j) = o;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (j + e < np) q[j + e] = (int8_t)k[e];
-    }
+    iv2_any o;
+    o[0] = (int)pack4(k[0], k[1], k[2], k[3]);
+    o[1] = (int)pack4(k[4], k[5], k[6], k[7]);
+    *reinterpret_cast<iv2_any*>(q + j) = o;
   };
 #pragma unroll
-  for (int c = 0; c < CH; ++c) emit((long long)(c * TPR + tid) * 8, v[c]);
-  for (long long j = (long long)(CH * TPR + tid) * 8; j < np; j += TPR * 8) {
+  for (int c = 0; c < CH; ++c) {
+    const int j = (c * TPR + tid) * 8;
+    if (j < whole) emit(j, v[c]);
+  }
+  for (long long j = (long long)(CH * TPR + tid) * 8; j < whole; j += TPR * 8) {
     float w[8];
-    if (j + 8 <= n) load8(x + j, w);
-    else load8_tail(x + j, n - j, w);
+    load8(x + j, w);
     emit(j, w);
   }
+  if (tid < rest) {
+    const float w[8] = {last, 0, 0, 0, 0, 0, 0, 0};
+    int k[8];
+    rs.quantize(w, k);
+    q[whole + tid] = (int8_t)k[0];
+  }
+  if (tid < np - n) q[n + tid] = 0;
 }
 
 template <typename T>
@@ -138,12 +146,13 @@ static hipError_t quantize_typed(const T* X, long long rows, int n, long long ld
   // runs of 2^23 rows: a launch holds below 2^32 threads
   for (long long r = 0; r < rows; r += 1ll << 23) {
     const long long c = rows - r < (1ll << 23) ? rows - r : 1ll << 23;
-    if (n <= 64 * 8 * 2)
-      hipLaunchKernelGGL((quantize_kernel<T, 64, 2>), dim3((unsigned)((c + 3) / 4)), dim3(256), 0, st, X + r * ldx, c, n,
-                         ldx, Q + r * ldq, ldq, np, scale + r);
-    else
-      hipLaunchKernelGGL((quantize_kernel<T, 256, 5>), dim3((unsigned)c), dim3(256), 0, st, X + r * ldx, c, n, ldx,
-                         Q + r * ldq, ldq, np, scale + r);
+    auto go = [&](auto kernel, long long blocks) {
+      hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(256), 0, st, X + r * ldx, c, n, ldx, Q + r * ldq, ldq, np,
+                         scale + r);
+    };
+    if (n <= 64 * 8 * 2) go(quantize_kernel<T, 64, 2>, (c + 3) / 4);
+    else if (n <= 256 * 8 * 2) go(quantize_kernel<T, 256, 2>, c);
+    else go(quantize_kernel<T, 256, 5>, c);
   }
   return hipGetLastError();
 }
@@ -164,8 +173,10 @@ __device__ __forceinline__ void store_y(T* p, float v) {
 }
 
 // ---- few tokens -------------------------------------------------------------------------------
-// Workgroup: 16 MT output channels and 16 NT tokens; the row length goes round eight waves in chunks
-// of 128 bytes, so that each wave reads whole cache lines of W and two chunks' loads are in flight.
+// Workgroup: 16 output channels and 16 NT tokens; the row length goes round eight waves in chunks of 128
+// bytes, so that each wave reads whole cache lines of W and two chunks' loads are in flight.  (32
+// channels a workgroup read X half as often and were slower wherever that left fewer workgroups than
+// CUs, and no faster elsewhere.)
 // MFMA D(16 x 16) += A(16 x 64) B(64 x 16): A row = channel, B column = token, lane l holding the
 // 16 bytes at 16 (l / 16) of row (column) l % 16 of the step.  The waves' partial tiles add in LDS.
 //
@@ -173,20 +184,20 @@ __device__ __forceinline__ void store_y(T* p, float v) {
 // itself into LDS while the first loads of W are on their way.
 constexpr int kFewWaves = 8;
 constexpr int kFewTokens = 16;
-constexpr int kFewFused = 4;           // tokens quantised on the way
+constexpr int kFewFused = 8;          // most tokens quantised on the way
 constexpr int kFewLds = 48 * 1024;    // bytes of their rows
 
 // distance of the quantised rows in LDS: 16 rows' pieces of one column in different banks
 __host__ __device__ constexpr int few_pitch(int n) { return (n + 127) / 128 * 128 % 256 == 0 ? (n + 127) / 128 * 128 + 16
                                                                                            : (n + 127) / 128 * 128 + 144; }
 
-// The tokens' rows quantised into LDS by the workgroup's eight waves, G = 8, 4 or 2 of them to a
-// token (tokens <= 4), and their scales; ends with a barrier.
+// The tokens' rows quantised into LDS by the workgroup's eight waves, G = 8, 4, 2 or 1 of them to a
+// token (tokens <= 8), and their scales; ends with a barrier.
 template <typename T>
 __device__ __forceinline__ void few_quantize(const T* __restrict__ X, long long ldx, int tokens, int n,
                                              int8_t* __restrict__ q, float* srow, unsigned* wmx) {
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int G = tokens == 1 ? 8 : tokens == 2 ? 4 : 2, t = wv / G, first = ((wv % G) * 64 + lane) * 8, step = 512 * G;
+  const int G = tokens == 1 ? 8 : tokens == 2 ? 4 : tokens <= 4 ? 2 : 1, t = wv / G, first = ((wv % G) * 64 + lane) * 8, step = 512 * G;
   const bool mine = t < tokens;
   const T* x = X + (mine ? t : 0) * ldx;
   constexpr int H = 2;  // steps kept in registers; a longer row's rest is read again
@@ -196,13 +207,7 @@ __device__ __forceinline__ void few_quantize(const T* __restrict__ X, long long 
     if (j + 8 <= n) load8(x + j, w);
     else load8_tail(x + j, (long long)n - j, w);
   };
-  auto top = [&](const float (&w)[8]) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const unsigned b = __float_as_uint(w[e]) & 0x7FFFFFFFu;
-      mx = b > mx ? b : mx;
-    }
-  };
+  auto top = [&](const float (&w)[8]) { mx = max_abs8(w, mx); };
 #pragma unroll
   for (int h = 0; h < H; ++h) get(first + h * step, v[h]);
 #pragma unroll
@@ -243,7 +248,7 @@ __device__ __forceinline__ void few_quantize(const T* __restrict__ X, long long 
   __syncthreads();
 }
 
-template <int MT, int NT, typename XT, typename YT>
+template <int NT, typename XT, typename YT>
 __global__ void __launch_bounds__(64 * kFewWaves) few_kernel(const int8_t* __restrict__ W, long long ldw, int m, int n,
                                                              const float* __restrict__ sw, const XT* __restrict__ X,
                                                              long long ldx, int tokens, const float* __restrict__ sx,
@@ -251,37 +256,30 @@ __global__ void __launch_bounds__(64 * kFewWaves) few_kernel(const int8_t* __res
   constexpr bool FUSED = !__is_same(XT, int8_t);
   static_assert(!FUSED || (NT == 1 && kFewFused <= 16), "quantised on the way: one column tile");
   extern __shared__ __attribute__((aligned(16))) int8_t rows[];
-  __shared__ int red[kFewWaves][MT * NT * 256];
+  __shared__ int red[kFewWaves][NT * 256];
   __shared__ float srow[16];
   __shared__ unsigned wmx[kFewWaves];
   // the wave's number in a scalar register: the branches on it must be jumps, since MFMA runs whatever
   // the lane mask
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15, gg = lane >> 4;
-  const int r0 = blockIdx.x * (16 * MT);
+  const int r0 = blockIdx.x * 16;
   const long long t0 = blockIdx.y * (16ll * NT);
-  const int8_t* wr[MT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i) wr[i] = W + (long long)(r0 + 16 * i + lr < m ? r0 + 16 * i + lr : m - 1) * ldw;
+  const int8_t* wr = W + (long long)(r0 + lr < m ? r0 + lr : m - 1) * ldw;
   const int8_t* xr[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     const long long c = t0 + 16 * t + lr < tokens ? t0 + 16 * t + lr : tokens - 1;
     xr[t] = FUSED ? rows + c * few_pitch(n) : reinterpret_cast<const int8_t*>(X + c * ldx);
   }
-  iv4 acc[MT][NT];
+  iv4 acc[NT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int t = 0; t < NT; ++t) acc[i][t] = iv4{0, 0, 0, 0};
+  for (int t = 0; t < NT; ++t) acc[t] = iv4{0, 0, 0, 0};
   const int full = n / 128;
-  iv4 a[4][MT], b[4][NT];
+  iv4 a[4], b[4][NT];
   auto load_w = [&](int c, int u) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-        a[2 * u + h][i] = *reinterpret_cast<const iv4_any*>(wr[i] + 128 * c + 64 * h + 16 * gg);
+    for (int h = 0; h < 2; ++h) a[2 * u + h] = *reinterpret_cast<const iv4_any*>(wr + 128 * c + 64 * h + 16 * gg);
   };
   auto load_x = [&](int c, int u) {
 #pragma unroll
@@ -296,10 +294,8 @@ __global__ void __launch_bounds__(64 * kFewWaves) few_kernel(const int8_t* __res
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-          acc[i][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[2 * u + h][i], b[2 * u + h][t], acc[i][t], 0, 0, 0);
+      for (int t = 0; t < NT; ++t)
+        acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[2 * u + h], b[2 * u + h][t], acc[t], 0, 0, 0);
   };
   int c = wv;
   const bool two = c + kFewWaves < full;
@@ -334,8 +330,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) few_kernel(const int8_t* __res
     const int k = 128 * full + 16 * gg;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int i = 0; i < MT; ++i) a[h][i] = n >= 16 ? row_load(wr[i], k + 64 * h, n) : row_short(wr[i], k + 64 * h, n);
+      a[h] = n >= 16 ? row_load(wr, k + 64 * h, n) : row_short(wr, k + 64 * h, n);
 #pragma unroll
       for (int t = 0; t < NT; ++t)
         b[h][t] = FUSED ? *reinterpret_cast<const iv4*>(xr[t] + k + 64 * h)  // zeros behind the row there
@@ -344,8 +339,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) few_kernel(const int8_t* __res
     if (n >= 16) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int i = 0; i < MT; ++i) a[h][i] = row_end(a[h][i], k + 64 * h, n);
+        a[h] = row_end(a[h], k + 64 * h, n);
         if (!FUSED) {
 #pragma unroll
           for (int t = 0; t < NT; ++t) b[h][t] = row_end(b[h][t], k + 64 * h, n);
@@ -356,14 +350,11 @@ __global__ void __launch_bounds__(64 * kFewWaves) few_kernel(const int8_t* __res
   }
   // acc[q] = D(channel 4 gg + q, token lr): stored token-major
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-      *reinterpret_cast<iv4*>(&red[wv][(t * 16 + lr) * (16 * MT) + 16 * i + 4 * gg]) = acc[i][t];
+  for (int t = 0; t < NT; ++t) *reinterpret_cast<iv4*>(&red[wv][(t * 16 + lr) * 16 + 4 * gg]) = acc[t];
   __syncthreads();
-  for (int x = tid; x < MT * NT * 256; x += 64 * kFewWaves) {
-    const long long tok = t0 + x / (16 * MT);
-    const int o = r0 + x % (16 * MT);
+  for (int x = tid; x < NT * 256; x += 64 * kFewWaves) {
+    const long long tok = t0 + (x >> 4);
+    const int o = r0 + (x & 15);
     if (tok < tokens && o < m) {
       int sum = 0;
 #pragma unroll
@@ -440,16 +431,16 @@ struct ScaledY {
   }
 };
 
-// MT x NT tiles a workgroup; the grid's limits are kept by taking the tokens in runs
-template <int MT, int NT, typename YT>
+// 16 NT tokens a workgroup; the grid's limits are kept by taking the tokens in runs
+template <int NT, typename YT>
 static hipError_t few_launch(const int8_t* W, const float* sw, int m, int n, long long ldw, const int8_t* Xq,
                              const float* sx, int tokens, long long ldx, YT* Y, long long ldy, hipStream_t st) {
-  const unsigned gx = (unsigned)((m + 16ll * MT - 1) / (16 * MT));
+  const unsigned gx = (unsigned)((m + 15ll) / 16);
   const long long groups = (tokens + 16ll * NT - 1) / (16 * NT);
   for (long long g = 0; g < groups; g += 65535) {
     const unsigned gy = (unsigned)(groups - g < 65535 ? groups - g : 65535);
     const long long t0 = 16ll * NT * g;
-    hipLaunchKernelGGL((few_kernel<MT, NT, int8_t, YT>), dim3(gx, gy), dim3(64 * kFewWaves), 0, st, W, ldw, m, n, sw,
+    hipLaunchKernelGGL((few_kernel<NT, int8_t, YT>), dim3(gx, gy), dim3(64 * kFewWaves), 0, st, W, ldw, m, n, sw,
                        Xq + t0 * ldx, ldx, (int)(tokens - t0), sx + t0, Y + t0 * ldy, ldy);
   }
   return hipGetLastError();
@@ -459,41 +450,45 @@ template <typename YT>
 static hipError_t product_typed(const int8_t* W, const float* sw, int m, int n, long long ldw, const int8_t* Xq,
                                 const float* sx, int tokens, long long ldx, YT* Y, long long ldy, void* parts,
                                 hipStream_t st) {
-  if (tokens <= kFewTokens) return few_launch<1, 1>(W, sw, m, n, ldw, Xq, sx, tokens, ldx, Y, ldy, st);
+  if (tokens <= kFewTokens) return few_launch<1>(W, sw, m, n, ldw, Xq, sx, tokens, ldx, Y, ldy, st);
   // rows too short for the tiles' loads come here whatever their number
-  if (tokens <= 32 || n < 16) return few_launch<1, 2>(W, sw, m, n, ldw, Xq, sx, tokens, ldx, Y, ldy, st);
+  if (tokens <= 32 || n < 16) return few_launch<2>(W, sw, m, n, ldw, Xq, sx, tokens, ldx, Y, ldy, st);
   return tile_product(Xq, ldx, tokens, W, ldw, m, n, ScaledY<YT>{sx, sw, Y, ldy}, parts, st);
 }
 
 template <typename XT, typename YT>
 static hipError_t fused_typed(const int8_t* W, const float* sw, int m, int n, long long ldw, const XT* X, int tokens,
                               long long ldx, YT* Y, long long ldy, hipStream_t st) {
-  hipLaunchKernelGGL((few_kernel<1, 1, XT, YT>), dim3((unsigned)((m + 15ll) / 16)), dim3(64 * kFewWaves),
+  hipLaunchKernelGGL((few_kernel<1, XT, YT>), dim3((unsigned)((m + 15ll) / 16)), dim3(64 * kFewWaves),
                      (size_t)tokens * few_pitch(n), st, W, ldw, m, n, sw, X, ldx, tokens, nullptr, Y, ldy);
   return hipGetLastError();
 }
 
-// Whether the tokens are quantised within the product's own launch.
-static bool fused(int x_type, long long tokens, int n) {
-  return x_type != 3 && tokens <= kFewFused && tokens * few_pitch(n) <= kFewLds;
+// Whether the tokens are quantised within the product's own launch: every workgroup does it for itself,
+// which pays while that is less than a launch more.  Measured (kernels alone), m x n and tokens, fused /
+// two launches, us: 2560 x 2560, 1 token 4.7 / 6.2, 4 5.8 / 6.6, 8 6.9 / 6.8; 9728 x 2560, 1 7.5 / 8.9, 4
+// 9.8 / 9.7; 2560 x 9728, 1 8.3 / 11.5, 2 10.3 / 12.0, 3 12.2 / 12.3; 700 x 700, 8 4.5 / 5.7.
+static bool fused(int x_type, long long tokens, int n, int m) {
+  return x_type != 3 && tokens <= kFewFused && tokens * few_pitch(n) <= kFewLds &&
+         (double)tokens * n * (m > 4096 ? m / 4096.0 : 1.0) <= 20000.0;
 }
 
 // Workspace: the scales and quantised rows (padded to a multiple of 16 bytes) of tokens that come as
 // floating-point rows, and the parts of a split product.
 static size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 static long long pad16(long long n) { return (n + 15) & ~15ll; }
-static size_t rows_bytes(int x_type, long long tokens, int n) {
-  return x_type == 3 || fused(x_type, tokens, n) ? 0 : al256((size_t)tokens * 4) + al256((size_t)tokens * pad16(n));
+static size_t rows_bytes(int x_type, long long tokens, int n, int m) {
+  return x_type == 3 || fused(x_type, tokens, n, m) ? 0 : al256((size_t)tokens * 4) + al256((size_t)tokens * pad16(n));
 }
 size_t product_workspace_bytes(int x_type, long long tokens, int n, int m) {
-  return rows_bytes(x_type, tokens, n) + (tokens > 32 && n >= 16 ? tile_plan(tokens, m, n).bytes : 0);
+  return rows_bytes(x_type, tokens, n, m) + (tokens > 32 && n >= 16 ? tile_plan(tokens, m, n).bytes : 0);
 }
 
 template <typename YT>
 static hipError_t product_to(const int8_t* W, const float* sw, int m, int n, long long ldw, const void* X, int x_type,
                              const float* sx, int tokens, long long ldx, YT* Y, long long ldy, void* ws,
                              hipStream_t st) {
-  if (fused(x_type, tokens, n)) {
+  if (fused(x_type, tokens, n, m)) {
     switch (x_type) {
       case 0: return fused_typed(W, sw, m, n, ldw, static_cast<const float*>(X), tokens, ldx, Y, ldy, st);
       case 1: return fused_typed(W, sw, m, n, ldw, static_cast<const _Float16*>(X), tokens, ldx, Y, ldy, st);
@@ -512,7 +507,7 @@ static hipError_t product_to(const int8_t* W, const float* sw, int m, int n, lon
     ldx = np;
   }
   return product_typed(W, sw, m, n, ldw, Xq, sx, tokens, ldx, Y, ldy,
-                       static_cast<char*>(ws) + rows_bytes(x_type, tokens, n), st);
+                       static_cast<char*>(ws) + rows_bytes(x_type, tokens, n, m), st);
 }
 
 hipError_t product_run(const int8_t* W, const float* sw, int m, int n, long long ldw, const void* X, int x_type,

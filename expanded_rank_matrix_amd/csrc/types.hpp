@@ -53,6 +53,26 @@ __device__ __forceinline__ void load8(const __bf16* p, float (&v)[8]) {
   }
 }
 
+// 8 consecutive elements as they are, in 16-byte words: word q of them
+template <typename T>
+constexpr int words8() {
+  return sizeof(T) == 4 ? 2 : 1;
+}
+template <typename T>
+__device__ __forceinline__ iv4 word8(const T* p, int q) {
+  return *reinterpret_cast<const iv4_any*>(reinterpret_cast<const char*>(p) + 16 * q);
+}
+// 8 elements of T as fp32 out of the 16-byte words that hold them
+template <typename T>
+__device__ __forceinline__ void unpack8(const iv4 (&h)[words8<T>()], float (&v)[8]) {
+  typedef T v8 __attribute__((ext_vector_type(16 / sizeof(T))));
+#pragma unroll
+  for (int q = 0; q < words8<T>(); ++q) {
+    const v8 x = __builtin_bit_cast(v8, h[q]);
+#pragma unroll
+    for (int e = 0; e < (int)(16 / sizeof(T)); ++e) v[q * 4 + e] = (float)x[e];
+  }
+}
 // the first `count` of 8 consecutive elements, zeros behind them
 template <typename T>
 __device__ __forceinline__ void load8_tail(const T* p, long long count, float (&v)[8]) {

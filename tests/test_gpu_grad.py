@@ -214,6 +214,7 @@ def test_repairing_a_factored_head():
     xx = x.clone().requires_grad_()
     f = total(d, xx)
     f.backward()
+    f = f.detach()
     # each step is good to a few 2^-24 of its terms; the chain's logits reach some tens
     assert abs(float(loss.double().sum().cpu() - f)) <= 1e-4 * float(f)
     for got, want in ((dD.cpu().double(), d.grad), (dX.cpu().double(), xx.grad)):
