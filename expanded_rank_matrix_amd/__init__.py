@@ -375,16 +375,17 @@ class _Run:
             self.guard = torch.cuda.device(index)
             self.guard.__enter__()
         self.ptr = torch._C._cuda_getCurrentRawStream(index)
-        if stream is not None and stream.cuda_stream != self.ptr:
+        if stream is not None:
             try:
                 if stream.device != device:
                     raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
-                for t in inputs:
-                    if t is not None:
-                        t.record_stream(stream)
-                self.on = torch.cuda.stream(stream)
-                self.on.__enter__()
-                self.ptr = stream.cuda_stream
+                if stream.cuda_stream != self.ptr:
+                    for t in inputs:
+                        if t is not None:
+                            t.record_stream(stream)
+                    self.on = torch.cuda.stream(stream)
+                    self.on.__enter__()
+                    self.ptr = stream.cuda_stream
             except BaseException:
                 self.__exit__(None, None, None)
                 raise

@@ -391,7 +391,7 @@ hipError_t grad_run(const uint32_t* B, const uint32_t* C, const float* D, int k,
     const int c = (int)(batch - b0 < kGChunk ? batch - b0 : kGChunk);
     const bool first = b0 == 0, last = b0 + c == batch;
     p.dY = dY + b0 * m;
-    p.X = X + b0 * n;
+    p.X = dD ? X + b0 * n : nullptr;
     p.batch = c;
     const long long count[5] = {c, dD ? c : 0, first && dX ? (k + 255ll) / 256 * ((np / 16 + 15) / 16) : 0,
                                 first ? (k * (mp / 16) + 255) / 256 : 0, first && dD ? (k * (np / 16) + 255) / 256 : 0};

@@ -47,7 +47,8 @@ def rand_i8(rows, n, seed):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("rows,n", [(1, 1), (3, 7), (5, 64), (4, 1000), (9, 1024), (2, 1025), (7, 2560), (3, 9728),
-                                    (2, 10240), (2, 10241), (1, 40000), (1027, 33)])
+                                    (2, 10240), (2, 10241), (1, 40000), (1027, 33), (6, 8), (5, 9), (6, 15),
+                                    (3, 4096), (3, 4097), (2, 4104)])
 def test_quantize_matches_definition(rows, n, dtype):
     x = rand(rows, n, TYPES[dtype], 17 + rows + n)
     q, s = erm.quantize_rows(x.cuda())
@@ -136,7 +137,14 @@ def test_product_matches_definition(tokens, n, m, xd, yd):
 @pytest.mark.parametrize("tokens,n,m,xd,yd", [(1, 2560, 2560, "bf16", "bf16"), (5, 9728, 2560, "i8", "f32"),
                                               (300, 2560, 1000, "bf16", "bf16"), (513, 1021, 2051, "f16", "f16"),
                                               (2, 131071, 40, "i8", "f32"), (70, 131071, 33, "i8", "f32"),
-                                              (1100, 512, 2600, "i8", "bf16")])
+                                              (1100, 512, 2600, "i8", "bf16"),
+                                              # ends of the row length within a stage of the tiles, whole
+                                              # and split, direct and through registers
+                                              (40, 16, 70, "i8", "f32"), (70, 48, 200, "i8", "f32"), (300, 144, 140, "i8", "bf16"),
+                                              (300, 272, 300, "i8", "f16"), (70, 2559, 300, "i8", "f32"), (40, 5001, 130, "i8", "f32"),
+                                              (100, 4096, 500, "bf16", "bf16"), (260, 2577, 250, "f32", "f32"),
+                                              (33, 4112, 129, "i8", "f32"), (8, 2560, 100, "bf16", "bf16"),
+                                              (7, 1000, 50, "f32", "f32"), (6, 130, 33, "f16", "f16")])
 def test_product_larger_sizes(tokens, n, m, xd, yd):
     check_product(tokens, n, m, xd, yd, seed=tokens)
 
@@ -173,6 +181,17 @@ def test_product_strided_offset_out_and_single(tokens):
     assert (room[:, :3] == 7).all() and (room[:, 78:] == 7).all() and (room[tokens:] == 7).all()
     one = erm.apply_quantized(W, sw, X[0], out_dtype=torch.float32)
     assert one.shape == (75,) and torch.equal(one, plain[0])
+
+
+@pytest.mark.parametrize("tokens", [3, 40, 90])
+def test_product_rows_far_apart(tokens):
+    """Row distances of 2^24 and more: offsets within a tile pass 32 bits."""
+    room = torch.zeros(((1 << 24) + 32) * 300, dtype=torch.int8, device="cuda")
+    W = torch.as_strided(room, (300, 160), ((1 << 24) + 16, 1), 5 * 16)
+    W.copy_(rand_i8(300, 160, 1))
+    X, sw, sx = rand_i8(tokens, 160, 2).cuda(), torch.rand(300, device="cuda"), torch.rand(tokens, device="cuda")
+    y = erm.apply_quantized(W, sw, X, sx)
+    assert torch.equal(y, erm.apply_quantized(W.contiguous(), sw, X, sx))
 
 
 def test_product_independent_of_batch():
@@ -215,6 +234,48 @@ def test_product_streams_and_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, erm.apply_quantized(W, sw, static)), k
+
+
+def test_product_two_graphs_and_two_threads():
+    """Two captured graphs with workspaces of their own, replayed at once; two host threads at once."""
+    import threading
+
+    W, sw = rand_i8(300, 3001, 3).cuda(), torch.rand(300, device="cuda")
+    x = [rand(t, 3001, torch.bfloat16, t).cuda() for t in (70, 100)]
+    want = [erm.apply_quantized(W, sw, v) for v in x]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for v in x:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(erm.apply_quantized(W, sw, v))
+        graphs.append(g)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for r in range(5):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w), r
+    got = [[], []]
+
+    def work(i):
+        with torch.cuda.stream(streams[i]):
+            for _ in range(20):
+                got[i].append(erm.apply_quantized(W, sw, x[i]))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert len(got[i]) == 20 and all(torch.equal(y, want[i]) for y in got[i])
 
 
 def test_binding_refusals():
