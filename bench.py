@@ -231,6 +231,75 @@ def infer_bench(args, erm, torch, A, h, c, k, m, n, out, stream):
     print(json.dumps(res), flush=True)
 
 
+def quantized_bench(args, erm, torch, A, m, n, stream):
+    """The same inference through the workload's matrix in 8-bit integers (--infer --int8): each step
+    is one externd_apply_quantized call on `batch` fp32 vectors, quantised on the way."""
+    W, w_scale = erm.quantize_rows(A, stream=stream)
+    X = torch.randn((args.batch, n), dtype=torch.float32, device="cuda")
+    Y = torch.empty((args.batch, m), dtype=torch.float32, device="cuda")
+    wall, gpu_ms = timed_steps(args, torch, stream, lambda: erm.apply_quantized(W, w_scale, X, stream=stream, out=Y))
+    nbytes = float(m * n + 4 * m + 4 * args.batch * (m + n))
+    achieved = nbytes / (gpu_ms * 1e-3) / 1e9
+    print(json.dumps({
+        "metric": f"8-bit inference vectors/s ({m}x{n})", "value": args.batch * args.steps / wall, "unit": "vectors/s",
+        "n_gpus": 1, "steps": args.steps, "warmup": args.warmup, "ms_per_step": wall * 1e3 / args.steps,
+        "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": "i8", "data": "synthetic",
+        "config": {"workload": f"infer_int8_{args.workload}", "m": m, "n": n, "batch": args.batch,
+                   "entry": "externd_apply_quantized"},
+        "roofline": {"bound": "hbm", "achieved": achieved, "peak": HBM_PEAK_GBPS, "unit": "GB/s",
+                     "frac": achieved / HBM_PEAK_GBPS, "traffic": None, "gpu_ms_per_call": gpu_ms,
+                     "bytes_per_call": nbytes, "tops": 2e-9 * args.batch * m * n / gpu_ms},
+    }), flush=True)
+
+
+def repair_bench(args, erm, torch, A, h, c, k, m, n, out, stream):
+    """One step of repairing the scales of the workload's factors (--repair): the matrix in 8-bit
+    integers teaches its factored form on `batch` vectors.  Untimed: the decomposition, the teacher's
+    logits and their top 64.  A step: the student's logits (externd_apply_factors), loss and gradient
+    (externd_distill_loss), the gradient of D and of the vectors (externd_apply_factors_grad), D's update."""
+    erm.decompose(A, c["mu"], c["tau"], h, c["als_iters"], c["block"], stream=stream, out=out)
+    X = torch.randn((args.batch, n), dtype=torch.float32, device="cuda")
+    W, w_scale = erm.quantize_rows(A, stream=stream)
+    teacher, index = torch.topk(erm.apply_quantized(W, w_scale, X, stream=stream), min(64, m), dim=1)
+    index = index.to(torch.int32)
+    weight = torch.full((args.batch,), 1.0 / args.batch, device="cuda")
+    B, C, D = out["B"], out["C"], out["D"].clone()
+    losses = []
+
+    def step():
+        Z = erm.apply_factors(B, C, D, m, n, X, stream=stream)
+        loss, _, dZ = erm.distill_loss(Z, teacher, index, weight=weight, stream=stream, out=Z)
+        _, dD = erm.apply_factors_grad(B, C, D, m, n, X, dZ, stream=stream)
+        D.add_(dD, alpha=-1e-4)
+        losses.append(loss)
+
+    wall, gpu_ms = timed_steps(args, torch, stream, step)
+    print(json.dumps({
+        "metric": f"scale repair steps, vectors/s ({m}x{n}, k={k})", "value": args.batch * args.steps / wall,
+        "unit": "vectors/s", "n_gpus": 1, "steps": args.steps, "warmup": args.warmup,
+        "ms_per_step": wall * 1e3 / args.steps, "higher_is_better": True, "scaling": "weak", "vs_baseline": None,
+        "dtype": "f32", "data": "synthetic",
+        "config": {"workload": f"repair_{args.workload}", "m": m, "n": n, "k": k, "batch": args.batch, "top": min(64, m),
+                   "loss_first": float(losses[0].sum()), "loss_last": float(losses[-1].sum()),
+                   "gpu_ms_per_step": gpu_ms},
+    }), flush=True)
+
+
+def timed_steps(args, torch, stream, step):
+    """(wall seconds of args.steps steps, GPU milliseconds a step) after the warm-up."""
+    for _ in range(max(1, args.warmup)):
+        step()
+    torch.cuda.synchronize()
+    e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    t0 = time.perf_counter()
+    e0.record(stream)
+    for _ in range(args.steps):
+        step()
+    e1.record(stream)
+    torch.cuda.synchronize()
+    return time.perf_counter() - t0, e0.elapsed_time(e1) / args.steps
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -242,7 +311,11 @@ def main():
                     help="run a plain copy of this many MiB first (counter calibration)")
     ap.add_argument("--infer", action="store_true",
                     help="time inference from the workload's packed factors instead of the decomposition")
-    ap.add_argument("--batch", type=int, default=1, help="vectors per inference call (--infer)")
+    ap.add_argument("--int8", action="store_true",
+                    help="--infer through the workload's matrix in 8-bit integers instead of its factors")
+    ap.add_argument("--repair", action="store_true",
+                    help="time a step of repairing the factors' scales by distillation from the 8-bit matrix")
+    ap.add_argument("--batch", type=int, default=1, help="vectors per inference call (--infer) or repair step")
     ap.add_argument("--static", action="store_true",
                     help="--infer through the allocation-free entry point (no per-call workspace)")
     ap.add_argument("--sweeps", type=int, default=0, help="refinement sweeps after the greedy pass")
@@ -295,6 +368,12 @@ def main():
                D=torch.empty(k, dtype=torch.float32, device="cuda"),
                energy=torch.empty(k, dtype=torch.float64, device="cuda"))
     stream = torch.cuda.current_stream()
+    if args.infer and args.int8:
+        quantized_bench(args, erm, torch, A, m, n, stream)
+        return
+    if args.repair:
+        repair_bench(args, erm, torch, A, h, c, k, m, n, out, stream)
+        return
     if args.infer:
         infer_bench(args, erm, torch, A, h, c, k, m, n, out, stream)
         return
