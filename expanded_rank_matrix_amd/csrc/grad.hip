@@ -315,11 +315,15 @@ __global__ void __launch_bounds__(256) dfin_kernel(const double* __restrict__ pa
   else sum[i] = s;
 }
 
-// Batches whose work is small enough for the inference kernels: they take about 6 10^-8 us per vector
-// and pair of a component and an element, in two launches, against the seven launches and 40 us or
-// more of the products.
+// Batches that the inference kernels serve sooner: their two launches take about 11 us and, per vector
+// and 32 components, 7.5 ns and 1.7 ps an element of the two vectors; the products take about 30 us and
+// 0.5 ps an element of the factors to widen.  Measured, k, m, n and batch, inference kernels / products, us:
+// 7680, 2560, 2560: 1 18.6 / 58.7, 8 44.8 / 62.8, 14 67.3 / 63.9, 64 228 / 75.6; 1203, 777, 1025: 37 29.6 /
+// 41.3, 100 60.7 / 43.6; 300, 200, 200: 100 18.9 / 26.6, 1000 99.2 / 30.0; 5000, 5000, 500: 10 41.8 / 53.4, 20
+// 72.5 / 55.0; 1536, 1024, 1024: 16 21.9 / 34.1, 64 45.4 / 42.0.
 static bool grad_few(int k, int m, int n, long long batch) {
-  return batch <= 4096 && (double)batch * k * ((double)m + 2.0 * n) <= 8.5e8;
+  const double few = 11.0 + (double)batch * ((k + 31) / 32) * (7.5e-3 + 1.7e-6 * ((double)m + n));
+  return batch <= 4096 && few <= 30.0 + 5e-7 * k * ((double)m + 2.0 * n);
 }
 
 struct GradSpace {

@@ -40,9 +40,9 @@ __device__ __forceinline__ iv4 row_short(const int8_t* __restrict__ row, int k, 
 //   DMA: rows go to LDS directly (16 bytes a lane); K, the rows' distances and bases are multiples of
 //        16 and the distances below 2^24, so that a row's offset in a tile fits 32 bits
 //   else: through registers, loaded one stage earlier, at any alignment (K >= 16)
-// The fragments of the next 32 bytes are read from LDS while the products of these run, two reads
-// between four products (the scheduling groups), and the barrier that hands the stage over comes
-// before the last of a stage's four steps, whose products cover the reads behind it.
+// The fragments of the next 32 bytes are read from LDS while the products of these run, one read
+// before each of the first products (the scheduling groups), and the barrier that hands the stage over
+// comes before the last of a stage's four steps, whose products cover the reads behind it.
 // Measured (256 x 256, 8 waves, 8192^3): 2.0 to 2.4 10^15 operations a second by the card's clock, which
 // falls to 1.8 GHz under this load; the matrix cores are busy 62% of the time.  Four waves of 128 x 128
 // each read less from LDS but were slower (2.2 to 2.3) for want of a second wave to cover the barrier;

@@ -183,7 +183,7 @@ __device__ __forceinline__ void store_y(T* p, float v) {
 // XT int8_t: the tokens are 8-bit rows.  Else they are quantised here first, by every workgroup for
 // itself into LDS while the first loads of W are on their way.
 constexpr int kFewWaves = 8;
-constexpr int kFewTokens = 16;
+constexpr int kFewTokens = 16;        // one column tile; up to 32 take two
 constexpr int kFewFused = 8;          // most tokens quantised on the way
 constexpr int kFewLds = 48 * 1024;    // bytes of their rows
 

@@ -75,12 +75,13 @@ def test_gradient_matches_formula(k, m, n, batch):
     run(k, m, n, batch)
 
 
-# the products: much work, or more than 4096 vectors; whole and split tiles, ragged in every size
+# both sides of the choice of kernels; whole and split tiles, ragged in every size
 @pytest.mark.parametrize("k,m,n,batch", [(7680, 2560, 2560, 1), (7680, 2560, 2560, 16), (7680, 2560, 2560, 17),
                                          (7680, 2560, 2560, 40), (3001, 2999, 2503, 37), (1003, 777, 1025, 334),
                                          (1536, 1024, 1024, 300), (900, 640, 2100, 513), (64, 48, 50, 4096),
                                          (64, 48, 50, 4097), (37, 110, 17, 8200), (1, 1, 1, 5000), (130, 257, 300, 9000),
-                                         (600, 5000, 7000, 5), (600, 5000, 7000, 90)])
+                                         (600, 5000, 7000, 5), (600, 5000, 7000, 90), (300, 200, 200, 700),
+                                         (33, 70, 45, 2500), (1203, 777, 1025, 37), (1203, 777, 1025, 130)])
 def test_gradient_larger_sizes(k, m, n, batch):
     run(k, m, n, batch)
 
