@@ -164,6 +164,29 @@ def test_misaligned_inputs_out_streams_and_graph():
             assert torch.equal(g[0], want[0]) and torch.equal(g[1], want[1]), r
 
 
+def test_offsets_past_32_bits():
+    """k = 131 072 components of 32 768 outputs: the widened factor passes 2^32 bytes.  70 vectors of
+    which two have a gradient, against those two alone (the inference kernels)."""
+    k, m, n = 1 << 17, 1 << 15, 48
+    g = torch.Generator(device="cuda").manual_seed(3)
+
+    def codes(words):  # any word whose codes are 0, 1 or 3
+        w = torch.randint(-(2**31), 2**31 - 1, (k, words), generator=g, device="cuda", dtype=torch.int64).to(torch.int32)
+        return w | ((w >> 1) & 0x55555555)
+
+    B, C = codes(m // 16), codes(n // 16)
+    D = torch.randn(k, generator=g, device="cuda")
+    X = torch.randn((70, n), generator=g, device="cuda")
+    dY = torch.zeros((70, m), device="cuda")
+    dY[:2] = torch.randn((2, m), generator=g, device="cuda")
+    dX, dD = erm.apply_factors_grad(B, C, D, m, n, X, dY)
+    wX, wD = erm.apply_factors_grad(B, C, D, m, n, X[:2].contiguous(), dY[:2].contiguous())
+    assert not dX[2:].any()
+    # both sides are within a few 2^-24 of their terms; the sums of 32768 and 131072 terms leave 2^-16
+    assert (dX[:2] - wX).norm() <= 2.0**-16 * wX.norm() and (dD - wD).norm() <= 2.0**-16 * wD.norm()
+    assert wX.norm() > 0 and wD[k // 2:].norm() > 0
+
+
 def test_binding_refusals():
     rng = np.random.default_rng(1)
     B, C, D = device(*random_factors(rng, 30, 20, 25))

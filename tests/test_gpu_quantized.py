@@ -194,6 +194,20 @@ def test_product_rows_far_apart(tokens):
     assert torch.equal(y, erm.apply_quantized(W.contiguous(), sw, X, sx))
 
 
+def test_offsets_past_32_bits():
+    """70 000 x 32 768: element offsets of the tokens' rows, the codes and Y pass 2^31."""
+    rows, n = 70000, 32768
+    few = rand(64, n, torch.bfloat16, 5).cuda()
+    q, s = erm.quantize_rows(few.repeat((rows + 63) // 64, 1)[:rows])
+    wq, ws = erm.quantize_rows(few)
+    assert torch.equal(q[:64], wq) and torch.equal(q[69952:], wq[:48]) and torch.equal(s[69952:], ws[:48])
+    W, sw = rand_i8(n, 64, 6).cuda(), torch.rand(n, device="cuda")
+    X, sx = q[:, :64], s
+    y = erm.apply_quantized(W, sw, X, sx, out_dtype=torch.bfloat16)
+    want = erm.apply_quantized(W, sw, X[:64].contiguous(), sx[:64].contiguous(), out_dtype=torch.bfloat16)
+    assert torch.equal(y[:64], want) and torch.equal(y[69952:], want[:48])
+
+
 def test_product_independent_of_batch():
     """The same token gives the same bits alone, in a small and in a large batch."""
     x = rand(300, 777, torch.bfloat16, 2).cuda()
