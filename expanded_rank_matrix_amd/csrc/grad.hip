@@ -2,16 +2,19 @@
 //   u_b = B^T dy_b,   t_b = C x_b,   dD_i = sum_b t_bi u_bi,   dx_b = C^T (D u_b)
 //
 // Little work goes through the inference kernels (apply.hip).  A larger batch is three products of
-// 8-bit integers (igemm.hpp): each vector enters as four rows of signed 8-bit digits of a
-// fixed-point image with its own power-of-two scale, N = rint(x 2^(30 - E)), |x| < 2^E for the
-// whole vector, N = d0 + 2^8 d1 + 2^16 d2 + 2^24 d3; the factors' codes are widened to bytes.  A
-// digit's sum is exact in int32 (lengths below 2^24), the four are joined in int64, scaled and
-// rounded once to fp32: the image's rounding, 2^-31 of the vector's largest power of two, is the
-// only error of a product besides.  t u and its sum over the batch are fp64, in a fixed order: the
-// product that makes t multiplies its tile by u's and adds over the tile's vectors, so t is never
-// stored (split products, which have no whole tiles, store it).
+// 8-bit integers: each vector enters as four rows of signed 8-bit digits of a fixed-point image with
+// its own power-of-two scale, N = rint(x 2^(30 - E)), |x| < 2^E for the whole vector,
+// N = d0 + 2^8 d1 + 2^16 d2 + 2^24 d3.  A digit's sum is exact in int32 (lengths below 2^24), the four
+// are joined in int64, scaled and rounded once to fp32: the image's rounding, 2^-31 of the vector's
+// largest power of two, is the only error of a product besides.  t u and its sum over the batch are
+// fp64, in a fixed order.
 //
-// Bound by the products (2048 vectors, k = 7680, 2560 x 2560: 966 10^9 operations of digits in about
+// Up to a few hundred vectors the codes are widened on their way into the products (codes_ut_kernel,
+// codes_x_kernel); a batch beyond has them widened to bytes once for igemm.hpp's tiles: the product that
+// makes t multiplies its tile by u's and adds over the tile's vectors, so t is never stored (split
+// products, which have no whole tiles, store it).
+//
+// The large ones are bound by the products (2048 vectors, k = 7680, 2560 x 2560: 966 10^9 operations of digits in about
 // 450 of 490 us, 2.1 10^15 a second).  Three digits would take a quarter less, but their 2^-23 of the
 // vector's largest element is worse than fp32 wherever a few channels are large.
 #include <algorithm>
@@ -29,6 +32,7 @@ constexpr int kGBad = 0x7FFFFFFF;   // exponent of a vector with a NaN or an inf
 
 static size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 static long long pad16(long long n) { return (n + 15) & ~15ll; }
+static long long pad_step(long long n) { return (n + 255) & ~255ll; }
 
 // four 2-bit codes (0 -> 0, 1 -> 1, 3 -> -1) of the low byte as four signed bytes
 __device__ __forceinline__ unsigned widen4(unsigned x) {
@@ -47,22 +51,35 @@ __device__ __forceinline__ void widen(const uint32_t* __restrict__ P, long long 
   *reinterpret_cast<iv4*>(out + 16 * x) = v;
 }
 
+// 256 rows from i0 on by 16 words from w0 on, through LDS (zeros outside); thread: 16 rows of one word,
+// w[r] = word tid >> 4 of row 16 (tid & 15) + r
+__device__ __forceinline__ void tile_words(const uint32_t* __restrict__ P, int k, int words, long long i0, long long w0,
+                                           unsigned* tile, unsigned (&w)[16]) {
+  const int tid = threadIdx.x, r0 = tid >> 4, c = tid & 15;
+  const long long col = w0 + c < words ? w0 + c : words - 1;
+#pragma unroll
+  for (int u = 0; u < 16; ++u) {
+    const long long row = i0 + r0 + 16 * u;
+    w[u] = P[(row < k ? row : k - 1) * words + col];
+  }
+#pragma unroll
+  for (int u = 0; u < 16; ++u) asm volatile("" : "+v"(w[u]));  // all in flight: not loaded one by one before its store
+#pragma unroll
+  for (int u = 0; u < 16; ++u) tile[(r0 + 16 * u) * 17 + c] = i0 + r0 + 16 * u < k && w0 + c < words ? w[u] : 0u;
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < 16; ++r) w[r] = tile[(16 * c + r) * 17 + r0];
+}
+
 // packed rows -> bytes of the transpose: out[j][i] = code j of row i, i < kp (zeros from k on).
 // Workgroup (bx, by): rows 256 bx on, words 16 by on; thread: 16 rows of one word.
 __device__ __forceinline__ void widen_t(const uint32_t* __restrict__ P, int k, int words, int n, long long bx,
                                         long long by, int8_t* __restrict__ out, long long kp, unsigned* tile) {
   const int tid = threadIdx.x;
   const long long i0 = bx * 256, w0 = by * 16;
-#pragma unroll
-  for (int u = 0; u < 16; ++u) {
-    const int r = (tid >> 4) + 16 * u, c = tid & 15;
-    tile[r * 17 + c] = i0 + r < k && w0 + c < words ? P[(i0 + r) * words + w0 + c] : 0u;
-  }
-  __syncthreads();
   const int g = tid & 15, c = tid >> 4;
   unsigned w[16];
-#pragma unroll
-  for (int r = 0; r < 16; ++r) w[r] = tile[(16 * g + r) * 17 + c];
+  tile_words(P, k, words, i0, w0, tile, w);
   const long long i = i0 + 16 * g;
   if (i >= kp) return;
 #pragma unroll
@@ -77,6 +94,37 @@ __device__ __forceinline__ void widen_t(const uint32_t* __restrict__ P, int k, i
     }
     if (j < n) *reinterpret_cast<iv4*>(out + j * kp + i) = v;
   }
+}
+
+// 16 words of 16 codes: bits 2 i of word j <-> bits 2 j of word i
+__device__ __forceinline__ void transpose_codes(unsigned (&w)[16]) {
+#pragma unroll
+  for (int s = 8; s >= 1; s >>= 1) {
+    const unsigned mask = s == 8 ? 0x0000FFFFu : s == 4 ? 0x00FF00FFu : s == 2 ? 0x0F0F0F0Fu : 0x33333333u;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (!(i & s)) {
+        const unsigned x = (w[i] >> 2 * s ^ w[i + s]) & mask;
+        w[i + s] ^= x;
+        w[i] ^= x << 2 * s;
+      }
+  }
+}
+
+// packed rows -> the packed transpose: word i / 16 of row j of out (kw words) holds code j of 16 rows i,
+// zeros from row k on.  Workgroups as for widen_t.
+__device__ __forceinline__ void pack_t(const uint32_t* __restrict__ P, int k, int words, long long bx, long long by,
+                                       uint32_t* __restrict__ out, int kw, unsigned* tile) {
+  const int tid = threadIdx.x;
+  const long long i0 = bx * 256, w0 = by * 16;
+  const int g = tid & 15, c = tid >> 4;
+  unsigned w[16];
+  tile_words(P, k, words, i0, w0, tile, w);
+  transpose_codes(w);
+  if (w0 + c >= words) return;
+  uint32_t* o = out + 16 * (w0 + c) * kw + i0 / 16 + g;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) o[(long long)e * kw] = w[e];
 }
 
 // digits of four values: word q holds digit q of values 0..3 (bytes 0..3)
@@ -95,7 +143,10 @@ __device__ __forceinline__ void digits4(const float (&x)[4], int sh, unsigned (&
 }
 
 // One vector a workgroup: x (times D where given) -> digit rows 4 b .. 4 b + 3 of np bytes, and the
-// exponent E - 30 of its image's unit.
+// exponent E - 30 of its image's unit.  TILED: the rows of four vectors in the order in which a wave's
+// MFMA operands take them, 1 KB a load (codes_kernel): of 256 columns the 16-byte pieces
+// [piece & 3][piece >> 2][row & 15].
+template <int TH, bool TILED>
 __device__ __forceinline__ void digits(const float* __restrict__ X, long long n, const float* __restrict__ D, long long b,
                                        int8_t* __restrict__ out, long long np, int* __restrict__ ex, unsigned* wmx) {
   const float* x = X + b * n;
@@ -115,7 +166,7 @@ __device__ __forceinline__ void digits(const float* __restrict__ X, long long n,
     }
   };
   unsigned mx = 0u;
-  for (long long j = 4 * threadIdx.x; j < n; j += 1024) {
+  for (long long j = 4 * threadIdx.x; j < n; j += 4 * TH) {
     float v[4];
     get(j, v);
 #pragma unroll
@@ -128,13 +179,33 @@ __device__ __forceinline__ void digits(const float* __restrict__ X, long long n,
   if ((threadIdx.x & 63) == 0) wmx[threadIdx.x >> 6] = mx;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < 4; ++w) mx = wmx[w] > mx ? wmx[w] : mx;
+  for (int w = 0; w < TH / 64; ++w) mx = wmx[w] > mx ? wmx[w] : mx;
   const bool bad = mx >= 0x7F800000u;
   const int E = mx >> 23 ? (int)(mx >> 23) - 126 : -126;  // |x| < 2^E
   const int sh = 30 - E;
   if (threadIdx.x == 0) ex[b] = bad ? kGBad : -sh;
+  if (TILED) {
+    int8_t* o = out + 16 * (b >> 2) * np + 64 * (b & 3);
+    for (long long j = 16 * threadIdx.x; j < np; j += 16 * TH) {
+      iv4 w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float v[4];
+        unsigned d[4] = {0u, 0u, 0u, 0u};
+        get(j + 4 * e, v);
+        if (!bad) digits4(v, sh, d);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) w[q][e] = (int)d[q];
+      }
+      const long long piece = j >> 4;
+      iv4* p = reinterpret_cast<iv4*>(o + (piece >> 4) * 4096 + (piece & 3) * 1024 + (piece >> 2 & 3) * 256);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) p[q] = w[q];
+    }
+    return;
+  }
   int8_t* o = out + 4 * b * np;
-  for (long long j = 4 * threadIdx.x; j < np; j += 1024) {
+  for (long long j = 4 * threadIdx.x; j < np; j += 4 * TH) {
     float v[4];
     unsigned w[4] = {0u, 0u, 0u, 0u};
     get(j, v);
@@ -148,7 +219,7 @@ __global__ void __launch_bounds__(256) digits_kernel(const float* __restrict__ X
                                                      const float* __restrict__ D, int8_t* __restrict__ out,
                                                      long long np, int* __restrict__ ex) {
   __shared__ unsigned wmx[4];
-  digits(X, n, D, blockIdx.x, out, np, ex, wmx);
+  digits<256, false>(X, n, D, blockIdx.x, out, np, ex, wmx);
 }
 
 // Everything the products need but D u, in one launch: digits of dY and X (the rows of one pass), the
@@ -164,19 +235,24 @@ struct Prep {
   int8_t* ce;
   int8_t* ct;
   int* ex;
+  long long yp, xp;  // bytes of a row of yd and xd
   int m, n, k, batch;
   unsigned count[5];
 };
+template <bool TILED>
 __global__ void __launch_bounds__(256) prep_kernel(Prep p) {
   __shared__ unsigned lds[256 * 17];
   const long long kp = (p.k + 15ll) & ~15ll, mp = (p.m + 15ll) & ~15ll, np = (p.n + 15ll) & ~15ll;
   unsigned b = blockIdx.x;
-  if (b < p.count[0]) return digits(p.dY, p.m, nullptr, b, p.yd, mp, p.ex, lds);
+  if (b < p.count[0]) return digits<256, TILED>(p.dY, p.m, nullptr, b, p.yd, p.yp, p.ex, lds);
   b -= p.count[0];
-  if (b < p.count[1]) return digits(p.X, p.n, nullptr, b, p.xd, np, p.ex + p.batch, lds);
+  if (b < p.count[1]) return digits<256, TILED>(p.X, p.n, nullptr, b, p.xd, p.xp, p.ex + p.batch, lds);
   b -= p.count[1];
   if (b < p.count[2]) {
     const unsigned across = (unsigned)((np / 16 + 15) / 16);
+    if (TILED)
+      return pack_t(p.C, p.k, (int)(np / 16), b / across, b % across, reinterpret_cast<uint32_t*>(p.ct),
+                    (int)((kp + 255) / 256 * 16), lds);
     return widen_t(p.C, p.k, (int)(np / 16), p.n, b / across, b % across, p.ct, kp, lds);
   }
   b -= p.count[2];
@@ -315,15 +391,184 @@ __global__ void __launch_bounds__(256) dfin_kernel(const double* __restrict__ pa
   else sum[i] = s;
 }
 
-// Batches that the inference kernels serve sooner: their two launches take about 11 us and, per vector
-// and 32 components, 7.5 ns and 1.7 ps an element of the two vectors; the products take about 30 us and
-// 0.5 ps an element of the factors to widen.  Measured, k, m, n and batch, inference kernels / products, us:
-// 7680, 2560, 2560: 1 18.6 / 58.7, 8 44.8 / 62.8, 14 67.3 / 63.9, 64 228 / 75.6; 1203, 777, 1025: 37 29.6 /
-// 41.3, 100 60.7 / 43.6; 300, 200, 200: 100 18.9 / 26.6, 1000 99.2 / 30.0; 5000, 5000, 500: 10 41.8 / 53.4, 20
-// 72.5 / 55.0; 1536, 1024, 1024: 16 21.9 / 34.1, 64 45.4 / 42.0.
-static bool grad_few(int k, int m, int n, long long batch) {
-  const double few = 11.0 + (double)batch * ((k + 31) / 32) * (7.5e-3 + 1.7e-6 * ((double)m + n));
-  return batch <= 4096 && few <= 30.0 + 5e-7 * k * ((double)m + 2.0 * n);
+// ---- small batches, from the packed codes ---------------------------------------------------------
+// Workgroup: 16 NT packed rows by 16 vectors (64 digit rows).  A wave walks the columns in steps of 256: a
+// lane takes the codes of its row at 64 consecutive columns (one 16-byte load), and its digit row's bytes
+// there; the order of the columns within a step does not matter, only that both operands have the same.
+// An accumulator's four registers are the four digits of one vector.  Bound by the digits' way from L2 (7680,
+// 2560, 2560: u and t of 16 vectors 10.6 us, 328 KB a workgroup; with their rows as they lie, 64 bytes of
+// each at a time, 23), small sizes by the four launches (1203, 777, 1025 with 37 vectors: 5.6 + 5.6 + 4.3 + 3.2).
+constexpr int kCVec = 16, kCStep = 256;
+template <int NT>
+__device__ __forceinline__ void codes_sums(const uint32_t* __restrict__ P, int count, int w, int i0,
+                                           const int8_t* __restrict__ dig, int pitch, int batch, int b0, int first,
+                                           int stride, int steps, long long (&sum)[NT][4]) {
+  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+  const uint32_t* codes[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int i = i0 + 16 * t + lr;
+    codes[t] = P + (long long)(i < count ? i : count - 1) * w;
+  }
+  const int8_t* rows[4];
+  const int tiles = (batch + 3) >> 2;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int tile = (b0 >> 2) + r;
+    rows[r] = dig + (tile < tiles ? tile : tiles - 1) * (16ll * pitch) + 16 * lane;
+  }
+  iv4 acc[NT][4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) acc[t][r] = iv4{0, 0, 0, 0};
+  for (int c = first; c < steps; c += stride) {
+    const int x = 16 * c + 4 * lg;  // the lane's first word
+    iv4 v[NT], a[4][4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) a[r][q] = *reinterpret_cast<const iv4*>(rows[r] + 16ll * kCStep * c + 1024 * q);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      if (x + 4 <= w) {
+        v[t] = *reinterpret_cast<const iv4_any*>(codes[t] + x);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[t][q] = x + q < w ? (int)codes[t][x + q] : 0;
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const unsigned y = (unsigned)v[t][q];
+        const iv4 b = {(int)widen4(y & 255u), (int)widen4(y >> 8 & 255u), (int)widen4(y >> 16 & 255u),
+                       (int)widen4(y >> 24)};
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[t][r] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[r][q], b, acc[t][r], 0, 0, 0);
+      }
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      sum[t][r] = (long long)acc[t][r][0] + ((long long)acc[t][r][1] << 8) + ((long long)acc[t][r][2] << 16) +
+                  ((long long)acc[t][r][3] << 24);
+}
+__device__ __forceinline__ double scaled(long long v, int e) {
+  return e == kGBad ? (double)__builtin_nanf("") : ldexp((double)v, e);
+}
+
+// u (waves 0-3) and t (waves 4-7), each wave a quarter of the columns.  The quarters meet in LDS as int64,
+// u and t of a pair in one thread, which adds t u over the workgroup's vectors.
+template <int NT>
+__global__ void __launch_bounds__(512) codes_ut_kernel(const uint32_t* __restrict__ B, int wm,
+                                                       const uint32_t* __restrict__ C, int wn, int k,
+                                                       const int8_t* __restrict__ yd, int yp,
+                                                       const int8_t* __restrict__ xd, int xp, const int* __restrict__ ex,
+                                                       int batch, float* __restrict__ U, double* __restrict__ part) {
+  __shared__ long long sums[8][256 * NT];
+  __shared__ double ds[8][16];
+  const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lg = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);  // scalar: MFMA runs whatever the lane mask
+  const int i0 = blockIdx.x * 16 * NT, b0 = blockIdx.y * kCVec;
+  const bool fwd = wv >= 4;
+  const int pitch = fwd ? xp : yp;
+  long long own[NT][4];
+  codes_sums<NT>(fwd ? C : B, k, fwd ? wn : wm, i0, fwd ? xd : yd, pitch, batch, b0, wv & 3, 4,
+                 fwd && !part ? 0 : pitch / kCStep, own);
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) sums[wv][t * 256 + (4 * r + lg) * 16 + lr] = own[t][r];
+  __syncthreads();
+  const int t = tid >> 8, b = b0 + (tid >> 4 & 15), i = i0 + 16 * t + lr;
+  if (t < NT) {
+    double s = 0.0;
+    if (b < batch) {
+      const double u = scaled(sums[0][tid] + sums[1][tid] + sums[2][tid] + sums[3][tid], ex[b]);
+      if (U && i < k) U[(size_t)b * k + i] = (float)u;
+      if (part) s = u * scaled(sums[4][tid] + sums[5][tid] + sums[6][tid] + sums[7][tid], ex[batch + b]);
+    }
+    s += __shfl_xor(s, 16);
+    s += __shfl_xor(s, 32);
+    if (lg == 0) ds[wv][lr] = s;
+  }
+  __syncthreads();
+  if (part && tid < 16 * NT && i0 + tid < k) {
+    const int q = 4 * (tid >> 4);
+    part[(size_t)blockIdx.y * k + i0 + tid] = ds[q][tid & 15] + ds[q + 1][tid & 15] + ds[q + 2][tid & 15] + ds[q + 3][tid & 15];
+  }
+}
+
+// Between the products: the images of D u (nd workgroups, one a vector), and dD from its parts.
+constexpr int kCJoin = 1024;
+__global__ void __launch_bounds__(kCJoin) codes_join_kernel(int nd, const float* __restrict__ U, int k,
+                                                            const float* __restrict__ D, int8_t* __restrict__ sd, int sp,
+                                                            int* __restrict__ ex, const double* __restrict__ part,
+                                                            int parts, float* __restrict__ dD) {
+  __shared__ unsigned wmx[kCJoin / 64];
+  if ((int)blockIdx.x < nd) return digits<kCJoin, true>(U, k, D, blockIdx.x, sd, sp, ex, wmx);
+  const int i = ((int)blockIdx.x - nd) * kCJoin + (int)threadIdx.x;
+  if (i >= k) return;
+  double s = 0.0;
+#pragma unroll 4
+  for (int p = 0; p < parts; ++p) s += part[(size_t)p * k + i];
+  dD[i] = (float)s;
+}
+
+// dX from C's transpose and the images of D u, all eight waves over the components
+template <int NT>
+__global__ void __launch_bounds__(512) codes_x_kernel(const uint32_t* __restrict__ Ct, int n, const int8_t* __restrict__ sd,
+                                                      int sp, const int* __restrict__ ex, int batch,
+                                                      float* __restrict__ dX) {
+  __shared__ long long sums[8][256 * NT];
+  const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lg = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int j0 = blockIdx.x * 16 * NT, b0 = blockIdx.y * kCVec;
+  long long own[NT][4];
+  codes_sums<NT>(Ct, n, sp / 16, j0, sd, sp, batch, b0, wv, 8, sp / kCStep, own);
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) sums[wv][t * 256 + (4 * r + lg) * 16 + lr] = own[t][r];
+  __syncthreads();
+  const int t = tid >> 8, b = b0 + (tid >> 4 & 15), j = j0 + 16 * t + lr;
+  if (t < NT && b < batch && j < n) {
+    long long s = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) s += sums[w][tid];
+    dX[(long long)b * n + j] = (float)scaled(s, ex[b]);
+  }
+}
+
+// Two tiles of rows a workgroup (the digits are read half as often) where that still leaves one for every
+// CU.  Measured, one / two, us of a whole gradient: k, m, n = 7680, 2560, 2560, batch 32 44.9 / 37.3, 256
+// 170 / 116; 4000, 9728, 2560, 16 32.9 / 36.0, 64 62.8 / 50.0; 1203, 777, 1025, 64 20.7 / 21.1, 250 37.4 / 33.8.
+static bool codes_wide(int rows, int groups) { return (rows + 31) / 32 * (long long)groups >= 256; }
+static unsigned codes_blocks(int rows, int groups) {
+  return codes_wide(rows, groups) ? (rows + 31) / 32 : (rows + 15) / 16;
+}
+
+// Which kernels serve a batch: the least of their times in us, fitted to measurements (within a fifth of
+// nearly all of them; a wrong choice cost a tenth).  kFew: two launches of the inference kernels, two
+// vectors a workgroup.  kCodes: four launches, from the packed codes, 16 vectors a workgroup.  kProducts: up
+// to nine, the codes widened to bytes once.  Measured, k, m, n and batch, kFew / kCodes / kProducts, us:
+// 7680, 2560, 2560: 1 18.4 / 29.2 / 56.6, 4 28.5 / 29.5 / 58.0, 16 72 / 33.0 / 61.3, 128 432 / 73 / 82, 256
+// 850 / 120 / 103; 1203, 777, 1025: 1 14.3 / 17.3 / 33.2, 37 30.1 / 18.7 / 40.7, 250 128 / 33.9 / 46.7, 1000
+// - / 74 / 57; 96, 9728, 9728: 16 29.0 / 32.9 / 38.3, 256 116 / 62 / 57; 300, 200, 200: 2 13.1 / 14.7 / 19.7, 100
+// 19.5 / 15.8 / 25.6, 1000 - / 31.7 / 29.3.
+enum class GradWay { kFew, kCodes, kProducts };
+static GradWay grad_way(int k, int m, int n, long long batch) {
+  if (batch > kGChunk) return GradWay::kProducts;
+  const double l = std::max(m, n), b = (double)batch, g = (double)((batch + kCVec - 1) / kCVec);
+  const double w = k * ((double)m + 2.0 * n);
+  const double few = 11.7 + 1.38e-3 * l + b * ((k + 31) / 32) * (7.1e-3 + 1.64e-6 * ((double)m + n));
+  const double codes = 13.7 + 1.06e-3 * l + 4e-4 * k + 2.5e-7 * k * n + g * (0.14 + 2.9e-4 * k + 1.9e-4 * l + 4.6e-8 * w);
+  const double products = 21.7 + 1.95e-3 * l + 1.73e-3 * k + 2.8e-7 * w + b * (2.7e-3 + 5.8e-6 * k + 4.6e-6 * l + 2.9e-9 * w);
+  if (few <= codes && few <= products) return GradWay::kFew;
+  return codes <= products ? GradWay::kCodes : GradWay::kProducts;
 }
 
 struct GradSpace {
@@ -331,7 +576,9 @@ struct GradSpace {
 };
 static GradSpace grad_space(int k, int m, int n, long long batch) {
   const size_t c = (size_t)(batch < kGChunk ? batch : kGChunk);
-  const size_t kp = pad16(k), mp = pad16(m), np = pad16(n);
+  const bool codes = grad_way(k, m, n, batch) == GradWay::kCodes;
+  const size_t kp = pad16(k), mp = codes ? pad_step(m) : pad16(m), np = codes ? pad_step(n) : pad16(n);
+  const size_t np16 = pad16(n);
   GradSpace s;
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -339,12 +586,13 @@ static GradSpace grad_space(int k, int m, int n, long long batch) {
     off = al256(off + bytes);
     return o;
   };
-  s.be = take(k * mp);
-  s.ce = take(k * np);
-  s.ct = take(n * kp);
-  s.xd = take(4 * c * np);
-  s.yd = take(4 * c * mp);
-  s.sd = take(4 * c * kp);
+  s.be = take(codes ? 0 : k * mp);
+  s.ce = take(codes ? 0 : k * np);
+  s.ct = take(codes ? np16 * pad_step(k) / 4 : n * kp);
+  const size_t c4 = codes ? (c + 3) & ~(size_t)3 : c;  // whole tiles
+  s.xd = take(4 * c4 * np);
+  s.yd = take(4 * c4 * mp);
+  s.sd = take(codes ? 4 * c4 * pad_step(k) : 4 * c * kp);
   s.u = take(4 * c * k);
   s.ex = take(3 * c * 4);
   s.part = take(std::max<size_t>(kGParts, 4 * c / 32 + 2) * k * 8);
@@ -353,7 +601,7 @@ static GradSpace grad_space(int k, int m, int n, long long batch) {
   // where the others do not
   size_t split = 0, t = 0;
   for (const long long b : {(long long)c, batch % kGChunk})
-    if (b > 0) {
+    if (b > 0 && !codes) {
       const TilePlan pt = tile_plan(4 * b, k, (int)np);
       if (pt.parts > 1) t = std::max(t, (size_t)(4 * b * k));
       split = std::max({split, pt.bytes, tile_plan(4 * b, k, (int)mp).bytes, tile_plan(4 * b, n, (int)kp).bytes});
@@ -366,7 +614,7 @@ static GradSpace grad_space(int k, int m, int n, long long batch) {
 
 size_t grad_workspace_bytes(int k, int m, int n, long long batch) {
   if (batch == 0) return 0;
-  if (grad_few(k, m, n, batch)) return infer_grad_workspace_bytes(k, n, (int)batch);
+  if (grad_way(k, m, n, batch) == GradWay::kFew) return infer_grad_workspace_bytes(k, n, (int)batch);
   return grad_space(k, m, n, batch).bytes;
 }
 
@@ -377,7 +625,8 @@ hipError_t grad_run(const uint32_t* B, const uint32_t* C, const float* D, int k,
     if (dD) hipLaunchKernelGGL(dfin_kernel, gk, dim3(256), 0, st, nullptr, 0, k, 1, 1, nullptr, dD);
     return hipGetLastError();
   }
-  if (grad_few(k, m, n, batch)) return infer_grad_run(B, C, D, k, m, n, X, dY, (int)batch, dX, dD, ws, st);
+  const GradWay way = grad_way(k, m, n, batch);
+  if (way == GradWay::kFew) return infer_grad_run(B, C, D, k, m, n, X, dY, (int)batch, dX, dD, ws, st);
   const GradSpace s = grad_space(k, m, n, batch);
   char* base = static_cast<char*>(ws);
   auto at = [&](size_t o) { return static_cast<void*>(base + o); };
@@ -388,9 +637,11 @@ hipError_t grad_run(const uint32_t* B, const uint32_t* C, const float* D, int k,
   int* ex = static_cast<int*>(at(s.ex));
   int8_t* sd = static_cast<int8_t*>(at(s.sd));
   void* split = at(s.split);
+  const bool codes = way == GradWay::kCodes;
   const long long kp = pad16(k), mp = pad16(m), np = pad16(n);
+  const long long yp = codes ? pad_step(m) : mp, xp = codes ? pad_step(n) : np;
   Prep p{dY, X, B, C, static_cast<int8_t*>(at(s.yd)), static_cast<int8_t*>(at(s.xd)), static_cast<int8_t*>(at(s.be)),
-         static_cast<int8_t*>(at(s.ce)), static_cast<int8_t*>(at(s.ct)), ex, m, n, k, 0, {}};
+         static_cast<int8_t*>(at(s.ce)), static_cast<int8_t*>(at(s.ct)), ex, yp, xp, m, n, k, 0, {}};
   for (long long b0 = 0; b0 < batch; b0 += kGChunk) {
     const int c = (int)(batch - b0 < kGChunk ? batch - b0 : kGChunk);
     const bool first = b0 == 0, last = b0 + c == batch;
@@ -398,14 +649,31 @@ hipError_t grad_run(const uint32_t* B, const uint32_t* C, const float* D, int k,
     p.X = dD ? X + b0 * n : nullptr;
     p.batch = c;
     const long long count[5] = {c, dD ? c : 0, first && dX ? (k + 255ll) / 256 * ((np / 16 + 15) / 16) : 0,
-                                first ? (k * (mp / 16) + 255) / 256 : 0, first && dD ? (k * (np / 16) + 255) / 256 : 0};
+                                first && !codes ? (k * (mp / 16) + 255) / 256 : 0,
+                                first && dD && !codes ? (k * (np / 16) + 255) / 256 : 0};
     long long all = 0;
     for (int q = 0; q < 5; ++q) {
       p.count[q] = (unsigned)count[q];
       all += count[q];
     }
     if (all > (1ll << 23)) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(prep_kernel, dim3((unsigned)all), dim3(256), 0, st, p);
+    if (codes) hipLaunchKernelGGL(prep_kernel<true>, dim3((unsigned)all), dim3(256), 0, st, p);
+    else hipLaunchKernelGGL(prep_kernel<false>, dim3((unsigned)all), dim3(256), 0, st, p);
+    if (codes) {
+      const int groups = (c + kCVec - 1) / kCVec, nd = dX ? c : 0, ns = dD ? (k + kCJoin - 1) / kCJoin : 0;
+      const int sp = (int)pad_step(k), wm = (int)(mp / 16), wn = (int)(np / 16);
+      const auto ut = codes_wide(k, groups) ? codes_ut_kernel<2> : codes_ut_kernel<1>;
+      hipLaunchKernelGGL(ut, dim3(codes_blocks(k, groups), groups), dim3(512), 0, st, B, wm, C, wn, k, p.yd, (int)yp, p.xd,
+                         (int)xp, ex, c, dX ? u : nullptr, dD ? part : nullptr);
+      hipLaunchKernelGGL(codes_join_kernel, dim3(nd + ns), dim3(kCJoin), 0, st, nd, u, k, D, sd, sp, ex + 2 * c, part, groups,
+                         dD);
+      if (dX) {
+        const auto xk = codes_wide(n, groups) ? codes_x_kernel<2> : codes_x_kernel<1>;
+        hipLaunchKernelGGL(xk, dim3(codes_blocks(n, groups), groups), dim3(512), 0, st,
+                           reinterpret_cast<const uint32_t*>(p.ct), n, sd, sp, ex + 2 * c, c, dX);
+      }
+      return hipGetLastError();
+    }
     hipError_t e = tile_product(p.yd, mp, 4 * c, p.be, mp, k, (int)mp, JoinDigits{ex, u, k}, split, st);
     if (e != hipSuccess) return e;
     if (dD) {

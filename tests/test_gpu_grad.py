@@ -86,13 +86,38 @@ def test_gradient_larger_sizes(k, m, n, batch):
     run(k, m, n, batch)
 
 
+# small batches straight from the packed codes: one or two tiles of components and of columns a workgroup,
+# rows of a single word and of words that end inside a step, vectors that end inside a tile
+@pytest.mark.parametrize("k,m,n,batch", [(4097, 17, 33, 9), (2049, 1, 1, 50), (2100, 50, 4000, 23), (513, 3000, 31, 61),
+                                         (1000, 1, 700, 70), (4111, 515, 1031, 100), (640, 64, 8200, 130),
+                                         (8200, 255, 257, 35), (515, 300, 12, 460), (257, 256, 4097, 250),
+                                         (2560, 1024, 512, 16), (7680, 2560, 2560, 199)])
+def test_gradient_from_packed_codes(k, m, n, batch):
+    run(k, m, n, batch)
+
+
+# long sums over few tiles: the widened products split them, each of the three in its turn
+@pytest.mark.parametrize("k,m,n,batch", [(100, 60, 9000, 900), (100, 9000, 60, 900), (7680, 48, 48, 600)])
+def test_gradient_of_split_products(k, m, n, batch):
+    run(k, m, n, batch)
+
+
+@pytest.mark.parametrize("batch", [5, 300, 4300])
+def test_a_bad_vector_stays_alone(batch):
+    Bt, Ct, D, X, dY, dX, _ = run(130, 75, 93, batch, seed=6)
+    X[2, 5], dY[3, 7] = np.inf, np.nan
+    got, _ = erm.apply_factors_grad(*device(Bt, Ct, D), 75, 93, torch.from_numpy(X).cuda(), torch.from_numpy(dY).cuda())
+    good = torch.arange(batch, device="cuda") != 3  # dX does not depend on X
+    assert torch.equal(got[good], dX[good])
+
+
 @pytest.mark.parametrize("scale", [1e-38, 1e-42, 1e30])
-@pytest.mark.parametrize("batch", [2, 20, 4100])
+@pytest.mark.parametrize("batch", [2, 20, 700, 4100])
 def test_gradient_extreme_scales(batch, scale):
     run(50, 40, 60, batch, scale=scale)
 
 
-@pytest.mark.parametrize("batch", [4, 50, 4200])
+@pytest.mark.parametrize("batch", [4, 50, 700, 4200])
 def test_zero_parts(batch):
     Bt, Ct, D, X, dY, _, _ = run(40, 50, 60, batch)
     Z = np.zeros_like(Bt)
@@ -136,7 +161,7 @@ def test_gradient_against_the_forward_pass(batch):
 
 
 def test_misaligned_inputs_out_streams_and_graph():
-    for batch in (5, 70, 4300):
+    for batch in (5, 70, 300, 4300):
         Bt, Ct, D, X, dY, dX, dD = run(130, 75, 93, batch, seed=5)
         f = device(Bt, Ct, D)
         put = lambda a: torch.cat([torch.zeros(1), torch.from_numpy(a).reshape(-1)]).cuda()[1:].reshape(a.shape)
@@ -164,9 +189,10 @@ def test_misaligned_inputs_out_streams_and_graph():
             assert torch.equal(g[0], want[0]) and torch.equal(g[1], want[1]), r
 
 
-def test_offsets_past_32_bits():
-    """k = 131 072 components of 32 768 outputs: the widened factor passes 2^32 bytes.  70 vectors of
-    which two have a gradient, against those two alone (the inference kernels)."""
+@pytest.mark.parametrize("batch", [70, 1200])
+def test_offsets_past_32_bits(batch):
+    """k = 131 072 components of 32 768 outputs, 2^32 of them (as bytes where the batch is large).  Two
+    vectors have a gradient, against those two alone (the inference kernels)."""
     k, m, n = 1 << 17, 1 << 15, 48
     g = torch.Generator(device="cuda").manual_seed(3)
 
@@ -176,8 +202,8 @@ def test_offsets_past_32_bits():
 
     B, C = codes(m // 16), codes(n // 16)
     D = torch.randn(k, generator=g, device="cuda")
-    X = torch.randn((70, n), generator=g, device="cuda")
-    dY = torch.zeros((70, m), device="cuda")
+    X = torch.randn((batch, n), generator=g, device="cuda")
+    dY = torch.zeros((batch, m), device="cuda")
     dY[:2] = torch.randn((2, m), generator=g, device="cuda")
     dX, dD = erm.apply_factors_grad(B, C, D, m, n, X, dY)
     wX, wD = erm.apply_factors_grad(B, C, D, m, n, X[:2].contiguous(), dY[:2].contiguous())
