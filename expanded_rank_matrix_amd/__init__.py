@@ -342,8 +342,11 @@ def _apply_factors_grad(B, C, D, k, m, n, X, dY, batch, lead, need_dX, need_dD, 
     dev = D.device
     lib = load()
     if out is None:
-        dX = torch.empty((*lead, n), dtype=torch.float32, device=dev) if need_dX else None
-        dD = torch.empty(k, dtype=torch.float32, device=dev) if need_dD else None
+        dX = dD = None
+        if need_dX:
+            dX = torch.empty((*lead, n), dtype=torch.float32, device=dev) if X is None else torch.empty_like(X)
+        if need_dD:
+            dD = torch.empty_like(D)
     else:
         dX, dD = (t if need else None for t, need in zip(out, (need_dX, need_dD)))
         if (dX is None) == need_dX or (dD is None) == need_dD:

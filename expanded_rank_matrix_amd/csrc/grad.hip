@@ -552,7 +552,7 @@ static unsigned codes_blocks(int rows, int groups) {
 }
 
 // Which kernels serve a batch: the least of their times in us, fitted to measurements (within a fifth of
-// nearly all of them; a wrong choice cost a tenth).  kFew: two launches of the inference kernels, two
+// nearly all of them; a wrong choice cost 15% at most).  kFew: two launches of the inference kernels, two
 // vectors a workgroup.  kCodes: four launches, from the packed codes, 16 vectors a workgroup.  kProducts: up
 // to nine, the codes widened to bytes once.  Measured, k, m, n and batch, kFew / kCodes / kProducts, us:
 // 7680, 2560, 2560: 1 18.4 / 29.2 / 56.6, 4 28.5 / 29.5 / 58.0, 16 72 / 33.0 / 61.3, 128 432 / 73 / 82, 256

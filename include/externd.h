@@ -275,7 +275,8 @@ int64_t externd_apply_quantized_workspace(int x_type, int64_t tokens, int64_t n,
  *   workspace    externd_distill_workspace(rows, vocab) bytes, 16-byte aligned (NULL where that is
  *                0), used by this call alone until it has run
  * Statistics, sums and losses are kept in fp32 and fp64 as the row is read once; the gradient is
- * rounded once to z_type; exp((z - largest) / T) below 2^-126 counts as 0.  Deterministic.  0 <= rows < 2^31, 1 <= vocab <= 2^30, 1 <= top <= 1024. */
+ * rounded once to z_type; exp((z - largest) / T) below 2^-126 counts as 0.  Deterministic.
+ * 0 <= rows < 2^31, 1 <= vocab <= 2^30, 1 <= top <= 1024. */
 int externd_distill_loss(const void* logits, int z_type, int64_t rows, int64_t vocab, int64_t ldz, const void* teacher,
                          int t_type, const void* index, int index_bytes, int64_t top, float temperature,
                          const float* weight, float* loss, float* stats, void* dlogits, int64_t ldd, void* workspace,
@@ -305,8 +306,8 @@ int externd_distill_grad(const void* logits, int z_type, int64_t rows, int64_t v
  *   dX  batch x n fp32, or NULL                       dD  k fp32, or NULL (0 for batch 0)
  *   workspace  externd_apply_factors_grad_workspace(k, m, n, batch) bytes, 16-byte aligned, used
  *              by this call alone until it has run
- * 1 <= k, m, n <= 2^23, k m and k n <= 2^33, 0 <= batch < 2^31.  A non-finite X or dY gives meaningless values in
- * dD and in its vector of dX. */
+ * 1 <= k, m, n <= 2^23, k m and k n <= 2^33, 0 <= batch < 2^31.  A non-finite X or dY gives
+ * meaningless values in dD and in its vector of dX. */
 int externd_apply_factors_grad(const uint32_t* B_packed, const uint32_t* C_packed, const float* D, int64_t k, int64_t m,
                                int64_t n, const float* X, const float* dY, int64_t batch, float* dX, float* dD,
                                void* workspace, void* stream);
