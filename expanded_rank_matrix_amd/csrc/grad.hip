@@ -551,23 +551,24 @@ static unsigned codes_blocks(int rows, int groups) {
   return codes_wide(rows, groups) ? (rows + 31) / 32 : (rows + 15) / 16;
 }
 
-// Which kernels serve a batch: the least of their times in us, fitted to measurements (within a fifth of
-// nearly all of them; a wrong choice cost 15% at most).  kFew: two launches of the inference kernels, two
-// vectors a workgroup.  kCodes: four launches, from the packed codes, 16 vectors a workgroup.  kProducts: up
-// to nine, the codes widened to bytes once.  Measured, k, m, n and batch, kFew / kCodes / kProducts, us:
-// 7680, 2560, 2560: 1 18.4 / 29.2 / 56.6, 4 28.5 / 29.5 / 58.0, 16 72 / 33.0 / 61.3, 128 432 / 73 / 82, 256
-// 850 / 120 / 103; 1203, 777, 1025: 1 14.3 / 17.3 / 33.2, 37 30.1 / 18.7 / 40.7, 250 128 / 33.9 / 46.7, 1000
-// - / 74 / 57; 96, 9728, 9728: 16 29.0 / 32.9 / 38.3, 256 116 / 62 / 57; 300, 200, 200: 2 13.1 / 14.7 / 19.7, 100
-// 19.5 / 15.8 / 25.6, 1000 - / 31.7 / 29.3.
+// Which kernels serve a batch: the least of their times in us, fitted to measurements of 75 sizes (1% lost
+// on average to the best choice, 30% in the worst).  kFew: two launches of the inference kernels, two
+// vectors a workgroup; its sums of t u are chains over the batch.  kCodes: four launches, from the packed
+// codes, 16 vectors a workgroup.  kProducts: up to nine, the codes widened to bytes once.  Measured, k, m, n
+// and batch, kFew / kCodes / kProducts, us: 7680, 2560, 2560: 1 18.4 / 29.2 / 56.6, 4 28.5 / 29.5 / 58.0, 16 72 /
+// 33.0 / 61.3, 128 432 / 73 / 82, 256 850 / 120 / 103; 1203, 777, 1025: 1 14.3 / 17.3 / 33.2, 37 30.1 / 18.7 /
+// 40.7, 250 128 / 33.9 / 46.7, 1000 - / 74 / 57; 96, 9728, 9728: 16 29.0 / 32.9 / 38.3, 256 116 / 62 / 57; 300,
+// 200, 200: 2 13.1 / 14.7 / 19.7, 100 19.5 / 15.8 / 25.6, 1000 98 / 31.7 / 29.3; 9728, 100, 9728: 1 45.5 / 58 / 95,
+// 64 - / 113 / 138, 256 - / 355 / 242.
 enum class GradWay { kFew, kCodes, kProducts };
 static GradWay grad_way(int k, int m, int n, long long batch) {
   if (batch > kGChunk) return GradWay::kProducts;
-  const double l = std::max(m, n), b = (double)batch, g = (double)((batch + kCVec - 1) / kCVec);
-  const double w = k * ((double)m + 2.0 * n);
-  const double few = 11.7 + 1.38e-3 * l + b * ((k + 31) / 32) * (7.1e-3 + 1.64e-6 * ((double)m + n));
-  const double codes = 13.7 + 1.06e-3 * l + 4e-4 * k + 2.5e-7 * k * n + g * (0.14 + 2.9e-4 * k + 1.9e-4 * l + 4.6e-8 * w);
-  const double products = 21.7 + 1.95e-3 * l + 1.73e-3 * k + 2.8e-7 * w + b * (2.7e-3 + 5.8e-6 * k + 4.6e-6 * l + 2.9e-9 * w);
-  if (few <= codes && few <= products) return GradWay::kFew;
+  const double l = std::max(m, n), s = (double)m + n, w = k * ((double)m + 2.0 * n);
+  const double b = (double)batch, g = (double)((batch + kCVec - 1) / kCVec);
+  const double few = 11.7 + 1.2e-3 * l + b * ((k + 31) / 32 * (7.1e-3 + 1.5e-6 * s) + 1.2e-5 * s);
+  const double codes = 13.6 + 1.1e-3 * l + 6.6e-4 * k + 1.6e-7 * k * n + g * (0.13 + 2.7e-4 * k + 1.7e-4 * l + 5.4e-8 * w);
+  const double products = 21.1 + 2.0e-3 * l + 2.2e-3 * k + 1.6e-7 * w + b * (3.3e-3 + 5e-6 * k + 5e-6 * l + 2.8e-9 * w);
+  if (batch <= 512 && few <= codes && few <= products) return GradWay::kFew;
   return codes <= products ? GradWay::kCodes : GradWay::kProducts;
 }
 

@@ -91,7 +91,7 @@ def test_gradient_larger_sizes(k, m, n, batch):
 @pytest.mark.parametrize("k,m,n,batch", [(4097, 17, 33, 9), (2049, 1, 1, 50), (2100, 50, 4000, 23), (513, 3000, 31, 61),
                                          (1000, 1, 700, 70), (4111, 515, 1031, 100), (640, 64, 8200, 130),
                                          (8200, 255, 257, 35), (515, 300, 12, 460), (257, 256, 4097, 250),
-                                         (2560, 1024, 512, 16), (7680, 2560, 2560, 199)])
+                                         (2560, 1024, 512, 16), (7680, 2560, 2560, 130)])
 def test_gradient_from_packed_codes(k, m, n, batch):
     run(k, m, n, batch)
 
