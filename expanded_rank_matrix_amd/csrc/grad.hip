@@ -15,7 +15,7 @@
 // products, which have no whole tiles, store it).
 //
 // The large ones are bound by the products (2048 vectors, k = 7680, 2560 x 2560: 966 10^9 operations of digits in about
-// 450 of 490 us, 2.1 10^15 a second).  Three digits would take a quarter less, but their 2^-23 of the
+// 430 of 495 us, 2.2 10^15 a second).  Three digits would take a quarter less, but their 2^-23 of the
 // vector's largest element is worse than fp32 wherever a few channels are large.
 #include <algorithm>
 
