@@ -311,11 +311,24 @@ static inline bool tile_dma(const void* p, long long ld, int K) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 16 == 0 && K % 16 == 0 && ld < (1ll << 24);
 }
 
+// Most tiles of a launch: its threads (up to 512 a tile) stay below 2^32.
+constexpr long long kMaxTiles = 1ll << 22;
+// Rows of one launch for a matrix of N columns: whole rows of every tile shape, at most kMaxTiles of the
+// smallest tile of more than 64 rows, 128 x 128.  N is at most 2^26 (2^19 tiles across), so 1024 rows
+// fit at the least.
+constexpr long long tile_run(long long N) { return kMaxTiles / ((N + 127) / 128) * 128 / 256 * 256; }
+constexpr bool tile_run_fits(long long N) {
+  return tile_run(N) > 0 && tile_run(N) < (1ll << 31) && (tile_run(N) + 127) / 128 * ((N + 127) / 128) <= kMaxTiles;
+}
+static_assert(tile_run_fits(1) && tile_run_fits(128) && tile_run_fits(129) && tile_run_fits(1000003) &&
+                  tile_run_fits(1ll << 26),
+              "a run's tiles fit a launch");
+
 template <int BM, int BN, int WR, int WC, typename EPI>
 static hipError_t tile_launch(const int8_t* A, long long lda, int M, const int8_t* B, long long ldb, int N, int K,
                               int parts, const EPI& epi, hipStream_t st) {
   const long long ntm = (M + BM - 1ll) / BM, ntn = (N + BN - 1ll) / BN;
-  if (ntm * ntn > (1ll << 22)) return hipErrorInvalidValue;
+  if (ntm * ntn > kMaxTiles) return hipErrorInvalidValue;
   const int kper = parts == 1 ? K : ((K + 127) / 128 + parts - 1) / parts * 128;
   const dim3 grid((unsigned)(ntm * ntn), (unsigned)parts);
   if (tile_dma(A, lda, K) && tile_dma(B, ldb, K))

@@ -453,7 +453,15 @@ static hipError_t product_typed(const int8_t* W, const float* sw, int m, int n, 
   if (tokens <= kFewTokens) return few_launch<1>(W, sw, m, n, ldw, Xq, sx, tokens, ldx, Y, ldy, st);
   // rows too short for the tiles' loads come here whatever their number
   if (tokens <= 32 || n < 16) return few_launch<2>(W, sw, m, n, ldw, Xq, sx, tokens, ldx, Y, ldy, st);
-  return tile_product(Xq, ldx, tokens, W, ldw, m, n, ScaledY<YT>{sx, sw, Y, ldy}, parts, st);
+  const long long run = tile_run(m);
+  if (tokens <= run) return tile_product(Xq, ldx, tokens, W, ldw, m, n, ScaledY<YT>{sx, sw, Y, ldy}, parts, st);
+  // more tiles than a launch holds: the tokens in runs (never split, there are tiles enough)
+  for (long long t = 0; t < tokens; t += run) {
+    const int c = tokens - t < run ? (int)(tokens - t) : (int)run;
+    const hipError_t e = tile_whole(Xq + t * ldx, ldx, c, W, ldw, m, n, ScaledY<YT>{sx + t, sw, Y + t * ldy, ldy}, st);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <typename XT, typename YT>

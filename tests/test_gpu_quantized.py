@@ -315,3 +315,18 @@ def test_binding_refusals():
     with pytest.raises(erm.ExterndError) as e:
         erm.apply_quantized(big, sw[:1], big, torch.ones(1, device="cuda"))
     assert e.value.status == erm.EINVAL
+
+
+def test_product_of_more_tiles_than_a_launch_holds():
+    """2^29 + 300 tokens by one channel: 2^22 + 3 tiles of 128 rows."""
+    tokens, n = 2**29 + 300, 16
+    g = torch.Generator(device="cuda").manual_seed(1)
+    X = torch.randint(-128, 128, (tokens, n), generator=g, device="cuda", dtype=torch.int8)
+    sx = torch.rand(tokens, generator=g, device="cuda")
+    W, sw = rand_i8(1, n, 2).cuda(), torch.rand(1, device="cuda")
+    room = torch.full((tokens, 2), 7.0, device="cuda")
+    y = erm.apply_quantized(W, sw, X, sx, out=room[:, 1:])
+    assert (room[:, 0] == 7).all()
+    for t in range(0, tokens, 1 << 24):
+        total = (X[t:t + (1 << 24)].int() * W.int()).sum(1)  # below 2^19: exact in fp32
+        assert torch.equal(y[t:t + (1 << 24), 0], total.float() * sw * sx[t:t + (1 << 24)]), t
