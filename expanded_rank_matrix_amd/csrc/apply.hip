@@ -107,7 +107,8 @@ __device__ __forceinline__ void fx_digits7(const unsigned long long (&b)[4], uns
 // (the 16 lanes of a group still read the word's 256 contiguous bytes; the builders' stores of one
 // column for 16 words fall in distinct banks).
 // smax[b gridDim.x + blockIdx.x] receives the workgroup's max |s_b| (high word of the fp64 bits).
-// RAW (the layer's gradient): t itself goes to Traw, and s only where S is given.
+// RAW (the layer's gradient): t itself goes to Traw, and s only where S is given; a vector with a NaN or
+// an infinity, which no image holds, gives NaN.
 template <bool RAW>
 __device__ __forceinline__ void t_pass(const uint32_t* __restrict__ C, int wn, int n, const float* __restrict__ D, int k,
                                        const float* __restrict__ X, int batch, int x_vec4, int c_vec4,
@@ -138,6 +139,7 @@ __device__ __forceinline__ void t_pass(const uint32_t* __restrict__ C, int wn, i
   const int fi = blockIdx.x * kTComp + 16 * ((tid >> 5) & 1) + ((tid >> 1) & 15);
   const float dfin = RAW && !S ? 1.0f : D[fi < k ? fi : 0];  // an unconditional load: nothing waits for it until the end
   int e0 = 0, e1 = 0;
+  bool bad0 = false, bad1 = false;
   long long T = 0;  // threads 0..63: (tile tid >> 5, row (tid >> 1) & 15, vector tid & 1)
   for (int cw0 = 0; cw0 < wnp; cw0 += kTWords) {
     const int cwn = wnp - cw0 < kTWords ? wnp - cw0 : kTWords;  // multiple of 16
@@ -228,6 +230,10 @@ __device__ __forceinline__ void t_pass(const uint32_t* __restrict__ C, int wn, i
       const int px = inf_bits(n);
       e0 = m0 ? px - f32_bound_exp(m0) : 0;
       e1 = m1 ? px - f32_bound_exp(m1) : 0;
+      if (RAW) {
+        bad0 = m0 >= 0x7F800000u;
+        bad1 = m1 >= 0x7F800000u;
+      }
     } else {
       __syncthreads();  // the last chunk's operands are read
     }
@@ -310,7 +316,8 @@ __device__ __forceinline__ void t_pass(const uint32_t* __restrict__ C, int wn, i
     const int b = b0 + v;
     unsigned hb = 0u;
     if (i < k && b < batch) {
-      const double t = ldexp((double)T, -(v ? e1 : e0));
+      double t = ldexp((double)T, -(v ? e1 : e0));
+      if (RAW && (v ? bad1 : bad0)) t = __builtin_nan("");
       const double s = (double)dfin * t;
       if (RAW) Traw[(size_t)b * k + i] = t;
       if (!RAW || S) S[(size_t)b * k + i] = s;
@@ -375,6 +382,8 @@ __device__ __forceinline__ void infer_s_scales(unsigned h0, unsigned h1, int k, 
 // itself, and the last one reads the sums back with atomic adds of zero, at the same place the
 // adds were made.
 // Every global load of the workgroup is issued before the first is used.
+// GRAD (the layer's gradient): a vector whose s holds a NaN or an infinity gives NaN.
+template <bool GRAD>
 __device__ __forceinline__ void y_pass(const uint32_t* __restrict__ B, int wm, int m, int k,
                                        const double* __restrict__ S, int batch, const unsigned* __restrict__ smax,
                                        int gxt, int nwg, int b_vec4, long long* __restrict__ Yacc,
@@ -516,12 +525,14 @@ __device__ __forceinline__ void y_pass(const uint32_t* __restrict__ B, int wm, i
   if (tid == 0) last = atomicAdd(cnt + (size_t)blockIdx.y * nwg + grp, 1u) == (unsigned)(nch - 1);
   __syncthreads();
   if (last) {  // every chunk of this output group has been added: round its outputs
+    const int fbad = inf_bits(k) - f64_bound_exp(0x7FF00000u);  // the scale of no finite s
     for (int x = tid; x < 2 * 16 * kYWords; x += kYThreads) {
       const int v = x / (16 * kYWords), r = 16 * w0 + x % (16 * kYWords), b = b0 + v;
       if (r < m && b < batch) {
         const long long val =
             (long long)atomicAdd(reinterpret_cast<unsigned long long*>(Yacc + (size_t)b * m + r), 0ull);
-        Y[(size_t)b * m + r] = (float)ldexp((double)val, -(v ? f1 : f0));
+        const int f = v ? f1 : f0;
+        Y[(size_t)b * m + r] = GRAD && f == fbad ? __builtin_nanf("") : (float)ldexp((double)val, -f);
       }
     }
   }
@@ -532,7 +543,7 @@ __global__ void __launch_bounds__(kYThreads) infer_y_kernel(const uint32_t* __re
                                                       const unsigned* __restrict__ smax, int gxt, int nwg,
                                                       int b_vec4, long long* __restrict__ Yacc,
                                                       unsigned* __restrict__ cnt, float* __restrict__ Y) {
-  y_pass(B, wm, m, k, S, batch, smax, gxt, nwg, b_vec4, Yacc, cnt, Y);
+  y_pass<false>(B, wm, m, k, S, batch, smax, gxt, nwg, b_vec4, Yacc, cnt, Y);
 }
 
 static int infer_gxt(int k) { return (k + kTComp - 1) / kTComp; }
@@ -599,7 +610,7 @@ __global__ void __launch_bounds__(kYThreads) infer_grad_y_kernel(const uint32_t*
                                                            const double* __restrict__ Tr,
                                                            const double* __restrict__ U, float* __restrict__ dD) {
   if ((int)blockIdx.x < ny) {
-    y_pass(C, wn, n, k, S, batch, smax, gxt, nwg, c_vec4, acc, cnt, dX);
+    y_pass<true>(C, wn, n, k, S, batch, smax, gxt, nwg, c_vec4, acc, cnt, dX);
     return;
   }
   if (blockIdx.y != 0) return;

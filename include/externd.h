@@ -306,8 +306,9 @@ int externd_distill_grad(const void* logits, int z_type, int64_t rows, int64_t v
  *   dX  batch x n fp32, or NULL                       dD  k fp32, or NULL (0 for batch 0)
  *   workspace  externd_apply_factors_grad_workspace(k, m, n, batch) bytes, 16-byte aligned, used
  *              by this call alone until it has run
- * 1 <= k, m, n <= 2^23, k m and k n <= 2^33, 0 <= batch < 2^31.  A non-finite X or dY gives
- * meaningless values in dD and in its vector of dX. */
+ * 1 <= k, m, n <= 2^23, k m and k n <= 2^33, 0 <= batch < 2^31.  A NaN or an infinity in a vector
+ * of dY gives NaN in that vector of dX and throughout dD, one in X NaN throughout dD, one in D NaN
+ * throughout dX. */
 int externd_apply_factors_grad(const uint32_t* B_packed, const uint32_t* C_packed, const float* D, int64_t k, int64_t m,
                                int64_t n, const float* X, const float* dY, int64_t batch, float* dX, float* dD,
                                void* workspace, void* stream);

@@ -275,3 +275,27 @@ def test_repairing_a_factored_head():
         slope = (total(d + h * v, x) - total(d - h * v, x)) / (2 * h)
     # the central difference's own error is h^2 times a third derivative
     assert abs(float(slope - (dD.cpu().double() * v).sum())) <= 1e-3 * float((dD.cpu().double() * v).abs().sum())
+
+
+@pytest.mark.parametrize("batch", [4, 9, 70, 300, 4300])
+def test_a_bad_vector_gives_nan(batch):
+    """The same on every way through the kernels: a NaN or an infinity in dY gives its vector of dX NaN, one
+    in X or dY all of dD, one in D all of dX; the rest is untouched."""
+    k, m, n = 130, 75, 93
+    Bt, Ct, D, X, dY, dX, dD = run(k, m, n, batch, seed=6)
+    f = device(Bt, Ct, D)
+    for v in (np.inf, -np.inf, np.nan):
+        badX, badY = X.copy(), dY.copy()
+        badX[1, 5], badY[batch - 1, 7] = v, v
+        Xc, Yc, bX, bY = (torch.from_numpy(t).cuda() for t in (X, dY, badX, badY))
+        got = erm.apply_factors_grad(*f, m, n, bX, Yc)
+        assert torch.equal(got[0], dX) and torch.isnan(got[1]).all()
+        got = erm.apply_factors_grad(*f, m, n, Xc, bY)
+        assert torch.equal(got[0][:-1], dX[:-1]) and torch.isnan(got[0][-1]).all() and torch.isnan(got[1]).all()
+        got = erm.apply_factors_grad(*f, m, n, None, bY, need_dD=False)
+        assert torch.equal(got[0][:-1], dX[:-1]) and torch.isnan(got[0][-1]).all()
+        assert torch.isnan(erm.apply_factors_grad(*f, m, n, Xc, bY, need_dX=False)[1]).all()
+        bad = f[2].clone()
+        bad[3] = v
+        got = erm.apply_factors_grad(*f[:2], bad, m, n, Xc, Yc)
+        assert torch.isnan(got[0]).all() and torch.equal(got[1], dD)
