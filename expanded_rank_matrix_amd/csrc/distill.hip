@@ -11,8 +11,9 @@
 // log p - log q is a difference of numbers many times its size.  The gradient is a second pass: g q_v
 // for every element, rounded once to z's type, and after it, behind a barrier, the teacher's at most K
 // elements once more, with p in the difference before its rounding.  Equal indices of one row meet in
-// hashed lists in LDS; their p add in 64-bit fixed point (units of 2^-60), so the order does not
-// matter and each of them writes the same value.
+// hashed lists in LDS; their exponentials add as whole numbers of 2^-50 of the largest one's binade, so
+// the order does not matter and each of them writes the same value.  p keeps fp32's relative precision
+// however small it is: where the student gives less, it is the gradient.
 #include "common.hpp"
 #include "externd_internal.hpp"
 #include "types.hpp"
@@ -22,7 +23,6 @@ namespace externd {
 constexpr int kDThreads = 256;           // of streaming workgroups
 constexpr int kDBuckets = 2048;          // lists of the teacher's indices
 constexpr unsigned short kDNone = 0xFFFF;
-constexpr unsigned long long kDNaN = ~0ull;
 
 __device__ __forceinline__ float wave_max_f32(float v) {
 #pragma unroll
@@ -81,7 +81,9 @@ __device__ __forceinline__ TeacherSums teacher_row(const Teacher& t, long long r
     float e = 0.0f;
     if (idx[k] >= 0) {
       const double x = ((double)ex[k] - (double)mx) * rT;
-      e = expf((float)x);
+      const float xf = (float)x;
+      e = expf(xf);
+      if (e != 0.0f) e = fmaf(e, (float)(x - (double)xf), e);  // what x lost by its rounding, up to 2^-24 |x| of e
       s += (double)e;
       if (e != 0.0f) sx += x * (double)e;
     }
@@ -237,7 +239,7 @@ __device__ __forceinline__ void slice_grad(const T* z, T* d, int lo, int hi, flo
   }
 }
 
-// the teacher's elements of lo .. hi - 1: g (q - p), p = the sum of e pinv over equal indices
+// the teacher's elements of lo .. hi - 1: g (q - p), p = pinv times the sum of e over equal indices
 template <typename T, int TH>
 __device__ __forceinline__ void teacher_grad(T* d, int lo, int hi, float m, float c, float g, float gi, double pinv,
                                              int top, const int* idx, const float* ex, const float* zk,
@@ -245,13 +247,22 @@ __device__ __forceinline__ void teacher_grad(T* d, int lo, int hi, float m, floa
   for (int k = threadIdx.x; k < top; k += TH) {
     const int i = idx[k];
     if (i < lo || i >= hi) continue;
-    unsigned long long sum = 0;
+    float most = ex[k];  // all of a row's are NaN or none
+    int same = 0;
     for (unsigned x = heads[bucket(i)]; x != kDNone; x = next[x])
       if (idx[x] == i) {
-        const double q = (double)ex[x] * pinv;  // all of a row's are NaN or none
-        sum = q == q ? sum + (unsigned long long)(q * 0x1p60) : kDNaN;
+        most = fmaxf(most, ex[x]);
+        ++same;
       }
-    const float p = sum == kDNaN ? __builtin_nanf("") : (float)((double)sum * 0x1p-60);
+    double sum = (double)ex[k];
+    if (same > 1 && most > 0.0f) {
+      const int sh = 50 + 127 - (int)(__float_as_uint(most) >> 23);  // most 2^sh < 2^51: 1024 of them fit
+      unsigned long long whole = 0;
+      for (unsigned x = heads[bucket(i)]; x != kDNone; x = next[x])
+        if (idx[x] == i) whole += (unsigned long long)ldexp((double)ex[x], sh);
+      sum = ldexp((double)whole, -sh);
+    }
+    const float p = (float)(sum * pinv);
     d[i] = (T)(__builtin_amdgcn_exp2f((zk[k] - m) * c) * gi - g * p);
   }
 }

@@ -283,3 +283,28 @@ def test_empty_and_binding_refusals():
     for T in (0.0, float("nan"), 1e4):
         with pytest.raises(erm.ExterndError):
             erm.distill_loss(z, a, i, T)
+
+
+@pytest.mark.parametrize("rows,vocab", [(3, 400), (2, 9000), (1030, 400), (1030, 8205)])
+def test_small_teacher_probabilities_keep_their_bits(rows, vocab):
+    """Teacher entries down to p = e^-80 whose students' logits are far below: the gradient there is
+    -w T p, good to 10 eps of p however small it is, for single indices and for repeated ones."""
+    g = torch.Generator().manual_seed(rows + vocab)
+    top, T = 40, float(np.float32(0.7))  # as the entry takes it: 0.7 in 64 bits is 80 1.7e-8 away in an exponent
+    z = torch.randn((16, vocab), generator=g)
+    a = -56.0 * torch.rand((16, top), generator=g)
+    a[:, 0] = 0.0
+    i = torch.stack([torch.randperm(vocab, generator=g)[:top] for _ in range(16)])
+    i[:, 30:] = i[:, 20:30]                        # ten indices twice, their p far apart
+    i[:, 38:] = i[:, 21:23]                        # two of them three times
+    z.scatter_(1, i, -150.0)
+    z, a, i = (t.repeat((rows + 15) // 16, 1)[:rows].contiguous() for t in (z, a, i.to(torch.int32)))
+    w = torch.full((rows,), 2.0**30)
+    zc, ac, ic, wc = z.cuda(), a.cuda(), i.cuda(), w.cuda()
+    out = erm.distill_loss(zc, ac, ic, T, wc, grad=True)
+    d = erm.distill_grad(zc, out[1], ac, ic, T, wc)
+    few = min(rows, 16)
+    check([t[:few] for t in out], z[:few], a[:few], i[:few], T, w[:few])
+    check(None, z[:few], a[:few], i[:few], T, w[:few], grad_only=d[:few])
+    for t in (*out, d):
+        assert torch.equal(t, t[:few].repeat((rows + 15) // 16, *[1] * (t.dim() - 1))[:rows])
