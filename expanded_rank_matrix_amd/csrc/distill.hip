@@ -30,6 +30,30 @@ __device__ __forceinline__ float wave_max_f32(float v) {
   return v;
 }
 
+// log2 e / T in two fp32 numbers.  An exponent is d log2 e / T with d = z - m <= 0; with the constant in
+// one fp32 number each exponential of a row would be off by the same 2^-24 |x| or so, which no sum averages
+// out (S by 5 10^-8 at 50 021 logits).  The first part is cut towards zero and the second above it, so that
+// d = -inf gives -inf.
+struct Log2eT {
+  float hi, lo, near;  // near: the nearest fp32 number alone
+  __device__ __forceinline__ explicit Log2eT(float T) {
+    const double c = 1.4426950408889634 / (double)T;
+    near = hi = (float)c;
+    if ((double)hi >= c) hi = __uint_as_float(__float_as_uint(hi) - 1u);
+    lo = (float)(c - (double)hi);
+  }
+};
+// e^(d / T); 0 below 2^-126
+__device__ __forceinline__ float exp_t(float d, const Log2eT& c) {
+  return __builtin_amdgcn_exp2f(fmaf(d, c.hi, d * c.lo));
+}
+// The same for an element of T's gradient.  Of 16 bits, one constant will do: 2^-24 |x| is nothing beside
+// their own rounding (2^-9 or 2^-12 at the least), and the product less is 2.5% of a step over 131072 logits.
+template <typename T>
+__device__ __forceinline__ float exp_grad(float d, const Log2eT& c) {
+  return sizeof(T) == 4 ? exp_t(d, c) : __builtin_amdgcn_exp2f(d * c.near);
+}
+
 struct Teacher {
   const void* a;
   const void* index;
@@ -94,50 +118,50 @@ __device__ __forceinline__ TeacherSums teacher_row(const Teacher& t, long long r
   return {1.0 / s, sx / s - log(s)};
 }
 
-// running maximum m and sum s of exp2((z - m) c)
-__device__ __forceinline__ void stats8(const float (&z)[8], float c, float& m, float& s) {
+// running maximum m and sum s of exp((z - m) / T)
+__device__ __forceinline__ void stats8(const float (&z)[8], const Log2eT& c, float& m, float& s) {
   float cm = z[0];
 #pragma unroll
   for (int e = 1; e < 8; ++e) cm = fmaxf(cm, z[e]);
   if (cm > m) {
-    s *= __builtin_amdgcn_exp2f((m - cm) * c);
+    s *= exp_t(m - cm, c);
     m = cm;
   }
 #pragma unroll
-  for (int e = 0; e < 8; ++e) s += __builtin_amdgcn_exp2f((z[e] - m) * c);
+  for (int e = 0; e < 8; ++e) s += exp_t(z[e] - m, c);
 }
 
-__device__ __forceinline__ void stats1(float z, float c, float& m, float& s) {
+__device__ __forceinline__ void stats1(float z, const Log2eT& c, float& m, float& s) {
   if (z > m) {
-    s *= __builtin_amdgcn_exp2f((m - z) * c);
+    s *= exp_t(m - z, c);
     m = z;
   }
-  s += __builtin_amdgcn_exp2f((z - m) * c);
+  s += exp_t(z - m, c);
 }
 
 // The waves' (m, s) joined, in two steps around the caller's barrier; the result is the same in every
 // thread.  A wave without elements, or with -inf alone, has s = 0 and m = -FLT_MAX (which, unlike
 // -inf, lets elements of -inf add exp2(-inf) = 0).
-__device__ __forceinline__ void stats_put(float m, float s, float c, float* wm, double* ws) {
+__device__ __forceinline__ void stats_put(float m, float s, const Log2eT& c, float* wm, double* ws) {
   const float M = wave_max_f32(m);
-  const double S = wave_sum_f64(s == 0.0f ? 0.0 : (double)s * (double)__builtin_amdgcn_exp2f((m - M) * c));
+  const double S = wave_sum_f64(s == 0.0f ? 0.0 : (double)s * (double)exp_t(m - M, c));
   if ((threadIdx.x & 63) == 0) {
     wm[threadIdx.x >> 6] = M;
     ws[threadIdx.x >> 6] = S;
   }
 }
 template <int TH>
-__device__ __forceinline__ void stats_get(float c, const float* wm, const double* ws, float& M, double& S) {
+__device__ __forceinline__ void stats_get(const Log2eT& c, const float* wm, const double* ws, float& M, double& S) {
   const int lane = threadIdx.x & 63;
   const float m = lane < TH / 64 ? wm[lane] : -__FLT_MAX__;
   const double s = lane < TH / 64 ? ws[lane] : 0.0;
   M = wave_max_f32(m);
-  S = wave_sum_f64(s == 0.0 ? 0.0 : s * (double)__builtin_amdgcn_exp2f((m - M) * c));
+  S = wave_sum_f64(s == 0.0 ? 0.0 : s * (double)exp_t(m - M, c));
 }
 
 // running (m, s) of this thread over elements lo .. hi - 1
 template <typename T, int TH>
-__device__ __forceinline__ void slice_stats(const T* z, int lo, int hi, float c, float& m, float& s) {
+__device__ __forceinline__ void slice_stats(const T* z, int lo, int hi, const Log2eT& c, float& m, float& s) {
   m = -__FLT_MAX__;
   s = 0.0f;
   int j = lo + 8 * (int)threadIdx.x;
@@ -206,14 +230,15 @@ __device__ __forceinline__ void lists_link(const int* idx, int top, unsigned* he
 }
 
 // g q of 8 elements
-__device__ __forceinline__ void grad8(const float (&v)[8], float m, float c, float gi, float (&o)[8]) {
+template <typename T>
+__device__ __forceinline__ void grad8(const float (&v)[8], float m, const Log2eT& c, float gi, float (&o)[8]) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) o[e] = __builtin_amdgcn_exp2f((v[e] - m) * c) * gi;
+  for (int e = 0; e < 8; ++e) o[e] = exp_grad<T>(v[e] - m, c) * gi;
 }
 
 // g q of elements lo .. hi - 1 (lo a multiple of 8)
 template <typename T, int TH>
-__device__ __forceinline__ void slice_grad(const T* z, T* d, int lo, int hi, float m, float c, float gi) {
+__device__ __forceinline__ void slice_grad(const T* z, T* d, int lo, int hi, float m, const Log2eT& c, float gi) {
   int j = lo + 8 * (int)threadIdx.x;
   constexpr int step = 8 * TH, U = 2;
   for (; (long long)j + (U - 1) * step + 8 <= hi; j += U * step) {
@@ -222,26 +247,26 @@ __device__ __forceinline__ void slice_grad(const T* z, T* d, int lo, int hi, flo
     for (int u = 0; u < U; ++u) load8(z + j + u * step, v[u]);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      grad8(v[u], m, c, gi, o);
+      grad8<T>(v[u], m, c, gi, o);
       store8(d + j + u * step, o);
     }
   }
   if ((long long)j + 8 <= hi) {
     float v[8], o[8];
     load8(z + j, v);
-    grad8(v, m, c, gi, o);
+    grad8<T>(v, m, c, gi, o);
     store8(d + j, o);
   }
   const int rest = hi & 7;
   if ((int)threadIdx.x < rest && hi > lo) {
     const int x = hi - rest + (int)threadIdx.x;
-    d[x] = (T)(__builtin_amdgcn_exp2f(((float)z[x] - m) * c) * gi);
+    d[x] = (T)(exp_grad<T>((float)z[x] - m, c) * gi);
   }
 }
 
 // the teacher's elements of lo .. hi - 1: g (q - p), p = pinv times the sum of e over equal indices
 template <typename T, int TH>
-__device__ __forceinline__ void teacher_grad(T* d, int lo, int hi, float m, float c, float g, float gi, double pinv,
+__device__ __forceinline__ void teacher_grad(T* d, int lo, int hi, float m, const Log2eT& c, float g, float gi, double pinv,
                                              int top, const int* idx, const float* ex, const float* zk,
                                              const unsigned short* heads, const unsigned short* next) {
   for (int k = threadIdx.x; k < top; k += TH) {
@@ -263,7 +288,7 @@ __device__ __forceinline__ void teacher_grad(T* d, int lo, int hi, float m, floa
       sum = ldexp((double)whole, -sh);
     }
     const float p = (float)(sum * pinv);
-    d[i] = (T)(__builtin_amdgcn_exp2f((zk[k] - m) * c) * gi - g * p);
+    d[i] = (T)(exp_t(zk[k] - m, c) * gi - g * p);
   }
 }
 
@@ -291,7 +316,7 @@ __device__ __forceinline__ void cross_sums(int lo, int hi, const int* idx, const
 
 // a slice's share of a split row, in the workspace
 struct Part {
-  double s;      // sum of exp2((z - m) c)
+  double s;      // sum of exp((z - m) / T)
   double mass;   // sums of e and of e (z - m) over the slice's teacher entries
   double cross;
   TeacherSums t;
@@ -308,14 +333,14 @@ __device__ __forceinline__ void write_loss(long long row, float w, float Tmp, co
 }
 
 // the parts of a row joined, the same in every lane of a wave
-__device__ __forceinline__ void join_parts(const Part* q, int slices, float c, float& m, double& S, double& cross) {
+__device__ __forceinline__ void join_parts(const Part* q, int slices, const Log2eT& c, float& m, double& S, double& cross) {
   const int lane = threadIdx.x & 63;
   m = -__FLT_MAX__;
   for (int i = lane; i < slices; i += 64) m = fmaxf(m, q[i].m);
   m = wave_max_f32(m);
   S = cross = 0.0;
   for (int i = lane; i < slices; i += 64) {
-    if (q[i].s != 0.0) S += q[i].s * (double)__builtin_amdgcn_exp2f((q[i].m - m) * c);
+    if (q[i].s != 0.0) S += q[i].s * (double)exp_t(q[i].m - m, c);
     if (q[i].mass != 0.0) cross += q[i].cross + q[i].mass * ((double)q[i].m - (double)m);
   }
   S = wave_sum_f64(S);
@@ -338,7 +363,7 @@ __global__ void __launch_bounds__(64) distill_join_kernel(const Part* __restrict
   }
   float m;
   double S, cross;
-  join_parts(parts + row * slices, slices, (float)(1.4426950408889634 / (double)Tmp), m, S, cross);
+  join_parts(parts + row * slices, slices, Log2eT(Tmp), m, S, cross);
   if (threadIdx.x == 0) write_loss(row, w, Tmp, parts[row * slices].t, cross, m, S, loss, stats);
 }
 
@@ -381,7 +406,7 @@ __global__ void __launch_bounds__(TH) distill_kernel(const T* Z, int V, long lon
     if (D) slice_zero<T, TH>(d, lo, hi);
     return;
   }
-  const float c = (float)(1.4426950408889634 / (double)Tmp);
+  const Log2eT c(Tmp);
   const double rT = 1.0 / (double)Tmp;
   constexpr int W = words8<T>();
   iv4 held[CH > 0 ? CH : 1][W];
@@ -454,10 +479,10 @@ __global__ void __launch_bounds__(TH) distill_kernel(const T* Z, int V, long lon
       for (int q = 0; q < W; ++q) asm volatile("" : "+v"(held[i][q]));
       float v[8], o[8];
       unpack8<T>(held[i], v);
-      grad8(v, m, c, gi, o);
+      grad8<T>(v, m, c, gi, o);
       if (j + 8 <= V) store8(d + j, o);
     }
-    if ((int)threadIdx.x < rest) d[V - rest + (int)threadIdx.x] = (T)(__builtin_amdgcn_exp2f((last - m) * c) * gi);
+    if ((int)threadIdx.x < rest) d[V - rest + (int)threadIdx.x] = (T)(exp_grad<T>(last - m, c) * gi);
   } else {
     slice_grad<T, TH>(z, d, lo, hi, m, c, gi);
   }

@@ -308,3 +308,36 @@ def test_small_teacher_probabilities_keep_their_bits(rows, vocab):
     check(None, z[:few], a[:few], i[:few], T, w[:few], grad_only=d[:few])
     for t in (*out, d):
         assert torch.equal(t, t[:few].repeat((rows + 15) // 16, *[1] * (t.dim() - 1))[:rows])
+
+
+def furthest_temperature():
+    """A temperature whose log2 e / T lies nearly half a step from the nearest fp32 number."""
+    t = np.float32(1.4426) + np.arange(300, dtype=np.float32) * np.float32(2.0**-23)
+    c = np.log2(np.e) / t.astype(np.float64)
+    return float(t[np.argmax(np.abs(c.astype(np.float32).astype(np.float64) / c - 1))])
+
+
+@pytest.mark.parametrize("rows,vocab", [(4, 300), (3, 9000), (1030, 300), (1030, 8205), (1026, 33001)])
+def test_exponents_lose_only_their_rounding(rows, vocab):
+    """Logits whose differences from the row's largest are exact, one of them far above the others, so
+    S = 1 + vocab e^-30 (its error is below eps).  The exponent y = (z - m) log2(e) / T then rounds once,
+    by 2^-24 |y|, which is 2^-24 |x| in its power.  Besides: exp2 2 eps, 1 / S, its product with w T, the
+    product with it and S's own rounding eps each, second orders: 8 eps.  A constant rounded to fp32 would
+    add up to eps |x|."""
+    T = furthest_temperature()
+    g = torch.Generator().manual_seed(rows + vocab)
+    base = -torch.randint(int(30 * 8 * 1.45), int(84 * 8 * 1.44), (16, vocab), generator=g).float() / 8
+    base[:, 5] = 0
+    z = base.repeat((rows + 15) // 16, 1)[:rows].contiguous()
+    w = 2.0**40
+    a, i = torch.zeros((rows, 1)), torch.full((rows, 1), 5, dtype=torch.int32)
+    zc, ac, ic, wc = z.cuda(), a.cuda(), i.cuda(), torch.full((rows,), w).cuda()
+    _, stats, d = erm.distill_loss(zc, ac, ic, T, wc, grad=True)
+    x = base[:rows].double() / T
+    q = x.exp() / x.exp().sum(1, keepdim=True)
+    tol = w * T * q * EPS * (x.abs() + 8)
+    for got in (d, erm.distill_grad(zc, stats, ac, ic, T, wc)):
+        off = (got[:16].cpu().double() - w * T * q).abs()
+        off[:, 5], tol[:, 5] = 0, 1
+        assert (off <= tol).all(), float((off / tol).max())
+        assert torch.equal(got, got[:16].repeat((rows + 15) // 16, 1)[:rows])
