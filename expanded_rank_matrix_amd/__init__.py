@@ -312,6 +312,7 @@ def apply_factors_grad(B, C, D, m: int, n: int, X, dY, need_dX: bool = True, nee
     on the stream without waiting."""
     import torch
 
+    _given(B=B, C=C, D=D, dY=dY)
     _require(D, torch.float32, "D")
     if D.dim() != 1:
         raise ValueError("D must be a vector of k scales")
@@ -362,6 +363,12 @@ def _apply_factors_grad(B, C, D, k, m, n, X, dY, batch, lead, need_dX, need_dD, 
         None if dX is None else dX.data_ptr(), None if dD is None else dD.data_ptr(),
         None if ws is None else ws.data_ptr(), stream))
     return dX, dD
+
+
+def _given(**tensors):
+    for name, t in tensors.items():
+        if t is None:
+            raise ValueError(f"{name} is missing")
 
 
 class _Run:
@@ -433,7 +440,7 @@ def _here(device, stream):
 def _rows(t, types, name, shape=None, device=None):
     """t as rows of the C ABI: a CUDA matrix of one of ``types`` whose rows are contiguous and do
     not overlap, on ``device`` and of exactly ``shape`` when given.  Returns its row distance."""
-    if not (t.is_cuda and t.dtype in types and t.dim() == 2):
+    if t is None or not (t.is_cuda and t.dtype in types and t.dim() == 2):
         raise ValueError(f"{name} must be a CUDA matrix of {' or '.join(map(str, types))}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
@@ -476,6 +483,7 @@ def _quantize_rows(X, x_type, ldx, out, stream):
         out = (torch.empty((rows, n), dtype=torch.int8, device=dev), torch.empty(rows, dtype=torch.float32, device=dev))
         ldq = n
     else:
+        _given(**{"out[1]": out[1]})
         ldq = _rows(out[0], (torch.int8,), "out[0]", shape=(rows, n), device=dev)
         _require(out[1], torch.float32, "out[1]", shape=(rows,), device=dev)
     Q, scale = out
@@ -492,6 +500,8 @@ def apply_quantized(W, w_scale, X, x_scale=None, out_dtype=None, stream=None, ou
     (fp32, fp16 or bf16; by default X's type, fp32 for int8 tokens).  The integer sum is exact; Y is
     rounded once.  Enqueued on the stream without waiting."""
     types = _types()
+    if X is None or w_scale is None:
+        _given(X=X, w_scale=w_scale)
     x_type = types.get(X.dtype)
     ldw = _rows(W, _INT8 or _int8(), "W")
     m, n = W.shape
@@ -559,6 +569,8 @@ def _distill_args(logits, teacher, index, weight, name, out):
     import torch
 
     types = _types()
+    if teacher is None or index is None:
+        _given(teacher=teacher, index=index)
     ldz = _rows(logits, _FLOAT, "logits")
     rows, vocab = logits.shape
     dev = logits.device
@@ -618,6 +630,7 @@ def distill_grad(logits, stats, teacher, index, temperature: float = 1.0, grad_l
     dlogits[r][v] = grad_loss[r] T (q[v] - sum of p_k with index_k = v), of logits' type; grad_loss
     (rows fp32, 1 where None) takes the weight's place, and a row where it is 0 is not read.  ``out``
     may be a preallocated tensor, or logits itself.  Enqueued on the stream without waiting."""
+    _given(stats=stats)
     z, t, ldd = _distill_args(logits, teacher, index, grad_loss, "grad_loss", out)
     _require(stats, _FLOAT[0], "stats", shape=(logits.shape[0], 2), device=logits.device)
     args = (logits, z, t, ldd, stats, temperature, grad_loss, out)

@@ -60,3 +60,9 @@ def test_binding_refuses_host_tensors():
         erm.distill_loss(z, t, i)
     with pytest.raises(ValueError):
         erm.distill_grad(z, torch.zeros((2, 2)), t, i)
+
+
+@pytest.mark.parametrize("entry, count", [(erm.distill_loss, 3), (erm.distill_grad, 4)])
+def test_missing_tensors_are_refused(entry, count):
+    with pytest.raises(ValueError):
+        entry(*[None] * count)

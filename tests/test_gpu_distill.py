@@ -341,3 +341,14 @@ def test_exponents_lose_only_their_rounding(rows, vocab):
         off[:, 5], tol[:, 5] = 0, 1
         assert (off <= tol).all(), float((off / tol).max())
         assert torch.equal(got, got[:16].repeat((rows + 15) // 16, 1)[:rows])
+
+
+def test_missing_tensors_are_refused():
+    z, a, i = (t.cuda() for t in make(3, 50, 4, torch.float32, 1))
+    stats = torch.zeros((3, 2), device="cuda")
+    for call in (lambda: erm.distill_loss(None, a, i), lambda: erm.distill_loss(z, None, i),
+                 lambda: erm.distill_loss(z, a, None), lambda: erm.distill_grad(z, None, a, i),
+                 lambda: erm.distill_grad(None, stats, a, i), lambda: erm.distill_grad(z, stats, None, i),
+                 lambda: erm.distill_grad(z, stats, a, None)):
+        with pytest.raises(ValueError):
+            call()

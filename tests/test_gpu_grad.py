@@ -299,3 +299,13 @@ def test_a_bad_vector_gives_nan(batch):
         bad[3] = v
         got = erm.apply_factors_grad(*f[:2], bad, m, n, Xc, Yc)
         assert torch.isnan(got[0]).all() and torch.equal(got[1], dD)
+
+
+def test_missing_tensors_are_refused():
+    B, C, D = device(*random_factors(np.random.default_rng(1), 30, 20, 25))
+    x, y = torch.zeros((4, 25), device="cuda"), torch.zeros((4, 20), device="cuda")
+    for f in ((None, C, D), (B, None, D), (B, C, None)):
+        with pytest.raises(ValueError):
+            erm.apply_factors_grad(*f, 20, 25, x, y)
+    with pytest.raises(ValueError):
+        erm.apply_factors_grad(B, C, D, 20, 25, x, None)

@@ -330,3 +330,13 @@ def test_product_of_more_tiles_than_a_launch_holds():
     for t in range(0, tokens, 1 << 24):
         total = (X[t:t + (1 << 24)].int() * W.int()).sum(1)  # below 2^19: exact in fp32
         assert torch.equal(y[t:t + (1 << 24), 0], total.float() * sw * sx[t:t + (1 << 24)]), t
+
+
+def test_missing_tensors_are_refused():
+    X, W, sw = torch.zeros((3, 16), device="cuda"), rand_i8(8, 16, 0).cuda(), torch.ones(8, device="cuda")
+    q = torch.empty((3, 16), dtype=torch.int8, device="cuda")
+    for call in (lambda: erm.quantize_rows(None), lambda: erm.quantize_rows(X, out=(q, None)),
+                 lambda: erm.quantize_rows(X, out=(None, sw[:3])), lambda: erm.apply_quantized(None, sw, X),
+                 lambda: erm.apply_quantized(W, None, X), lambda: erm.apply_quantized(W, sw, None)):
+        with pytest.raises(ValueError):
+            call()

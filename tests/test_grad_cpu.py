@@ -40,3 +40,8 @@ def test_binding_refuses_host_tensors():
     w = torch.zeros((3, 1), dtype=torch.int32)
     with pytest.raises(ValueError):
         erm.apply_factors_grad(w, w, torch.zeros(3), 4, 4, torch.zeros((2, 4)), torch.zeros((2, 4)))
+
+
+def test_missing_tensors_are_refused():
+    with pytest.raises(ValueError):
+        erm.apply_factors_grad(None, None, None, 4, 4, None, None)

@@ -64,3 +64,9 @@ def test_binding_refuses_host_tensors():
         erm.quantize_rows(x)
     with pytest.raises(ValueError):
         erm.apply_quantized(w, torch.zeros(4), x)
+
+
+@pytest.mark.parametrize("entry, count", [(erm.quantize_rows, 1), (erm.apply_quantized, 3)])
+def test_missing_tensors_are_refused(entry, count):
+    with pytest.raises(ValueError):
+        entry(*[None] * count)
