@@ -307,9 +307,10 @@ def apply_factors_grad(B, C, D, m: int, n: int, X, dY, need_dX: bool = True, nee
     dX = (C^T diag(D) B^T dY^T)^T and dD_i = sum over the batch of (C x)_i (B^T dy)_i.
 
     Returns (dX, dD) (fp32; dX of X's shape), None for one that is not needed (X may be None where
-    dD is not needed).  ``out`` may supply the pair.  A NaN or an infinity in a vector of dY gives NaN
-    in that vector of dX and throughout dD, one in X throughout dD, one in D throughout dX.  Enqueued
-    on the stream without waiting."""
+    dD is not needed).  ``out`` may supply the pair, which must not overlap the inputs
+    (dX may be X itself, or dY where m = n).  A NaN or an infinity in a vector of dY gives NaN in that
+    vector of dX and throughout dD, one in X throughout dD, one in D throughout dX.  Enqueued on the
+    stream without waiting."""
     import torch
 
     _given(B=B, C=C, D=D, dY=dY)

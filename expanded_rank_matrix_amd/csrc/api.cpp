@@ -599,6 +599,15 @@ int externd_distill_grad(const void* logits, int z_type, int64_t rows, int64_t v
 constexpr int64_t kMaxFactorSize = (int64_t)1 << 33;  // elements of a factor: a launch's threads
 constexpr int64_t kMaxFactorLen = (int64_t)1 << 23;  // 128 len < 2^31: a digit's sum fits int32
 
+struct Span {
+  const void* p;
+  int64_t bytes;
+};
+static bool meet(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.p && b.p && a.bytes > 0 && b.bytes > 0 && x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
+}
+
 int64_t externd_apply_factors_grad_workspace(int64_t k, int64_t m, int64_t n, int64_t batch) {
   if (k < 1 || m < 1 || n < 1 || k > kMaxFactorLen || m > kMaxFactorLen || n > kMaxFactorLen || batch < 0 ||
       batch > kMaxCount || k * m > kMaxFactorSize || k * n > kMaxFactorSize)
@@ -623,6 +632,16 @@ int externd_apply_factors_grad(const uint32_t* B_packed, const uint32_t* C_packe
   if (batch > 0 && (!dY || (dD && !X))) return fail(EXTERND_EINVAL, "null pointer argument");
   if (batch > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15)))
     return fail(EXTERND_EINVAL, "workspace of externd_apply_factors_grad_workspace() bytes, 16-byte aligned, is needed");
+  // An output over an input would be written by a launch that others of it still read.  dX in the place of
+  // the vectors is none: every way reads a pass's vectors in a launch before the one that writes theirs.
+  const Span in[] = {{B_packed, k * ((m + 15) / 16) * 4}, {C_packed, k * ((n + 15) / 16) * 4}, {D, k * 4},
+                     {X, batch * n * 4}, {dY, batch * m * 4}};
+  const Span gx{dX, batch * n * 4}, gd{dD, k * 4};
+  const bool over_x = dX && dX == X, over_dy = dX && dX == dY && m == n;
+  for (const Span& s : in)
+    if (meet(gd, s) || (meet(gx, s) && !(over_x && s.p == X) && !(over_dy && s.p == dY)))
+      return fail(EXTERND_EINVAL, "dX and dD must not overlap the inputs");
+  if (meet(gx, gd)) return fail(EXTERND_EINVAL, "dX and dD must not overlap");
   HIP_OR_FAIL(grad_run(B_packed, C_packed, D, (int)k, (int)m, (int)n, X, dY, batch, dX, dD, workspace,
                        reinterpret_cast<hipStream_t>(stream)));
   return EXTERND_OK;

@@ -303,7 +303,8 @@ int externd_distill_grad(const void* logits, int z_type, int64_t rows, int64_t v
  * work keeps t, u and D u in fp64), dD is summed in fp64 in a fixed order.  Deterministic.
  *   B_packed, C_packed, D   as externd_apply_factors
  *   X   batch x n fp32 (may be NULL where dD is)      dY  batch x m fp32
- *   dX  batch x n fp32, or NULL                       dD  k fp32, or NULL (0 for batch 0)
+ *   dX  batch x n fp32, or NULL                       dD  k fp32, or NULL (0 for batch 0); neither
+ *       overlaps the other or an input (EXTERND_EINVAL), but dX may be X itself, or dY where m = n
  *   workspace  externd_apply_factors_grad_workspace(k, m, n, batch) bytes, 16-byte aligned, used
  *              by this call alone until it has run
  * 1 <= k, m, n <= 2^23, k m and k n <= 2^33, 0 <= batch < 2^31.  A NaN or an infinity in a vector

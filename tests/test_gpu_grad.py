@@ -309,3 +309,21 @@ def test_missing_tensors_are_refused():
             erm.apply_factors_grad(*f, 20, 25, x, y)
     with pytest.raises(ValueError):
         erm.apply_factors_grad(B, C, D, 20, 25, x, None)
+
+
+@pytest.mark.parametrize("batch", [4, 300, 4300])
+def test_outputs_in_place_and_over_inputs(batch):
+    """dX may take the vectors' place, on every way through the kernels; other overlaps are refused."""
+    Bt, Ct, D, X, dY, dX, dD = run(130, 93, 93, batch, seed=6)
+    f = device(Bt, Ct, D)
+    for place in (0, 1):
+        v = [torch.from_numpy(t).cuda() for t in (X, dY)]
+        got = erm.apply_factors_grad(*f, 93, 93, *v, out=(v[place], torch.empty_like(dD)))
+        assert got[0] is v[place] and torch.equal(got[0], dX) and torch.equal(got[1], dD)
+    room = torch.zeros(batch * 93 + 93, device="cuda")
+    Xc, late = room[:-93].view(batch, 93), room[93:].view(batch, 93)
+    Yc = torch.from_numpy(dY).cuda()
+    for out in ((late, torch.empty_like(dD)), (torch.empty_like(dX), f[2]), (room[:-93].view(batch, 93), room[-130:])):
+        with pytest.raises(erm.ExterndError) as e:
+            erm.apply_factors_grad(*f, 93, 93, Xc, Yc, out=out)
+        assert e.value.status == erm.EINVAL

@@ -45,3 +45,12 @@ def test_binding_refuses_host_tensors():
 def test_missing_tensors_are_refused():
     with pytest.raises(ValueError):
         erm.apply_factors_grad(None, None, None, 4, 4, None, None)
+
+
+@pytest.mark.parametrize("change", [dict(dD=1 << 16), dict(dX=(1 << 16) + 28), dict(dX=(1 << 18) + 16), dict(dX=(1 << 18) - 28),
+                                    dict(dX=(1 << 19) + 28), dict(dD=(1 << 17) + 28), dict(dD=(1 << 20) + 4)])
+def test_outputs_over_inputs_are_refused(change):
+    """k = 8, m = n = 4, batch 2: B and C 32 bytes each, D 32, X, dY and dX 32, dD 32."""
+    at = dict(B=1 << 17, C=(1 << 17) + 64, D=1 << 16, X=1 << 18, dY=1 << 19, dX=1 << 20, dD=1 << 21)
+    assert grad(**{k: ctypes.c_void_p(v) for k, v in (at | change).items()}) == erm.EINVAL
+    assert "overlap" in erm.last_error()
