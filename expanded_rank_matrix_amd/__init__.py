@@ -597,8 +597,8 @@ def distill_loss(logits, teacher, index, temperature: float = 1.0, weight=None, 
     these types) and index (rows x top, int32 or int64; an entry outside the vocabulary, such as -1,
     or with a teacher logit of -inf does not count), weight (rows fp32; rows of weight 0 are not
     read).  Returns (loss fp32 rows, stats fp32 rows x 2); with ``grad`` or ``out`` also dlogits, the
-    gradient of the losses' sum, formed in the same call (``out`` may be a preallocated tensor, or
-    logits itself).  ``stats`` feeds ``distill_grad``.  Enqueued on the stream without waiting."""
+    gradient of the losses' sum, formed in the same call (``out`` may be a preallocated tensor apart
+    from logits, or logits itself).  ``stats`` feeds ``distill_grad``.  Enqueued on the stream without waiting."""
     args = (logits, *_distill_args(logits, teacher, index, weight, "weight", out), temperature, weight, grad, out)
     ptr = _here(logits.device, stream)
     if ptr is not None:
@@ -630,7 +630,7 @@ def distill_grad(logits, stats, teacher, index, temperature: float = 1.0, grad_l
     """The gradient of ``distill_loss`` from its ``stats`` on the same logits:
     dlogits[r][v] = grad_loss[r] T (q[v] - sum of p_k with index_k = v), of logits' type; grad_loss
     (rows fp32, 1 where None) takes the weight's place, and a row where it is 0 is not read.  ``out``
-    may be a preallocated tensor, or logits itself.  Enqueued on the stream without waiting."""
+    may be a preallocated tensor apart from logits, or logits itself.  Enqueued on the stream without waiting."""
     _given(stats=stats)
     z, t, ldd = _distill_args(logits, teacher, index, grad_loss, "grad_loss", out)
     _require(stats, _FLOAT[0], "stats", shape=(logits.shape[0], 2), device=logits.device)

@@ -487,6 +487,26 @@ constexpr int64_t kMaxProductLen = 131071; // 128 128 n < 2^31: the sum of produ
 constexpr int64_t kMaxChannels = (int64_t)1 << 26;
 constexpr int64_t kMaxLd = (int64_t)1 << 40;
 
+// `rows` rows of `len` bytes, `pitch` bytes apart.
+struct Rows {
+  const void* p;
+  int64_t rows, len, pitch;
+};
+static Rows dense(const void* p, int64_t bytes) { return {p, 1, bytes, bytes}; }
+// Whether two arguments share memory: an output over an input is written by workgroups, or by a launch,
+// that others of the call still read.  Rows of one pitch may lie side by side; of two pitches, any meeting
+// of the whole counts.
+static bool meet(const Rows& a, const Rows& b) {
+  if (!a.p || !b.p || a.rows * a.len == 0 || b.rows * b.len == 0) return false;
+  const __int128 x = (__int128)reinterpret_cast<uintptr_t>(a.p), y = (__int128)reinterpret_cast<uintptr_t>(b.p);
+  const __int128 xe = x + (__int128)(a.rows - 1) * a.pitch + a.len, ye = y + (__int128)(b.rows - 1) * b.pitch + b.len;
+  if (xe <= y || ye <= x) return false;
+  if (a.rows == 1 ? b.rows == 1 : b.rows > 1 && a.pitch != b.pitch) return true;
+  const int64_t pitch = a.rows > 1 ? a.pitch : b.pitch;
+  const __int128 at = ((y - x) % pitch + pitch) % pitch;  // where a row of b starts among a's
+  return at < a.len || at > pitch - b.len;
+}
+
 int externd_quantize_rows(const void* X, int x_type, int64_t rows, int64_t n, int64_t ldx, int8_t* Q, int64_t ldq,
                           float* scale, void* stream) {
   g_last_error.clear();
@@ -570,6 +590,9 @@ int externd_distill_loss(const void* logits, int z_type, int64_t rows, int64_t v
   if (rc == 1) return EXTERND_OK;
   if (!loss || !stats) return fail(EXTERND_EINVAL, "null pointer argument");
   if (dlogits == logits && ldd != ldz) return fail(EXTERND_EINVAL, "a gradient in the logits' place needs ldd = ldz");
+  const int64_t es = z_type == EXTERND_F32 ? 4 : 2;
+  if (dlogits != logits && meet({logits, rows, vocab * es, ldz * es}, {dlogits, rows, vocab * es, ldd * es}))
+    return fail(EXTERND_EINVAL, "the gradient must be apart from the logits or in their place");
   if (distill_workspace_bytes(rows, (int)vocab) > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15)))
     return fail(EXTERND_EINVAL, "workspace of externd_distill_workspace() bytes, 16-byte aligned, is needed");
   const DistillLaunch L{logits, teacher, index, weight, loss, stats, dlogits, workspace, rows, ldz, ldd,
@@ -588,6 +611,9 @@ int externd_distill_grad(const void* logits, int z_type, int64_t rows, int64_t v
   if (rc == 1) return EXTERND_OK;
   if (!stats || !dlogits) return fail(EXTERND_EINVAL, "null pointer argument");
   if (dlogits == logits && ldd != ldz) return fail(EXTERND_EINVAL, "a gradient in the logits' place needs ldd = ldz");
+  const int64_t es = z_type == EXTERND_F32 ? 4 : 2;
+  if (dlogits != logits && meet({logits, rows, vocab * es, ldz * es}, {dlogits, rows, vocab * es, ldd * es}))
+    return fail(EXTERND_EINVAL, "the gradient must be apart from the logits or in their place");
   const DistillLaunch L{logits, teacher, index, grad_loss, nullptr, const_cast<float*>(stats), dlogits, nullptr, rows, ldz,
                         ldd, (int)vocab, (int)top, z_type, t_type, index_bytes, temperature};
   HIP_OR_FAIL(distill_run(L, reinterpret_cast<hipStream_t>(stream)));
@@ -598,15 +624,6 @@ int externd_distill_grad(const void* logits, int z_type, int64_t rows, int64_t v
 
 constexpr int64_t kMaxFactorSize = (int64_t)1 << 33;  // elements of a factor: a launch's threads
 constexpr int64_t kMaxFactorLen = (int64_t)1 << 23;  // 128 len < 2^31: a digit's sum fits int32
-
-struct Span {
-  const void* p;
-  int64_t bytes;
-};
-static bool meet(const Span& a, const Span& b) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-  return a.p && b.p && a.bytes > 0 && b.bytes > 0 && x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
-}
 
 int64_t externd_apply_factors_grad_workspace(int64_t k, int64_t m, int64_t n, int64_t batch) {
   if (k < 1 || m < 1 || n < 1 || k > kMaxFactorLen || m > kMaxFactorLen || n > kMaxFactorLen || batch < 0 ||
@@ -634,11 +651,11 @@ int externd_apply_factors_grad(const uint32_t* B_packed, const uint32_t* C_packe
     return fail(EXTERND_EINVAL, "workspace of externd_apply_factors_grad_workspace() bytes, 16-byte aligned, is needed");
   // An output over an input would be written by a launch that others of it still read.  dX in the place of
   // the vectors is none: every way reads a pass's vectors in a launch before the one that writes theirs.
-  const Span in[] = {{B_packed, k * ((m + 15) / 16) * 4}, {C_packed, k * ((n + 15) / 16) * 4}, {D, k * 4},
-                     {X, batch * n * 4}, {dY, batch * m * 4}};
-  const Span gx{dX, batch * n * 4}, gd{dD, k * 4};
+  const Rows in[] = {dense(B_packed, k * ((m + 15) / 16) * 4), dense(C_packed, k * ((n + 15) / 16) * 4), dense(D, k * 4),
+                     dense(X, batch * n * 4), dense(dY, batch * m * 4)};
+  const Rows gx = dense(dX, batch * n * 4), gd = dense(dD, k * 4);
   const bool over_x = dX && dX == X, over_dy = dX && dX == dY && m == n;
-  for (const Span& s : in)
+  for (const Rows& s : in)
     if (meet(gd, s) || (meet(gx, s) && !(over_x && s.p == X) && !(over_dy && s.p == dY)))
       return fail(EXTERND_EINVAL, "dX and dD must not overlap the inputs");
   if (meet(gx, gd)) return fail(EXTERND_EINVAL, "dX and dD must not overlap");

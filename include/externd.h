@@ -271,7 +271,8 @@ int64_t externd_apply_quantized_workspace(int x_type, int64_t tokens, int64_t n,
  *                the vocabulary, for externd_distill_grad
  *   dlogits      NULL, or rows x vocab of z_type, row distance ldd: the gradient of the losses' sum,
  *                  weight T (q[v] - sum of p_k with index[k] = v),  0 in rows without valid entry.
- *                It may be logits itself (with ldd = ldz), and must not overlap it otherwise.
+ *                It may be logits itself (with ldd = ldz), and must not overlap it otherwise
+ *                (EXTERND_EINVAL).
  *   workspace    externd_distill_workspace(rows, vocab) bytes, 16-byte aligned (NULL where that is
  *                0), used by this call alone until it has run
  * Statistics, sums and losses are kept in fp32 and fp64 as the row is read once; the gradient is

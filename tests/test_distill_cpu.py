@@ -66,3 +66,13 @@ def test_binding_refuses_host_tensors():
 def test_missing_tensors_are_refused(entry, count):
     with pytest.raises(ValueError):
         entry(*[None] * count)
+
+
+# 4 rows of 100 fp32 (ldz 100: bytes 65536 .. 67135; ldz 250: rows 1000 bytes apart)
+@pytest.mark.parametrize("at, ldz, ldd", [(65540, 100, 100), (67132, 100, 100), (65536 - 1596, 100, 100), (65536 + 400, 100, 100),
+                                          (65536 + 396, 250, 250), (65536 - 396, 250, 250), (65536 + 604, 250, 250),
+                                          (65536 + 2004, 250, 250), (65536 + 400, 250, 300), (65536, 250, 300)])
+def test_gradient_over_the_logits_is_refused(at, ldz, ldd):
+    z, d = ctypes.c_void_p(65536), ctypes.c_void_p(at)
+    assert loss(z=z, ldz=ldz, d=d, ldd=ldd) == erm.EINVAL and "logits" in erm.last_error()
+    assert grad(z=z, ldz=ldz, d=d, ldd=ldd) == erm.EINVAL and "logits" in erm.last_error()

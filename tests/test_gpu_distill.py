@@ -352,3 +352,20 @@ def test_missing_tensors_are_refused():
                  lambda: erm.distill_grad(z, stats, a, None)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_gradient_beside_the_logits_and_over_them():
+    """Both as columns of one matrix, and a single row; a shifted overlap is refused."""
+    for rows in (1, 3, 1100):
+        z, a, i = make(rows, 301, 12, torch.bfloat16, 8)
+        room = torch.zeros((rows, 602), dtype=torch.bfloat16, device="cuda")
+        room[:, :301] = z.cuda()
+        want = erm.distill_loss(z.cuda(), a.cuda(), i.cuda(), grad=True)
+        for x, y in zip(erm.distill_loss(room[:, :301], a.cuda(), i.cuda(), out=room[:, 301:]), want):
+            assert torch.equal(x, y)
+        assert torch.equal(room[:, :301], z.cuda())
+        with pytest.raises(erm.ExterndError):
+            erm.distill_loss(room[:, :301], a.cuda(), i.cuda(), out=room[:, 300:601])
+        erm.distill_grad(room[:, 301:], want[1], a.cuda(), i.cuda(), out=room[:, :301])
+        with pytest.raises(erm.ExterndError):
+            erm.distill_grad(room[:, 301:], want[1], a.cuda(), i.cuda(), out=room[:, 1:302])
