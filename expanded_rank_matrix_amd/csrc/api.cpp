@@ -517,6 +517,9 @@ int externd_quantize_rows(const void* X, int x_type, int64_t rows, int64_t n, in
     return fail(EXTERND_EINVAL, "ldx and ldq must be at least n (and at most 2^40)");
   if (rows == 0) return EXTERND_OK;
   if (!X || !Q || !scale) return fail(EXTERND_EINVAL, "null pointer argument");
+  const int64_t es = x_type == EXTERND_F32 ? 4 : 2;
+  const Rows in{X, rows, n * es, ldx * es}, out{Q, rows, n, ldq}, sc = dense(scale, rows * 4);
+  if (meet(out, in) || meet(sc, in) || meet(sc, out)) return fail(EXTERND_EINVAL, "Q and scale must not overlap X or each other");
   HIP_OR_FAIL(quantize_run(X, x_type, rows, (int)n, ldx, Q, ldq, (int)n, scale, reinterpret_cast<hipStream_t>(stream)));
   return EXTERND_OK;
 }
@@ -547,6 +550,11 @@ int externd_apply_quantized(const int8_t* W, const float* w_scale, int64_t m, in
     return fail(EXTERND_EINVAL, "x_scale is given with x_type EXTERND_I8 and only then");
   if (product_workspace_bytes(x_type, tokens, (int)n, (int)m) > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15)))
     return fail(EXTERND_EINVAL, "workspace of externd_apply_quantized_workspace() bytes, 16-byte aligned, is needed");
+  const int64_t xs = x_type == EXTERND_F32 ? 4 : x_type == EXTERND_I8 ? 1 : 2, ys = y_type == EXTERND_F32 ? 4 : 2;
+  const Rows out{Y, tokens, m * ys, ldy * ys};
+  if (meet(out, {X, tokens, n * xs, ldx * xs}) || meet(out, {W, m, n, ldw}) || meet(out, dense(w_scale, m * 4)) ||
+      meet(out, dense(x_scale, x_scale ? tokens * 4 : 0)))
+    return fail(EXTERND_EINVAL, "Y must not overlap the inputs");
   HIP_OR_FAIL(product_run(W, w_scale, (int)m, (int)n, ldw, X, x_type, x_scale, (int)tokens, ldx, Y, y_type, ldy,
                           workspace, reinterpret_cast<hipStream_t>(stream)));
   return EXTERND_OK;

@@ -224,6 +224,7 @@ int externd_apply_factors_static(const uint32_t* B_packed, const uint32_t* C_pac
  *   X      rows x n of x_type (EXTERND_F32, _F16 or _BF16), row distance ldx
  *   Q      rows x n int8, row distance ldq
  *   scale  rows fp32
+ * Q and scale must not overlap X or each other (EXTERND_EINVAL).
  * 0 <= rows < 2^31, 1 <= n < 2^31 - 4096. */
 int externd_quantize_rows(const void* X, int x_type, int64_t rows, int64_t n, int64_t ldx, int8_t* Q, int64_t ldq,
                           float* scale, void* stream);
@@ -238,7 +239,8 @@ int externd_quantize_rows(const void* X, int x_type, int64_t rows, int64_t n, in
  *            or EXTERND_F32, _F16, _BF16 with x_scale NULL: the tokens are then quantised on the
  *            way exactly as externd_quantize_rows does (a token with a NaN or an infinity gives a
  *            row of NaN)
- *   Y        tokens x m of y_type (EXTERND_F32, _F16 or _BF16), row distance ldy
+ *   Y        tokens x m of y_type (EXTERND_F32, _F16 or _BF16), row distance ldy; must not overlap the
+ *            inputs (EXTERND_EINVAL)
  *   workspace  externd_apply_quantized_workspace(x_type, tokens, n, m) bytes, 16-byte aligned (NULL
  *            where that is 0), used by this call alone until it has run
  * 0 <= tokens < 2^31, 1 <= m <= 2^26, 1 <= n <= 131071 (the largest n whose sum of products of

@@ -340,3 +340,21 @@ def test_missing_tensors_are_refused():
                  lambda: erm.apply_quantized(W, None, X), lambda: erm.apply_quantized(W, sw, None)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_outputs_beside_the_inputs_and_over_them():
+    """X and Y as columns of one matrix (rows of one pitch) stay allowed; an output over an input is not."""
+    for tokens in (1, 5, 40):
+        room = torch.zeros((tokens, 500), dtype=torch.bfloat16, device="cuda")
+        x = rand(tokens, 250, torch.bfloat16, tokens).cuda()
+        room[:, :250] = x
+        W, sw = rand_i8(250, 250, 1).cuda(), torch.rand(250, device="cuda")
+        y = erm.apply_quantized(W, sw, room[:, :250], out=room[:, 250:])
+        assert torch.equal(y, erm.apply_quantized(W, sw, x)) and torch.equal(room[:, :250], x)
+        q = room.view(torch.int8)[:, 500:750]
+        erm.quantize_rows(room[:, :250], out=(q, torch.empty(tokens, device="cuda")))
+        assert torch.equal(q, erm.quantize_rows(x)[0]) and torch.equal(room[:, :250], x)
+        for call in (lambda: erm.apply_quantized(W, sw, x, out=x), lambda: erm.apply_quantized(W, sw, room[:, :250], out=room[:, 249:499]),
+                     lambda: erm.quantize_rows(x, out=(x.view(torch.int8)[:, :250], torch.empty(tokens, device="cuda")))):
+            with pytest.raises(erm.ExterndError):
+                call()

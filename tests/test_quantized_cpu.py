@@ -70,3 +70,21 @@ def test_binding_refuses_host_tensors():
 def test_missing_tensors_are_refused(entry, count):
     with pytest.raises(ValueError):
         entry(*[None] * count)
+
+
+@pytest.mark.parametrize("at, ldq", [(65536, 8), (65536 + 127, 8), (65536 - 31, 8), (65536 + 64, 64), (65536 + 33, 40)])
+def test_quantize_over_its_rows_is_refused(at, ldq):
+    """4 rows of 8 fp32: bytes 65536 .. 65663 (ldx 8), or rows of 32 of every 64 bytes (ldx 16)."""
+    p = ctypes.c_void_p
+    ldx = 16 if ldq == 64 else 8
+    assert quantize(X=p(65536), Q=p(at), ldx=ldx, ldq=ldq, scale=p(1 << 20)) == erm.EINVAL and "overlap" in erm.last_error()
+    assert quantize(X=p(1 << 18), Q=p(at), scale=p(at + 20)) == erm.EINVAL and "overlap" in erm.last_error()
+    assert quantize(X=p(65536), Q=p(1 << 20), scale=p(65536 + 124)) == erm.EINVAL and "overlap" in erm.last_error()
+
+
+@pytest.mark.parametrize("at", [65536 + 71, (1 << 17) + 28, (1 << 18) + 12, (1 << 19) + 32, (1 << 17) - 140])
+def test_product_over_its_inputs_is_refused(at):
+    """9 tokens of 8 codes by 4 channels: X 72 bytes, W 32, its scales 16, the tokens' 36, Y 144."""
+    p = ctypes.c_void_p
+    rc = product(X=p(65536), W=p(1 << 17), sw=p(1 << 18), sx=p(1 << 19), Y=p(at))
+    assert rc == erm.EINVAL and "overlap" in erm.last_error()
