@@ -331,6 +331,12 @@ def main():
     ap.add_argument("--probe", action="store_true", help="bandwidth probe only")
     ap.add_argument("--oracle-timings", action="store_true", help="oracle timings only (host)")
     args = ap.parse_args()
+    if args.int8 and not args.infer:
+        ap.error("--int8 is a way of --infer")
+    if args.int8 and args.static:
+        ap.error("--static is a way of the factors' inference, not of --int8")
+    if args.infer and args.repair:
+        ap.error("--infer and --repair exclude each other")
     if args.oracle_timings:
         oracle_timings()
         return
