@@ -461,8 +461,8 @@ def _rows(t, types, name, shape=None, device=None):
 def quantize_rows(X, stream=None, out=None):
     """Rows of X (rows x n, fp32, fp16 or bf16, device; rows may be strided) to 8-bit integers with
     one scale a row: scale = max |x| / 127 and Q the whole numbers nearest to 127 x / max |x|, ties
-    to even.  Returns (Q int8 rows x n, scale fp32 rows); ``out`` may supply that pair (Q's rows may
-    be strided), apart from X.  A row of zeros gets scale 0, one with a NaN or an infinity scale NaN; both get
+    to even.  Returns (Q int8 rows x n, scale fp32 rows); ``out`` may supply that pair, apart from X
+    (Q's rows may be strided).  A row of zeros gets scale 0, one with a NaN or an infinity scale NaN; both get
     zeros.  Quantises the weights of ``apply_quantized`` (rows are output channels) and tokens that
     several products share.  Enqueued on the stream without waiting."""
     types = _types()
@@ -497,10 +497,10 @@ def apply_quantized(W, w_scale, X, x_scale=None, out_dtype=None, stream=None, ou
     ``apply_factors`` for the layers that stay unfactored.  W (m x n int8) and w_scale (m fp32) are
     as ``quantize_rows`` gives them.  X (n or tokens x n) is int8 with x_scale (tokens fp32), or
     fp32, fp16 or bf16 without it: its tokens are then quantised on the way as ``quantize_rows``
-    does.  W, X and ``out`` may have strided rows; ``out`` lies
-    apart from the inputs.  Returns Y (m or tokens x m) of ``out_dtype``
-    (fp32, fp16 or bf16; by default X's type, fp32 for int8 tokens).  The integer sum is exact; Y is
-    rounded once.  Enqueued on the stream without waiting."""
+    does.  W, X and ``out`` may have strided rows; ``out`` lies apart from the inputs.  Returns Y (m or
+    tokens x m) of ``out_dtype`` (fp32, fp16 or bf16; by default X's type, fp32 for int8 tokens).  The
+    integer sum is exact; its conversion and the two scales round in fp32, then Y's type does.
+    Enqueued on the stream without waiting."""
     types = _types()
     if X is None or w_scale is None:
         _given(X=X, w_scale=w_scale)
