@@ -369,3 +369,93 @@ def test_gradient_beside_the_logits_and_over_them():
         erm.distill_grad(room[:, 301:], want[1], a.cuda(), i.cuda(), out=room[:, :301])
         with pytest.raises(erm.ExterndError):
             erm.distill_grad(room[:, 301:], want[1], a.cuda(), i.cuda(), out=room[:, 1:302])
+
+
+# rows held in registers between the passes: at least 1024 rows and a gradient, each number of threads and chunks
+HELD = [("f32", 8205), ("f16", 16389), ("bf16", 33001), ("f32", 33001), ("f16", 66003)]
+
+
+def spread(rows, vocab, top, dtype, seed):
+    """`rows` rows that repeat 24 different ones."""
+    z, a, i = make(24, vocab, top, dtype, seed)
+    return z, a, i, torch.arange(rows) % 24
+
+
+@pytest.mark.parametrize("dtype,vocab", HELD)
+def test_held_rows_with_masks_weights_and_bad_lists(dtype, vocab):
+    rows, T = 1030, 1.5
+    z, a, i, pick = spread(rows, vocab, 40, TYPES[dtype], vocab)
+    last = torch.arange(vocab) >= vocab - vocab % 8
+    i[0] = -1                                                # no entry
+    a[1] = -float("inf")                                     # entries, none with a logit
+    i[2, 3], i[2, 4], i[2, 5] = vocab, 2**31 - 1, -(2**31)
+    i[3] = i[3, 0]                                           # one index 40 times
+    i[4, 1::2] = i[4, 0::2]                                  # each twice
+    free = torch.ones((24, vocab), dtype=torch.bool).scatter_(1, i.clamp(0, vocab - 1).long(), False)
+    z[5][free[5]] = -float("inf")
+    z[6][free[6]] = torch.finfo(TYPES[dtype]).min
+    z[7, :] = torch.finfo(TYPES[dtype]).min
+    z[8][free[8] & last] = -float("inf")                     # the row's end masked, and all but it
+    z[9][free[9] & ~last] = -float("inf")
+    a[10, 3:9] = -float("inf")
+    w = torch.rand(24, generator=torch.Generator().manual_seed(1)) * 3 - 1
+    w[11] = 0
+    z[11, 5] = float("nan")                                  # not read
+    good = [r for r in range(24) if r != 11]
+    zc, ac, ic, wc = (t[pick].contiguous().cuda() for t in (z, a, i, w))
+    out = erm.distill_loss(zc, ac, ic, T, wc, grad=True)
+    d = erm.distill_grad(zc, out[1], ac, ic, T, wc)
+    check([t[:24][good] for t in out], z[good], a[good], i[good], T, w[good])
+    check(None, z[good], a[good], i[good], T, w[good], grad_only=d[:24][good])
+    for t in (*out, d):
+        assert not t[11].any()
+        assert torch.equal(t, t[:24][pick.cuda()])
+    assert not out[2][0].any() and not out[2][1].any() and out[0][0] == 0 and not out[2][5].cpu()[free[5]].any()
+    same = erm.distill_loss(zc, ac, ic, T, wc, out=zc)       # in the logits' place
+    for x, y in zip(same, out):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("dtype,vocab", HELD)
+def test_held_rows_with_nan_and_infinity(dtype, vocab):
+    z, a, i, pick = spread(1030, vocab, 9, TYPES[dtype], vocab + 1)
+    plain = erm.distill_loss(*(t[pick].contiguous().cuda() for t in (z, a, i)), grad=True)
+    z[0, 7], z[1, vocab - 1], z[2, 7], z[3, :] = float("nan"), float("nan"), float("inf"), -float("inf")
+    a[4, 2], a[5, 2] = float("nan"), float("inf")
+    z[6, i[6, 0]] = -float("inf")                            # the student gives a wanted token nothing
+    out = erm.distill_loss(*(t[pick].contiguous().cuda() for t in (z, a, i)), grad=True)
+    loss, stats, d = (t[:24] for t in out)
+    assert torch.isnan(loss[:6]).all() and loss[6] == float("inf")
+    assert torch.isnan(d[:4]).all() and torch.isnan(d[4:6]).any(1).all() and torch.isfinite(d[6:]).all()
+    for x, y in zip(out, plain):
+        assert torch.equal(x[7:24], y[7:24])
+        assert torch.equal(torch.nan_to_num(x, 5.0), torch.nan_to_num(x[:24][pick.cuda()], 5.0))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_vocabularies_past_the_held_ones(dtype):
+    """Over 131072 logits of 16 bits or 65536 of fp32 the rows stream twice."""
+    z, a, i, pick = spread(1025, 140003, 70, TYPES[dtype], 5)
+    zc, ac, ic = (t[pick].contiguous().cuda() for t in (z, a, i))
+    out = erm.distill_loss(zc, ac, ic, 1.5, grad=True)
+    d = erm.distill_grad(zc, out[1], ac, ic, 1.5)
+    check([t[:24] for t in out], z, a, i, 1.5)
+    check(None, z, a, i, 1.5, grad_only=d[:24])
+    for t in (*out, d):
+        assert torch.equal(t, t[:24][pick.cuda()])
+
+
+def test_more_rows_than_a_launch():
+    """2^21 + 3 rows: the last three are a launch of their own."""
+    rows = 2**21 + 3
+    z, a, i = make(4096, 5, 2, torch.float32, 3)
+    pick = torch.arange(rows) % 4093
+    w = torch.rand(rows, generator=torch.Generator().manual_seed(2))
+    zc, ac, ic, wc = (t.contiguous().cuda() for t in (z[pick], a[pick], i[pick], w))
+    out = erm.distill_loss(zc, ac, ic, 2.0, wc, grad=True)
+    d = erm.distill_grad(zc, out[1], ac, ic, 2.0, wc)
+    for s in (slice(0, 50), slice(2**21 - 20, rows)):
+        check([t[s] for t in out], z[pick[s]], a[pick[s]], i[pick[s]], 2.0, w[s])
+        check(None, z[pick[s]], a[pick[s]], i[pick[s]], 2.0, w[s], grad_only=d[s])
+    one = erm.distill_loss(zc, ac, ic, 2.0)
+    assert torch.equal(one[0][:4093], one[0][4093:8186]) and torch.equal(one[1][pick[-3:]], one[1][-3:])

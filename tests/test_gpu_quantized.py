@@ -358,3 +358,19 @@ def test_outputs_beside_the_inputs_and_over_them():
                      lambda: erm.quantize_rows(x, out=(x.view(torch.int8)[:, :250], torch.empty(tokens, device="cuda")))):
             with pytest.raises(erm.ExterndError):
                 call()
+
+
+def test_more_rows_than_a_launch():
+    """Quantisation runs of 2^23 rows; runs of 65535 groups of 32 tokens of rows too short for tiles."""
+    rows = 2**23 + 3
+    x = rand(4096, 3, torch.float32, 1)
+    pick = torch.arange(rows) % 4093
+    q, s = erm.quantize_rows(x[pick].cuda())
+    wq, ws = quantized(x)
+    assert torch.equal(q.cpu(), wq[pick]) and torch.equal(s.cpu(), ws[pick])
+    tokens = 32 * 65535 + 5
+    X, W, sw = rand_i8(4096, 7, 2), rand_i8(3, 7, 3), torch.rand(3)
+    pick = torch.arange(tokens) % 4093
+    sx = torch.rand(tokens)
+    y = erm.apply_quantized(W.cuda(), sw.cuda(), X[pick].cuda(), sx.cuda())
+    close(y, (X.double() @ W.double().t())[pick] * sx.double()[:, None] * sw.double(), torch.float32)
