@@ -96,19 +96,24 @@ __device__ __forceinline__ void widen_t(const uint32_t* __restrict__ P, int k, i
   }
 }
 
-// 16 words of 16 codes: bits 2 i of word j <-> bits 2 j of word i
+// 16 words of 16 codes: bits 2 i of word j <-> bits 2 j of word i.  Step S swaps the off-diagonal blocks of
+// S words by S codes.
+template <int S>
+__device__ __forceinline__ void transpose_step(unsigned (&w)[16]) {
+  constexpr unsigned mask = S == 8 ? 0x0000FFFFu : S == 4 ? 0x00FF00FFu : S == 2 ? 0x0F0F0F0Fu : 0x33333333u;
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (!(i & S)) {
+      const unsigned x = (w[i] >> 2 * S ^ w[i + S]) & mask;
+      w[i + S] ^= x;
+      w[i] ^= x << 2 * S;
+    }
+}
 __device__ __forceinline__ void transpose_codes(unsigned (&w)[16]) {
-#pragma unroll
-  for (int s = 8; s >= 1; s >>= 1) {
-    const unsigned mask = s == 8 ? 0x0000FFFFu : s == 4 ? 0x00FF00FFu : s == 2 ? 0x0F0F0F0Fu : 0x33333333u;
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (!(i & s)) {
-        const unsigned x = (w[i] >> 2 * s ^ w[i + s]) & mask;
-        w[i + s] ^= x;
-        w[i] ^= x << 2 * s;
-      }
-  }
+  transpose_step<8>(w);
+  transpose_step<4>(w);
+  transpose_step<2>(w);
+  transpose_step<1>(w);
 }
 
 // packed rows -> the packed transpose: word i / 16 of row j of out (kw words) holds code j of 16 rows i,
