@@ -1,4 +1,4 @@
-// Element types of the entry points that take more than fp32, and unaligned 16-byte access.
+// Vector types, and unaligned 16-byte access to the element types fp32, fp16 and bf16.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -12,22 +12,6 @@ typedef float fv4 __attribute__((ext_vector_type(4)));
 // alignment, so rows of odd length need no path of their own.
 typedef int iv4_any __attribute__((ext_vector_type(4), aligned(1)));
 typedef int iv2_any __attribute__((ext_vector_type(2), aligned(1)));
-
-// Element types by their number in the C ABI (EXTERND_F32, EXTERND_F16, EXTERND_BF16).
-template <int TYPE>
-struct Elem;
-template <>
-struct Elem<0> {
-  typedef float type;
-};
-template <>
-struct Elem<1> {
-  typedef _Float16 type;
-};
-template <>
-struct Elem<2> {
-  typedef __bf16 type;
-};
 
 // 8 consecutive elements as fp32
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
