@@ -491,8 +491,8 @@ __global__ void __launch_bounds__(TH) distill_kernel(const T* Z, int V, long lon
                       reinterpret_cast<const unsigned short*>(heads), next);
 }
 
-// Slices of a row, so that few rows fill the card: about four workgroups a CU, none with less than
-// 4096 elements.
+// Slices of a row, so that few rows fill the card: about four workgroups a CU, each of 4096 elements or
+// more but the row's last, which takes what is left (4097 elements: 4096 and 1).
 static void split(long long rows, int V, int* slices, int* slice) {
   long long s = (1024 + rows - 1) / rows;
   const long long most = (V + 4095) / 4096;

@@ -149,7 +149,7 @@ __device__ __forceinline__ void digits4(const float (&x)[4], int sh, unsigned (&
 
 // One vector a workgroup: x (times D where given) -> digit rows 4 b .. 4 b + 3 of np bytes, and the
 // exponent E - 30 of its image's unit.  TILED: the rows of four vectors in the order in which a wave's
-// MFMA operands take them, 1 KB a load (codes_kernel): of 256 columns the 16-byte pieces
+// MFMA operands take them, 1 KB a load (codes_sums): of 256 columns the 16-byte pieces
 // [piece & 3][piece >> 2][row & 15].
 template <int TH, bool TILED>
 __device__ __forceinline__ void digits(const float* __restrict__ X, long long n, const float* __restrict__ D, long long b,

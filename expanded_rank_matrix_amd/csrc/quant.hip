@@ -18,8 +18,8 @@ namespace externd {
 // q = rint(127 x / a) of the exact quotient.  The fp32 estimate x fl(127 / a) is off by less than
 // 127 2^-22.9 < 2^-15: only an estimate that close to a border between two whole numbers can round
 // to the wrong side, and those few are redone in fp64, whose rounded quotient is never on the wrong
-// side: 254 x and (2 q + 1) a are 32-bit integers times a power of two, so a quotient that is no
-// tie is at least 2^-25 from one.
+// side: in units of x's last place 254 x and (2 q + 1) a are whole numbers, the first below 2^32, so a
+// quotient that is no tie differs from the border by at least 2^-32 of it, and fp64's is good to 2^-53.
 __device__ __forceinline__ int quant1(float x, float inv, float a) {
   const float r = x * inv;
   float q = rintf(r);
