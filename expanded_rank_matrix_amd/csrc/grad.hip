@@ -271,7 +271,7 @@ struct JoinDigits {
   const int* ex;
   float* out;
   long long ld;
-  static constexpr bool kLds = false;
+  static constexpr bool kLds = false, kAligned = true;  // rows padded to 16 bytes, in the workspace
   struct Row {
     int e[4];
   };
@@ -314,7 +314,7 @@ struct DotDigits {
   long long ld;
   double* part;
   long long row0;
-  static constexpr bool kLds = false;
+  static constexpr bool kLds = false, kAligned = true;
   __device__ __forceinline__ void at(long long m0, long long n0) {
     ex += m0 >> 2;
     u += (m0 >> 2) * ld + n0;

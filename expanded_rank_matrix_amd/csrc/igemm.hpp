@@ -272,7 +272,7 @@ struct PartTile {
   int* part;  // [parts][rows of 4][N][4]: the four consecutive rows of an accumulator lie together
   long long N, stride;
   int* p;
-  static constexpr bool kLds = false;
+  static constexpr bool kLds = false, kAligned = false;
   struct Row {};
   __device__ __forceinline__ void at(long long m0, long long n0) {
     p = part + blockIdx.y * stride + ((m0 >> 2) * N + n0) * 4;
@@ -324,6 +324,7 @@ static_assert(tile_run_fits(1) && tile_run_fits(128) && tile_run_fits(129) && ti
                   tile_run_fits(1ll << 26),
               "a run's tiles fit a launch");
 
+// EPI::kAligned: the operands always can, so the other kernels are not built.
 template <int BM, int BN, int WR, int WC, typename EPI>
 static hipError_t tile_launch(const int8_t* A, long long lda, int M, const int8_t* B, long long ldb, int N, int K,
                               int parts, const EPI& epi, hipStream_t st) {
@@ -331,12 +332,15 @@ static hipError_t tile_launch(const int8_t* A, long long lda, int M, const int8_
   if (ntm * ntn > kMaxTiles) return hipErrorInvalidValue;
   const int kper = parts == 1 ? K : ((K + 127) / 128 + parts - 1) / parts * 128;
   const dim3 grid((unsigned)(ntm * ntn), (unsigned)parts);
-  if (tile_dma(A, lda, K) && tile_dma(B, ldb, K))
+  if (tile_dma(A, lda, K) && tile_dma(B, ldb, K)) {
     hipLaunchKernelGGL((tile_kernel<BM, BN, WR, WC, true, EPI>), grid, dim3(64 * WR * WC), 0, st, A, lda, M, B, ldb, N,
                        K, kper, (int)ntm, (int)ntn, epi);
-  else
-    hipLaunchKernelGGL((tile_kernel<BM, BN, WR, WC, false, EPI>), grid, dim3(64 * WR * WC), 0, st, A, lda, M, B, ldb, N,
-                       K, kper, (int)ntm, (int)ntn, epi);
+  } else {
+    if constexpr (EPI::kAligned) return hipErrorInvalidValue;
+    else
+      hipLaunchKernelGGL((tile_kernel<BM, BN, WR, WC, false, EPI>), grid, dim3(64 * WR * WC), 0, st, A, lda, M, B, ldb, N,
+                         K, kper, (int)ntm, (int)ntn, epi);
+  }
   return hipGetLastError();
 }
 

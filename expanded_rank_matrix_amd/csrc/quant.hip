@@ -376,7 +376,7 @@ struct ScaledY {
   const float* sw;
   YT* Y;
   long long ldy;
-  static constexpr bool kLds = true;
+  static constexpr bool kLds = true, kAligned = false;
   __device__ __forceinline__ void at(long long m0, long long n0) {
     sx += m0;
     sw += n0;
