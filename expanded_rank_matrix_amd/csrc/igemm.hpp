@@ -344,9 +344,11 @@ static hipError_t tile_launch(const int8_t* A, long long lda, int M, const int8_
   return hipGetLastError();
 }
 
-// Parts of the row length for few tiles.  A stage of a tile takes about 0.6 us however few
-// workgroups run (the latency of its loads; 128 x 128 and 64 x 128), so a long row length on a card
-// that is not full costs more than joining parts does: about 4 us and 8 bytes an element and part.
+// Parts of the row length for few tiles.  A stage of a tile with direct loads takes about 0.6 us however
+// few workgroups run (the latency of its loads; 128 x 128 and 64 x 128), so a long row length on a card
+// that is not full costs more than joining parts does: about 4 us and 8 bytes an element and part.  The
+// rule counts a stage through registers the same, though it takes about 1.5 us (333 x 1021 x 2051: 12.5 us
+// for eight), so rows at odd addresses are split later than they could be.
 // At least three stages and sixteen bytes are left to every part.
 struct TilePlan {
   bool small;  // 64 x 128 tiles (M <= 64)
