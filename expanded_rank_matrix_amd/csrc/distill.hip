@@ -7,8 +7,9 @@
 //
 // One pass over z keeps the running maximum m and the sum S of exp((z - m) / T) (8 elements a step:
 // one rescaling of the sum per step at most), so q_v = exp((z_v - m) / T) / S.  z is handled in
-// fp32, each thread's sum too; the threads' sums, log S and the K terms of the loss are fp64, since
-// log p - log q is a difference of numbers many times its size.  The gradient is a second pass: g q_v
+// fp32, each thread's sum too (of V / 256 terms or fewer, whose roundings average out to 10^-9 to 10^-8 of S;
+// an fp64 addition an element would cost as much as the rest of its work); the threads' sums, log S and the
+// K terms of the loss are fp64, since log p - log q is a difference of numbers many times its size.  The gradient is a second pass: g q_v
 // for every element, rounded once to z's type, and after it, behind a barrier, the teacher's at most K
 // elements once more, with p in the difference before its rounding.  Equal indices of one row meet in
 // hashed lists in LDS; their exponentials add as whole numbers of 2^-50 of the largest one's binade, so
@@ -43,7 +44,8 @@ struct Log2eT {
     lo = (float)(c - (double)hi);
   }
 };
-// e^(d / T); 0 below 2^-126
+// e^(d / T).  0 below 2^-126, where the instruction flushes: an element's gradient loses at most w T 2^-126
+// by it, and S, which is 1 or more, nothing.
 __device__ __forceinline__ float exp_t(float d, const Log2eT& c) {
   return __builtin_amdgcn_exp2f(fmaf(d, c.hi, d * c.lo));
 }

@@ -327,3 +327,41 @@ def test_outputs_in_place_and_over_inputs(batch):
         with pytest.raises(erm.ExterndError) as e:
             erm.apply_factors_grad(*f, 93, 93, Xc, Yc, out=out)
         assert e.value.status == erm.EINVAL
+
+
+def test_every_entry_on_a_stream_of_its_own():
+    """The chain of a repair step on a side stream, plain and captured, as on the current one."""
+    Bt, Ct, D, X, dY, _, _ = run(130, 75, 93, 40, seed=9)
+    f = device(Bt, Ct, D)
+    Xc = torch.from_numpy(X).cuda()
+
+    def chain(stream=None):
+        q, s = erm.quantize_rows(Xc, stream=stream)
+        W, sw = erm.quantize_rows(torch.ones((75, 93), device="cuda").cumsum(1), stream=stream) if stream is None else weights
+        teacher = erm.apply_quantized(W, sw, q, s, stream=stream)
+        Z = erm.apply_factors_static(*f, 75, 93, Xc, stream=stream)
+        loss, stats, d = erm.distill_loss(Z, teacher[:, :20].contiguous(), index, 2.0, grad=True, stream=stream)
+        d2 = erm.distill_grad(Z, stats, teacher[:, :20].contiguous(), index, 2.0, stream=stream)
+        return (q, s, loss, stats, d, d2, *erm.apply_factors_grad(*f, 75, 93, Xc, d, stream=stream))
+
+    index = torch.arange(20, dtype=torch.int32, device="cuda").repeat(40, 1)
+    weights = erm.quantize_rows(torch.ones((75, 93), device="cuda").cumsum(1))
+    want = chain()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = chain(side)
+    torch.cuda.synchronize()
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = chain(torch.cuda.current_stream())
+    for _ in range(3):
+        for x in got:
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert torch.equal(x, y)
+        assert torch.equal(chain()[6], want[6])
