@@ -313,7 +313,8 @@ def apply_factors_grad(B, C, D, m: int, n: int, X, dY, need_dX: bool = True, nee
     stream without waiting."""
     import torch
 
-    _given(B=B, C=C, D=D, dY=dY)
+    if B is None or C is None or D is None or dY is None:
+        _given(B=B, C=C, D=D, dY=dY)
     _require(D, torch.float32, "D")
     if D.dim() != 1:
         raise ValueError("D must be a vector of k scales")
@@ -632,7 +633,8 @@ def distill_grad(logits, stats, teacher, index, temperature: float = 1.0, grad_l
     dlogits[r][v] = grad_loss[r] T (q[v] - sum of p_k with index_k = v), of logits' type; grad_loss
     (rows fp32, 1 where None) takes the weight's place, and a row where it is 0 is not read.  ``out``
     may be a preallocated tensor apart from logits, or logits itself.  Enqueued on the stream without waiting."""
-    _given(stats=stats)
+    if stats is None:
+        _given(stats=stats)
     z, t, ldd = _distill_args(logits, teacher, index, grad_loss, "grad_loss", out)
     _require(stats, _FLOAT[0], "stats", shape=(logits.shape[0], 2), device=logits.device)
     args = (logits, z, t, ldd, stats, temperature, grad_loss, out)
