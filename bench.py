@@ -270,7 +270,7 @@ def repair_bench(args, erm, torch, A, h, c, k, m, n, out, stream):
         Z = erm.apply_factors(B, C, D, m, n, X, stream=stream)
         loss, _, dZ = erm.distill_loss(Z, teacher, index, weight=weight, stream=stream, out=Z)
         _, dD = erm.apply_factors_grad(B, C, D, m, n, X, dZ, stream=stream)
-        D.add_(dD, alpha=-1e-4)
+        D.add_(dD, alpha=-1e-6)  # 10^-5 overshoots on a single vector
         losses.append(loss)
 
     wall, gpu_ms = timed_steps(args, torch, stream, step)
