@@ -553,7 +553,7 @@ static hipError_t distill_typed(const DistillLaunch& all, hipStream_t st) {
       // The shape by the row's length: held where a thread has 8 or 16 chunks, with as few threads as
       // hold it (several rows share a CU, one's stores under another's loads).  Measured, 2048 rows of
       // bf16, step in us, held / 256 threads streaming / 1024 streaming: 8192: 19.5 / 18.7 / 29.5;
-      // 32768: 52.7 / 64.5 / 62.2; 65536: 115 / 163 / 137; 131072: 233 / 334 / 267.
+      // 32768: 52.7 / 64.5 / 62.2; 65536: 115 / 163 / 137; 131072: 235 / 334 / 267.
       constexpr bool f32 = sizeof(T) == 4;
       if (L.vocab <= 8 * 256 * 4) distill_launch<T, 0, kDThreads, 0>(L, true, 1, slice, st);
       else if (L.vocab <= 8 * 256 * 8) distill_launch<T, 0, 256, 8>(L, true, 1, slice, st);
