@@ -497,7 +497,7 @@ static Rows dense(const void* p, int64_t bytes) { return {p, 1, bytes, bytes}; }
 // that others of the call still read.  Rows of one pitch may lie side by side; of two pitches, any meeting
 // of the whole counts.
 static bool meet(const Rows& a, const Rows& b) {
-  if (!a.p || !b.p || a.rows * a.len == 0 || b.rows * b.len == 0) return false;
+  if (!a.p || !b.p || a.rows == 0 || a.len == 0 || b.rows == 0 || b.len == 0) return false;
   const __int128 x = (__int128)reinterpret_cast<uintptr_t>(a.p), y = (__int128)reinterpret_cast<uintptr_t>(b.p);
   const __int128 xe = x + (__int128)(a.rows - 1) * a.pitch + a.len, ye = y + (__int128)(b.rows - 1) * b.pitch + b.len;
   if (xe <= y || ye <= x) return false;

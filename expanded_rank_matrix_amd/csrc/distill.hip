@@ -7,14 +7,15 @@
 //
 // One pass over z keeps the running maximum m and the sum S of exp((z - m) / T) (8 elements a step:
 // one rescaling of the sum per step at most), so q_v = exp((z_v - m) / T) / S.  z is handled in
-// fp32, each thread's sum too (of V / 256 terms or fewer, whose roundings average out to 10^-9 to 10^-8 of S;
-// an fp64 addition an element would cost as much as the rest of its work); the threads' sums, log S and the
-// K terms of the loss are fp64, since log p - log q is a difference of numbers many times its size.  The gradient is a second pass: g q_v
-// for every element, rounded once to z's type, and after it, behind a barrier, the teacher's at most K
-// elements once more, with p in the difference before its rounding.  Equal indices of one row meet in
-// hashed lists in LDS; their exponentials add as whole numbers of 2^-50 of the largest one's binade, so
-// the order does not matter and each of them writes the same value.  p keeps fp32's relative precision
-// however small it is: where the student gives less, it is the gradient.
+// fp32, each thread's sum too (about V / 256 terms or fewer, whose roundings average out to 10^-9 to
+// 10^-8 of S; in fp64 every element would take a conversion and an fp64 addition more); the threads'
+// sums, log S and the K terms of the loss are fp64, since log p - log q is a difference of numbers many
+// times its size.  The gradient is a second pass: g q_v for every element, rounded once to z's type, and
+// after it, behind a barrier, the teacher's at most K elements once more, with p in the difference before
+// its rounding.  Equal indices of one row meet in hashed lists in LDS; their exponentials add as whole
+// numbers of 2^-50 of the largest one's binade, so the order does not matter and each of them writes the
+// same value.  p keeps fp32's relative precision however small it is: where the student gives less, it
+// is the gradient.
 #include "common.hpp"
 #include "externd_internal.hpp"
 #include "types.hpp"
