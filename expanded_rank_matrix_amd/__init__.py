@@ -105,6 +105,13 @@ def load():
         lib.externd_apply_factors_grad.argtypes = [vp, vp, vp, i64, i64, i64, vp, vp, i64, vp, vp, vp, vp]
         lib.externd_apply_factors_grad_workspace.restype = i64
         lib.externd_apply_factors_grad_workspace.argtypes = [i64, i64, i64, i64]
+        lib.externd_token_loss.restype = ci
+        lib.externd_token_loss.argtypes = [vp, ci, i64, i64, i64, vp, i64, i64, vp, ci, vp, vp, vp, vp, i64, vp, i64,
+                                           vp, vp]
+        lib.externd_token_grad.restype = ci
+        lib.externd_token_grad.argtypes = [vp, ci, i64, i64, i64, vp, i64, i64, vp, vp, ci, vp, vp, i64, vp, i64, vp, vp]
+        lib.externd_token_workspace.restype = i64
+        lib.externd_token_workspace.argtypes = [ci, i64, i64, i64, vp, i64, ci, ci, ci]
         lib.externd_status_string.restype = ctypes.c_char_p
         lib.externd_status_string.argtypes = [ci]
         lib.externd_last_error.restype = ctypes.c_char_p
@@ -653,6 +660,99 @@ def _distill_grad(logits, z, t, ldd, stats, temperature, grad_loss, out, stream)
     _check(load().externd_distill_grad(*z, stats.data_ptr(), *t, temperature,
                                        None if grad_loss is None else grad_loss.data_ptr(), out.data_ptr(), ldd, stream))
     return out
+
+
+def _token_args(X, W, target, weight, name, out):
+    """Validated arguments of the token loss's entry points: X's and W's, the target's, and the row
+    distances of given gradients."""
+    import torch
+
+    types = _types()
+    if W is None or target is None:
+        _given(W=W, target=target)
+    ldx = _rows(X, _FLOAT, "X")
+    rows, n = X.shape
+    dev = X.device
+    ldw = _rows(W, (X.dtype,), "W", device=dev)
+    if W.shape[1] != n:
+        raise ValueError(f"W must be vocab x n with n = {n}")
+    _require(target, (torch.int32, torch.int64), "target", shape=(rows,), device=dev)
+    _require(weight, torch.float32, name, shape=(rows,), device=dev)
+    lds = (n, n)
+    if out is not None:
+        lds = tuple(n if t is None else _rows(t, (X.dtype,), f"out[{i}]", shape=tuple(s.shape), device=dev)
+                    for i, (t, s) in enumerate(zip(out, (X, W))))
+    return (X.data_ptr(), types[X.dtype], rows, n, ldx, W.data_ptr(), W.shape[0], ldw), (
+        target.data_ptr(), target.element_size(), None if weight is None else weight.data_ptr()), lds
+
+
+def token_loss(X, W, target, weight=None, grad: bool = False, need_dX: bool = True, need_dW: bool = True,
+               stream=None, out=None):
+    """Softmax cross entropy of tokens through an output matrix, without the logits z = X W^T kept:
+    loss[t] = weight[t] (log sum_v exp z[t][v] - z[t][target[t]]), beside ``distill_loss`` where a model
+    learns from text instead of from a teacher.
+
+    X (rows x n, fp32, fp16 or bf16: the tokens' hidden rows) and W (vocab x n, of X's type) may have strided rows;
+    target (rows, int32 or int64), weight (rows fp32, 1 where None).  A row whose target lies outside
+    the vocabulary (such as -100) or whose weight is 0 is not read and has loss and gradient 0.
+    Returns (loss fp32 rows, stats fp32 rows x 2); with ``grad`` or ``out`` (loss, stats, dX, dW), the gradients
+    of the losses' sum, of X's type, None for one that is not needed (a fixed W: need_dW=False).
+    ``out`` may supply the pair (dX, dW), apart from the inputs, but dX may be X itself.  ``stats`` feeds
+    ``token_grad``.  Enqueued on the stream without waiting."""
+    x, t, lds = _token_args(X, W, target, weight, "weight", out)
+    args = (X, W, x, t, None, lds, (grad or out is not None) and need_dX, (grad or out is not None) and need_dW,
+            grad or out is not None, out)
+    ptr = _here(X.device, stream)
+    if ptr is not None:
+        return _token(*args, ptr)
+    with _Run(X.device, stream, (X, W, target, weight, *(out or ()))) as run:
+        return _token(*args, run.ptr)
+
+
+def token_grad(X, W, stats, target, grad_loss=None, need_dX: bool = True, need_dW: bool = True, stream=None,
+               out=None):
+    """The gradient of ``token_loss`` from its ``stats`` on the same X and W: with
+    P[t][v] = grad_loss[t] (softmax(z[t])[v] - [v = target[t]]), dX = P W and dW = P^T X, of X's type;
+    grad_loss (rows fp32, 1 where None) takes the weight's place, and a row where it is 0 is not read.
+    Returns (dX, dW), None for one that is not needed.  ``out`` may supply the pair, apart from the inputs, but dX may
+    be X itself.  Enqueued on the stream without waiting."""
+    if stats is None:
+        _given(stats=stats)
+    if not (need_dX or need_dW):
+        raise ValueError("need_dX or need_dW must be set")
+    x, t, lds = _token_args(X, W, target, grad_loss, "grad_loss", out)
+    _require(stats, _FLOAT[0], "stats", shape=(X.shape[0], 2), device=X.device)
+    args = (X, W, x, t, stats, lds, need_dX, need_dW, True, out)
+    ptr = _here(X.device, stream)
+    if ptr is not None:
+        return _token(*args, ptr)
+    with _Run(X.device, stream, (X, W, stats, target, grad_loss, *(out or ()))) as run:
+        return _token(*args, run.ptr)
+
+
+def _token(X, W, x, t, stats, lds, need_dX, need_dW, grad, out, stream):
+    import torch
+
+    dev, rows = X.device, X.shape[0]
+    lib = load()
+    if out is None:
+        dX = torch.empty(X.shape, dtype=X.dtype, device=dev) if need_dX else None
+        dW = torch.empty(W.shape, dtype=X.dtype, device=dev) if need_dW else None
+    else:
+        dX, dW = (o if need else None for o, need in zip(out, (need_dX, need_dW)))
+        if (dX is None) == need_dX or (dW is None) == need_dW:
+            raise ValueError("out must hold dX and dW where they are needed")
+    size = lib.externd_token_workspace(x[1], rows, x[3], x[6], x[5], x[7], stats is None, need_dX, need_dW)
+    ws = torch.empty(size, dtype=torch.uint8, device=dev) if size > 0 else None
+    tail = (None if dX is None else dX.data_ptr(), lds[0], None if dW is None else dW.data_ptr(), lds[1],
+            None if ws is None else ws.data_ptr(), stream)
+    if stats is not None:
+        _check(lib.externd_token_grad(*x, stats.data_ptr(), *t, *tail))
+        return dX, dW
+    loss = torch.empty(rows, dtype=torch.float32, device=dev)
+    stats = torch.empty((rows, 2), dtype=torch.float32, device=dev)
+    _check(lib.externd_token_loss(*x, *t, loss.data_ptr(), stats.data_ptr(), *tail))
+    return (loss, stats, dX, dW) if grad else (loss, stats)
 
 
 def unpack(packed, length: int) -> np.ndarray:

@@ -672,4 +672,68 @@ int externd_apply_factors_grad(const uint32_t* B_packed, const uint32_t* C_packe
   return EXTERND_OK;
 }
 
+// ---- cross entropy through an output matrix
+
+constexpr int64_t kMaxTokenRows = (int64_t)1 << 20;
+constexpr int64_t kMaxTokenLen = (int64_t)1 << 17;
+constexpr int64_t kMaxTokenVocab = (int64_t)1 << 24;
+
+int64_t externd_token_workspace(int x_type, int64_t rows, int64_t n, int64_t vocab, const void* W, int64_t ldw, int loss,
+                                int dX, int dW) {
+  if (!float_type(x_type) || rows < 0 || rows > kMaxTokenRows || n < 1 || n > kMaxTokenLen || vocab < 1 ||
+      vocab > kMaxTokenVocab || ldw < n || ldw > kMaxLd)
+    return -1;
+  return (int64_t)token_workspace_bytes(x_type, rows, (int)n, (int)vocab, W, ldw, loss != 0, dX != 0, dW != 0);
+}
+
+// both directions, loss null in the gradient's
+static int token_entry(const void* X, int x_type, int64_t rows, int64_t n, int64_t ldx, const void* W, int64_t vocab,
+                       int64_t ldw, const void* target, int target_bytes, const float* weight, float* loss, float* stats,
+                       bool forward, void* dX, int64_t lddx, void* dW, int64_t lddw, void* workspace, void* stream) {
+  g_last_error.clear();
+  if (!float_type(x_type)) return fail(EXTERND_EINVAL, "x_type must be EXTERND_F32, EXTERND_F16 or EXTERND_BF16");
+  if (target_bytes != 4 && target_bytes != 8) return fail(EXTERND_EINVAL, "target_bytes must be 4 or 8");
+  if (rows < 0 || rows > kMaxTokenRows) return fail(EXTERND_EINVAL, "need 0 <= rows <= 2^20");
+  if (n < 1 || n > kMaxTokenLen) return fail(EXTERND_EINVAL, "need 1 <= n <= 2^17");
+  if (vocab < 1 || vocab > kMaxTokenVocab) return fail(EXTERND_EINVAL, "need 1 <= vocab <= 2^24");
+  if (ldx < n || ldx > kMaxLd || ldw < n || ldw > kMaxLd || (dX && (lddx < n || lddx > kMaxLd)) ||
+      (dW && (lddw < n || lddw > kMaxLd)))
+    return fail(EXTERND_EINVAL, "ldx, ldw, lddx and lddw must be at least n (and at most 2^40)");
+  if (!forward && !dX && !dW) return fail(EXTERND_EINVAL, "dX or dW must be given");
+  if (rows == 0 && !dW) return EXTERND_OK;
+  if (!W || (rows > 0 && (!X || !target || !stats || (forward && !loss)))) return fail(EXTERND_EINVAL, "null pointer argument");
+  if (rows > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15)))
+    return fail(EXTERND_EINVAL, "workspace of externd_token_workspace() bytes, 16-byte aligned, is needed");
+  const int64_t es = x_type == EXTERND_F32 ? 4 : 2;
+  const Rows in[] = {{X, rows, n * es, ldx * es}, {W, vocab, n * es, ldw * es}, dense(target, rows * target_bytes),
+                     dense(weight, weight ? rows * 4 : 0), dense(stats, forward ? 0 : rows * 8)};
+  const Rows out[] = {{dX, rows, n * es, lddx * es}, {dW, vocab, n * es, lddw * es}, dense(loss, forward ? rows * 4 : 0),
+                      dense(stats, forward ? rows * 8 : 0)};
+  if (dX && dX == X && lddx != ldx) return fail(EXTERND_EINVAL, "a gradient in X's place needs lddx = ldx");
+  for (const Rows& o : out) {
+    for (const Rows& i : in)
+      if (meet(o, i) && !(o.p == dX && i.p == X && dX == X)) return fail(EXTERND_EINVAL, "outputs must not overlap the inputs");
+    for (const Rows& p : out)
+      if (&p != &o && meet(o, p)) return fail(EXTERND_EINVAL, "outputs must not overlap each other");
+  }
+  const TokenLaunch L{X, W, target, weight, loss, stats, dX, dW, workspace, rows, ldx, ldw, lddx, lddw, (int)n, (int)vocab,
+                      target_bytes};
+  HIP_OR_FAIL(token_run(x_type, L, reinterpret_cast<hipStream_t>(stream)));
+  return EXTERND_OK;
+}
+
+int externd_token_loss(const void* X, int x_type, int64_t rows, int64_t n, int64_t ldx, const void* W, int64_t vocab,
+                       int64_t ldw, const void* target, int target_bytes, const float* weight, float* loss,
+                       float* stats, void* dX, int64_t lddx, void* dW, int64_t lddw, void* workspace, void* stream) {
+  return token_entry(X, x_type, rows, n, ldx, W, vocab, ldw, target, target_bytes, weight, loss, stats, true, dX, lddx, dW,
+                     lddw, workspace, stream);
+}
+
+int externd_token_grad(const void* X, int x_type, int64_t rows, int64_t n, int64_t ldx, const void* W, int64_t vocab,
+                       int64_t ldw, const float* stats, const void* target, int target_bytes, const float* grad_loss,
+                       void* dX, int64_t lddx, void* dW, int64_t lddw, void* workspace, void* stream) {
+  return token_entry(X, x_type, rows, n, ldx, W, vocab, ldw, target, target_bytes, grad_loss, nullptr,
+                     const_cast<float*>(stats), false, dX, lddx, dW, lddw, workspace, stream);
+}
+
 }  // extern "C"

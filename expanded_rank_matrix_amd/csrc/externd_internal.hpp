@@ -128,4 +128,26 @@ size_t grad_workspace_bytes(int k, int m, int n, long long batch);
 hipError_t grad_run(const uint32_t* B, const uint32_t* C, const float* D, int k, int m, int n, const float* X,
                     const float* dY, long long batch, float* dX, float* dD, void* ws, hipStream_t st);
 
+// Softmax cross entropy through an output matrix and its gradient (token.hpp).  loss null: the gradient
+// from given stats (weight is then the loss's gradient); else loss and stats, and the gradients where
+// dX or dW is given.
+struct TokenLaunch {
+  const void* X;
+  const void* W;
+  const void* target;
+  const float* weight;
+  float* loss;
+  float* stats;
+  void* dX;
+  void* dW;
+  void* ws;
+  long long rows, ldx, ldw, lddx, lddw;
+  int n, vocab, target_bytes;
+};
+size_t token_workspace_bytes(int x_type, long long rows, int n, int vocab, const void* W, long long ldw, bool loss, bool dX,
+                             bool dW);
+hipError_t token_run(int x_type, const TokenLaunch& L, hipStream_t st);
+hipError_t token_run_f32(const TokenLaunch& L, hipStream_t st);
+hipError_t token_run_f16(const TokenLaunch& L, hipStream_t st);
+
 }  // namespace externd

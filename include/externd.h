@@ -320,6 +320,49 @@ int externd_apply_factors_grad(const uint32_t* B_packed, const uint32_t* C_packe
 /* Bytes of workspace externd_apply_factors_grad needs; -1 for sizes it refuses. */
 int64_t externd_apply_factors_grad_workspace(int64_t k, int64_t m, int64_t n, int64_t batch);
 
+/* ---- Softmax cross entropy through an output matrix ----------------------------------------
+ * The loss of tokens that a repaired model is trained and judged by, straight from its hidden rows:
+ * logits z[t][v] = X[t] . W[v] are formed and used a tile at a time and never stored.
+ *   loss[t] = weight[t] (log sum_v exp z[t][v] - z[t][target[t]])
+ * A row counts if its weight is not 0 and 0 <= target < vocab; the others (padding: target -100) are not
+ * read, and their loss, statistics and gradient are 0.
+ *   X        rows x n of x_type (EXTERND_F32, _F16, _BF16), row distance ldx
+ *   W        vocab x n of x_type, row distance ldw: one row per word of the vocabulary
+ *   target   rows int32 (target_bytes 4) or int64 (8)
+ *   weight   rows fp32, or NULL for 1
+ *   loss     rows fp32
+ *   stats    rows x 2 fp32: the row's largest logit and the sum of exp(z - largest) over the
+ *            vocabulary, for externd_token_grad
+ *   dX       NULL, or rows x n of x_type, row distance lddx: the gradient of the losses' sum,
+ *              sum_v P[t][v] W[v],  P[t][v] = weight[t] (softmax(z[t])[v] - [v = target[t]])
+ *            It may be X itself (with lddx = ldx).
+ *   dW       NULL, or vocab x n of x_type, row distance lddw:  sum_t P[t][v] X[t]
+ *            Outputs must not overlap the inputs or each other otherwise (EXTERND_EINVAL).
+ *   workspace  externd_token_workspace(x_type, rows, n, vocab, W, ldw, 1, dX != NULL, dW != NULL) bytes, 16-byte
+ *            aligned, used by this call alone until it has run
+ * Products are summed in fp32, the losses in fp64.  P is rounded to x_type before the two products
+ * that take it (for fp16 times a power of two that the result is divided by again).  A NaN or an infinity in a counted row
+ * gives NaN in that row's outputs and throughout dW; in W, everywhere.  exp(z - largest) and P below
+ * 2^-126 count as 0.  Deterministic.
+ * 0 <= rows <= 2^20, 1 <= n <= 2^17, 1 <= vocab <= 2^24. */
+int externd_token_loss(const void* X, int x_type, int64_t rows, int64_t n, int64_t ldx, const void* W, int64_t vocab,
+                       int64_t ldw, const void* target, int target_bytes, const float* weight, float* loss,
+                       float* stats, void* dX, int64_t lddx, void* dW, int64_t lddw, void* workspace, void* stream);
+
+/* The gradient alone, from the stats of externd_token_loss on the same X and W:
+ * grad_loss (rows fp32, NULL for 1) takes the weights' place.  Rows whose forward weight was 0 have no
+ * stats and must have grad_loss 0.  dX or dW may be NULL.  Other arguments as for
+ * externd_token_loss; the workspace's size is asked for with loss 0. */
+int externd_token_grad(const void* X, int x_type, int64_t rows, int64_t n, int64_t ldx, const void* W, int64_t vocab,
+                       int64_t ldw, const float* stats, const void* target, int target_bytes, const float* grad_loss,
+                       void* dX, int64_t lddx, void* dW, int64_t lddw, void* workspace, void* stream);
+
+/* Bytes of workspace that the two need; -1 for sizes or a type they refuse.  loss, dX and dW say which
+ * outputs are asked for.  W's address and row distance decide whether its rows, where they do not start
+ * at multiples of 16 bytes, are copied to aligned ones, up to 128 MiB of them at a time. */
+int64_t externd_token_workspace(int x_type, int64_t rows, int64_t n, int64_t vocab, const void* W, int64_t ldw, int loss,
+                                int dX, int dW);
+
 /* Human-readable name of a status code (static string). */
 const char* externd_status_string(int status);
 
