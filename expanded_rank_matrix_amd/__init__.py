@@ -105,6 +105,12 @@ def load():
         lib.externd_apply_factors_grad.argtypes = [vp, vp, vp, i64, i64, i64, vp, vp, i64, vp, vp, vp, vp]
         lib.externd_apply_factors_grad_workspace.restype = i64
         lib.externd_apply_factors_grad_workspace.argtypes = [i64, i64, i64, i64]
+        lib.externd_quantize_groups.restype = ci
+        lib.externd_quantize_groups.argtypes = [vp, ci, i64, i64, i64, i64, vp, vp, vp, ci, vp]
+        lib.externd_apply_grouped.restype = ci
+        lib.externd_apply_grouped.argtypes = [vp, vp, vp, ci, i64, i64, i64, i64, vp, ci, i64, i64, vp, ci, i64, vp, vp]
+        lib.externd_apply_grouped_workspace.restype = i64
+        lib.externd_apply_grouped_workspace.argtypes = [ci, i64, i64, i64, i64]
         lib.externd_token_loss.restype = ci
         lib.externd_token_loss.argtypes = [vp, ci, i64, i64, i64, vp, i64, i64, vp, ci, vp, vp, vp, vp, i64, vp, i64,
                                            vp, vp]
@@ -660,6 +666,125 @@ def _distill_grad(logits, z, t, ldd, stats, temperature, grad_loss, out, stream)
     _check(load().externd_distill_grad(*z, stats.data_ptr(), *t, temperature,
                                        None if grad_loss is None else grad_loss.data_ptr(), out.data_ptr(), ldd, stream))
     return out
+
+
+def quantize_groups(W, group: int = 128, offsets: bool = False, scale_dtype=None, stream=None, out=None):
+    """Weights W (rows x n, fp32, fp16 or bf16, device; rows may be strided) to 4-bit codes with a scale for each
+    ``group`` (32, 64 or 128) of consecutive elements of a row, w = scale c + offset: c in -7 .. 7 and no
+    offset (scale = max |w| / 7), or with ``offsets`` c in -8 .. 7 over the group's range
+    (scale = (hi - lo) / 15, offset = lo + 8 scale), the whole numbers nearest to the quotients.
+
+    Returns (Q, scale, offset): Q int32 rows x ceil(n / group) group / 8, eight codes a word, the first in the
+    lowest four bits; scale and offset rows x ceil(n / group) of ``scale_dtype`` (by default W's type), offset None
+    without ``offsets``.  ``out`` may supply the three, apart from W.  A group with a NaN or an infinity gets codes 0
+    and scale NaN.  Makes the weights of ``apply_grouped``.  Enqueued on the stream without waiting."""
+    types = _types()
+    ldw = _rows(W, _FLOAT, "W")
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128")
+    if scale_dtype is None:
+        scale_dtype = W.dtype if out is None else out[1].dtype
+    if scale_dtype not in _FLOAT:
+        raise ValueError("scale_dtype must be torch.float32, torch.float16 or torch.bfloat16")
+    args = (W, types[W.dtype], ldw, group, offsets, scale_dtype, out)
+    ptr = _here(W.device, stream)
+    if ptr is not None:
+        return _quantize_groups(*args, ptr)
+    with _Run(W.device, stream, (W,) if out is None else (W, *out)) as run:
+        return _quantize_groups(*args, run.ptr)
+
+
+def _quantize_groups(W, w_type, ldw, group, offsets, scale_dtype, out, stream):
+    import torch
+
+    rows, n = W.shape
+    dev, groups = W.device, (n + group - 1) // group
+    shapes = ((rows, groups * group // 8), (rows, groups), (rows, groups))
+    if out is None:
+        Q = torch.empty(shapes[0], dtype=torch.int32, device=dev)
+        scale = torch.empty(shapes[1], dtype=scale_dtype, device=dev)
+        offset = torch.empty(shapes[2], dtype=scale_dtype, device=dev) if offsets else None
+    else:
+        Q, scale, offset = out
+        _given(**{"out[0]": Q, "out[1]": scale})
+        if (offset is None) == bool(offsets):
+            raise ValueError("out must hold an offset with offsets and only then")
+        _require(Q, (torch.int32, torch.uint32), "out[0]", shape=shapes[0], device=dev)
+        _require(scale, scale_dtype, "out[1]", shape=shapes[1], device=dev)
+        _require(offset, scale_dtype, "out[2]", shape=shapes[2], device=dev)
+    _check(load().externd_quantize_groups(W.data_ptr(), w_type, rows, n, ldw, group, Q.data_ptr(), scale.data_ptr(),
+                                          None if offset is None else offset.data_ptr(), _TYPE[scale_dtype], stream))
+    return Q, scale, offset
+
+
+def apply_grouped(Q, scale, X, offset=None, group: int = 128, out_dtype=None, stream=None, out=None):
+    """Y[t][o] = sum_j (scale[o][j // group] c[o][j] + offset[o][j // group]) X[t][j]: a layer in 4 bits, beside
+    ``apply_quantized`` for layers in 8.  Q (int32, m x ceil(n / group) group / 8; rows may be strided), scale and
+    offset (m x ceil(n / group), fp32, fp16 or bf16, both of one type) are as ``quantize_groups`` gives them.
+    X (n or tokens x n, fp32, fp16 or bf16; rows may be strided) enters exactly.  Returns Y (m or tokens x m) of
+    ``out_dtype`` (by default X's type), summed in fp32 and rounded once; ``out`` may supply it, apart from the inputs.
+    Enqueued on the stream without waiting."""
+    types = _types()
+    if scale is None or X is None:
+        _given(scale=scale, X=X)
+    ldq = _rows(Q, _WORDS or _words(), "Q")
+    m, words = Q.shape
+    dev = Q.device
+    single = X.dim() == 1
+    X2 = X.unsqueeze(0) if single else X
+    ldx = _rows(X2, _FLOAT, "X", device=dev)
+    tokens, n = X2.shape
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128")
+    groups = (n + group - 1) // group
+    if words != groups * group // 8:
+        raise ValueError(f"Q has {words} words a row, {groups * group // 8} hold n = {n} in groups of {group}")
+    _require(scale, _FLOAT, "scale", shape=(m, groups), device=dev)
+    _require(offset, scale.dtype, "offset", shape=(m, groups), device=dev)
+    if out is not None:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError("out must be of out_dtype")
+        out_dtype = out.dtype
+    elif out_dtype is None:
+        out_dtype = X.dtype
+    if out_dtype not in _FLOAT:
+        raise ValueError("out_dtype must be torch.float32, torch.float16 or torch.bfloat16")
+    args = (Q, scale, offset, group, m, n, ldq, X2, types[X.dtype], tokens, ldx, out_dtype, out, single)
+    ptr = _here(dev, stream)
+    if ptr is not None:
+        return _apply_grouped(*args, ptr)
+    with _Run(dev, stream, (Q, scale, offset, X, out)) as run:
+        return _apply_grouped(*args, run.ptr)
+
+
+_WORDS = ()
+
+
+def _words():
+    global _WORDS
+    import torch
+
+    _WORDS = (torch.int32, torch.uint32)
+    return _WORDS
+
+
+def _apply_grouped(Q, scale, offset, group, m, n, ldq, X, x_type, tokens, ldx, y_type, out, single, stream):
+    import torch
+
+    dev = Q.device
+    lib = load()
+    if out is None:
+        Y = torch.empty((tokens, m), dtype=y_type, device=dev)
+        ldy = m
+    else:
+        Y = out.unsqueeze(0) if single and out.dim() == 1 else out
+        ldy = _rows(Y, _FLOAT, "out", shape=(tokens, m), device=dev)
+    size = lib.externd_apply_grouped_workspace(x_type, tokens, n, m, group)
+    ws = torch.empty(size, dtype=torch.uint8, device=dev) if size > 0 else None
+    _check(lib.externd_apply_grouped(
+        Q.data_ptr(), scale.data_ptr(), None if offset is None else offset.data_ptr(), _TYPE[scale.dtype], group, m, n, ldq,
+        X.data_ptr(), x_type, tokens, ldx, Y.data_ptr(), _TYPE[y_type], ldy, None if ws is None else ws.data_ptr(), stream))
+    return Y[0] if single else Y
 
 
 def _token_args(X, W, target, weight, name, out):

@@ -672,6 +672,70 @@ int externd_apply_factors_grad(const uint32_t* B_packed, const uint32_t* C_packe
   return EXTERND_OK;
 }
 
+// ---- layers in 4 bits with group scales
+
+constexpr int64_t kMaxGroupedLen = (int64_t)1 << 20;
+
+static bool group_size(int64_t g) { return g == 32 || g == 64 || g == 128; }
+static int64_t group_count(int64_t n, int64_t group) { return (n + group - 1) / group; }
+
+int externd_quantize_groups(const void* W, int w_type, int64_t rows, int64_t n, int64_t ldw, int64_t group, uint32_t* Q,
+                            void* scale, void* offset, int s_type, void* stream) {
+  g_last_error.clear();
+  if (!float_type(w_type) || !float_type(s_type))
+    return fail(EXTERND_EINVAL, "w_type and s_type must be EXTERND_F32, EXTERND_F16 or EXTERND_BF16");
+  if (!group_size(group)) return fail(EXTERND_EINVAL, "group must be 32, 64 or 128");
+  if (rows < 0 || rows > kMaxChannels) return fail(EXTERND_EINVAL, "need 0 <= rows <= 2^26");
+  if (n < 1 || n > kMaxGroupedLen) return fail(EXTERND_EINVAL, "need 1 <= n <= 2^20");
+  if (ldw < n || ldw > kMaxLd) return fail(EXTERND_EINVAL, "ldw must be at least n (and at most 2^40)");
+  if (rows == 0) return EXTERND_OK;
+  if (!W || !Q || !scale) return fail(EXTERND_EINVAL, "null pointer argument");
+  const int64_t es = w_type == EXTERND_F32 ? 4 : 2, ss = s_type == EXTERND_F32 ? 4 : 2, g = group_count(n, group);
+  const Rows in{W, rows, n * es, ldw * es}, q = dense(Q, rows * g * group / 2), sc = dense(scale, rows * g * ss),
+             of = dense(offset, offset ? rows * g * ss : 0);
+  if (meet(q, in) || meet(sc, in) || meet(of, in) || meet(q, sc) || meet(q, of) || meet(sc, of))
+    return fail(EXTERND_EINVAL, "Q, scale and offset must not overlap W or each other");
+  HIP_OR_FAIL(quantize_groups_run(W, w_type, rows, (int)n, ldw, (int)group, reinterpret_cast<int*>(Q), scale, offset, s_type,
+                                  reinterpret_cast<hipStream_t>(stream)));
+  return EXTERND_OK;
+}
+
+int64_t externd_apply_grouped_workspace(int x_type, int64_t tokens, int64_t n, int64_t m, int64_t group) {
+  if (!float_type(x_type) || tokens < 0 || tokens > kMaxCount || n < 1 || n > kMaxGroupedLen || m < 1 || m > kMaxChannels ||
+      !group_size(group))
+    return -1;
+  return (int64_t)grouped_workspace_bytes(x_type, tokens, (int)n, (int)m, (int)group);
+}
+
+int externd_apply_grouped(const uint32_t* Q, const void* scale, const void* offset, int s_type, int64_t group, int64_t m,
+                          int64_t n, int64_t ldq, const void* X, int x_type, int64_t tokens, int64_t ldx, void* Y,
+                          int y_type, int64_t ldy, void* workspace, void* stream) {
+  g_last_error.clear();
+  if (!float_type(x_type) || !float_type(y_type) || !float_type(s_type))
+    return fail(EXTERND_EINVAL, "x_type, y_type and s_type must be EXTERND_F32, EXTERND_F16 or EXTERND_BF16");
+  if (!group_size(group)) return fail(EXTERND_EINVAL, "group must be 32, 64 or 128");
+  if (tokens < 0 || tokens > kMaxCount || m < 1 || m > kMaxChannels)
+    return fail(EXTERND_EINVAL, "need 0 <= tokens < 2^31 and 1 <= m <= 2^26");
+  if (n < 1 || n > kMaxGroupedLen) return fail(EXTERND_EINVAL, "need 1 <= n <= 2^20");
+  const int64_t g = group_count(n, group), words = g * group / 8;
+  if (ldq < words || ldq > kMaxLd || ldx < n || ldx > kMaxLd || ldy < m || ldy > kMaxLd)
+    return fail(EXTERND_EINVAL, "ldq must be at least ceil(n / group) group / 8, ldx n and ldy m (and at most 2^40)");
+  if (tokens == 0) return EXTERND_OK;
+  if (!Q || !scale || !X || !Y) return fail(EXTERND_EINVAL, "null pointer argument");
+  if (grouped_workspace_bytes(x_type, tokens, (int)n, (int)m, (int)group) > 0 &&
+      (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15)))
+    return fail(EXTERND_EINVAL, "workspace of externd_apply_grouped_workspace() bytes, 16-byte aligned, is needed");
+  const int64_t xs = x_type == EXTERND_F32 ? 4 : 2, ys = y_type == EXTERND_F32 ? 4 : 2, ss = s_type == EXTERND_F32 ? 4 : 2;
+  const Rows out{Y, tokens, m * ys, ldy * ys};
+  if (meet(out, {X, tokens, n * xs, ldx * xs}) || meet(out, {Q, m, words * 4, ldq * 4}) || meet(out, dense(scale, m * g * ss)) ||
+      meet(out, dense(offset, offset ? m * g * ss : 0)))
+    return fail(EXTERND_EINVAL, "Y must not overlap the inputs");
+  const GroupedLaunch L{reinterpret_cast<const int*>(Q), scale, offset, X, Y, workspace, ldq, tokens, ldx, ldy, (int)m, (int)n,
+                        (int)group, s_type, x_type, y_type};
+  HIP_OR_FAIL(grouped_run(L, reinterpret_cast<hipStream_t>(stream)));
+  return EXTERND_OK;
+}
+
 // ---- cross entropy through an output matrix
 
 constexpr int64_t kMaxTokenRows = (int64_t)1 << 20;

@@ -128,6 +128,22 @@ size_t grad_workspace_bytes(int k, int m, int n, long long batch);
 hipError_t grad_run(const uint32_t* B, const uint32_t* C, const float* D, int k, int m, int n, const float* X,
                     const float* dY, long long batch, float* dX, float* dD, void* ws, hipStream_t st);
 
+// Weights in 4 bits with group scales (grouped.hip).  offset null: none.
+hipError_t quantize_groups_run(const void* W, int type, long long rows, int n, long long ldw, int group, int* Q, void* scale,
+                               void* offset, int s_type, hipStream_t st);
+struct GroupedLaunch {
+  const int* Q;
+  const void* scale;
+  const void* offset;
+  const void* X;
+  void* Y;
+  void* ws;
+  long long ldq, tokens, ldx, ldy;
+  int m, n, group, s_type, x_type, y_type;
+};
+size_t grouped_workspace_bytes(int x_type, long long tokens, int n, int m, int group);
+hipError_t grouped_run(const GroupedLaunch& L, hipStream_t st);
+
 // Softmax cross entropy through an output matrix and its gradient (token.hpp).  loss null: the gradient
 // from given stats (weight is then the loss's gradient); else loss and stats, and the gradients where
 // dX or dW is given.

@@ -320,6 +320,43 @@ int externd_apply_factors_grad(const uint32_t* B_packed, const uint32_t* C_packe
 /* Bytes of workspace externd_apply_factors_grad needs; -1 for sizes it refuses. */
 int64_t externd_apply_factors_grad_workspace(int64_t k, int64_t m, int64_t n, int64_t batch);
 
+/* ---- Layers kept in 4 bits with group scales ------------------------------------------------
+ * Weights w = scale c + offset with 4-bit codes c in -8 .. 7, a scale (and, where given, an
+ * offset) for each group of 32, 64 or 128 consecutive elements of a row; a row's last group may be
+ * shorter.  words(n) = ceil(n / group) group / 8 words of a row hold its codes, eight a word, the
+ * first in the lowest four bits, two's complement; codes behind the row's n-th do not count. */
+
+/* Weights to 4 bits.  Without an offset: a = max |w| of the group, scale = a / 7 and c = the whole number
+ * nearest to 7 w / a (ties to even).  With one: lo and hi the group's least and largest value,
+ * scale = (hi - lo) / 15, offset = lo + 8 scale, c = the whole number nearest to
+ * 15 (w - lo) / (hi - lo), less 8.  Quotients are those of fp64; scale and offset are rounded to fp32 and
+ * then to s_type.  A group whose range is 0 gets codes 0 (and its value as the offset), one with a NaN or
+ * an infinity codes 0 and scale (and offset) NaN.
+ *   W       rows x n of w_type (EXTERND_F32, _F16 or _BF16), row distance ldw
+ *   Q       rows x words(n) uint32, dense, codes behind a row's n-th 0
+ *   scale   rows x ceil(n / group) of s_type (EXTERND_F32, _F16, _BF16), dense
+ *   offset  NULL, or as scale
+ * Outputs must not overlap W or each other (EXTERND_EINVAL).  0 <= rows <= 2^26, 1 <= n <= 2^20. */
+int externd_quantize_groups(const void* W, int w_type, int64_t rows, int64_t n, int64_t ldw, int64_t group, uint32_t* Q,
+                            void* scale, void* offset, int s_type, void* stream);
+
+/* Inference through a layer in 4 bits:  Y[t][o] = sum_j (scale[o][j / group] c[o][j] + offset[o][j / group]) X[t][j]
+ *   Q       m x words(n), row distance ldq in words (at least words(n))
+ *   scale, offset   as above, dense; offset may be NULL
+ *   X       tokens x n of x_type (EXTERND_F32, _F16 or _BF16), row distance ldx
+ *   Y       tokens x m of y_type (one of the same), row distance ldy; must not overlap the inputs
+ *           (EXTERND_EINVAL)
+ *   workspace  externd_apply_grouped_workspace(x_type, tokens, n, m, group) bytes, 16-byte aligned (NULL where
+ *           that is 0), used by this call alone until it has run
+ * Codes and X enter the products exactly; they are summed in fp32, and the result is rounded once to
+ * y_type.  Deterministic.  0 <= tokens < 2^31, 1 <= m <= 2^26, 1 <= n <= 2^20. */
+int externd_apply_grouped(const uint32_t* Q, const void* scale, const void* offset, int s_type, int64_t group, int64_t m,
+                          int64_t n, int64_t ldq, const void* X, int x_type, int64_t tokens, int64_t ldx, void* Y,
+                          int y_type, int64_t ldy, void* workspace, void* stream);
+
+/* Bytes of workspace externd_apply_grouped needs; -1 for sizes or a type it refuses. */
+int64_t externd_apply_grouped_workspace(int x_type, int64_t tokens, int64_t n, int64_t m, int64_t group);
+
 /* ---- Softmax cross entropy through an output matrix ----------------------------------------
  * The loss of tokens that a repaired model is trained and judged by, straight from its hidden rows:
  * logits z[t][v] = X[t] . W[v] are formed and used a tile at a time and never stored.
