@@ -143,6 +143,8 @@ struct GroupedLaunch {
 };
 size_t grouped_workspace_bytes(int x_type, long long tokens, int n, int m, int group);
 hipError_t grouped_run(const GroupedLaunch& L, hipStream_t st);
+hipError_t grouped_run_f16(const GroupedLaunch& L, hipStream_t st);
+hipError_t grouped_run_f32(const GroupedLaunch& L, hipStream_t st);
 
 // Softmax cross entropy through an output matrix and its gradient (token.hpp).  loss null: the gradient
 // from given stats (weight is then the loss's gradient); else loss and stats, and the gradients where

@@ -1,10 +1,9 @@
-// Weights in 4 bits with a scale, and an offset, for each group of a row, and products with them.
+// Weights in 4 bits with a scale, and an offset, for each group of a row: their quantisation, the products for bf16
+// tokens, and the choice of the type.
 //
 //   w_oj = s_og c_oj + o_og,  c in -8 .. 7,  g = j / group
 //   y_to = sum_j w_oj x_tj
-#include "common.hpp"
-#include "externd_internal.hpp"
-#include "types.hpp"
+#include "grouped.hpp"
 
 namespace externd {
 
@@ -17,17 +16,6 @@ __device__ __forceinline__ int group_code(float x, float inv, double num, double
   float q = rintf(r);
   if (!(fabsf(r - q) <= 0.5f - 0x1p-14f)) q = (float)rint(num / den);
   return (int)q;
-}
-
-__device__ __forceinline__ void put_scale(void* p, int type, long long at, float v) {
-  if (type == 0) static_cast<float*>(p)[at] = v;
-  else if (type == 1) static_cast<_Float16*>(p)[at] = (_Float16)v;
-  else static_cast<__bf16*>(p)[at] = (__bf16)v;
-}
-__device__ __forceinline__ float get_scale(const void* p, int type, long long at) {
-  if (type == 0) return static_cast<const float*>(p)[at];
-  if (type == 1) return (float)static_cast<const _Float16*>(p)[at];
-  return (float)static_cast<const __bf16*>(p)[at];
 }
 
 // A thread makes one word of eight codes, GROUP / 8 threads together a group.
@@ -115,74 +103,16 @@ hipError_t quantize_groups_run(const void* W, int type, long long rows, int n, l
   }
 }
 
-// ---- products -----------------------------------------------------------------------------------------------
-// A wave takes one channel and four tokens, its lanes the words of the row.
-template <typename XT, typename YT>
-__global__ void __launch_bounds__(256) grouped_kernel(const int* __restrict__ Q, long long ldq, const void* scale,
-                                                      const void* offset, int s_type, int group, int m, int n,
-                                                      const XT* __restrict__ X, long long ldx, int tokens, YT* __restrict__ Y,
-                                                      long long ldy) {
-  constexpr int NT = 4;
-  const int lane = threadIdx.x & 63, o = blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (o >= m) return;
-  const int groups = (n + group - 1) / group;
-  for (long long t0 = (long long)blockIdx.y * NT; t0 < tokens; t0 += (long long)gridDim.y * NT) {
-    float acc[NT] = {0, 0, 0, 0};
-    for (int j = lane * 8; j < n; j += 512) {
-      const int word = Q[o * ldq + j / 8];
-      const long long g = (long long)o * groups + j / group;
-      const float s = get_scale(scale, s_type, g), b = offset ? get_scale(offset, s_type, g) : 0.0f;
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        if (t0 + t >= tokens) break;
-        float v[8], sum = 0.0f, part = 0.0f;
-        const XT* x = X + (t0 + t) * ldx + j;
-        if (j + 8 <= n) load8(x, v);
-        else load8_tail(x, n - j, v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          part += (float)((word << (28 - 4 * e)) >> 28) * v[e];
-          sum += v[e];
-        }
-        acc[t] += s * part + (offset ? b * sum : 0.0f);
-      }
-    }
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      float v = acc[t];
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-      if (lane == 0 && t0 + t < tokens) Y[(t0 + t) * ldy + o] = (YT)v;
-    }
-  }
-}
-
-template <typename XT, typename YT>
-static hipError_t grouped_typed(const GroupedLaunch& L, hipStream_t st) {
-  const long long groups = (L.tokens + 3) / 4;
-  hipLaunchKernelGGL((grouped_kernel<XT, YT>), dim3((unsigned)((L.m + 3) / 4), (unsigned)(groups < 1024 ? groups : 1024)), dim3(256),
-                     0, st, L.Q, L.ldq, L.scale, L.offset, L.s_type, L.group, L.m, L.n, static_cast<const XT*>(L.X), L.ldx,
-                     (int)L.tokens, static_cast<YT*>(L.Y), L.ldy);
-  return hipGetLastError();
-}
-
-size_t grouped_workspace_bytes(int, long long, int, int, int) { return 0; }
-
-template <typename XT>
-static hipError_t grouped_from(const GroupedLaunch& L, hipStream_t st) {
-  switch (L.y_type) {
-    case 0: return grouped_typed<XT, float>(L, st);
-    case 1: return grouped_typed<XT, _Float16>(L, st);
-    case 2: return grouped_typed<XT, __bf16>(L, st);
-    default: return hipErrorInvalidValue;
-  }
+// ---- products -----------------------------------------------------------------------------------
+size_t grouped_workspace_bytes(int x_type, long long tokens, int n, int m, int group) {
+  return x_type == 0 ? grouped_bytes<float>(tokens, n, m, group) : grouped_bytes<__bf16>(tokens, n, m, group);
 }
 
 hipError_t grouped_run(const GroupedLaunch& L, hipStream_t st) {
   switch (L.x_type) {
-    case 0: return grouped_from<float>(L, st);
-    case 1: return grouped_from<_Float16>(L, st);
-    case 2: return grouped_from<__bf16>(L, st);
+    case 0: return grouped_run_f32(L, st);
+    case 1: return grouped_run_f16(L, st);
+    case 2: return grouped_typed<__bf16>(L, st);
     default: return hipErrorInvalidValue;
   }
 }
