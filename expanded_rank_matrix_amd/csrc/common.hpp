@@ -202,4 +202,10 @@ __device__ __forceinline__ u128 wave_sum128(u128 v) {
 // Ternary packing: element t in bits 2(t%16)..2(t%16)+1 of word t/16; 00 = 0, 01 = +1, 11 = -1.
 __device__ __forceinline__ unsigned tcode(int s) { return s == 0 ? 0u : (s > 0 ? 1u : 3u); }
 
+// The barrier that hands over a stage of LDS filled by direct loads: each wave's are in LDS before it arrives.
+__device__ __forceinline__ void stage_barrier() {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+}
+
 }  // namespace externd

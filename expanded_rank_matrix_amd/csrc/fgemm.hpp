@@ -2,6 +2,7 @@
 // of fp32, fp16 or bf16 operands, handed to an epilogue.  Each operand lies either with k running
 // along its rows, or with its rows along k ("across": element (r, k) at p[k ld + r]).
 #pragma once
+#include "common.hpp"
 #include "types.hpp"
 
 namespace externd {
@@ -245,7 +246,7 @@ __global__ void __launch_bounds__(64 * WR * WC, 1) ftile_kernel(FOperand A, int 
       interleave<reads, muls, reads < muls ? reads : muls>();
       __builtin_amdgcn_sched_barrier(0);
     };
-    __syncthreads();
+    stage_barrier();
     if (nk > 1) {
       fetch(l1, 1, 0);
       fetch(l1, 1, 1);
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(64 * WR * WC, 1) ftile_kernel(FOperand A, int 
       step(0, l0, 1);
       step(1, l0, 2);
       step(0, l0, 3);
-      __syncthreads();
+      stage_barrier();
       fetch(l0, t + 2, 0);
       step(1, l1, 0);
       fetch(l0, t + 2, 1);
@@ -266,7 +267,7 @@ __global__ void __launch_bounds__(64 * WR * WC, 1) ftile_kernel(FOperand A, int 
       fetch(l0, t + 2, 2);
       step(1, l1, 2);
       step(0, l1, 3);
-      __syncthreads();
+      stage_barrier();
       const bool more = t + 3 < nk;
       if (more) fetch(l1, t + 3, 0);
       step(1, l0, 0);
@@ -279,7 +280,7 @@ __global__ void __launch_bounds__(64 * WR * WC, 1) ftile_kernel(FOperand A, int 
     step(1, l0, 2);
     step(0, l0, 3);
     if (t + 1 < nk) {
-      __syncthreads();
+      stage_barrier();
       step(1, l1, 0);
       step(0, l1, 1);
       step(1, l1, 2);

@@ -12,6 +12,12 @@ __device__ __forceinline__ void put_scale(void* p, int type, long long at, float
   else if (type == 1) static_cast<_Float16*>(p)[at] = (_Float16)v;
   else static_cast<__bf16*>(p)[at] = (__bf16)v;
 }
+__device__ __forceinline__ float get_scale(const void* p, int type, long long at) {
+  if (type == 0) return static_cast<const float*>(p)[at];
+  if (type == 1) return (float)static_cast<const _Float16*>(p)[at];
+  return (float)static_cast<const __bf16*>(p)[at];
+}
+
 // A code enters the matrix cores as the number c + 8: its four bits, the sign turned, are an e4m3 number of 2^-9 (c + 8) as
 // they are (the smallest exponents of e4m3 are one straight line), and one conversion widens two of them.  So eight
 // codes cost nine instructions, and for each group
@@ -313,20 +319,37 @@ static hipError_t few_launch(const GroupedLaunch& all, hipStream_t st) {
 
 // ---- many tokens --------------------------------------------------------------------------------------
 // The tokens are laid out first: aligned rows of whole chunks of 128, fp32 as three planes of pieces, zeros behind a
-// row's end, and beside them -8 times each group's sum.  So the tiles need no other path for odd sizes or addresses, and
-// a group's partial sum starts from the excess it has to lose:
+// row's end, and beside them -8 times each group's sum; and the scales in fp32, a group's channels together.  So the tiles
+// need no other path for odd sizes, addresses or types, and a group's partial sum starts from the excess it has to lose:
 //   part = -8 sum x + sum (c + 8) x,   y += s part + o sum x
 struct GroupedX {
-  const void* x;      // [plane][padded][np]
-  const float* sums;  // [group][padded]
+  const void* x;        // [plane][padded][np]
+  const float* sums;    // [group][padded]
+  const float* scale;   // [group][channels]; groups behind the row's last are 0
+  const float* offset;  // the same, or null
   long long padded;
-  int np, groups;     // groups of np
+  int np, channels;     // channels: m up to a multiple of 128
 };
 
 template <typename XT, int GROUP>
-__global__ void __launch_bounds__(256) grouped_tokens_kernel(const XT* __restrict__ X, long long ldx, long long tokens, int n, int np,
-                                                             long long padded, iv4* __restrict__ out, float* __restrict__ sums) {
+__global__ void __launch_bounds__(256) grouped_tokens_kernel(GroupedLaunch A, GroupedX P, unsigned token_blocks, iv4* __restrict__ out,
+                                                             float* __restrict__ sums, float* __restrict__ scale,
+                                                             float* __restrict__ offset) {
   constexpr int NP = Pieces<XT>::count, L = GROUP / 8;
+  const XT* X = static_cast<const XT*>(A.X);
+  const long long ldx = A.ldx, tokens = A.tokens, padded = P.padded;
+  const int n = A.n, np = P.np;
+  if (blockIdx.x >= token_blocks) {
+    const int groups = (n + GROUP - 1) / GROUP, all = np / GROUP;
+    const long long i = (long long)(blockIdx.x - token_blocks) * 256 + threadIdx.x;
+    if (i >= (long long)P.channels * all) return;
+    const int ch = (int)(i / all), g = (int)(i - (long long)ch * all);
+    const bool in = ch < A.m && g < groups;
+    const long long at = (long long)ch * groups + g, to = (long long)g * P.channels + ch;
+    scale[to] = in ? get_scale(A.scale, A.s_type, at) : 0.0f;
+    if (offset) offset[to] = in ? -0.125f * get_scale(A.offset, A.s_type, at) : 0.0f;
+    return;
+  }
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;  // of eight elements
   const int row8 = np / 8;
   const long long t = i / row8;
@@ -356,6 +379,23 @@ __global__ void __launch_bounds__(256) grouped_tokens_kernel(const XT* __restric
 }
 
 typedef float fv16 __attribute__((ext_vector_type(16)));
+struct Even {
+  static constexpr bool value = true;
+};
+struct Odd {
+  static constexpr bool value = false;
+};
+// Scheduling groups that spread a step's reads of LDS and vector work evenly over its products.
+template <int READS, int MULS, int VEC>
+__device__ __forceinline__ void interleave3() {
+  if constexpr (MULS > 0) {
+    constexpr int r = (READS + MULS - 1) / MULS, v = (VEC + MULS - 1) / MULS;
+    if constexpr (r > 0) __builtin_amdgcn_sched_group_barrier(0x100, r, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if constexpr (v > 0) __builtin_amdgcn_sched_group_barrier(0x002, v, 0);
+    interleave3<READS - r, MULS - 1, VEC - v>();
+  }
+}
 __device__ __forceinline__ fv16 gmul32(__bf16, iv4 a, iv4 b, fv16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8, a), __builtin_bit_cast(bf8, b), c, 0, 0, 0);
 }
@@ -363,183 +403,222 @@ __device__ __forceinline__ fv16 gmul32(_Float16, iv4 a, iv4 b, fv16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(hf8, a), __builtin_bit_cast(hf8, b), c, 0, 0, 0);
 }
 
-// Workgroup: BM tokens and 64 WC channels (32 FN each of WC waves across), WR waves down.  The tokens go through LDS in stages of 128
-// elements a row, two in turn, by direct loads; row r's 16-byte piece c sits at c ^ r % 16, so that 32 rows' pieces of one column take every
-// bank twice.  The codes go from memory to registers, 16 bytes a lane, one stage ahead, and every wave widens its
-// own (the waves down the tile repeat that: it is vector work under the others' products).  A register swap between the
-// wave's halves puts the words where a product of 16 elements wants them.
+// A buffer and a direct load from it into LDS: 16 or 4 bytes a lane, from `at` (per lane) + `base` on, to `l` + the lane's place.  In
+// assembly, since the compiler would wait for every load on its way before it reads LDS; the kernel's own waits see to
+// it.  The scalar wait covers operands that a vector instruction has just written, and m0.
+struct Buffer {
+  iv4 r;
+  __device__ __forceinline__ explicit Buffer(const void* p) {
+    const unsigned long long a = reinterpret_cast<unsigned long long>(p);
+    r = iv4{__builtin_amdgcn_readfirstlane((int)a), __builtin_amdgcn_readfirstlane((int)(a >> 32) & 0xFFFF), -1, 0x00027000};
+  }
+  template <int BYTES>
+  __device__ __forceinline__ void to_lds(int8_t* l, unsigned at, unsigned base) const {
+    typedef __attribute__((address_space(3))) int8_t lbyte;
+    const unsigned m = (unsigned)__builtin_amdgcn_readfirstlane((int)(unsigned)(uintptr_t)(lbyte*)l);
+    if constexpr (BYTES == 16)
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(m), "v"(at), "s"(r), "s"(base) : "memory", "m0");
+    else
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(m), "v"(at), "s"(r), "s"(base) : "memory", "m0");
+  }
+};
+
+// Workgroup: BM tokens and 32 FN WC channels, WR waves down and WC across.  Tokens, codes, group sums and scales go through LDS in
+// stages of 64 elements of a row, four in turn, all by direct loads, so that three stages are on their way while one is
+// used: the codes come from memory once and a stage's products take half of a load's time.
+//   tokens: row r is 128 bytes, its 16-byte piece c at c ^ r / 2 % 8 (16 rows' pieces of one column in different banks)
+//   codes:  loaded a word a lane, so that any order costs nothing: a channel's eight words lie as the wave's halves take
+//           them, 0 2 4 6 and 1 3 5 7
+// Every wave widens its own fragments of codes (the waves down the tile repeat that: vector work under the others'
+// products), one step ahead of the products that take them, and the barrier that hands a stage over comes before
+// the last of its four steps.
 // MFMA D(32 x 32) += A(32 x 16) B(16 x 32): A row = token l % 32, B column = channel l % 32, both with the eight
 // elements at 8 (l / 32) of the step.
-template <typename XT, int BM, int WR, int WC, int FN, int GROUP, int SB>
-__global__ void __launch_bounds__(64 * WR * WC, 1) grouped_tile_kernel(GroupedLaunch L, GroupedX X, int ntm, int ntn, int sper,
-                                                                       float* __restrict__ partial) {
+template <typename XT, int BM, int WR, int WC, int FN, int GROUP>
+__device__ __forceinline__ void grouped_tile(const GroupedLaunch& L, const GroupedX& X, int ntm, int ntn, int sper,
+                                             float* __restrict__ partial) {
   using T = typename Pieces<XT>::type;
-  constexpr int NP = Pieces<XT>::count, G = 128 / GROUP, FM = BM / WR / 32, NW = WR * WC, BN = 32 * FN * WC;
-  constexpr int kRows = NP * BM, PL = kRows / 4 / NW;  // direct loads of a wave and stage: four rows each
-  constexpr int kSums = G * BM * 4 / 1024 > 0 ? G * BM * 4 / 1024 : 1;  // and of the group sums, in all
-  static_assert(PL * 4 * NW == kRows && FM * 32 * WR == BM && kSums <= NW, "tile shape");
-  typedef const __attribute__((address_space(1))) void gptr;
-  typedef __attribute__((address_space(3))) void lptr;
-  constexpr int kStage = kRows * 256 + kSums * 1024;
+  constexpr int NP = Pieces<XT>::count, FM = BM / WR / 32, NW = WR * WC, BN = 32 * FN * WC;
+  constexpr int G = GROUP == 32 ? 2 : 1;               // groups of a stage (two stages to one of 128)
+  constexpr int kRows = NP * BM, PL = kRows / 8 / NW;  // direct loads of a wave and stage: eight rows each
+  constexpr int CL = BN / 8 / NW;                      // of codes: eight channels each
+  constexpr int kSums = (G * BM * 4 + 1023) / 1024;    // of group sums, in all
+  static_assert(PL * 8 * NW == kRows && CL * 8 * NW == BN && FM * 32 * WR == BM && kSums + 2 <= NW && PL % NP == 0, "tile shape");
+  static_assert(G * BN * 4 <= 1024, "scales of a stage");
+  constexpr int kCodes = kRows * 128, kSum = kCodes + BN * 32, kScale = kSum + kSums * 1024, kOffset = kScale + 1024;
+  constexpr int kStage = kOffset + 1024;
   __shared__ __attribute__((aligned(1024))) int8_t l0[kStage];
   __shared__ __attribute__((aligned(1024))) int8_t l1[kStage];
+  __shared__ __attribute__((aligned(1024))) int8_t l2[kStage];
+  __shared__ __attribute__((aligned(1024))) int8_t l3[kStage];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wv / WC, wc = wv % WC, lr = lane & 31, lg = lane >> 5;
-  // workgroups go round the eight XCDs: each gets a run of neighbouring tiles, the tokens of one run of channels after each other
+  // workgroups go round the eight XCDs: each gets a run of neighbouring tiles, the channels of one run of tokens after each
+  // other, so that its L2 holds those tokens
   const int total = ntm * ntn, per = (total + 7) / 8, rem = total % 8;
   const int xcd = blockIdx.x % 8, at = blockIdx.x / 8;
   const int tile = rem == 0 || xcd < rem ? xcd * per + at : rem * per + (xcd - rem) * (per - 1) + at;
-  const long long m0 = (long long)(tile % ntm) * BM;
-  const int n0 = tile / ntm * BN;
-  const int stages = X.np / 128, s0 = blockIdx.y * sper, s1 = s0 + sper < stages ? s0 + sper : stages;
+  const long long m0 = (long long)(tile / ntn) * BM;
+  const int n0 = tile % ntn * BN;
+  const int stages = X.np / 64, s0 = blockIdx.y * sper, s1 = s0 + sper < stages ? s0 + sper : stages;
   const int groups = (L.n + GROUP - 1) / GROUP, words = groups * (GROUP / 8);
-  const bool half = L.s_type == 1, offsets = L.offset != nullptr;
-  const int8_t* xb = static_cast<const int8_t*>(X.x);
-  const int pitch = X.np * 2;
-  unsigned xo[PL];  // this lane's piece of each of the wave's loads, from the tile's first token of the plane
+  const bool offsets = X.offset != nullptr;
+  // Buffer loads: a lane keeps one offset a load, and what changes with the stage is a scalar.  Every offset stays inside
+  // what it is given.
+  const unsigned pitch = (unsigned)X.np * 2, ldq4 = (unsigned)(L.ldq * 4);  // the latter at most kGroupedPitch
+  unsigned xo[PL / NP];  // this lane's piece of each of the wave's loads of a plane, from the tile's first token
 #pragma unroll
-  for (int p = 0; p < PL; ++p) {
-    const int r = (p * NW + wv) * 4 + (lane >> 4);
-    const long long t = m0 + r % BM < L.tokens ? r % BM : L.tokens - 1 - m0;
-    xo[p] = (unsigned)t * (unsigned)pitch + (((lane & 15) ^ (r & 15)) << 4);
+  for (int p = 0; p < PL / NP; ++p) {
+    const int r = (p * NW + wv) * 8 + (lane >> 3);
+    const long long t = m0 + r < L.tokens ? r : L.tokens - 1 - m0;
+    xo[p] = (unsigned)t * pitch + (((lane & 7) ^ ((r >> 1) & 7)) << 4);
   }
-  const int* q[FN];
-  long long sbase[FN];
+  const int word = (lane & 3) * 2 + ((lane >> 2) & 1);  // of the channel's eight, as above
+  const int8_t* xb = static_cast<const int8_t*>(X.x) + m0 * pitch;
+  const int* qb = L.Q + (long long)n0 * L.ldq;
+  unsigned co[CL];
 #pragma unroll
-  for (int j = 0; j < FN; ++j) {
-    const int o = n0 + (wc * FN + j) * 32 + lr, ch = o < L.m ? o : L.m - 1;
-    q[j] = L.Q + (long long)ch * L.ldq;
-    sbase[j] = (long long)ch * groups;
+  for (int p = 0; p < CL; ++p) {
+    const int o = (p * NW + wv) * 8 + (lane >> 3);
+    co[p] = (unsigned)(n0 + o < L.m ? o : L.m - 1 - n0) * ldq4;
   }
-  struct Codes {
-    iv4 w[FN][2];
-    unsigned s[FN][G], o[FN][G];
-  };
-  auto codes = [&](int t) {  // words behind the row's end are its last, and meet zeros
-    Codes d;
-#pragma unroll
-    for (int j = 0; j < FN; ++j) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int k = 16 * t + 8 * h + 4 * lg;
-        d.w[j][h] = *reinterpret_cast<const iv4_any*>(q[j] + (k < words ? k : words - 4));
-      }
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const long long a = sbase[j] + (G * t + g < groups ? G * t + g : groups - 1);
-        d.s[j][g] = scale_bits<SB>(L.scale, a);
-        d.o[j][g] = offsets ? scale_bits<SB>(L.offset, a) : 0u;
-      }
-    }
-    return d;
-  };
   auto fetch = [&](int8_t* l, int t) {
 #pragma unroll
-    for (int p = 0; p < PL; ++p) {
-      const int8_t* x = xb + ((p * NW + wv) * 4 / BM * X.padded + m0) * pitch + t * 256ll;  // the same for the wave
-      __builtin_amdgcn_global_load_lds((gptr*)(x + xo[p]), (lptr*)(l + (p * NW + wv) * 1024), 16, 0, 0);
+    for (int h = 0; h < NP; ++h) {
+      const Buffer bx(xb + h * X.padded * pitch);
+#pragma unroll
+      for (int p = 0; p < PL / NP; ++p) bx.to_lds<16>(l + ((h * (PL / NP) + p) * NW + wv) * 1024, xo[p], t * 128);
     }
+    const int left = words - 8 * t;  // codes behind the row's end are its last word, and meet zeros
+    const unsigned at = (unsigned)(word < left ? 8 * t + word : words - 1) * 4;
+    const Buffer bq(qb);
+#pragma unroll
+    for (int p = 0; p < CL; ++p) bq.to_lds<4>(l + kCodes + (p * NW + wv) * 256, co[p] + at, 0);
+    const long long g0 = (long long)t * 64 / GROUP;
     if (wv < kSums) {
-      // group sums of the stage, [group][BM]: 256 of them a load; behind the last they repeat it
-      const int e = wv * 256 + lane * 4;
-      const int g = e / BM < G ? e / BM : G - 1;
-      const float* s = X.sums + (long long)(G * t + g) * X.padded + m0 + e % BM;
-      __builtin_amdgcn_global_load_lds((gptr*)s, (lptr*)(l + kRows * 256 + wv * 1024), 16, 0, 0);
+      // group sums, [group][BM]: 256 of them a load; behind the last they repeat it
+      const int e = wv * 256 + lane * 4, g = e / BM < G ? e / BM : G - 1;
+      Buffer(X.sums + g0 * X.padded + m0).to_lds<16>(l + kSum + wv * 1024, (unsigned)g * (unsigned)X.padded * 4 + e % BM * 4, 0);
+    } else if (wv < kSums + 2) {
+      // scales, offsets: [group][BN], likewise
+      const int e = lane * 4, g = e / BN < G ? e / BN : G - 1;
+      const float* s = wv == kSums || !offsets ? X.scale : X.offset;
+      Buffer(s + g0 * X.channels + n0).to_lds<16>(l + (wv == kSums ? kScale : kOffset), (unsigned)g * (unsigned)X.channels * 4 + e % BN * 4, 0);
     }
+    __builtin_amdgcn_sched_barrier(0);
   };
-  fv16 acc[FM][FN];
+  constexpr int kLeast = PL + CL;  // direct loads that every wave issues for a stage
+  // The next stage is in LDS: of this wave's loads at most those of the two stages behind it are on their way.  The
+  // reads of this one are done, so that its place may be filled.
+  auto handover = [&]() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(2 * kLeast) : "memory");
+  };
+  fv16 acc[FM][FN], part[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-  const int row = wr * (BM / WR) + lr;  // rows r + 32 f share r % 16
-  auto excess = [&](const float* s) {  // of the 16 rows of an accumulator
-    fv16 v;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const fv4 u = *reinterpret_cast<const fv4*>(s + 8 * x);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[4 * x + e] = u[e];
-    }
-    return v;
-  };
-  auto compute = [&](const int8_t* l, Codes d) {
+  const int row = wr * (BM / WR) + lr, zx = (row >> 1) & 7;  // rows r + 32 f share r / 2 % 8
+  iv4 w[2][FN];  // a stage's codes of this lane: the words of its half
+  iv4 fa[2][NP * FM], fb[2][FN];
+  float s[FN];
+  auto take = [&](int b, const int8_t* l) {
 #pragma unroll
     for (int j = 0; j < FN; ++j)
+      w[b][j] = *reinterpret_cast<const iv4*>(l + kCodes + ((wc * FN + j) * 32 + lr) * 32 + lg * 16) ^ (int)kSignTurn;
+  };
+  auto read = [&](int f, const int8_t* l, int b, int k) {  // fragments of step k
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const iv4 w = d.w[j][h] ^ (int)kSignTurn;
-        const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[1], false, false);
-        const auto b = __builtin_amdgcn_permlane32_swap(w[2], w[3], false, false);
-        d.w[j][h] = iv4{(int)a[0], (int)b[0], (int)a[1], (int)b[1]};
-      }
-    const float* sums = reinterpret_cast<const float*>(l + kRows * 256) + wr * (BM / WR) + 4 * lg;
+    for (int h = 0; h < NP; ++h)
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      fv16 part[FM][FN];
+      for (int i = 0; i < FM; ++i)
+        fa[f][h * FM + i] = *reinterpret_cast<const iv4*>(l + (h * BM + row + 32 * i) * 128 + (((2 * k + lg) ^ zx) << 4));
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        const fv16 lose = excess(sums + g * BM + 32 * i);
+    for (int j = 0; j < FN; ++j) fb[f][j] = widen<T>((unsigned)w[b][j][k]);
+  };
+  auto begin = [&](const int8_t* l, int g) {  // a group: its sums start from the excess
+    const float* sums = reinterpret_cast<const float*>(l + kSum) + g * BM + wr * (BM / WR) + 4 * lg;
+    const float* sc = reinterpret_cast<const float*>(l + kScale) + g * BN + wc * FN * 32 + lr;
+    const float* of = reinterpret_cast<const float*>(l + kOffset) + g * BN + wc * FN * 32 + lr;
 #pragma unroll
-        for (int j = 0; j < FN; ++j) part[i][j] = lose;
-      }
+    for (int j = 0; j < FN; ++j) s[j] = sc[32 * j];
 #pragma unroll
-      for (int k = g * (8 / G); k < (g + 1) * (8 / G); ++k) {
-        iv4 b[FN];
+    for (int i = 0; i < FM; ++i) {
+      fv16 lose;
 #pragma unroll
-        for (int j = 0; j < FN; ++j) b[j] = widen<T>((unsigned)d.w[j][k >> 2][k & 3]);
+      for (int x = 0; x < 4; ++x) {
+        const fv4 u = *reinterpret_cast<const fv4*>(sums + 32 * i + 8 * x);
 #pragma unroll
-        for (int h = 0; h < NP; ++h)
-#pragma unroll
-          for (int i = 0; i < FM; ++i) {
-            const iv4 a = *reinterpret_cast<const iv4*>(l + (h * BM + row + 32 * i) * 256 + (((2 * k + lg) ^ (lr & 15)) << 4));
-#pragma unroll
-            for (int j = 0; j < FN; ++j) part[i][j] = gmul32(T{}, a, b[j], part[i][j]);
-          }
+        for (int e = 0; e < 4; ++e) lose[4 * x + e] = u[e];
       }
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
-        const float s = scale_value<SB>(d.s[j][g], half);
+        part[i][j] = lose;
+        if (offsets) {
+          const float o = of[32 * j];
 #pragma unroll
-        for (int i = 0; i < FM; ++i)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) acc[i][j][e] = fmaf(s, part[i][j][e], acc[i][j][e]);
-      }
-      if (offsets) {
-#pragma unroll
-        for (int i = 0; i < FM; ++i) {
-          const fv16 lose = excess(sums + g * BM + 32 * i);
-#pragma unroll
-          for (int j = 0; j < FN; ++j) {
-            const float o = -0.125f * scale_value<SB>(d.o[j][g], half);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) acc[i][j][e] = fmaf(o, lose[e], acc[i][j][e]);
-          }
+          for (int e = 0; e < 16; ++e) acc[i][j][e] = fmaf(o, lose[e], acc[i][j][e]);
         }
       }
     }
   };
-  if (s0 < s1) {
-    fetch(l0, s0);
-    Codes d = codes(s0);
-    for (int t = s0; t < s1; t += 2) {
-      __syncthreads();  // stage t is in l0, and l1 is read
-      Codes e = d;
-      if (t + 1 < s1) {
-        fetch(l1, t + 1);
-        e = codes(t + 1);
+  auto end = [&]() {
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = fmaf(s[j], part[i][j][e], acc[i][j][e]);
+  };
+  // stage t in l, its codes in w[b] and first fragments read; ln is the next one's place.  EVEN: t is.
+  auto stage = [&](int t, int8_t* l, int8_t* ln, auto even) {
+    constexpr bool EVEN = decltype(even)::value;
+    constexpr int b = EVEN ? 0 : 1;
+    if (GROUP != 128 || EVEN) begin(l, 0);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (GROUP == 32 && k == 2) {
+        end();
+        begin(l, 1);
       }
-      compute(l0, d);
-      if (t + 1 >= s1) break;
-      __syncthreads();
-      if (t + 2 < s1) {
-        fetch(l0, t + 2);
-        d = codes(t + 2);
+      if (k < 3) {
+        read((k + 1) & 1, l, b, k + 1);
+      } else {
+        // behind the last stage it is loaded again, and read by no product: every path waits for the same number
+        handover();
+        fetch(l, t + 4 < s1 ? t + 4 : s1 - 1);
+        take(b ^ 1, ln);
+        read(0, ln, b ^ 1, 0);
       }
-      compute(l1, e);
+#pragma unroll
+      for (int h = 0; h < NP; ++h)
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j) part[i][j] = gmul32(T{}, fa[k & 1][h * FM + i], fb[k & 1][j], part[i][j]);
+      interleave3<NP * FM, NP * FM * FN, 9 * FN>();
+      __builtin_amdgcn_sched_barrier(0);
     }
+    if (GROUP != 128 || !EVEN) end();
+  };
+  if (s0 < s1) {  // s0 and s1 are even
+    fetch(l0, s0);
+    fetch(l1, s0 + 1);
+    fetch(l2, s0 + 2 < s1 ? s0 + 2 : s1 - 1);
+    fetch(l3, s0 + 3 < s1 ? s0 + 3 : s1 - 1);
+    handover();  // one more stage than it takes
+    take(0, l0);
+    read(0, l0, 0, 0);
+    for (int t = s0; t < s1; t += 4) {
+      stage(t, l0, l1, Even{});
+      stage(t + 1, l1, l2, Odd{});
+      if (t + 2 >= s1) break;
+      stage(t + 2, l2, l3, Even{});
+      stage(t + 3, l3, l0, Odd{});
+    }
+    stage_barrier();  // no load is on its way into LDS when the workgroup ends
   }
 #pragma unroll
   for (int i = 0; i < FM; ++i)
@@ -563,6 +642,12 @@ __global__ void __launch_bounds__(64 * WR * WC, 1) grouped_tile_kernel(GroupedLa
     }
 }
 
+template <typename XT, int BM, int WR, int WC, int FN, int GROUP>
+__global__ void __launch_bounds__(64 * WR * WC, 1) grouped_tile_kernel(GroupedLaunch L, GroupedX X, int ntm, int ntn, int sper,
+                                                                       float* __restrict__ partial) {
+  grouped_tile<XT, BM, WR, WC, FN, GROUP>(L, X, ntm, ntn, sper, partial);
+}
+
 // the parts of a row length added in their order
 static __global__ void __launch_bounds__(256) grouped_join_kernel(const float* __restrict__ partial, int parts, long long size, int m,
                                                                   void* Y, int y_type, long long ldy) {
@@ -576,11 +661,13 @@ static __global__ void __launch_bounds__(256) grouped_join_kernel(const float* _
 
 struct GroupedPlan {
   bool few, small;   // the kernel for few tokens; tiles of fewer tokens
-  int np, parts, sper;
+  int np, parts, sper;  // sper: stages of 64 elements of a part
   long long padded;
-  size_t sums, partial, bytes;  // offsets in the workspace, and its size
+  int channels;
+  size_t sums, scale, offset, partial, bytes;  // offsets in the workspace, and its size
 };
-constexpr long long kGroupedRun = 1 << 16;  // tokens of one run
+constexpr long long kGroupedRun = 1 << 16;    // tokens of one run
+constexpr long long kGroupedPitch = 1 << 24;  // bytes between rows of codes, so that a tile's offsets fit 32 bits
 
 template <typename XT>
 static GroupedPlan grouped_plan(long long tokens, int n, int m, int group) {
@@ -594,15 +681,20 @@ static GroupedPlan grouped_plan(long long tokens, int n, int m, int group) {
   P.small = NP == 1 && tokens <= 128;
   const int bm = NP == 3 ? 64 : P.small ? 128 : 256, bn = P.small ? 64 : 128;
   const long long tiles = (tokens + bm - 1) / bm * ((m + bn - 1ll) / bn);
-  const int stages = P.np / 128;
+  const int chunks = P.np / 128;
   long long parts = 512 / tiles;
-  if (parts > stages / 2) parts = stages / 2;
+  if (parts > chunks / 2) parts = chunks / 2;
   if (parts < 1) parts = 1;
-  P.sper = (int)((stages + parts - 1) / parts);
-  P.parts = (stages + P.sper - 1) / P.sper;
+  const int each = (int)((chunks + parts - 1) / parts);
+  P.sper = 2 * each;
+  P.parts = (chunks + each - 1) / each;
   auto al = [](size_t x) { return (x + 1023) / 1024 * 1024; };
   P.sums = al((size_t)NP * P.padded * P.np * 2);
-  P.partial = P.sums + al((size_t)(P.np / group) * P.padded * 4);
+  P.channels = (m + 127) / 128 * 128;
+  const size_t s = al((size_t)(P.np / group) * P.channels * 4);
+  P.scale = P.sums + al((size_t)(P.np / group) * P.padded * 4);
+  P.offset = P.scale + s;
+  P.partial = P.offset + s;
   P.bytes = P.partial + (P.parts > 1 ? al((size_t)P.parts * tokens * m * 4) : 0);
   return P;
 }
@@ -611,7 +703,7 @@ static size_t grouped_bytes(long long tokens, int n, int m, int group) {
   return grouped_plan<XT>(tokens, n, m, group).bytes;
 }
 
-template <typename XT, int GROUP, int SB>
+template <typename XT, int GROUP>
 static hipError_t grouped_tiles(const GroupedLaunch& all, hipStream_t st) {
   GroupedLaunch L = all;
   for (long long t = 0; t < all.tokens; t += kGroupedRun) {
@@ -622,20 +714,22 @@ static hipError_t grouped_tiles(const GroupedLaunch& all, hipStream_t st) {
     char* ws = static_cast<char*>(L.ws);
     float* sums = reinterpret_cast<float*>(ws + P.sums);
     float* partial = P.parts > 1 ? reinterpret_cast<float*>(ws + P.partial) : nullptr;
-    const long long threads = L.tokens * (P.np / 8);
-    hipLaunchKernelGGL((grouped_tokens_kernel<XT, GROUP>), dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, st,
-                       static_cast<const XT*>(L.X), L.ldx, L.tokens, L.n, P.np, P.padded, reinterpret_cast<iv4*>(ws), sums);
-    const GroupedX X{ws, sums, P.padded, P.np, P.np / GROUP};
+    float* scale = reinterpret_cast<float*>(ws + P.scale);
+    float* offset = L.offset ? reinterpret_cast<float*>(ws + P.offset) : nullptr;
+    const GroupedX X{ws, sums, scale, offset, P.padded, P.np, P.channels};
+    const unsigned tb = (unsigned)((L.tokens * (P.np / 8) + 255) / 256), sb = (unsigned)(((long long)P.channels * (P.np / GROUP) + 255) / 256);
+    hipLaunchKernelGGL((grouped_tokens_kernel<XT, GROUP>), dim3(tb + sb), dim3(256), 0, st, L, X, tb, reinterpret_cast<iv4*>(ws), sums,
+                       scale, offset);
     auto go = [&](auto kernel, int bm, int bn, int threads) {
       const long long ntm = (L.tokens + bm - 1) / bm, ntn = (L.m + bn - 1ll) / bn;
       hipLaunchKernelGGL(kernel, dim3((unsigned)(ntm * ntn), (unsigned)P.parts), dim3(threads), 0, st, L, X, (int)ntm, (int)ntn, P.sper,
                          partial);
     };
     if constexpr (Pieces<XT>::count == 3) {
-      go(grouped_tile_kernel<XT, 64, 2, 2, 2, GROUP, SB>, 64, 128, 256);
+      go(grouped_tile_kernel<XT, 64, 2, 2, 2, GROUP>, 64, 128, 256);
     } else {
-      if (P.small) go(grouped_tile_kernel<XT, 128, 2, 2, 1, GROUP, SB>, 128, 64, 256);
-      else go(grouped_tile_kernel<XT, 256, 4, 2, 2, GROUP, SB>, 256, 128, 512);
+      if (P.small) go(grouped_tile_kernel<XT, 128, 2, 2, 1, GROUP>, 128, 64, 256);
+      else go(grouped_tile_kernel<XT, 256, 4, 2, 2, GROUP>, 256, 128, 512);
     }
     if (partial) {
       const long long size = L.tokens * L.m;
@@ -648,7 +742,7 @@ static hipError_t grouped_tiles(const GroupedLaunch& all, hipStream_t st) {
 
 template <typename XT, int GROUP, int SB>
 static hipError_t grouped_sized(const GroupedLaunch& L, hipStream_t st) {
-  if (!grouped_plan<XT>(L.tokens, L.n, L.m, GROUP).few) return grouped_tiles<XT, GROUP, SB>(L, st);
+  if (!grouped_plan<XT>(L.tokens, L.n, L.m, GROUP).few && L.ldq * 4 <= kGroupedPitch) return grouped_tiles<XT, GROUP>(L, st);
   const bool wide = L.m >= 6144;  // 32 channels a workgroup still fill the card
   if (L.tokens <= 16) return wide ? few_launch<XT, 1, 2, GROUP, SB>(L, st) : few_launch<XT, 1, 1, GROUP, SB>(L, st);
   if (L.tokens <= 32) return wide ? few_launch<XT, 2, 2, GROUP, SB>(L, st) : few_launch<XT, 2, 1, GROUP, SB>(L, st);
