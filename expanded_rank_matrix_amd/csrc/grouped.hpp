@@ -18,6 +18,11 @@ __device__ __forceinline__ float get_scale(const void* p, int type, long long at
   return (float)static_cast<const __bf16*>(p)[at];
 }
 
+template <typename T>
+__device__ __forceinline__ void put(T* p, float v) {
+  *p = (T)v;
+}
+
 // A code enters the matrix cores as the number c + 8: its four bits, the sign turned, are an e4m3 number of 2^-9 (c + 8) as
 // they are (the smallest exponents of e4m3 are one straight line), and one conversion widens two of them.  So eight
 // codes cost nine instructions, and for each group
@@ -305,12 +310,14 @@ __global__ void __launch_bounds__(64 * kGroupedWaves) grouped_few_kernel(Grouped
 template <typename XT, int NT, int CT, int GROUP, int SB>
 static hipError_t few_launch(const GroupedLaunch& all, hipStream_t st) {
   GroupedLaunch L = all;
-  const long long step = 65535ll * 16 * NT;
+  // runs of tokens whose threads a launch holds
+  const long long wide = (all.m + 16ll * CT - 1) / (16 * CT), most = (1ll << 22) / wide;
+  const long long step = (most < 1 ? 1 : most < 65535 ? most : 65535) * 16 * NT;
   for (long long t = 0; t < all.tokens; t += step) {
     L.tokens = all.tokens - t < step ? all.tokens - t : step;
     L.X = static_cast<const XT*>(all.X) + t * L.ldx;
     L.Y = static_cast<char*>(all.Y) + t * L.ldy * (L.y_type == 0 ? 4 : 2);
-    hipLaunchKernelGGL((grouped_few_kernel<XT, NT, CT, GROUP, SB>), dim3((unsigned)((L.m + 16ll * CT - 1) / (16 * CT)), (unsigned)((L.tokens + 16 * NT - 1) / (16 * NT))),
+    hipLaunchKernelGGL((grouped_few_kernel<XT, NT, CT, GROUP, SB>), dim3((unsigned)wide, (unsigned)((L.tokens + 16 * NT - 1) / (16 * NT))),
                        dim3(64 * kGroupedWaves), 0, st, L);
   }
   return hipGetLastError();
@@ -403,29 +410,30 @@ __device__ __forceinline__ fv16 gmul32(_Float16, iv4 a, iv4 b, fv16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(hf8, a), __builtin_bit_cast(hf8, b), c, 0, 0, 0);
 }
 
-// A buffer and a direct load from it into LDS: 16 or 4 bytes a lane, from `at` (per lane) + `base` on, to `l` + the lane's place.  In
-// assembly, since the compiler would wait for every load on its way before it reads LDS; the kernel's own waits see to
-// it.  The scalar wait covers operands that a vector instruction has just written, and m0.
+// A buffer and a direct load from it into LDS: 16 or 4 bytes a lane, from `at` (per lane) + `base` on, to `l` + the lane's
+// place.  In assembly, since the compiler would wait for every load on its way before it reads LDS; the kernel's own
+// waits see to it.  Its scalar operands are uniform by construction, written by scalar instructions (which need no wait
+// before a load but m0's one).
 struct Buffer {
   iv4 r;
   __device__ __forceinline__ explicit Buffer(const void* p) {
     const unsigned long long a = reinterpret_cast<unsigned long long>(p);
-    r = iv4{__builtin_amdgcn_readfirstlane((int)a), __builtin_amdgcn_readfirstlane((int)(a >> 32) & 0xFFFF), -1, 0x00027000};
+    r = iv4{(int)a, (int)(a >> 32) & 0xFFFF, -1, 0x00027000};
   }
   template <int BYTES>
   __device__ __forceinline__ void to_lds(int8_t* l, unsigned at, unsigned base) const {
     typedef __attribute__((address_space(3))) int8_t lbyte;
-    const unsigned m = (unsigned)__builtin_amdgcn_readfirstlane((int)(unsigned)(uintptr_t)(lbyte*)l);
+    const unsigned m = (unsigned)(uintptr_t)(lbyte*)l;
     if constexpr (BYTES == 16)
-      asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(m), "v"(at), "s"(r), "s"(base) : "memory", "m0");
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(m), "v"(at), "s"(r), "s"(base) : "memory", "m0");
     else
-      asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(m), "v"(at), "s"(r), "s"(base) : "memory", "m0");
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(m), "v"(at), "s"(r), "s"(base) : "memory", "m0");
   }
 };
 
-// Workgroup: BM tokens and 32 FN WC channels, WR waves down and WC across.  Tokens, codes, group sums and scales go through LDS in
-// stages of 64 elements of a row, four in turn, all by direct loads, so that three stages are on their way while one is
-// used: the codes come from memory once and a stage's products take half of a load's time.
+// Workgroup: BM tokens and 32 FN WC channels, WR waves down and WC across, two workgroups a CU, whose barriers leave each
+// other's waves alone.  Tokens, codes, group sums and scales go through LDS in stages of 64 elements of a row, NB in turn, all by direct
+// loads, so that NB - 1 stages are on their way while one is used.
 //   tokens: row r is 128 bytes, its 16-byte piece c at c ^ r / 2 % 8 (16 rows' pieces of one column in different banks)
 //   codes:  loaded a word a lane, so that any order costs nothing: a channel's eight words lie as the wave's halves take
 //           them, 0 2 4 6 and 1 3 5 7
@@ -434,8 +442,8 @@ struct Buffer {
 // the last of its four steps.
 // MFMA D(32 x 32) += A(32 x 16) B(16 x 32): A row = token l % 32, B column = channel l % 32, both with the eight
 // elements at 8 (l / 32) of the step.
-template <typename XT, int BM, int WR, int WC, int FN, int GROUP>
-__device__ __forceinline__ void grouped_tile(const GroupedLaunch& L, const GroupedX& X, int ntm, int ntn, int sper,
+template <typename XT, int BM, int WR, int WC, int FN, int NB, int GROUP>
+__device__ __forceinline__ void grouped_tile(const GroupedLaunch& L, const GroupedX& X, int ntn, int whole, int parts, int sper,
                                              float* __restrict__ partial) {
   using T = typename Pieces<XT>::type;
   constexpr int NP = Pieces<XT>::count, FM = BM / WR / 32, NW = WR * WC, BN = 32 * FN * WC;
@@ -447,20 +455,26 @@ __device__ __forceinline__ void grouped_tile(const GroupedLaunch& L, const Group
   static_assert(G * BN * 4 <= 1024, "scales of a stage");
   constexpr int kCodes = kRows * 128, kSum = kCodes + BN * 32, kScale = kSum + kSums * 1024, kOffset = kScale + 1024;
   constexpr int kStage = kOffset + 1024;
-  __shared__ __attribute__((aligned(1024))) int8_t l0[kStage];
-  __shared__ __attribute__((aligned(1024))) int8_t l1[kStage];
-  __shared__ __attribute__((aligned(1024))) int8_t l2[kStage];
-  __shared__ __attribute__((aligned(1024))) int8_t l3[kStage];
+  __shared__ __attribute__((aligned(1024))) int8_t lds[NB * kStage];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wv / WC, wc = wv % WC, lr = lane & 31, lg = lane >> 5;
-  // workgroups go round the eight XCDs: each gets a run of neighbouring tiles, the channels of one run of tokens after each
-  // other, so that its L2 holds those tokens
-  const int total = ntm * ntn, per = (total + 7) / 8, rem = total % 8;
-  const int xcd = blockIdx.x % 8, at = blockIdx.x / 8;
-  const int tile = rem == 0 || xcd < rem ? xcd * per + at : rem * per + (xcd - rem) * (per - 1) + at;
+  // The first `whole` tiles are each one workgroup's; the others' row lengths are cut into parts.  Workgroups go round the eight
+  // XCDs: each gets a run of neighbouring tiles, the channels of one run of tokens after each other, so that its L2 holds
+  // those tokens.
+  const int stages = X.np / 64;
+  int tile, s0 = 0, s1 = stages;
+  long long place = -1;  // of the part's tile
+  if ((int)blockIdx.x < whole) {
+    tile = blockIdx.x % 8 * (whole / 8) + blockIdx.x / 8;  // whole is a multiple of 8
+  } else {
+    const int x = blockIdx.x - whole;
+    tile = whole + x / parts;
+    s0 = x % parts * sper;
+    s1 = s0 + sper < stages ? s0 + sper : stages;
+    if (parts > 1) place = x;
+  }
   const long long m0 = (long long)(tile / ntn) * BM;
   const int n0 = tile % ntn * BN;
-  const int stages = X.np / 64, s0 = blockIdx.y * sper, s1 = s0 + sper < stages ? s0 + sper : stages;
   const int groups = (L.n + GROUP - 1) / GROUP, words = groups * (GROUP / 8);
   const bool offsets = X.offset != nullptr;
   // Buffer loads: a lane keeps one offset a load, and what changes with the stage is a scalar.  Every offset stays inside
@@ -482,6 +496,11 @@ __device__ __forceinline__ void grouped_tile(const GroupedLaunch& L, const Group
     const int o = (p * NW + wv) * 8 + (lane >> 3);
     co[p] = (unsigned)(n0 + o < L.m ? o : L.m - 1 - n0) * ldq4;
   }
+  const Buffer bq(qb), bsum(X.sums + m0), bs(X.scale + n0), bo((offsets ? X.offset : X.scale) + n0);
+  // group sums [group][BM], 256 of them a load (behind the last they repeat it), and scales and offsets [group][BN] likewise
+  const int es = wv * 256 + lane * 4, ec = lane * 4;
+  const unsigned so = (unsigned)(es / BM < G ? es / BM : G - 1) * (unsigned)X.padded * 4 + es % BM * 4;
+  const unsigned cs = (unsigned)(ec / BN < G ? ec / BN : G - 1) * (unsigned)X.channels * 4 + ec % BN * 4;
   auto fetch = [&](int8_t* l, int t) {
 #pragma unroll
     for (int h = 0; h < NP; ++h) {
@@ -491,27 +510,19 @@ __device__ __forceinline__ void grouped_tile(const GroupedLaunch& L, const Group
     }
     const int left = words - 8 * t;  // codes behind the row's end are its last word, and meet zeros
     const unsigned at = (unsigned)(word < left ? 8 * t + word : words - 1) * 4;
-    const Buffer bq(qb);
 #pragma unroll
     for (int p = 0; p < CL; ++p) bq.to_lds<4>(l + kCodes + (p * NW + wv) * 256, co[p] + at, 0);
-    const long long g0 = (long long)t * 64 / GROUP;
-    if (wv < kSums) {
-      // group sums, [group][BM]: 256 of them a load; behind the last they repeat it
-      const int e = wv * 256 + lane * 4, g = e / BM < G ? e / BM : G - 1;
-      Buffer(X.sums + g0 * X.padded + m0).to_lds<16>(l + kSum + wv * 1024, (unsigned)g * (unsigned)X.padded * 4 + e % BM * 4, 0);
-    } else if (wv < kSums + 2) {
-      // scales, offsets: [group][BN], likewise
-      const int e = lane * 4, g = e / BN < G ? e / BN : G - 1;
-      const float* s = wv == kSums || !offsets ? X.scale : X.offset;
-      Buffer(s + g0 * X.channels + n0).to_lds<16>(l + (wv == kSums ? kScale : kOffset), (unsigned)g * (unsigned)X.channels * 4 + e % BN * 4, 0);
-    }
+    const unsigned g0 = (unsigned)t * 64 / GROUP * 4;
+    if (wv < kSums) bsum.to_lds<16>(l + kSum + wv * 1024, so, g0 * (unsigned)X.padded);
+    else if (wv == kSums) bs.to_lds<16>(l + kScale, cs, g0 * (unsigned)X.channels);
+    else if (wv == kSums + 1) bo.to_lds<16>(l + kOffset, cs, g0 * (unsigned)X.channels);
     __builtin_amdgcn_sched_barrier(0);
   };
   constexpr int kLeast = PL + CL;  // direct loads that every wave issues for a stage
-  // The next stage is in LDS: of this wave's loads at most those of the two stages behind it are on their way.  The
+  // The next stage is in LDS: of this wave's loads at most those of the NB - 2 stages behind it are on their way.  The
   // reads of this one are done, so that its place may be filled.
   auto handover = [&]() {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(2 * kLeast) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NB - 2) * kLeast) : "memory");
   };
   fv16 acc[FM][FN], part[FM][FN];
 #pragma unroll
@@ -588,7 +599,7 @@ __device__ __forceinline__ void grouped_tile(const GroupedLaunch& L, const Group
       } else {
         // behind the last stage it is loaded again, and read by no product: every path waits for the same number
         handover();
-        fetch(l, t + 4 < s1 ? t + 4 : s1 - 1);
+        fetch(l, t + NB < s1 ? t + NB : s1 - 1);
         take(b ^ 1, ln);
         read(0, ln, b ^ 1, 0);
       }
@@ -604,69 +615,79 @@ __device__ __forceinline__ void grouped_tile(const GroupedLaunch& L, const Group
     if (GROUP != 128 || !EVEN) end();
   };
   if (s0 < s1) {  // s0 and s1 are even
-    fetch(l0, s0);
-    fetch(l1, s0 + 1);
-    fetch(l2, s0 + 2 < s1 ? s0 + 2 : s1 - 1);
-    fetch(l3, s0 + 3 < s1 ? s0 + 3 : s1 - 1);
-    handover();  // one more stage than it takes
-    take(0, l0);
-    read(0, l0, 0, 0);
-    for (int t = s0; t < s1; t += 4) {
-      stage(t, l0, l1, Even{});
-      stage(t + 1, l1, l2, Odd{});
-      if (t + 2 >= s1) break;
-      stage(t + 2, l2, l3, Even{});
-      stage(t + 3, l3, l0, Odd{});
+#pragma unroll
+    for (int i = 0; i < NB; ++i) fetch(lds + i * kStage, s0 + i < s1 ? s0 + i : s1 - 1);
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((NB - 1) * kLeast) : "memory");
+    take(0, lds);
+    read(0, lds, 0, 0);
+    int at = 0;  // of the stage's place
+    auto next = [](int a) { return a == (NB - 1) * kStage ? 0 : a + kStage; };
+    for (int t = s0; t < s1; t += 2) {
+      const int n1 = next(at), n2 = next(n1);
+      stage(t, lds + at, lds + n1, Even{});
+      stage(t + 1, lds + n1, lds + n2, Odd{});
+      at = n2;
     }
     stage_barrier();  // no load is on its way into LDS when the workgroup ends
   }
+  if (place >= 0) {
+    float* p = partial + place * (BM * BN) + (wr * (BM / WR) + 4 * lg) * BN + wc * FN * 32 + lr;
 #pragma unroll
-  for (int i = 0; i < FM; ++i)
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      const int o = n0 + (wc * FN + j) * 32 + lr;
-      const long long t0 = m0 + wr * (BM / WR) + 32 * i + 4 * lg;
-      if (o < L.m) {
-        if (partial) {
-          float* p = partial + blockIdx.y * (L.tokens * L.m) + o;
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) p[(32 * i + 8 * (e >> 2) + (e & 3)) * BN + 32 * j] = acc[i][j][e];
+    return;
+  }
+  auto store = [&](auto* y) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const int o = n0 + (wc * FN + j) * 32 + lr;
+        const long long t0 = m0 + wr * (BM / WR) + 32 * i + 4 * lg;
+        if (o < L.m) {
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            if (t0 + 8 * (e >> 2) + (e & 3) < L.tokens) p[(t0 + 8 * (e >> 2) + (e & 3)) * L.m] = acc[i][j][e];
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (t0 + 8 * (e >> 2) + (e & 3) < L.tokens)
-              put_scale(L.Y, L.y_type, (t0 + 8 * (e >> 2) + (e & 3)) * L.ldy + o, acc[i][j][e]);
+            if (t0 + 8 * (e >> 2) + (e & 3) < L.tokens) put(y + (t0 + 8 * (e >> 2) + (e & 3)) * L.ldy + o, acc[i][j][e]);
         }
       }
-    }
+  };
+  if (L.y_type == 0) store(static_cast<float*>(L.Y));
+  else if (L.y_type == 1) store(static_cast<_Float16*>(L.Y));
+  else store(static_cast<__bf16*>(L.Y));
 }
 
-template <typename XT, int BM, int WR, int WC, int FN, int GROUP>
-__global__ void __launch_bounds__(64 * WR * WC, 1) grouped_tile_kernel(GroupedLaunch L, GroupedX X, int ntm, int ntn, int sper,
-                                                                       float* __restrict__ partial) {
-  grouped_tile<XT, BM, WR, WC, FN, GROUP>(L, X, ntm, ntn, sper, partial);
+template <typename XT, int BM, int WR, int WC, int FN, int NB, int GROUP>
+__global__ void __launch_bounds__(64 * WR * WC, 2) grouped_tile_kernel(GroupedLaunch L, GroupedX X, int ntn, int whole, int parts,
+                                                                       int sper, float* __restrict__ partial) {
+  grouped_tile<XT, BM, WR, WC, FN, NB, GROUP>(L, X, ntn, whole, parts, sper, partial);
 }
 
-// the parts of a row length added in their order
-static __global__ void __launch_bounds__(256) grouped_join_kernel(const float* __restrict__ partial, int parts, long long size, int m,
-                                                                  void* Y, int y_type, long long ldy) {
-  const long long x = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (x >= size) return;
-  float v = 0.0f;
-  for (int p = 0; p < parts; ++p) v += partial[p * size + x];
-  const long long t = x / m;
-  put_scale(Y, y_type, t * ldy + (x - t * m), v);
+// The parts of the tiles behind the whole ones added in their order; a thread adds four channels.
+template <int BM, int BN>
+__global__ void __launch_bounds__(256) grouped_join_kernel(GroupedLaunch L, int ntn, int whole, int parts, const float* __restrict__ partial) {
+  const int x = blockIdx.y * 1024 + threadIdx.x * 4, tile = whole + blockIdx.x;
+  const long long t = (long long)(tile / ntn) * BM + x / BN;
+  const int o = tile % ntn * BN + x % BN;
+  if (t >= L.tokens || o >= L.m) return;
+  const float* p = partial + (long long)blockIdx.x * parts * (BM * BN) + x;
+  fv4 v = {0, 0, 0, 0};
+  for (int i = 0; i < parts; ++i) v += *reinterpret_cast<const fv4*>(p + (long long)i * (BM * BN));
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (o + e < L.m) put_scale(L.Y, L.y_type, t * L.ldy + o + e, v[e]);
 }
 
 struct GroupedPlan {
-  bool few, small;   // the kernel for few tokens; tiles of fewer tokens
-  int np, parts, sper;  // sper: stages of 64 elements of a part
+  bool few, small;  // the kernel for few tokens; tiles of fewer channels
+  int np, channels;
+  int bm, bn, ntn, whole, rest, parts, sper;  // tiles whole and in parts, and stages of 64 elements of a part
   long long padded;
-  int channels;
   size_t sums, scale, offset, partial, bytes;  // offsets in the workspace, and its size
 };
-constexpr long long kGroupedRun = 1 << 16;    // tokens of one run
+constexpr long long kGroupedRun = 1 << 14;    // tokens of one run, so that the group sums' offsets fit 32 bits
 constexpr long long kGroupedPitch = 1 << 24;  // bytes between rows of codes, so that a tile's offsets fit 32 bits
 
 template <typename XT>
@@ -675,14 +696,19 @@ static GroupedPlan grouped_plan(long long tokens, int n, int m, int group) {
   GroupedPlan P{};
   P.few = tokens <= 64;
   if (P.few) return P;
-  if (tokens > kGroupedRun) tokens = kGroupedRun;
   P.np = (n + 127) / 128 * 128;
   P.padded = (tokens + 255) / 256 * 256;
   P.small = NP == 1 && tokens <= 128;
-  const int bm = NP == 3 ? 64 : P.small ? 128 : 256, bn = P.small ? 64 : 128;
-  const long long tiles = (tokens + bm - 1) / bm * ((m + bn - 1ll) / bn);
+  P.bm = NP == 3 ? 64 : 128;
+  P.bn = P.small ? 64 : 128;
+  P.ntn = (int)((m + P.bn - 1ll) / P.bn);
+  const long long tiles = (tokens + P.bm - 1) / P.bm * P.ntn;
+  // 512 workgroups run at a time.  Tiles behind the last whole round are cut along the row, into as many parts as fill
+  // it, of at least two chunks of 128 elements each.
   const int chunks = P.np / 128;
-  long long parts = 512 / tiles;
+  P.whole = (int)(tiles / 512 * 512);
+  P.rest = (int)(tiles - P.whole);
+  long long parts = P.rest ? 512 / P.rest : 1;
   if (parts > chunks / 2) parts = chunks / 2;
   if (parts < 1) parts = 1;
   const int each = (int)((chunks + parts - 1) / parts);
@@ -695,58 +721,71 @@ static GroupedPlan grouped_plan(long long tokens, int n, int m, int group) {
   P.scale = P.sums + al((size_t)(P.np / group) * P.padded * 4);
   P.offset = P.scale + s;
   P.partial = P.offset + s;
-  P.bytes = P.partial + (P.parts > 1 ? al((size_t)P.parts * tokens * m * 4) : 0);
+  P.bytes = P.partial + (P.parts > 1 ? al((size_t)P.parts * P.rest * P.bm * P.bn * 4) : 0);
   return P;
 }
 template <typename XT>
 static size_t grouped_bytes(long long tokens, int n, int m, int group) {
-  return grouped_plan<XT>(tokens, n, m, group).bytes;
+  const long long last = tokens % kGroupedRun;
+  size_t a = grouped_plan<XT>(tokens < kGroupedRun ? tokens : kGroupedRun, n, m, group).bytes;
+  const size_t b = tokens > kGroupedRun && last ? grouped_plan<XT>(last, n, m, group).bytes : 0;
+  return a > b ? a : b;
 }
 
+// one run of tokens
 template <typename XT, int GROUP>
-static hipError_t grouped_tiles(const GroupedLaunch& all, hipStream_t st) {
-  GroupedLaunch L = all;
-  for (long long t = 0; t < all.tokens; t += kGroupedRun) {
-    L.tokens = all.tokens - t < kGroupedRun ? all.tokens - t : kGroupedRun;
-    L.X = static_cast<const XT*>(all.X) + t * L.ldx;
-    L.Y = static_cast<char*>(all.Y) + t * L.ldy * (L.y_type == 0 ? 4 : 2);
-    const GroupedPlan P = grouped_plan<XT>(L.tokens < 65 ? 65 : L.tokens, L.n, L.m, GROUP);
-    char* ws = static_cast<char*>(L.ws);
-    float* sums = reinterpret_cast<float*>(ws + P.sums);
-    float* partial = P.parts > 1 ? reinterpret_cast<float*>(ws + P.partial) : nullptr;
-    float* scale = reinterpret_cast<float*>(ws + P.scale);
-    float* offset = L.offset ? reinterpret_cast<float*>(ws + P.offset) : nullptr;
-    const GroupedX X{ws, sums, scale, offset, P.padded, P.np, P.channels};
-    const unsigned tb = (unsigned)((L.tokens * (P.np / 8) + 255) / 256), sb = (unsigned)(((long long)P.channels * (P.np / GROUP) + 255) / 256);
-    hipLaunchKernelGGL((grouped_tokens_kernel<XT, GROUP>), dim3(tb + sb), dim3(256), 0, st, L, X, tb, reinterpret_cast<iv4*>(ws), sums,
-                       scale, offset);
-    auto go = [&](auto kernel, int bm, int bn, int threads) {
-      const long long ntm = (L.tokens + bm - 1) / bm, ntn = (L.m + bn - 1ll) / bn;
-      hipLaunchKernelGGL(kernel, dim3((unsigned)(ntm * ntn), (unsigned)P.parts), dim3(threads), 0, st, L, X, (int)ntm, (int)ntn, P.sper,
-                         partial);
-    };
-    if constexpr (Pieces<XT>::count == 3) {
-      go(grouped_tile_kernel<XT, 64, 2, 2, 2, GROUP>, 64, 128, 256);
-    } else {
-      if (P.small) go(grouped_tile_kernel<XT, 128, 2, 2, 1, GROUP>, 128, 64, 256);
-      else go(grouped_tile_kernel<XT, 256, 4, 2, 2, GROUP>, 256, 128, 512);
-    }
-    if (partial) {
-      const long long size = L.tokens * L.m;
-      hipLaunchKernelGGL(grouped_join_kernel, dim3((unsigned)((size + 255) / 256)), dim3(256), 0, st, partial, P.parts, size, L.m, L.Y,
-                         L.y_type, L.ldy);
-    }
+static hipError_t grouped_tiles(const GroupedLaunch& L, const GroupedPlan& P, hipStream_t st) {
+  char* ws = static_cast<char*>(L.ws);
+  float* sums = reinterpret_cast<float*>(ws + P.sums);
+  float* partial = P.parts > 1 ? reinterpret_cast<float*>(ws + P.partial) : nullptr;
+  float* scale = reinterpret_cast<float*>(ws + P.scale);
+  float* offset = L.offset ? reinterpret_cast<float*>(ws + P.offset) : nullptr;
+  const GroupedX X{ws, sums, scale, offset, P.padded, P.np, P.channels};
+  const unsigned tb = (unsigned)((L.tokens * (P.np / 8) + 255) / 256), sb = (unsigned)(((long long)P.channels * (P.np / GROUP) + 255) / 256);
+  hipLaunchKernelGGL((grouped_tokens_kernel<XT, GROUP>), dim3(tb + sb), dim3(256), 0, st, L, X, tb, reinterpret_cast<iv4*>(ws), sums,
+                     scale, offset);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(P.whole + P.rest * P.parts)), dim3(256), 0, st, L, X, P.ntn, P.whole, P.parts, P.sper, partial);
+  };
+  auto join = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)P.rest, (unsigned)(P.bm * P.bn / 1024)), dim3(256), 0, st, L, P.ntn, P.whole, P.parts, partial);
+  };
+  if constexpr (Pieces<XT>::count == 3) {
+    go(grouped_tile_kernel<XT, 64, 2, 2, 2, 2, GROUP>);
+    if (partial) join(grouped_join_kernel<64, 128>);
+  } else if (P.small) {
+    go(grouped_tile_kernel<XT, 128, 2, 2, 1, 3, GROUP>);
+    if (partial) join(grouped_join_kernel<128, 64>);
+  } else {
+    go(grouped_tile_kernel<XT, 128, 2, 2, 2, 3, GROUP>);
+    if (partial) join(grouped_join_kernel<128, 128>);
   }
   return hipGetLastError();
 }
 
 template <typename XT, int GROUP, int SB>
-static hipError_t grouped_sized(const GroupedLaunch& L, hipStream_t st) {
-  if (!grouped_plan<XT>(L.tokens, L.n, L.m, GROUP).few && L.ldq * 4 <= kGroupedPitch) return grouped_tiles<XT, GROUP>(L, st);
+static hipError_t grouped_few(const GroupedLaunch& L, hipStream_t st) {
   const bool wide = L.m >= 6144;  // 32 channels a workgroup still fill the card
   if (L.tokens <= 16) return wide ? few_launch<XT, 1, 2, GROUP, SB>(L, st) : few_launch<XT, 1, 1, GROUP, SB>(L, st);
   if (L.tokens <= 32) return wide ? few_launch<XT, 2, 2, GROUP, SB>(L, st) : few_launch<XT, 2, 1, GROUP, SB>(L, st);
   return wide ? few_launch<XT, 4, 2, GROUP, SB>(L, st) : few_launch<XT, 4, 1, GROUP, SB>(L, st);
+}
+
+template <typename XT, int GROUP, int SB>
+static hipError_t grouped_sized(const GroupedLaunch& all, hipStream_t st) {
+  // matrices whose offsets in a tile or number of tiles pass 32 bits take the kernel for few tokens, whatever their number
+  const long long scales = (all.n + 127ll) / 128 * 128 / GROUP * ((all.m + 127ll) / 128 * 128) * 4;
+  if (all.ldq * 4 > kGroupedPitch || scales >= 1ll << 32 || all.m > 1 << 22) return grouped_few<XT, GROUP, SB>(all, st);
+  GroupedLaunch L = all;
+  for (long long t = 0; t < all.tokens; t += kGroupedRun) {
+    L.tokens = all.tokens - t < kGroupedRun ? all.tokens - t : kGroupedRun;
+    L.X = static_cast<const XT*>(all.X) + t * L.ldx;
+    L.Y = static_cast<char*>(all.Y) + t * L.ldy * (L.y_type == 0 ? 4 : 2);
+    const GroupedPlan P = grouped_plan<XT>(L.tokens, L.n, L.m, GROUP);
+    const hipError_t e = P.few ? grouped_few<XT, GROUP, SB>(L, st) : grouped_tiles<XT, GROUP>(L, P, st);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <typename XT>
