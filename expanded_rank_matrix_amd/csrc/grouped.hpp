@@ -29,21 +29,30 @@ __device__ __forceinline__ void put(T* p, float v) {
 //   y += s sum (c + 8) x + (o - 8 s) sum x
 // with sum x from the same x by products with ones.  The excess costs the sums one to two of fp32's bits.
 template <typename T>
-__device__ __forceinline__ iv4 widen(unsigned w) {  // eight codes, signs turned, in their order
-  const unsigned even = w & 0x0F0F0F0Fu, odd = (w >> 4) & 0x0F0F0F0Fu;
-  const unsigned p[2] = {__builtin_amdgcn_perm(odd, even, 0x05010400u), __builtin_amdgcn_perm(odd, even, 0x07030602u)};
+__device__ __forceinline__ iv4 widen_pairs(unsigned a, unsigned b) {  // four bytes each
   iv4 r;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
+    const unsigned p = i == 0 ? a : b;
     if constexpr (__is_same(T, _Float16)) {
-      r[2 * i] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(p[i], 512.0f, false));
-      r[2 * i + 1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(p[i], 512.0f, true));
+      r[2 * i] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(p, 512.0f, false));
+      r[2 * i + 1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(p, 512.0f, true));
     } else {
-      r[2 * i] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(p[i], 512.0f, false));
-      r[2 * i + 1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(p[i], 512.0f, true));
+      r[2 * i] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(p, 512.0f, false));
+      r[2 * i + 1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(p, 512.0f, true));
     }
   }
   return r;
+}
+template <typename T>
+__device__ __forceinline__ iv4 widen(unsigned w) {  // eight codes, signs turned, in their order
+  const unsigned even = w & 0x0F0F0F0Fu, odd = (w >> 4) & 0x0F0F0F0Fu;
+  return widen_pairs<T>(__builtin_amdgcn_perm(odd, even, 0x05010400u), __builtin_amdgcn_perm(odd, even, 0x07030602u));
+}
+// the even ones, then the odd: two instructions fewer, where the tokens are laid out the same
+template <typename T>
+__device__ __forceinline__ iv4 widen_apart(unsigned w) {
+  return widen_pairs<T>(w & 0x0F0F0F0Fu, (w >> 4) & 0x0F0F0F0Fu);
 }
 constexpr unsigned kSignTurn = 0x88888888u;
 
@@ -160,16 +169,15 @@ __device__ __forceinline__ void spread(float v, float (&o)[128 / GROUP]) {
 // 8 (l / 16) of row (column) l % 16; D's column l % 16, rows 4 (l / 16) on.  A lane loads 16 bytes of its channel's codes, and
 // the transposition gives each product 32 consecutive ones, so that groups of 32 need nothing else.  The waves' partial
 // sums add in LDS in their order.
-constexpr int kGroupedWaves = 8;
 
-template <typename XT, int NT, int CT, int GROUP, int SB>
-__global__ void __launch_bounds__(64 * kGroupedWaves) grouped_few_kernel(GroupedLaunch L) {
+template <typename XT, int NT, int CT, int WAVES, int GROUP, int SB>
+__global__ void __launch_bounds__(64 * WAVES) grouped_few_kernel(GroupedLaunch L) {
   using T = typename Pieces<XT>::type;
   constexpr int NP = Pieces<XT>::count, G = 128 / GROUP;
   // chunks whose loads are in flight together, the tokens' among them where those fit the registers
-  constexpr int U = NT * CT == 1 && sizeof(XT) == 2 ? 4 : 2;
+  constexpr int U = NT == 1 && sizeof(XT) == 2 ? 3 : 2;
   constexpr bool EARLY = NT == 1;
-  __shared__ float red[kGroupedWaves][CT * NT * 256];
+  __shared__ float red[WAVES][CT * NT * 256];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lr = lane & 15, lg = lane >> 4;
   const int r0 = blockIdx.x * (16 * CT), n = L.n;
   const long long t0 = (long long)blockIdx.y * (16 * NT);
@@ -261,12 +269,12 @@ __global__ void __launch_bounds__(64 * kGroupedWaves) grouped_few_kernel(Grouped
     }
   };
   const int full = n / 128;
-  for (int c = wv; c < full; c += U * kGroupedWaves) {
+  for (int c = wv; c < full; c += U * WAVES) {
     Chunk d[U];
     iv4 raw[EARLY ? U : 1][4][words8<XT>()];
     // the first chunk again where there are fewer: loads that depend on no branch
 #pragma unroll
-    for (int u = 0; u < U; ++u) d[u] = load(c + u * kGroupedWaves < full ? c + u * kGroupedWaves : c);
+    for (int u = 0; u < U; ++u) d[u] = load(c + u * WAVES < full ? c + u * WAVES : c);
     if constexpr (EARLY) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -274,11 +282,11 @@ __global__ void __launch_bounds__(64 * kGroupedWaves) grouped_few_kernel(Grouped
         for (int k = 0; k < 4; ++k)
 #pragma unroll
           for (int h = 0; h < words8<XT>(); ++h)
-            raw[u][k][h] = word8(x[0] + 128 * (c + u * kGroupedWaves < full ? c + u * kGroupedWaves : c) + 32 * k, h);
+            raw[u][k][h] = word8(x[0] + 128 * (c + u * WAVES < full ? c + u * WAVES : c) + 32 * k, h);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int at = c + u * kGroupedWaves;
+      const int at = c + u * WAVES;
       if (at < full)
         chunk(d[u], [&](int k, int t, iv4 (&p)[NP]) {
           if constexpr (EARLY) whole8<XT>(raw[u][k], p);
@@ -286,7 +294,7 @@ __global__ void __launch_bounds__(64 * kGroupedWaves) grouped_few_kernel(Grouped
         });
     }
   }
-  if (full % kGroupedWaves == wv && n % 128 != 0)  // the rows' end: one wave
+  if (full % WAVES == wv && n % 128 != 0)  // the rows' end: one wave
     chunk(load(full), [&](int k, int t, iv4 (&p)[NP]) { token8<true>(x[t], 128 * full + 32 * k, n - 8 * lg, p); });
 #pragma unroll
   for (int i = 0; i < CT; ++i)
@@ -295,30 +303,30 @@ __global__ void __launch_bounds__(64 * kGroupedWaves) grouped_few_kernel(Grouped
 #pragma unroll
       for (int e = 0; e < 4; ++e) red[wv][(16 * t + 4 * lg + e) * (16 * CT) + 16 * i + lr] = acc[i][t][e];
   __syncthreads();
-  for (int i = threadIdx.x; i < CT * NT * 256; i += 64 * kGroupedWaves) {
+  for (int i = threadIdx.x; i < CT * NT * 256; i += 64 * WAVES) {
     const long long t = t0 + i / (16 * CT);
     const int o = r0 + i % (16 * CT);
     if (t < L.tokens && o < L.m) {
       float v = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kGroupedWaves; ++w) v += red[w][i];
+      for (int w = 0; w < WAVES; ++w) v += red[w][i];
       put_scale(L.Y, L.y_type, t * L.ldy + o, v);
     }
   }
 }
 
-template <typename XT, int NT, int CT, int GROUP, int SB>
+template <typename XT, int NT, int CT, int WAVES, int GROUP, int SB>
 static hipError_t few_launch(const GroupedLaunch& all, hipStream_t st) {
   GroupedLaunch L = all;
   // runs of tokens whose threads a launch holds
-  const long long wide = (all.m + 16ll * CT - 1) / (16 * CT), most = (1ll << 22) / wide;
+  const long long wide = (all.m + 16ll * CT - 1) / (16 * CT), most = (1ll << 21) / wide;
   const long long step = (most < 1 ? 1 : most < 65535 ? most : 65535) * 16 * NT;
   for (long long t = 0; t < all.tokens; t += step) {
     L.tokens = all.tokens - t < step ? all.tokens - t : step;
     L.X = static_cast<const XT*>(all.X) + t * L.ldx;
     L.Y = static_cast<char*>(all.Y) + t * L.ldy * (L.y_type == 0 ? 4 : 2);
-    hipLaunchKernelGGL((grouped_few_kernel<XT, NT, CT, GROUP, SB>), dim3((unsigned)wide, (unsigned)((L.tokens + 16 * NT - 1) / (16 * NT))),
-                       dim3(64 * kGroupedWaves), 0, st, L);
+    hipLaunchKernelGGL((grouped_few_kernel<XT, NT, CT, WAVES, GROUP, SB>), dim3((unsigned)wide, (unsigned)((L.tokens + 16 * NT - 1) / (16 * NT))),
+                       dim3(64 * WAVES), 0, st, L);
   }
   return hipGetLastError();
 }
@@ -367,13 +375,16 @@ __global__ void __launch_bounds__(256) grouped_tokens_kernel(GroupedLaunch A, Gr
   const XT* x = X + t * ldx;
   if (j + 8 <= n) load8(x + j, v);
   else load8_tail(x + j, (long long)n - j, v);
+  float u[8];  // the even ones, then the odd, as the codes are widened
+#pragma unroll
+  for (int e = 0; e < 8; ++e) u[e] = v[e < 4 ? 2 * e : 2 * e - 7];
   if constexpr (NP == 3) {
-    pieces8(v, p);
+    pieces8(u, p);
   } else {
     typedef XT v8 __attribute__((ext_vector_type(8)));
     v8 o;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = (XT)v[e];  // as it was
+    for (int e = 0; e < 8; ++e) o[e] = (XT)u[e];  // as it was
     p[0] = __builtin_bit_cast(iv4, o);
   }
 #pragma unroll
@@ -547,7 +558,7 @@ __device__ __forceinline__ void grouped_tile(const GroupedLaunch& L, const Group
       for (int i = 0; i < FM; ++i)
         fa[f][h * FM + i] = *reinterpret_cast<const iv4*>(l + (h * BM + row + 32 * i) * 128 + (((2 * k + lg) ^ zx) << 4));
 #pragma unroll
-    for (int j = 0; j < FN; ++j) fb[f][j] = widen<T>((unsigned)w[b][j][k]);
+    for (int j = 0; j < FN; ++j) fb[f][j] = widen_apart<T>((unsigned)w[b][j][k]);
   };
   auto begin = [&](const int8_t* l, int g) {  // a group: its sums start from the excess
     const float* sums = reinterpret_cast<const float*>(l + kSum) + g * BM + wr * (BM / WR) + 4 * lg;
@@ -609,7 +620,7 @@ __device__ __forceinline__ void grouped_tile(const GroupedLaunch& L, const Group
         for (int i = 0; i < FM; ++i)
 #pragma unroll
           for (int j = 0; j < FN; ++j) part[i][j] = gmul32(T{}, fa[k & 1][h * FM + i], fb[k & 1][j], part[i][j]);
-      interleave3<NP * FM, NP * FM * FN, 9 * FN>();
+      interleave3<NP * FM, NP * FM * FN, 7 * FN>();
       __builtin_amdgcn_sched_barrier(0);
     }
     if (GROUP != 128 || !EVEN) end();
@@ -757,7 +768,7 @@ static hipError_t grouped_tiles(const GroupedLaunch& L, const GroupedPlan& P, hi
     go(grouped_tile_kernel<XT, 128, 2, 2, 1, 3, GROUP>);
     if (partial) join(grouped_join_kernel<128, 64>);
   } else {
-    go(grouped_tile_kernel<XT, 128, 2, 2, 2, 3, GROUP>);
+    go(grouped_tile_kernel<XT, 128, 2, 2, 2, 2, GROUP>);
     if (partial) join(grouped_join_kernel<128, 128>);
   }
   return hipGetLastError();
@@ -766,9 +777,12 @@ static hipError_t grouped_tiles(const GroupedLaunch& L, const GroupedPlan& P, hi
 template <typename XT, int GROUP, int SB>
 static hipError_t grouped_few(const GroupedLaunch& L, hipStream_t st) {
   const bool wide = L.m >= 6144;  // 32 channels a workgroup still fill the card
-  if (L.tokens <= 16) return wide ? few_launch<XT, 1, 2, GROUP, SB>(L, st) : few_launch<XT, 1, 1, GROUP, SB>(L, st);
-  if (L.tokens <= 32) return wide ? few_launch<XT, 2, 2, GROUP, SB>(L, st) : few_launch<XT, 2, 1, GROUP, SB>(L, st);
-  return wide ? few_launch<XT, 4, 2, GROUP, SB>(L, st) : few_launch<XT, 4, 1, GROUP, SB>(L, st);
+  // sixteen waves where long rows would take eight more than two turns
+  if (L.tokens <= 16)
+    return wide ? few_launch<XT, 1, 2, 8, GROUP, SB>(L, st)
+                : L.n > 4096 ? few_launch<XT, 1, 1, 16, GROUP, SB>(L, st) : few_launch<XT, 1, 1, 8, GROUP, SB>(L, st);
+  if (L.tokens <= 32) return wide ? few_launch<XT, 2, 2, 8, GROUP, SB>(L, st) : few_launch<XT, 2, 1, 8, GROUP, SB>(L, st);
+  return wide ? few_launch<XT, 4, 2, 8, GROUP, SB>(L, st) : few_launch<XT, 4, 1, 8, GROUP, SB>(L, st);
 }
 
 template <typename XT, int GROUP, int SB>
