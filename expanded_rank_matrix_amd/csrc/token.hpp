@@ -251,25 +251,24 @@ struct TokenP {
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
       const TokenCoef c = coef[n0 + c0 + 32 * j + lr];
+      const long long d64 = (long long)c.target - first - m0 - r0 - 4 * lg;
+      const int d = d64 >= 0 && d64 < 32 * FM ? (int)d64 : -1;  // the target among this lane's words
 #pragma unroll
       for (int i = 0; i < FM; ++i)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[i][j][e] = c.gi * exp_neg(acc[i][j][e] - c.m);
-      const long long d = (long long)c.target - first - m0 - r0 - 4 * lg;
-      if (__any(d >= 0 && d < 32 * FM)) {
+        for (int e = 0; e < 16; ++e) {
+          const float q = c.gi * exp_neg(acc[i][j][e] - c.m);
+          acc[i][j][e] = d == 32 * i + 8 * (e >> 2) + (e & 3) ? q - c.g : q;
+        }
+    }
+    if (mr < BM) {
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
 #pragma unroll
         for (int i = 0; i < FM; ++i)
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            if (d == 32 * i + 8 * (e >> 2) + (e & 3)) acc[i][j][e] -= c.g;
-      }
-      if (mr < BM) {
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (r0 + 32 * i + 8 * (e >> 2) + 4 * lg + (e & 3) >= mr) acc[i][j][e] = 0.0f;
-      }
+            acc[i][j][e] = r0 + 32 * i + 8 * (e >> 2) + 4 * lg + (e & 3) < mr ? acc[i][j][e] : 0.0f;
     }
     PT* p = P + n0 * ldp + m0;
     store_columns<PT, BM, BN, WR, WC, FM, FN>(
@@ -350,13 +349,17 @@ __global__ void __launch_bounds__(256) token_join_kernel(const float2* __restric
   if ((long long)blockIdx.x * 16 >= count) return;
   float m = -__FLT_MAX__;
   double s = 0.0;
-  for (int i = k; i < tiles; i += 16) {
-    const float2 p = parts[i * padded + c];  // padded is a multiple of 32
-    if (p.x > m) {
-      s *= (double)exp_neg(m - p.x);
-      m = p.x;
-    }
-    s += (double)p.y * (double)exp_neg(p.x - m);
+  for (int i = k; i < tiles; i += 128) {
+    float2 p[8];  // padded is a multiple of 32
+#pragma unroll
+    for (int u = 0; u < 8; ++u) p[u] = i + 16 * u < tiles ? parts[(i + 16 * u) * padded + c] : make_float2(-__FLT_MAX__, 0.0f);
+    float top = m;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) top = fmaxf(top, p[u].x);
+    s *= (double)exp_neg(m - top);
+    m = top;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) s += (double)p[u].y * (double)exp_neg(p[u].x - m);
   }
   sm[k][t] = m;
   ss[k][t] = s;
@@ -396,8 +399,18 @@ __global__ void __launch_bounds__(256) token_dx_kernel(const float* __restrict__
   const int at = place[r], scale = -meta->scale;
   for (int j = ((int)blockIdx.y * 256 + (int)threadIdx.x) * 4; j < nq; j += (int)gridDim.y * 1024) {
     fv4 s = {0, 0, 0, 0};
-    if (at >= 0)
-      for (int p = 0; p < parts; ++p) s += *reinterpret_cast<const fv4*>(sum + p * stride + (long long)at * nq + j);
+    if (at >= 0) {
+      const float* q = sum + (long long)at * nq + j;
+      int p = 0;
+      for (; p + 8 <= parts; p += 8) {
+        fv4 v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = *reinterpret_cast<const fv4*>(q + (p + u) * stride);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) s += v[u];
+      }
+      for (; p < parts; ++p) s += *reinterpret_cast<const fv4*>(q + p * stride);
+    }
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       if (j + e < n) dX[r * ldx + j + e] = (T)(__is_same(T, _Float16) ? ldexpf(s[e], scale) : s[e]);
@@ -413,8 +426,8 @@ __global__ void __launch_bounds__(256) zero_rows_kernel(T* __restrict__ p, long 
 static inline size_t token_al(size_t x) { return (x + 255) & ~(size_t)255; }
 
 struct TokenPlan {
-  int bn;             // tokens of a tile
-  int bm;             // words, or elements of a hidden row, of a tile of the first two products
+  int shape;          // of the tiles: words (or elements of a hidden row) by tokens, bm x bn
+  int bm, bn;
   int nq;             // n up to a multiple of 16 bytes
   long long padded;   // rows up to a multiple of bn
   int piece;          // words of a piece
@@ -423,10 +436,44 @@ struct TokenPlan {
   size_t meta, list, place, coef, zt, tiles, x, w, p, dx, bytes;  // offsets in the workspace, and its size
 };
 
+// Tile shapes, and how many workgroups of each the card runs at a time with a product's rate.
+struct TokenShape {
+  int bm, bn, slots;
+};
+constexpr TokenShape kTokenShapes[] = {{64, 32, 512}, {128, 32, 1024}, {128, 64, 512}, {128, 128, 512}, {256, 256, 256}};
+
+// 16 bits: up to 128 tokens the narrowest tiles that hold them in one column (reading W is what counts there); more by
+// rounds of 128 x 128 (512 at a time, 0.62 of a 256 x 256 round's time; a round of at most 256 of them 0.38) against
+// 256 x 256.  fp32, whose products are sixteen times slower, by the work of the busiest CU.
+static inline int token_shape(int es, long long rows, int V) {
+  auto tiles = [&](int s) {
+    return (V + kTokenShapes[s].bm - 1ll) / kTokenShapes[s].bm * ((rows + kTokenShapes[s].bn - 1) / kTokenShapes[s].bn);
+  };
+  if (es == 2) {
+    if (rows <= 32) return 1;
+    if (rows <= 64) return 2;
+    if (rows <= 128) return 3;
+    const long long t3 = tiles(3), rest = t3 % 512;
+    const double c3 = 0.62 * (double)(t3 / 512) + (rest == 0 ? 0.0 : rest <= 256 ? 0.38 : 0.62), c4 = (double)((tiles(4) + 255) / 256);
+    return c3 < c4 ? 3 : 4;
+  }
+  int best = 4;
+  double least = 1e300;
+  for (int s : {4, 3, 2, 0}) {
+    const double per = s == 0 ? 512 : 256, c = (double)((tiles(s) + (long long)per - 1) / (long long)per) * kTokenShapes[s].bm * kTokenShapes[s].bn * (256 / per);
+    if (c < least) {
+      least = c;
+      best = s;
+    }
+  }
+  return best;
+}
+
 static inline TokenPlan token_plan(int es, long long rows, int n, int V, bool aligned, bool loss, bool dX, bool dW) {
   TokenPlan P{};
-  P.bn = rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
-  P.bm = P.bn == 256 ? 256 : 128;
+  P.shape = token_shape(es, rows, V);
+  P.bm = kTokenShapes[P.shape].bm;
+  P.bn = kTokenShapes[P.shape].bn;
   const int q = 16 / es;
   P.nq = (n + q - 1) / q * q;
   P.padded = (rows + P.bn - 1) / P.bn * P.bn;
@@ -444,7 +491,7 @@ static inline TokenPlan token_plan(int es, long long rows, int n, int V, bool al
   P.piece = (int)(most < vr ? most : vr);
   // parts of the length, so that dX's few tiles fill the card
   const long long tiles = (P.nq + P.bm - 1) / P.bm * (P.padded / P.bn);
-  long long parts = (P.bn == 256 ? 256 : 512) / tiles;
+  long long parts = kTokenShapes[P.shape].slots / tiles;
   const long long longest = (P.piece * es + 1023) / 1024;  // at least eight stages each
   if (parts > longest) parts = longest;
   P.parts = (int)(parts < 1 ? 1 : parts);
@@ -483,10 +530,15 @@ template <typename T, bool AX, typename EPI>
 static hipError_t token_product(const TokenPlan& P, FOperand A, long long M, FOperand B, long long N, long long K, int parts,
                                 const TokenMeta* meta, const EPI& epi, hipStream_t st) {
   const int* c = &meta->count;
-  switch (P.bn) {
-    case 32: return ftile_launch<T, 128, 32, 4, 1, AX, false, kRowsOfB>(A, M, B, N, K, parts, c, epi, st);
-    case 64: return ftile_launch<T, 128, 64, 2, 2, AX, false, kRowsOfB>(A, M, B, N, K, parts, c, epi, st);
-    case 128: return ftile_launch<T, 128, 128, 2, 2, AX, false, kRowsOfB>(A, M, B, N, K, parts, c, epi, st);
+  switch (P.shape) {
+    case 0:
+      if constexpr (sizeof(T) == 4) return ftile_launch<T, 64, 32, 2, 1, AX, false, kRowsOfB>(A, M, B, N, K, parts, c, epi, st);
+      else return hipErrorInvalidValue;
+    case 1:
+      if constexpr (sizeof(T) == 2) return ftile_launch<T, 128, 32, 4, 1, AX, false, kRowsOfB>(A, M, B, N, K, parts, c, epi, st);
+      else return hipErrorInvalidValue;
+    case 2: return ftile_launch<T, 128, 64, 2, 2, AX, false, kRowsOfB>(A, M, B, N, K, parts, c, epi, st);
+    case 3: return ftile_launch<T, 128, 128, 2, 2, AX, false, kRowsOfB>(A, M, B, N, K, parts, c, epi, st);
     default: return ftile_launch<T, 256, 256, 2, 4, AX, false, kRowsOfB>(A, M, B, N, K, parts, c, epi, st);
   }
 }
@@ -528,10 +580,12 @@ static hipError_t token_typed(const TokenLaunch& L, hipStream_t st) {
   gather(static_cast<const T*>(L.X), L.ldx, P.padded, list, x);
   const FOperand X{x, nq};
   // words first .. first + c - 1, aligned
+  int copied = -1;  // the piece whose copy is there
   auto words = [&](int first, int c) {
     const T* w = W + first * L.ldw;
     if (!P.copy) return FOperand{w, L.ldw};
-    gather(w, L.ldw, c, nullptr, wc);
+    if (copied != first) gather(w, L.ldw, c, nullptr, wc);
+    copied = first;
     return FOperand{wc, nq};
   };
   if (forward) {
