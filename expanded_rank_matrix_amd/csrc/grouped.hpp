@@ -355,14 +355,14 @@ __global__ void __launch_bounds__(256) grouped_tokens_kernel(GroupedLaunch A, Gr
   const long long ldx = A.ldx, tokens = A.tokens, padded = P.padded;
   const int n = A.n, np = P.np;
   if (blockIdx.x >= token_blocks) {
-    const int groups = (n + GROUP - 1) / GROUP, all = np / GROUP;
+    const int groups = (n + GROUP - 1) / GROUP;
     const long long i = (long long)(blockIdx.x - token_blocks) * 256 + threadIdx.x;
-    if (i >= (long long)P.channels * all) return;
-    const int ch = (int)(i / all), g = (int)(i - (long long)ch * all);
+    if (i >= (long long)P.channels * (np / GROUP)) return;
+    const int g = (int)(i / P.channels), ch = (int)(i - (long long)g * P.channels);
     const bool in = ch < A.m && g < groups;
-    const long long at = (long long)ch * groups + g, to = (long long)g * P.channels + ch;
-    scale[to] = in ? get_scale(A.scale, A.s_type, at) : 0.0f;
-    if (offset) offset[to] = in ? -0.125f * get_scale(A.offset, A.s_type, at) : 0.0f;
+    const long long at = (long long)ch * groups + g;
+    scale[i] = in ? get_scale(A.scale, A.s_type, at) : 0.0f;
+    if (offset) offset[i] = in ? -0.125f * get_scale(A.offset, A.s_type, at) : 0.0f;
     return;
   }
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;  // of eight elements

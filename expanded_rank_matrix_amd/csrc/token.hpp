@@ -21,6 +21,8 @@
 // Rows that do not count (target outside the vocabulary, g = 0) are left out: the others' rows are gathered
 // at the start, their number stays on the device and cuts the products.
 #pragma once
+#include <type_traits>
+
 #include "common.hpp"
 #include "externd_internal.hpp"
 #include "fgemm.hpp"
@@ -45,6 +47,29 @@ __device__ __forceinline__ float exp_neg(float d) {
   constexpr float hi = 1.44269502162933349609375f;  // fp32 just below log2 e
   constexpr float lo = (float)(c - (double)hi);
   return __builtin_amdgcn_exp2f(fmaf(d, hi, d * lo));
+}
+
+// A row gathered into an aligned copy by `threads` threads: row r of X (zeros where that is -1), n elements and zeros up to nq.
+template <typename T>
+__device__ __forceinline__ void gather_row(const T* __restrict__ X, long long ldx, int n, long long r, T* __restrict__ out, int nq,
+                                           int thread, int threads) {
+  constexpr int E = 16 / sizeof(T);
+  for (int j = thread * E; j < nq; j += threads * E) {
+    iv4 v = {0, 0, 0, 0};
+    if (r >= 0) {
+      const T* x = X + r * ldx + j;
+      if (j + E <= n) {
+        v = *reinterpret_cast<const iv4_any*>(x);
+      } else {
+        typedef T ev __attribute__((ext_vector_type(E)));
+        ev t;
+#pragma unroll
+        for (int e = 0; e < E; ++e) t[e] = j + e < n ? x[e] : (T)0.0f;
+        v = __builtin_bit_cast(iv4, t);
+      }
+    }
+    *reinterpret_cast<iv4*>(out + j) = v;
+  }
 }
 
 // ---- rows that count ------------------------------------------------------------------------------
@@ -110,30 +135,86 @@ __global__ void __launch_bounds__(kTokenScan) token_rows_kernel(const TI* __rest
   }
 }
 
-// Rows of up to 2^31 elements gathered into an aligned copy: row i of `out` is row list[i] of X (zeros where that is
-// -1), or row i without a list; n elements and zeros up to nq.
+// Up to 1024 rows: the same and the gathering in one launch.  Workgroup i finds the i-th row that counts for itself (four
+// rows a thread) and copies it; the first writes the lists too.
+template <typename T, typename TI>
+__global__ void __launch_bounds__(256) token_start_kernel(const TI* __restrict__ target, const float* __restrict__ weight, int rows,
+                                                          int padded, int V, bool scaled, TokenMeta* meta, int* __restrict__ list,
+                                                          int* __restrict__ place, TokenCoef* __restrict__ coef,
+                                                          float* __restrict__ loss, float* __restrict__ stats,
+                                                          const T* __restrict__ X, long long ldx, int n, T* __restrict__ out, int nq) {
+  __shared__ int sums[4];
+  __shared__ float tops[4];
+  __shared__ int mine;
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  long long tg[4];
+  float g[4], top = 0.0f;
+  int counts[4], n4 = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int r = 4 * (int)threadIdx.x + e;
+    tg[e] = r < rows ? (long long)target[r] : -1;
+    g[e] = r < rows ? (weight ? weight[r] : 1.0f) : 0.0f;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    counts[e] = tg[e] >= 0 && tg[e] < V && g[e] != 0.0f;
+    n4 += counts[e];
+    top = fmaxf(top, counts[e] ? fabsf(g[e]) : 0.0f);
+  }
+  int before = n4;  // the sum over the lanes up to this one
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(before, d);
+    before += lane >= d ? o : 0;
+    top = fmaxf(top, __shfl_xor(top, d));
+  }
+  if (lane == 63) sums[wv] = before;
+  if (lane == 0) tops[wv] = top;
+  if (threadIdx.x == 0) mine = -1;
+  __syncthreads();
+  before -= n4;
+  int count = 0;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    before += w < wv ? sums[w] : 0;
+    count += sums[w];
+    top = fmaxf(top, tops[w]);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int r = 4 * (int)threadIdx.x + e;
+    if (counts[e] && before == (int)blockIdx.x) mine = r;
+    if (blockIdx.x == 0 && r < rows) {
+      place[r] = counts[e] ? before : -1;
+      if (counts[e]) {
+        list[before] = r;
+        coef[before] = TokenCoef{0.0f, 0.0f, g[e], (int)tg[e]};
+      } else if (loss) {
+        loss[r] = 0.0f;
+        stats[2ll * r] = 0.0f;
+        stats[2ll * r + 1] = 0.0f;
+      }
+    }
+    before += counts[e];
+  }
+  if (blockIdx.x == 0) {
+    for (int i = count + (int)threadIdx.x; i < padded; i += 256) {
+      list[i] = -1;
+      coef[i] = TokenCoef{0.0f, 0.0f, 0.0f, -1};
+    }
+    if (threadIdx.x == 0) *meta = TokenMeta{count, scaled && top > 0.0f && top <= __FLT_MAX__ ? 14 - ilogbf(top) : 0};
+  }
+  __syncthreads();
+  gather_row(X, ldx, n, mine, out + blockIdx.x * (long long)nq, nq, (int)threadIdx.x, 256);
+}
+
+// Row i of `out` is row list[i] of X (zeros where that is -1), or row i without a list.
 template <typename T>
 __global__ void __launch_bounds__(256) gather_kernel(const T* __restrict__ X, long long ldx, int n, const int* __restrict__ list,
                                                      T* __restrict__ out, int nq) {
-  constexpr int E = 16 / sizeof(T);
   const long long i = blockIdx.x;
-  const long long r = list ? list[i] : i;
-  for (int j = ((int)blockIdx.y * 256 + (int)threadIdx.x) * E; j < nq; j += (int)gridDim.y * 256 * E) {
-    iv4 v = {0, 0, 0, 0};
-    if (r >= 0) {
-      const T* x = X + r * ldx + j;
-      if (j + E <= n) {
-        v = *reinterpret_cast<const iv4_any*>(x);
-      } else {
-        typedef T ev __attribute__((ext_vector_type(E)));
-        ev t;
-#pragma unroll
-        for (int e = 0; e < E; ++e) t[e] = j + e < n ? x[e] : (T)0.0f;
-        v = __builtin_bit_cast(iv4, t);
-      }
-    }
-    *reinterpret_cast<iv4*>(out + i * nq + j) = v;
-  }
+  gather_row(X, ldx, n, list ? list[i] : i, out + i * nq, nq, (int)(blockIdx.y * 256 + threadIdx.x), (int)gridDim.y * 256);
 }
 
 // ---- the tiles' epilogues ---------------------------------------------------------------------------
@@ -334,25 +415,32 @@ struct TokenDW {
 };
 
 // ---- the launches between ------------------------------------------------------------------------------
-// The tiles' maxima and sums of 16 tokens joined by 16 threads each; loss, stats and what the gradient needs of
-// them.  coef is written where the gradient follows.
+// The tiles' maxima and sums of 16 tokens joined by 64 threads each, all their loads in flight at once for up to 512 tiles; loss,
+// stats and what the gradient needs of them.  coef is written where the gradient follows.
 template <bool GRAD>
-__global__ void __launch_bounds__(256) token_join_kernel(const float2* __restrict__ parts, int tiles, long long padded,
-                                                         const float* __restrict__ zt, const TokenMeta* __restrict__ meta,
-                                                         const int* __restrict__ list, TokenCoef* __restrict__ coef,
-                                                         float* __restrict__ loss, float* __restrict__ stats) {
-  __shared__ float sm[16][17];
-  __shared__ double ss[16][17];
-  const int t = threadIdx.x & 15, k = threadIdx.x >> 4;
-  const long long c = (long long)blockIdx.x * 16 + t;
-  const int count = meta->count;
-  if ((long long)blockIdx.x * 16 >= count) return;
+__global__ void __launch_bounds__(1024) token_join_kernel(const float2* __restrict__ parts, int tiles, long long padded,
+                                                          const float* __restrict__ zt, const TokenMeta* __restrict__ meta,
+                                                          const int* __restrict__ list, TokenCoef* __restrict__ coef,
+                                                          float* __restrict__ loss, float* __restrict__ stats) {
+  __shared__ float sm[16][16];
+  __shared__ double ss[16][16];
+  const int t = threadIdx.x & 15, k = threadIdx.x >> 4, wv = threadIdx.x >> 6;
+  const long long c = (long long)blockIdx.x * 16 + t;  // padded is a multiple of 32
   float m = -__FLT_MAX__;
   double s = 0.0;
-  for (int i = k; i < tiles; i += 128) {
-    float2 p[8];  // padded is a multiple of 32
+  auto add = [&](float pm, double ps) {
+    const float top = fmaxf(m, pm);
+    s = s * (double)exp_neg(m - top) + ps * (double)exp_neg(pm - top);
+    m = top;
+  };
+  const int r = list[c];  // on their way with the parts
+  const TokenCoef k0 = coef[c];
+  const float target = zt[c];
+  const TokenMeta M = *meta;
+  for (int i = k; i < tiles; i += 512) {
+    float2 p[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) p[u] = i + 16 * u < tiles ? parts[(i + 16 * u) * padded + c] : make_float2(-__FLT_MAX__, 0.0f);
+    for (int u = 0; u < 8; ++u) p[u] = i + 64 * u < tiles ? parts[(i + 64 * u) * padded + c] : make_float2(-__FLT_MAX__, 0.0f);
     float top = m;
 #pragma unroll
     for (int u = 0; u < 8; ++u) top = fmaxf(top, p[u].x);
@@ -361,20 +449,26 @@ __global__ void __launch_bounds__(256) token_join_kernel(const float2* __restric
 #pragma unroll
     for (int u = 0; u < 8; ++u) s += (double)p[u].y * (double)exp_neg(p[u].x - m);
   }
-  sm[k][t] = m;
-  ss[k][t] = s;
+#pragma unroll
+  for (int d = 16; d < 64; d <<= 1) add(__shfl_xor(m, d), __shfl_xor(s, d));
+  if ((threadIdx.x & 63) < 16) {
+    sm[wv][t] = m;
+    ss[wv][t] = s;
+  }
   __syncthreads();
-  if (k != 0 || c >= count) return;
-  for (int i = 1; i < 16; ++i) m = fmaxf(m, sm[i][t]);
+  if (wv != 0) return;
+  m = -__FLT_MAX__;
   s = 0.0;
-  for (int i = 0; i < 16; ++i) s += ss[i][t] * (double)exp_neg(sm[i][t] - m);
-  const int r = list[c];
-  const TokenCoef k0 = coef[c];
-  loss[r] = (float)((double)k0.g * ((double)m - (double)zt[c] + log(s)));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) add(sm[4 * k + i][t], ss[4 * k + i][t]);
+#pragma unroll
+  for (int d = 16; d < 64; d <<= 1) add(__shfl_xor(m, d), __shfl_xor(s, d));
+  if (k != 0 || c >= M.count) return;
+  loss[r] = (float)((double)k0.g * ((double)m - (double)target + log(s)));
   stats[2ll * r] = s == 0.0 ? -__builtin_inff() : m;
   stats[2ll * r + 1] = (float)s;
   if (GRAD) {
-    const float g = ldexpf(k0.g, meta->scale);
+    const float g = ldexpf(k0.g, M.scale);
     coef[c] = TokenCoef{m, g / (float)s, g, k0.target};  // as from the stats, to the bit
   }
 }
@@ -543,6 +637,15 @@ static hipError_t token_product(const TokenPlan& P, FOperand A, long long M, FOp
   }
 }
 
+// dW: few tokens make short products, whose stores two workgroups a CU cover
+template <typename T>
+static hipError_t token_dw(int rows, FOperand A, long long M, FOperand B, long long N, long long K, const TokenMeta* meta,
+                           const TokenDW<T>& epi, hipStream_t st) {
+  const int* c = &meta->count;
+  if (rows <= 512) return ftile_launch<T, 128, 128, 2, 2, true, true, kLength>(A, M, B, N, K, 1, c, epi, st);
+  return ftile_launch<T, 256, 256, 2, 4, true, true, kLength>(A, M, B, N, K, 1, c, epi, st);
+}
+
 template <typename T>
 static hipError_t token_typed(const TokenLaunch& L, hipStream_t st) {
   constexpr int ES = (int)sizeof(T);
@@ -566,18 +669,26 @@ static hipError_t token_typed(const TokenLaunch& L, hipStream_t st) {
   const T* W = static_cast<const T*>(L.W);
   const int rows = (int)L.rows, n = L.n, V = L.vocab, nq = P.nq;
   const bool scaled = grad && __is_same(T, _Float16);
-  if (L.target_bytes == 8)
-    hipLaunchKernelGGL((token_rows_kernel<long long>), dim3(1), dim3(kTokenScan), 0, st, static_cast<const long long*>(L.target),
-                       L.weight, rows, (int)P.padded, V, scaled, meta, list, place, coef, L.loss, forward ? L.stats : nullptr);
-  else
-    hipLaunchKernelGGL((token_rows_kernel<int>), dim3(1), dim3(kTokenScan), 0, st, static_cast<const int*>(L.target), L.weight,
-                       rows, (int)P.padded, V, scaled, meta, list, place, coef, L.loss, forward ? L.stats : nullptr);
   auto gather = [&](const T* src, long long ld, long long count, const int* l, T* dst) {
     const int blocks = (nq * ES / 16 + 255) / 256;
     hipLaunchKernelGGL((gather_kernel<T>), dim3((unsigned)count, (unsigned)(blocks < 65535 ? blocks : 65535)), dim3(256), 0, st,
                        src, ld, n, l, dst, nq);
   };
-  gather(static_cast<const T*>(L.X), L.ldx, P.padded, list, x);
+  auto start = [&](auto* target) {
+    using TI = std::remove_pointer_t<decltype(target)>;
+    float* stats = forward ? L.stats : nullptr;
+    if (rows <= 1024) {
+      hipLaunchKernelGGL((token_start_kernel<T, std::remove_const_t<TI>>), dim3((unsigned)P.padded), dim3(256), 0, st, target, L.weight,
+                         rows, (int)P.padded, V, scaled, meta, list, place, coef, L.loss, stats, static_cast<const T*>(L.X), L.ldx, n, x,
+                         nq);
+    } else {
+      hipLaunchKernelGGL((token_rows_kernel<std::remove_const_t<TI>>), dim3(1), dim3(kTokenScan), 0, st, target, L.weight, rows,
+                         (int)P.padded, V, scaled, meta, list, place, coef, L.loss, stats);
+      gather(static_cast<const T*>(L.X), L.ldx, P.padded, list, x);
+    }
+  };
+  if (L.target_bytes == 8) start(static_cast<const long long*>(L.target));
+  else start(static_cast<const int*>(L.target));
   const FOperand X{x, nq};
   // words first .. first + c - 1, aligned
   int copied = -1;  // the piece whose copy is there
@@ -597,9 +708,9 @@ static hipError_t token_typed(const TokenLaunch& L, hipStream_t st) {
     const dim3 g((unsigned)((P.padded + 15) / 16));
     const int nt = (V + P.bm - 1) / P.bm;
     if (grad)
-      hipLaunchKernelGGL((token_join_kernel<true>), g, dim3(256), 0, st, tiles, nt, P.padded, zt, meta, list, coef, L.loss, L.stats);
+      hipLaunchKernelGGL((token_join_kernel<true>), g, dim3(1024), 0, st, tiles, nt, P.padded, zt, meta, list, coef, L.loss, L.stats);
     else
-      hipLaunchKernelGGL((token_join_kernel<false>), g, dim3(256), 0, st, tiles, nt, P.padded, zt, meta, list, coef, L.loss, L.stats);
+      hipLaunchKernelGGL((token_join_kernel<false>), g, dim3(1024), 0, st, tiles, nt, P.padded, zt, meta, list, coef, L.loss, L.stats);
   } else {
     hipLaunchKernelGGL(token_coef_kernel, dim3((unsigned)((P.padded + 255) / 256)), dim3(256), 0, st, L.stats, meta, list, coef);
   }
@@ -612,8 +723,7 @@ static hipError_t token_typed(const TokenLaunch& L, hipStream_t st) {
       if (L.dX)
         TOKEN_TRY((token_product<T, true>(P, w, nq, pp, P.padded, c, P.parts, meta, TokenDX{dx, stride, nq, v == 0}, st)));
       if (L.dW)
-        TOKEN_TRY((ftile_launch<T, 256, 256, 2, 4, true, true, kLength>(
-            X, nq, pp, c, P.padded, 1, &meta->count, TokenDW<T>{meta, static_cast<T*>(L.dW) + v * L.lddw, L.lddw, n}, st)));
+        TOKEN_TRY((token_dw<T>(rows, X, nq, pp, c, P.padded, meta, TokenDW<T>{meta, static_cast<T*>(L.dW) + v * L.lddw, L.lddw, n}, st)));
     }
     if (L.dX) {
       const int blocks = (nq + 1023) / 1024;
