@@ -252,6 +252,27 @@ def quantized_bench(args, erm, torch, A, m, n, stream):
     }), flush=True)
 
 
+def grouped_bench(args, erm, torch, A, m, n, stream):
+    """The same inference through the workload's matrix in 4 bits with group scales (--infer --int4): each
+    step is one externd_apply_grouped call on `batch` fp32 vectors."""
+    Q, scale, offset = erm.quantize_groups(A, 128, scale_dtype=torch.float16, stream=stream)
+    X = torch.randn((args.batch, n), dtype=torch.float32, device="cuda")
+    Y = torch.empty((args.batch, m), dtype=torch.float32, device="cuda")
+    wall, gpu_ms = timed_steps(args, torch, stream, lambda: erm.apply_grouped(Q, scale, X, stream=stream, out=Y))
+    nbytes = float(4 * Q.numel() + 2 * scale.numel() + 4 * args.batch * (m + n))
+    achieved = nbytes / (gpu_ms * 1e-3) / 1e9
+    print(json.dumps({
+        "metric": f"4-bit inference vectors/s ({m}x{n})", "value": args.batch * args.steps / wall, "unit": "vectors/s",
+        "n_gpus": 1, "steps": args.steps, "warmup": args.warmup, "ms_per_step": wall * 1e3 / args.steps,
+        "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": "i4", "data": "synthetic",
+        "config": {"workload": f"infer_int4_{args.workload}", "m": m, "n": n, "batch": args.batch, "group": 128,
+                   "entry": "externd_apply_grouped"},
+        "roofline": {"bound": "hbm", "achieved": achieved, "peak": HBM_PEAK_GBPS, "unit": "GB/s",
+                     "frac": achieved / HBM_PEAK_GBPS, "traffic": None, "gpu_ms_per_call": gpu_ms,
+                     "bytes_per_call": nbytes, "tops": 2e-9 * args.batch * m * n / gpu_ms},
+    }), flush=True)
+
+
 def repair_bench(args, erm, torch, A, h, c, k, m, n, out, stream):
     """One step of repairing the scales of the workload's factors (--repair): the matrix in 8-bit
     integers teaches its factored form on `batch` vectors.  Untimed: the decomposition, the teacher's
@@ -313,6 +334,8 @@ def main():
                     help="time inference from the workload's packed factors instead of the decomposition")
     ap.add_argument("--int8", action="store_true",
                     help="--infer through the workload's matrix in 8-bit integers instead of its factors")
+    ap.add_argument("--int4", action="store_true",
+                    help="--infer through the workload's matrix in 4 bits with group scales")
     ap.add_argument("--repair", action="store_true",
                     help="time a step of repairing the factors' scales by distillation from the 8-bit matrix")
     ap.add_argument("--batch", type=int, default=1, help="vectors per inference call (--infer) or repair step")
@@ -333,8 +356,10 @@ def main():
     args = ap.parse_args()
     if args.int8 and not args.infer:
         ap.error("--int8 is a way of --infer")
-    if args.int8 and args.static:
-        ap.error("--static is a way of the factors' inference, not of --int8")
+    if args.int4 and (not args.infer or args.int8):
+        ap.error("--int4 is a way of --infer, apart from --int8")
+    if (args.int8 or args.int4) and args.static:
+        ap.error("--static is a way of the factors' inference, not of --int8 or --int4")
     if args.infer and args.repair:
         ap.error("--infer and --repair exclude each other")
     if args.oracle_timings:
@@ -376,6 +401,9 @@ def main():
     stream = torch.cuda.current_stream()
     if args.infer and args.int8:
         quantized_bench(args, erm, torch, A, m, n, stream)
+        return
+    if args.infer and args.int4:
+        grouped_bench(args, erm, torch, A, m, n, stream)
         return
     if args.repair:
         repair_bench(args, erm, torch, A, h, c, k, m, n, out, stream)

@@ -15,7 +15,7 @@
 // Roundings: sums of products, exponentials and a tile's sum of them are fp32, the sums over tiles, log S and
 // the loss fp64.  P is rounded once to X's type for the products that follow (as a gradient of logits held in that
 // type would be); its errors are independent and each at most half a step, like those of the
-// result's own rounding.  fp16 P carries a power of two that brings the largest |g| to 2^14 .. 2^15, taken out of
+// result's own rounding, and the largest of a row, the target's, is put back into dX.  fp16 P carries a power of two that brings the largest |g| to 2^14 .. 2^15, taken out of
 // the sums in fp32, so that small probabilities stay above fp16's smallest numbers.
 //
 // Rows that do not count (target outside the vocabulary, g = 0) are left out: the others' rows are gathered
@@ -321,8 +321,9 @@ template <typename PT>
 struct TokenP {
   const TokenCoef* coef;
   PT* P;
+  float* lost;  // what the rounding of the target's P takes
   long long ldp;
-  int first;  // of the piece's words
+  int first;    // of the piece's words
   static constexpr bool kLds = true;
   template <typename T, int BM, int BN, int WR, int WC, int FM, int FN>
   __device__ __forceinline__ void finish(fv16 (&acc)[FM][FN], long long m0, long long n0, int mr, int, int wr, int wc,
@@ -341,6 +342,13 @@ struct TokenP {
           const float q = c.gi * exp_neg(acc[i][j][e] - c.m);
           acc[i][j][e] = d == 32 * i + 8 * (e >> 2) + (e & 3) ? q - c.g : q;
         }
+      if (sizeof(PT) < 4 && __any(d >= 0)) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (d == 32 * i + 8 * (e >> 2) + (e & 3)) lost[n0 + c0 + 32 * j + lr] = acc[i][j][e] - (float)(PT)acc[i][j][e];
+      }
     }
     if (mr < BM) {
 #pragma unroll
@@ -484,13 +492,18 @@ static __global__ void __launch_bounds__(256) token_coef_kernel(const float* __r
   coef[c] = TokenCoef{stats[2 * r], g / stats[2 * r + 1], g, k0.target};
 }
 
-// dX: the parts added and rounded, rows back in their places; rows that do not count are zeros
+// dX: the parts added and rounded, rows back in their places; rows that do not count are zeros.  The target's P is most of a
+// row's, so what its rounding took comes back here: `lost` times its word.  (dW keeps it: its rows are the words'.)
 template <typename T>
 __global__ void __launch_bounds__(256) token_dx_kernel(const float* __restrict__ sum, int parts, long long stride, int nq,
                                                        const TokenMeta* __restrict__ meta, const int* __restrict__ place,
-                                                       T* __restrict__ dX, long long ldx, int n) {
+                                                       const TokenCoef* __restrict__ coef, const float* __restrict__ lost,
+                                                       const T* __restrict__ W, long long ldw, T* __restrict__ dX, long long ldx,
+                                                       int n) {
   const long long r = blockIdx.x;
   const int at = place[r], scale = -meta->scale;
+  const float l = sizeof(T) < 4 && at >= 0 ? lost[at] : 0.0f;
+  const T* w = W + (at >= 0 ? coef[at].target : 0) * ldw;
   for (int j = ((int)blockIdx.y * 256 + (int)threadIdx.x) * 4; j < nq; j += (int)gridDim.y * 1024) {
     fv4 s = {0, 0, 0, 0};
     if (at >= 0) {
@@ -504,6 +517,10 @@ __global__ void __launch_bounds__(256) token_dx_kernel(const float* __restrict__
         for (int u = 0; u < 8; ++u) s += v[u];
       }
       for (; p < parts; ++p) s += *reinterpret_cast<const fv4*>(q + p * stride);
+      if (sizeof(T) < 4) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] = fmaf(l, j + e < n ? (float)w[j + e] : 0.0f, s[e]);
+      }
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e)
@@ -527,7 +544,7 @@ struct TokenPlan {
   int piece;          // words of a piece
   int parts;          // of a piece's length in dX
   bool copy;          // W's rows are copied to aligned ones, a piece at a time
-  size_t meta, list, place, coef, zt, tiles, x, w, p, dx, bytes;  // offsets in the workspace, and its size
+  size_t meta, list, place, coef, zt, lost, tiles, x, w, p, dx, bytes;  // offsets in the workspace, and its size
 };
 
 // Tile shapes, and how many workgroups of each the card runs at a time with a product's rate.
@@ -600,6 +617,7 @@ static inline TokenPlan token_plan(int es, long long rows, int n, int V, bool al
   P.place = take((size_t)rows * 4);
   P.coef = take((size_t)P.padded * sizeof(TokenCoef));
   P.zt = take(loss ? (size_t)P.padded * 4 : 0);
+  P.lost = take(grad ? (size_t)P.padded * 4 : 0);
   P.tiles = take(loss ? (size_t)((V + P.bm - 1) / P.bm) * P.padded * 8 : 0);
   P.x = take((size_t)P.padded * P.nq * es);
   P.w = take(P.copy ? (size_t)P.piece * P.nq * es : 0);
@@ -661,6 +679,7 @@ static hipError_t token_typed(const TokenLaunch& L, hipStream_t st) {
   int* place = reinterpret_cast<int*>(ws + P.place);
   TokenCoef* coef = reinterpret_cast<TokenCoef*>(ws + P.coef);
   float* zt = reinterpret_cast<float*>(ws + P.zt);
+  float* lost = reinterpret_cast<float*>(ws + P.lost);
   float2* tiles = reinterpret_cast<float2*>(ws + P.tiles);
   T* x = reinterpret_cast<T*>(ws + P.x);
   T* wc = reinterpret_cast<T*>(ws + P.w);
@@ -719,7 +738,7 @@ static hipError_t token_typed(const TokenLaunch& L, hipStream_t st) {
     for (int v = 0; v < V; v += P.piece) {
       const int c = V - v < P.piece ? V - v : P.piece;
       const FOperand w = words(v, c), pp{p, P.piece};
-      TOKEN_TRY((token_product<T, false>(P, w, c, X, P.padded, nq, 1, meta, TokenP<T>{coef, p, P.piece, v}, st)));
+      TOKEN_TRY((token_product<T, false>(P, w, c, X, P.padded, nq, 1, meta, TokenP<T>{coef, p, lost, P.piece, v}, st)));
       if (L.dX)
         TOKEN_TRY((token_product<T, true>(P, w, nq, pp, P.padded, c, P.parts, meta, TokenDX{dx, stride, nq, v == 0}, st)));
       if (L.dW)
@@ -728,7 +747,7 @@ static hipError_t token_typed(const TokenLaunch& L, hipStream_t st) {
     if (L.dX) {
       const int blocks = (nq + 1023) / 1024;
       hipLaunchKernelGGL((token_dx_kernel<T>), dim3((unsigned)rows, (unsigned)blocks), dim3(256), 0, st, dx, P.parts, stride, nq,
-                         meta, place, static_cast<T*>(L.dX), L.lddx, n);
+                         meta, place, coef, lost, W, L.ldw, static_cast<T*>(L.dX), L.lddx, n);
     }
   }
   return hipGetLastError();
