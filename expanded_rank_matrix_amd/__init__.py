@@ -682,6 +682,8 @@ def quantize_groups(W, group: int = 128, offsets: bool = False, scale_dtype=None
     ldw = _rows(W, _FLOAT, "W")
     if group not in (32, 64, 128):
         raise ValueError("group must be 32, 64 or 128")
+    if out is not None:
+        _given(**{"out[0]": out[0], "out[1]": out[1]})
     if scale_dtype is None:
         scale_dtype = W.dtype if out is None else out[1].dtype
     if scale_dtype not in _FLOAT:
@@ -706,7 +708,6 @@ def _quantize_groups(W, w_type, ldw, group, offsets, scale_dtype, out, stream):
         offset = torch.empty(shapes[2], dtype=scale_dtype, device=dev) if offsets else None
     else:
         Q, scale, offset = out
-        _given(**{"out[0]": Q, "out[1]": scale})
         if (offset is None) == bool(offsets):
             raise ValueError("out must hold an offset with offsets and only then")
         _require(Q, (torch.int32, torch.uint32), "out[0]", shape=shapes[0], device=dev)

@@ -705,7 +705,9 @@ template <typename XT>
 static GroupedPlan grouped_plan(long long tokens, int n, int m, int group) {
   constexpr int NP = Pieces<XT>::count;
   GroupedPlan P{};
-  P.few = tokens <= 64;
+  // and matrices whose offsets in a tile, or number of tiles, pass 32 bits take the kernel for few tokens, whatever their number
+  const long long scales = (n + 127ll) / 128 * 128 / group * ((m + 127ll) / 128 * 128) * 4;
+  P.few = tokens <= 64 || scales >= 1ll << 32 || m > 1 << 22;
   if (P.few) return P;
   P.np = (n + 127) / 128 * 128;
   P.padded = (tokens + 255) / 256 * 256;
@@ -787,9 +789,7 @@ static hipError_t grouped_few(const GroupedLaunch& L, hipStream_t st) {
 
 template <typename XT, int GROUP, int SB>
 static hipError_t grouped_sized(const GroupedLaunch& all, hipStream_t st) {
-  // matrices whose offsets in a tile or number of tiles pass 32 bits take the kernel for few tokens, whatever their number
-  const long long scales = (all.n + 127ll) / 128 * 128 / GROUP * ((all.m + 127ll) / 128 * 128) * 4;
-  if (all.ldq * 4 > kGroupedPitch || scales >= 1ll << 32 || all.m > 1 << 22) return grouped_few<XT, GROUP, SB>(all, st);
+  if (all.ldq * 4 > kGroupedPitch) return grouped_few<XT, GROUP, SB>(all, st);
   GroupedLaunch L = all;
   for (long long t = 0; t < all.tokens; t += kGroupedRun) {
     L.tokens = all.tokens - t < kGroupedRun ? all.tokens - t : kGroupedRun;

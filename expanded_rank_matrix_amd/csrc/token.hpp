@@ -529,8 +529,9 @@ __global__ void __launch_bounds__(256) token_dx_kernel(const float* __restrict__
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256) zero_rows_kernel(T* __restrict__ p, long long ld, int n) {
-  for (int j = (int)threadIdx.x; j < n; j += 256) p[blockIdx.x * ld + j] = (T)0.0f;
+__global__ void __launch_bounds__(256) zero_rows_kernel(T* __restrict__ p, long long ld, int rows, int n) {
+  for (long long r = blockIdx.x; r < rows; r += gridDim.x)
+    for (int j = (int)threadIdx.x; j < n; j += 256) p[r * ld + j] = (T)0.0f;
 }
 
 // ---- the plan ----------------------------------------------------------------------------------------------
@@ -595,9 +596,10 @@ static inline TokenPlan token_plan(int es, long long rows, int n, int V, bool al
   const long long row = (grad ? P.padded * es : 0) > (P.copy ? (long long)P.nq * es : 0) ? P.padded * es : (long long)P.nq * es;
   long long most = !grad && !P.copy ? vr : (128ll << 20) / row / 256 * 256;
   if (most < 256) most = 256;
-  // and tiles that a launch holds: 2^20 words by up to 2^17 elements, or 2^21 tiles of words and tokens
-  const long long held = (1ll << 21) / (P.padded / P.bn) * P.bm / 256 * 256;
+  // and 2^21 tiles, which a launch holds: of words and tokens, and (dW) of words and elements of a hidden row
+  const long long held = (1ll << 21) / (P.padded / P.bn) * P.bm / 256 * 256, wide = (1ll << 21) / ((P.nq + 127) / 128) * 128 / 256 * 256;
   if (most > held) most = held;
+  if (most > wide) most = wide;
   if (most > 1 << 20) most = 1 << 20;
   P.piece = (int)(most < vr ? most : vr);
   // parts of the length, so that dX's few tiles fill the card
@@ -664,11 +666,18 @@ static hipError_t token_dw(int rows, FOperand A, long long M, FOperand B, long l
   return ftile_launch<T, 256, 256, 2, 4, true, true, kLength>(A, M, B, N, K, 1, c, epi, st);
 }
 
+// Blocks of a row beside `count` rows: a launch holds below 2^32 threads, the kernels go on from there.
+static inline unsigned token_blocks(long long count, int wanted) {
+  const long long most = (1ll << 23) / count;
+  return (unsigned)(most < 1 ? 1 : wanted < most ? wanted : most);
+}
+
 template <typename T>
 static hipError_t token_typed(const TokenLaunch& L, hipStream_t st) {
   constexpr int ES = (int)sizeof(T);
   if (L.rows == 0) {  // dW alone: zeros
-    hipLaunchKernelGGL((zero_rows_kernel<T>), dim3((unsigned)L.vocab), dim3(256), 0, st, static_cast<T*>(L.dW), L.lddw, L.n);
+    hipLaunchKernelGGL((zero_rows_kernel<T>), dim3((unsigned)(L.vocab < 1 << 20 ? L.vocab : 1 << 20)), dim3(256), 0, st,
+                       static_cast<T*>(L.dW), L.lddw, L.vocab, L.n);
     return hipGetLastError();
   }
   const bool forward = L.loss != nullptr, grad = L.dX || L.dW;
@@ -689,9 +698,8 @@ static hipError_t token_typed(const TokenLaunch& L, hipStream_t st) {
   const int rows = (int)L.rows, n = L.n, V = L.vocab, nq = P.nq;
   const bool scaled = grad && __is_same(T, _Float16);
   auto gather = [&](const T* src, long long ld, long long count, const int* l, T* dst) {
-    const int blocks = (nq * ES / 16 + 255) / 256;
-    hipLaunchKernelGGL((gather_kernel<T>), dim3((unsigned)count, (unsigned)(blocks < 65535 ? blocks : 65535)), dim3(256), 0, st,
-                       src, ld, n, l, dst, nq);
+    hipLaunchKernelGGL((gather_kernel<T>), dim3((unsigned)count, token_blocks(count, (nq * ES / 16 + 255) / 256)), dim3(256), 0, st, src,
+                       ld, n, l, dst, nq);
   };
   auto start = [&](auto* target) {
     using TI = std::remove_pointer_t<decltype(target)>;
@@ -745,8 +753,7 @@ static hipError_t token_typed(const TokenLaunch& L, hipStream_t st) {
         TOKEN_TRY((token_dw<T>(rows, X, nq, pp, c, P.padded, meta, TokenDW<T>{meta, static_cast<T*>(L.dW) + v * L.lddw, L.lddw, n}, st)));
     }
     if (L.dX) {
-      const int blocks = (nq + 1023) / 1024;
-      hipLaunchKernelGGL((token_dx_kernel<T>), dim3((unsigned)rows, (unsigned)blocks), dim3(256), 0, st, dx, P.parts, stride, nq,
+      hipLaunchKernelGGL((token_dx_kernel<T>), dim3((unsigned)rows, token_blocks(rows, (nq + 1023) / 1024)), dim3(256), 0, st, dx, P.parts, stride, nq,
                          meta, place, coef, lost, W, L.ldw, static_cast<T*>(L.dX), L.lddx, n);
     }
   }

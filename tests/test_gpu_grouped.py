@@ -288,6 +288,43 @@ def test_offsets_past_32_bits():
     assert torch.equal(y.cpu().double(), product(c, s, o, big, 64)[0])
 
 
+@pytest.mark.parametrize("tokens", [2, 90])
+def test_rows_of_codes_too_far_apart_for_a_tile(tokens):
+    """2^23 words between rows: a tile's offsets would pass 32 bits."""
+    c, s, o, x = exact_inputs(tokens, 200, 20, 64, "bf16", "f32", True)
+    Q = packed(c, 64)
+    room = torch.empty(20 << 23, dtype=torch.int32, device="cuda")
+    far = room.as_strided((20, Q.shape[1]), (1 << 23, 1))
+    far.copy_(Q)
+    y = erm.apply_grouped(far, s.cuda(), x.cuda(), offset=o.cuda(), group=64, out_dtype=torch.float32)
+    assert torch.equal(y.cpu().double(), product(c, s, o, x, 64)[0])
+
+
+@pytest.mark.parametrize("tokens", [1, 30, 90])
+def test_smallest_fp16_tokens_count(tokens):
+    """Multiples of fp16's smallest number, 2^-24: whole numbers once scaled, so the products are exact."""
+    c, s, o, x = exact_inputs(tokens, 300, 50, 32, "f16", "f32", True)
+    y = erm.apply_grouped(packed(c, 32).cuda(), s.cuda(), (x.float() * 2.0**-24).half().cuda(), offset=o.cuda(), group=32, out_dtype=torch.float32)
+    assert torch.equal(y.cpu().double() * 2.0**24, product(c, s, o, x, 32)[0])
+
+
+@pytest.mark.parametrize("xd,tokens", [("bf16", 16384 + 30), ("f32", 16384 + 100)])
+def test_more_tokens_than_a_run(xd, tokens):
+    c, s, o, x = exact_inputs(tokens, 70, 40, 32, xd, "f16", True)
+    y = erm.apply_grouped(packed(c, 32).cuda(), s.cuda(), x.cuda(), offset=o.cuda(), group=32, out_dtype=torch.float32)
+    assert torch.equal(y.cpu().double(), product(c, s, o, x, 32)[0])
+
+
+@pytest.mark.parametrize("xd", TYPES)
+def test_whole_rounds_of_tiles_and_tiles_in_parts(xd):
+    """More tiles than the card holds at once (512), a last round of some."""
+    tokens, m = (1100, 8200) if xd != "f32" else (500, 8300)
+    c, s, o, x = exact_inputs(tokens, 520, m, 64, xd, "f32", True)
+    y = erm.apply_grouped(packed(c, 64).cuda(), s.cuda(), x.cuda(), offset=o.cuda(), group=64, out_dtype=torch.float32)
+    w = (c.cuda().double() * spread(s.cuda(), 64, 520) + spread(o.cuda(), 64, 520)).t().contiguous()
+    assert torch.equal(y.double(), x.cuda().double() @ w)
+
+
 def test_binding_refusals():
     Q, s, o = erm.quantize_groups(torch.randn((8, 100)).cuda(), 32, True)
     x = torch.randn((3, 100)).cuda()
@@ -303,6 +340,6 @@ def test_binding_refusals():
         ok(out=x[:, :8])
     w = torch.randn((8, 100)).cuda()
     for bad in (dict(W=w.cpu()), dict(W=w.t()), dict(W=w.int()), dict(group=48), dict(scale_dtype=torch.int8), dict(out=(Q, s, o)),
-                dict(out=(Q, s, None), offsets=True), dict(W=None)):
+                dict(out=(Q, s, None), offsets=True), dict(out=(Q, None, None)), dict(W=None)):
         with pytest.raises(ValueError):
             erm.quantize_groups(**{**dict(W=w, group=32), **bad})
