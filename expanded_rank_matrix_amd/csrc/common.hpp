@@ -202,6 +202,20 @@ __device__ __forceinline__ u128 wave_sum128(u128 v) {
 // Ternary packing: element t in bits 2(t%16)..2(t%16)+1 of word t/16; 00 = 0, 01 = +1, 11 = -1.
 __device__ __forceinline__ unsigned tcode(int s) { return s == 0 ? 0u : (s > 0 ? 1u : 3u); }
 
+// Direct loads of 16 bytes a lane into LDS at l + 16 (lane), from a lane's own address, or from a lane's offset behind a
+// uniform one.  In assembly, since the compiler would wait for every load on its way before it reads LDS; the kernels'
+// own waits see to it.  l and the uniform address come from scalar instructions, which need no wait before a load but m0's one.
+__device__ __forceinline__ unsigned lds_address(int8_t* l) {
+  typedef __attribute__((address_space(3))) int8_t lbyte;
+  return (unsigned)(uintptr_t)(lbyte*)l;
+}
+__device__ __forceinline__ void lds_load16(int8_t* l, const int8_t* p) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds_address(l)), "v"(p) : "memory", "m0");
+}
+__device__ __forceinline__ void lds_load16(int8_t* l, const int8_t* base, unsigned at) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds_address(l)), "v"(at), "s"(base) : "memory", "m0");
+}
+
 // The barrier that hands over a stage of LDS filled by direct loads: each wave's are in LDS before it arrives.
 __device__ __forceinline__ void stage_barrier() {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");

@@ -56,41 +56,40 @@ __device__ __forceinline__ void interleave() {
 // row l % 32 of lane l, with 16 bytes of k each at 16 (l / 32) of the step; accumulator element i of lane l
 // is row 8 (i / 4) + 4 (l / 32) + i % 4, column l % 32).
 //
-// The operands pass through LDS in stages of 128 bytes of k a row (64 or 32 elements), two stages in turn,
-// by direct loads of 16 bytes a lane.
-//   along:  row r is 128 bytes and its 16-byte piece c sits at c ^ (r / 2 % 8), so that 16 consecutive
+// The operands pass through LDS in stages of KB bytes of k a row (64 or 128), NB stages in turn, by direct loads of 16
+// bytes a lane, so that NB - 1 stages are on their way while one is used.
+//   along:  row r is KB bytes and its 16-byte pieces change places with r (see place()), so that 16 consecutive
 //           rows' pieces of one column lie in different banks
 //   across: row k holds the tile's elements, 16-byte pieces.  fp16 and bf16 fragments are read by the
 //           transposing load (16 lanes read four rows of 16 elements and get four k of an element each);
 //           a wave's read takes 64 bytes of each of four rows at a time, so 64-byte chunk x of row k sits
-//           at x ^ k % 4, all banks once.  fp32 fragments are four reads of one row each, the wave's halves four rows apart, and
-//           the chunks of 128 bytes change places with k / 4.
+//           at x ^ k % 4, all banks once.  fp32 fragments are four reads of one row each, the wave's halves four rows
+//           apart, and the chunks of 128 bytes change places with k / 4.
 // The fragments of the next step are read under the products of this one, and the barrier that hands a
-// stage over comes before the last of its four steps.
+// stage over comes before the last of its steps.
 constexpr int kFGroup = 4;
 
-template <typename T, int ROWS, bool ACROSS>
-struct FStage {  // where an operand's piece lies in a stage
-  static constexpr int PPR = ACROSS ? ROWS * (int)sizeof(T) / 16 : 8;  // pieces of a row in LDS
-  // across: what row k's pieces are moved by (xor)
-  __device__ __forceinline__ static int swap(int k) {
-    if (sizeof(T) == 4) return PPR >= 16 ? ((k >> 2) & 1) << 3 : 0;
-    return PPR >= 16 ? (k & 3) << 2 : PPR == 8 ? ((k >> 1) & 1) << 2 : 0;
+template <typename T, int ROWS, bool ACROSS, int KB>
+struct FStage {  // where an operand's pieces lie in a stage
+  static constexpr int PPR = ACROSS ? ROWS * (int)sizeof(T) / 16 : KB / 16;  // pieces of a row in LDS
+  // what row r's pieces are moved by (xor)
+  __device__ __forceinline__ static int place(int r) {
+    if (!ACROSS) return KB == 128 ? (r >> 1) & 7 : (r >> 2) & 3;
+    if (sizeof(T) == 4) return PPR >= 16 ? ((r >> 2) & 1) << 3 : 0;
+    return PPR >= 16 ? (r & 3) << 2 : PPR == 8 ? ((r >> 1) & 1) << 2 : 0;
   }
 };
 
-template <typename T, int BM, int BN, int WR, int WC, bool AX, bool BX, FCount CUT, typename EPI>
-__global__ void __launch_bounds__(64 * WR * WC, 1) ftile_kernel(FOperand A, int M, FOperand B, int N, int Kall, int kper,
-                                                                int ntm, int ntn, const int* __restrict__ count, EPI epi) {
-  typedef const __attribute__((address_space(1))) void gptr;
-  typedef __attribute__((address_space(3))) void lptr;
-  constexpr int NW = WR * WC, PA = BM / 8 / NW, PB = BN / 8 / NW, KS = 128 / (int)sizeof(T), ES = (int)sizeof(T);
-  constexpr int FM = BM / WR / 32, FN = BN / WC / 32;
-  static_assert(PA * 8 * NW == BM && PB * 8 * NW == BN && FM * 32 * WR == BM && FN * 32 * WC == BN, "tile shape");
-  using SA = FStage<T, BM, AX>;
-  using SB = FStage<T, BN, BX>;
-  __shared__ __attribute__((aligned(1024))) int8_t l0[(BM + BN) * 128];
-  __shared__ __attribute__((aligned(1024))) int8_t l1[(BM + BN) * 128];
+template <typename T, int BM, int BN, int WR, int WC, int KB, int NB, bool AX, bool BX, FCount CUT, typename EPI>
+__global__ void __launch_bounds__(64 * WR * WC, WR * WC >= 8 ? 1 : 2) ftile_kernel(FOperand A, int M, FOperand B, int N, int Kall,
+                                                                                   int kper, int ntm, int ntn,
+                                                                                   const int* __restrict__ count, EPI epi) {
+  constexpr int NW = WR * WC, PA = BM * KB / 1024 / NW, PB = BN * KB / 1024 / NW, ES = (int)sizeof(T), KS = KB / ES;
+  constexpr int FM = BM / WR / 32, FN = BN / WC / 32, S = KB / 32, kStage = (BM + BN) * KB;
+  static_assert(PA * 1024 * NW == BM * KB && PB * 1024 * NW == BN * KB && FM * 32 * WR == BM && FN * 32 * WC == BN, "tile shape");
+  using SA = FStage<T, BM, AX, KB>;
+  using SB = FStage<T, BN, BX, KB>;
+  __shared__ __attribute__((aligned(1024))) int8_t lds[NB * kStage];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wv / WC, wc = wv % WC;
   // workgroups go round the eight XCDs: each gets a run of neighbouring tiles, in groups of kFGroup tile rows
@@ -127,55 +126,41 @@ __global__ void __launch_bounds__(64 * WR * WC, 1) ftile_kernel(FOperand A, int 
 #pragma unroll
     for (int p = 0; p < PA; ++p) {
       const int q = (p * NW + wv) * 64 + lane, r = q / SA::PPR, c = q % SA::PPR;
-      if (AX) {
-        ka[p] = r;
-        const int x = (c ^ SA::swap(r)) * 16;
-        oka[p] = m0 + x / ES < M;
-        ao[p] = (unsigned)r * lda + x;
-      } else {
-        ka[p] = (c ^ ((r >> 1) & 7)) * 16;
-        oka[p] = true;
-        ao[p] = (unsigned)(m0 + r < M ? r : M - 1 - m0) * lda + ka[p];
-      }
+      const int x = (c ^ SA::place(r)) * 16;
+      ka[p] = AX ? r : x;
+      oka[p] = !AX || m0 + x / ES < M;
+      ao[p] = AX ? (unsigned)r * lda + x : (unsigned)(m0 + r < M ? r : M - 1 - m0) * lda + x;
     }
 #pragma unroll
     for (int p = 0; p < PB; ++p) {
       const int q = (p * NW + wv) * 64 + lane, r = q / SB::PPR, c = q % SB::PPR;
-      if (BX) {
-        kb[p] = r;
-        const int x = (c ^ SB::swap(r)) * 16;
-        okb[p] = n0 + x / ES < N;
-        bo[p] = (unsigned)r * ldb + x;
-      } else {
-        kb[p] = (c ^ ((r >> 1) & 7)) * 16;
-        okb[p] = true;
-        bo[p] = (unsigned)(n0 + r < N ? r : N - 1 - n0) * ldb + kb[p];
-      }
+      const int x = (c ^ SB::place(r)) * 16;
+      kb[p] = BX ? r : x;
+      okb[p] = !BX || n0 + x / ES < N;
+      bo[p] = BX ? (unsigned)r * ldb + x : (unsigned)(n0 + r < N ? r : N - 1 - n0) * ldb + x;
     }
     const int8_t* zeros = reinterpret_cast<const int8_t*>(kFZeros);
-    auto direct = [&](int8_t* l, int p, const int8_t* s) {
-      __builtin_amdgcn_global_load_lds((gptr*)s, (lptr*)(l + (p * NW + wv) * 1024), 16, 0, 0);
-    };
     // Stage 0 is the last of k, of which some may be missing; stage t > 0 the whole one from KS (t - 1) on.
     const int nk = (K + KS - 1) / KS, kl = KS * (nk - 1);
-    const long long sta = AX ? (long long)lda * KS : 128, stb = BX ? (long long)ldb * KS : 128;
-    // a third of stage t > 0 into l: three of the four steps between two barriers issue one each.  Every
-    // direct load issued is waited for by a barrier before the kernel's end.
-    auto fetch = [&](int8_t* l, int t, int third) {
+    const long long sta = AX ? (long long)lda * KS : KB, stb = BX ? (long long)ldb * KS : KB;
+    const bool wa = !AX || m0 + BM <= M, wb = !BX || n0 + BN <= N;  // no row of the operand ends in the tile
+    auto fetch = [&](int8_t* l, int t) {
       const int8_t* a = ab + (t - 1) * sta;
       const int8_t* b = bb + (t - 1) * stb;
-      constexpr int all = PA + PB, each = (all + 2) / 3;
+      if (wa) {
 #pragma unroll
-      for (int p = 0; p < all; ++p)
-        if (p / each == third) {
-          if (p < PA) {
-            const int8_t* s = a + ao[p < PA ? p : 0];
-            direct(l, p, AX && !oka[p < PA ? p : 0] ? zeros : s);
-          } else {
-            const int8_t* s = b + bo[p < PA ? 0 : p - PA];
-            direct(l + BM * 128, p - PA, BX && !okb[p < PA ? 0 : p - PA] ? zeros : s);
-          }
-        }
+        for (int p = 0; p < PA; ++p) lds_load16(l + (p * NW + wv) * 1024, a, ao[p]);
+      } else {
+#pragma unroll
+        for (int p = 0; p < PA; ++p) lds_load16(l + (p * NW + wv) * 1024, oka[p] ? a + ao[p] : zeros);
+      }
+      if (wb) {
+#pragma unroll
+        for (int p = 0; p < PB; ++p) lds_load16(l + BM * KB + (p * NW + wv) * 1024, b, bo[p]);
+      } else {
+#pragma unroll
+        for (int p = 0; p < PB; ++p) lds_load16(l + BM * KB + (p * NW + wv) * 1024, okb[p] ? b + bo[p] : zeros);
+      }
       __builtin_amdgcn_sched_barrier(0);
     };
     {
@@ -183,28 +168,29 @@ __global__ void __launch_bounds__(64 * WR * WC, 1) ftile_kernel(FOperand A, int 
       const int8_t* a = ab + (nk - 1) * sta;
       const int8_t* b = bb + (nk - 1) * stb;
 #pragma unroll
-      for (int p = 0; p < PA; ++p) direct(l0, p, oka[p] && ka[p] < (AX ? left : left * ES) ? a + ao[p] : zeros);
+      for (int p = 0; p < PA; ++p)
+        lds_load16(lds + (p * NW + wv) * 1024, oka[p] && ka[p] < (AX ? left : left * ES) ? a + ao[p] : zeros);
 #pragma unroll
-      for (int p = 0; p < PB; ++p) direct(l0 + BM * 128, p, okb[p] && kb[p] < (BX ? left : left * ES) ? b + bo[p] : zeros);
+      for (int p = 0; p < PB; ++p)
+        lds_load16(lds + BM * KB + (p * NW + wv) * 1024, okb[p] && kb[p] < (BX ? left : left * ES) ? b + bo[p] : zeros);
     }
     const int lr = lane & 31, lg = lane >> 5;
-    // along: the rows' offsets and their pieces' change of place
-    const int ra = wr * (BM / WR) + lr, rb = wc * (BN / WC) + lr;  // rows r + 32 f share r / 2 % 8
-    const int za = (ra >> 1) & 7, zb = (rb >> 1) & 7;
+    // along: the rows' offsets and their pieces' change of place (the same for rows 32 apart)
+    const int ra = wr * (BM / WR) + lr, rb = wc * (BN / WC) + lr, za = SA::place(ra), zb = SB::place(rb);
     // across, 16 bits: of the transposing read, lane i of sixteen reads row 8 (l / 32) + i / 4, elements
     // 16 (l / 16 % 2) + 4 (i % 4) on of the fragment's 32
     const int xk = 8 * lg + ((lane >> 2) & 3), xm = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
     iv4 fa[2][FM], fb[2][FN];
-    auto across = [&](const int8_t* l, int row0, int ks, auto S) -> iv4 {
-      using ST = decltype(S);
+    auto across = [&](const int8_t* l, int row0, int ks, auto which) -> iv4 {
+      using ST = decltype(which);
       constexpr int pitch = ST::PPR * 16;
       iv4 v;
       if constexpr (ES == 2) {
         typedef short s4 __attribute__((ext_vector_type(4)));
         typedef __attribute__((address_space(3))) s4 ls4;
         const int b = (row0 + xm) * 2;
-        // k % 4 and, where rows are short, k / 2 % 2 do not change with ks or the two reads (multiples of 4)
-        const int8_t* p = l + xk * pitch + (((b >> 4) ^ ST::swap(xk)) << 4) + (b & 15);
+        // what the rows change by does not change with ks or between the two reads (multiples of 4)
+        const int8_t* p = l + xk * pitch + (((b >> 4) ^ ST::place(xk)) << 4) + (b & 15);
         const s4 u0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ls4*)(p + 16 * ks * pitch));
         const s4 u1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ls4*)(p + (16 * ks + 4) * pitch));
         typedef int i2 __attribute__((ext_vector_type(2)));
@@ -215,7 +201,7 @@ __global__ void __launch_bounds__(64 * WR * WC, 1) ftile_kernel(FOperand A, int 
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int k = 8 * ks + 4 * lg + e;
-          v[e] = *reinterpret_cast<const int*>(l + k * pitch + (((b >> 4) ^ ST::swap(k)) << 4) + (b & 15));
+          v[e] = *reinterpret_cast<const int*>(l + k * pitch + (((b >> 4) ^ ST::place(k)) << 4) + (b & 15));
         }
       }
       return v;
@@ -224,12 +210,12 @@ __global__ void __launch_bounds__(64 * WR * WC, 1) ftile_kernel(FOperand A, int 
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
         if constexpr (AX) fa[f][i] = across(l, wr * (BM / WR) + 32 * i, ks, SA{});
-        else fa[f][i] = *reinterpret_cast<const iv4*>(l + (ra + 32 * i) * 128 + (((2 * ks + lg) ^ za) << 4));
+        else fa[f][i] = *reinterpret_cast<const iv4*>(l + (ra + 32 * i) * KB + (((2 * ks + lg) ^ za) << 4));
       }
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
-        if constexpr (BX) fb[f][j] = across(l + BM * 128, wc * (BN / WC) + 32 * j, ks, SB{});
-        else fb[f][j] = *reinterpret_cast<const iv4*>(l + BM * 128 + (rb + 32 * j) * 128 + (((2 * ks + lg) ^ zb) << 4));
+        if constexpr (BX) fb[f][j] = across(l + BM * KB, wc * (BN / WC) + 32 * j, ks, SB{});
+        else fb[f][j] = *reinterpret_cast<const iv4*>(l + BM * KB + (rb + 32 * j) * KB + (((2 * ks + lg) ^ zb) << 4));
       }
     };
     auto mul = [&](int f) {
@@ -238,69 +224,64 @@ __global__ void __launch_bounds__(64 * WR * WC, 1) ftile_kernel(FOperand A, int 
 #pragma unroll
         for (int j = 0; j < FN; ++j) acc[i][j] = fmul(T{}, fa[f][i], fb[f][j], acc[i][j]);
     };
-    auto step = [&](int f, const int8_t* l, int ks) {  // products of fragments f under the reads of the next
-      read(f ^ 1, l, ks);
-      mul(f);
-      constexpr int per_x = ES == 2 ? 2 : 4;
-      constexpr int reads = FM * (AX ? per_x : 1) + FN * (BX ? per_x : 1), muls = FM * FN * (ES == 2 ? 1 : 4);
+    constexpr int each = ES == 2 ? 2 : 4, reads = FM * (AX ? each : 1) + FN * (BX ? each : 1), muls = FM * FN * (ES == 2 ? 1 : 4);
+    auto spread = [&]() {
       interleave<reads, muls, reads < muls ? reads : muls>();
       __builtin_amdgcn_sched_barrier(0);
     };
-    stage_barrier();
-    if (nk > 1) {
-      fetch(l1, 1, 0);
-      fetch(l1, 1, 1);
-      fetch(l1, 1, 2);
-    }
-    read(0, l0, 0);
+    // The stage behind t is in LDS (of this wave's loads at most those of NB - 2 stages behind that are on their way), and
+    // the reads of t are done, so that its place may be filled.
+    constexpr int kLoads = PA + PB;
+    auto handover = [&](int t) {
+      if (t + NB - 1 < nk) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NB - 2) * kLoads) : "memory");
+      else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      asm volatile("s_barrier" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 1; i < NB; ++i)
+      if (i < nk) fetch(lds + i * kStage, i);
+    if (nk >= NB) asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NB - 1) * kLoads) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    asm volatile("s_barrier" ::: "memory");
+    read(0, lds, 0);
     __builtin_amdgcn_sched_barrier(0);
-    int t = 0;
-    for (; t + 2 < nk; t += 2) {  // stage t in l0, its first fragments read; stage t + 1 on its way to l1
-      step(0, l0, 1);
-      step(1, l0, 2);
-      step(0, l0, 3);
-      stage_barrier();
-      fetch(l0, t + 2, 0);
-      step(1, l1, 0);
-      fetch(l0, t + 2, 1);
-      step(0, l1, 1);
-      fetch(l0, t + 2, 2);
-      step(1, l1, 2);
-      step(0, l1, 3);
-      stage_barrier();
-      const bool more = t + 3 < nk;
-      if (more) fetch(l1, t + 3, 0);
-      step(1, l0, 0);
-      if (more) {
-        fetch(l1, t + 3, 1);
-        fetch(l1, t + 3, 2);
+    int here = 0;  // of the stage's place
+    for (int t = 0; t < nk - 1; ++t) {
+      int8_t* l = lds + here;
+      here = here == (NB - 1) * kStage ? 0 : here + kStage;
+#pragma unroll
+      for (int k = 0; k < S; ++k) {
+        if (k < S - 1) {
+          read((k + 1) & 1, l, k + 1);
+        } else {
+          handover(t);
+          if (t + NB < nk) fetch(l, t + NB);
+          read(0, lds + here, 0);
+        }
+        mul(k & 1);
+        spread();
       }
     }
-    step(0, l0, 1);
-    step(1, l0, 2);
-    step(0, l0, 3);
-    if (t + 1 < nk) {
-      stage_barrier();
-      step(1, l1, 0);
-      step(0, l1, 1);
-      step(1, l1, 2);
-      step(0, l1, 3);
+#pragma unroll
+    for (int k = 0; k < S; ++k) {
+      if (k < S - 1) read((k + 1) & 1, lds + here, k + 1);
+      mul(k & 1);
+      if (k < S - 1) spread();
     }
-    mul(1);
     if (EPI::kLds) __syncthreads();  // the stages are read: LDS is free
   }
   const int mr = M - m0 < BM ? (int)(M - m0) : BM, nr = N - n0 < BN ? (int)(N - n0) : BN;
-  epi.template finish<T, BM, BN, WR, WC, FM, FN>(acc, m0, n0, mr, nr, wr, wc, l0, l1);
+  epi.template finish<T, BM, BN, WR, WC, FM, FN, NB * kStage>(acc, m0, n0, mr, nr, wr, wc, lds);
 }
 
-template <typename T, int BM, int BN, int WR, int WC, bool AX, bool BX, FCount CUT, typename EPI>
+template <typename T, int BM, int BN, int WR, int WC, int KB, int NB, bool AX, bool BX, FCount CUT, typename EPI>
 static hipError_t ftile_launch(FOperand A, long long M, FOperand B, long long N, long long K, int parts, const int* count,
                                const EPI& epi, hipStream_t st) {
   const long long ntm = (M + BM - 1) / BM, ntn = (N + BN - 1) / BN;
   if (ntm * ntn >= (1ll << 22) || M >= (1ll << 31) - 256 || N >= (1ll << 31) - 256 || K >= (1ll << 30)) return hipErrorInvalidValue;
-  constexpr int KS = 128 / (int)sizeof(T);
+  constexpr int KS = KB / (int)sizeof(T);
   const long long kper = ((K + KS - 1) / KS + parts - 1) / parts * KS;
-  hipLaunchKernelGGL((ftile_kernel<T, BM, BN, WR, WC, AX, BX, CUT, EPI>), dim3((unsigned)(ntm * ntn), (unsigned)parts),
+  hipLaunchKernelGGL((ftile_kernel<T, BM, BN, WR, WC, KB, NB, AX, BX, CUT, EPI>), dim3((unsigned)(ntm * ntn), (unsigned)parts),
                      dim3(64 * WR * WC), 0, st, A, (int)M, B, (int)N, (int)K, (int)kper, (int)ntm, (int)ntn, count, epi);
   return hipGetLastError();
 }

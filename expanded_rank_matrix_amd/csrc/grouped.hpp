@@ -433,8 +433,7 @@ struct Buffer {
   }
   template <int BYTES>
   __device__ __forceinline__ void to_lds(int8_t* l, unsigned at, unsigned base) const {
-    typedef __attribute__((address_space(3))) int8_t lbyte;
-    const unsigned m = (unsigned)(uintptr_t)(lbyte*)l;
+    const unsigned m = lds_address(l);
     if constexpr (BYTES == 16)
       asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(m), "v"(at), "s"(r), "s"(base) : "memory", "m0");
     else

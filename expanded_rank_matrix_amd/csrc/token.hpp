@@ -227,13 +227,13 @@ struct TokenStats {
   long long padded;
   int first;      // of the piece's words
   static constexpr bool kLds = true;
-  template <typename T, int BM, int BN, int WR, int WC, int FM, int FN>
+  template <typename T, int BM, int BN, int WR, int WC, int FM, int FN, int LDS>
   __device__ __forceinline__ void finish(fv16 (&acc)[FM][FN], long long m0, long long n0, int mr, int, int wr, int wc,
-                                         int8_t* l0, int8_t*) const {
+                                         int8_t* lds) const {
     const int lane = threadIdx.x & 63, lr = lane & 31, lg = lane >> 5;
     const int r0 = wr * (BM / WR), c0 = wc * (BN / WC);
-    float2* red = reinterpret_cast<float2*>(l0);  // [WR][BN]
-    static_assert(WR * BN * 8 <= (BM + BN) * 128, "epilogue in LDS");
+    float2* red = reinterpret_cast<float2*>(lds);  // [WR][BN]
+    static_assert(WR * BN * 8 <= LDS, "epilogue in LDS");
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
       const long long t = n0 + c0 + 32 * j + lr;
@@ -283,14 +283,14 @@ struct TokenStats {
 // A tile stored with its columns as rows: the accumulators pass through LDS, 32 columns of up to 256 bytes at
 // a time, so that each lane stores 16 bytes of a row.  A lane's four consecutive rows of D are one write there.
 //   value(j, i, e) gives the OT to store, put(column, row, piece) stores 16 bytes from `row` on
-template <typename OT, int BM, int BN, int WR, int WC, int FM, int FN, typename V, typename P>
-__device__ __forceinline__ void store_columns(int wr, int wc, int8_t* l0, int8_t* l1, const V& value, const P& put) {
+template <typename OT, int BM, int BN, int WR, int WC, int FM, int FN, int LDS, typename V, typename P>
+__device__ __forceinline__ void store_columns(int wr, int wc, int8_t* lds, const V& value, const P& put) {
   constexpr int ES = (int)sizeof(OT), IC = FM * 32 * ES <= 256 ? FM : 256 / (32 * ES), RB = IC * 32 * ES, PITCH = RB + 16;
   static_assert(FM % IC == 0, "whole chunks");
-  constexpr int kBytes = 32 * PITCH, NW = WR * WC;
-  static_assert(kBytes * ((NW + 1) / 2) <= (BM + BN) * 128, "epilogue in LDS");
+  constexpr int kBytes = 32 * PITCH;
+  static_assert(kBytes * WR * WC <= LDS, "epilogue in LDS");
   const int lane = threadIdx.x & 63, lr = lane & 31, lg = lane >> 5, wv = wr * WC + wc;
-  int8_t* l = (wv & 1 ? l1 : l0) + (wv >> 1) * kBytes;
+  int8_t* l = lds + wv * kBytes;
   const int r0 = wr * (BM / WR), c0 = wc * (BN / WC);
 #pragma unroll
   for (int j = 0; j < FN; ++j)
@@ -325,9 +325,9 @@ struct TokenP {
   long long ldp;
   int first;    // of the piece's words
   static constexpr bool kLds = true;
-  template <typename T, int BM, int BN, int WR, int WC, int FM, int FN>
+  template <typename T, int BM, int BN, int WR, int WC, int FM, int FN, int LDS>
   __device__ __forceinline__ void finish(fv16 (&acc)[FM][FN], long long m0, long long n0, int mr, int, int wr, int wc,
-                                         int8_t* l0, int8_t* l1) const {
+                                         int8_t* lds) const {
     const int lane = threadIdx.x & 63, lr = lane & 31, lg = lane >> 5;
     const int r0 = wr * (BM / WR), c0 = wc * (BN / WC);
 #pragma unroll
@@ -360,8 +360,8 @@ struct TokenP {
             acc[i][j][e] = r0 + 32 * i + 8 * (e >> 2) + 4 * lg + (e & 3) < mr ? acc[i][j][e] : 0.0f;
     }
     PT* p = P + n0 * ldp + m0;
-    store_columns<PT, BM, BN, WR, WC, FM, FN>(
-        wr, wc, l0, l1, [&](int j, int i, int e) { return (PT)acc[i][j][e]; },
+    store_columns<PT, BM, BN, WR, WC, FM, FN, LDS>(
+        wr, wc, lds, [&](int j, int i, int e) { return (PT)acc[i][j][e]; },
         [&](int c, int r, const iv4& v) { *reinterpret_cast<iv4*>(p + c * ldp + r) = v; });
   }
 };
@@ -373,12 +373,12 @@ struct TokenDX {
   int nq;
   bool first;
   static constexpr bool kLds = true;
-  template <typename T, int BM, int BN, int WR, int WC, int FM, int FN>
+  template <typename T, int BM, int BN, int WR, int WC, int FM, int FN, int LDS>
   __device__ __forceinline__ void finish(fv16 (&acc)[FM][FN], long long m0, long long n0, int mr, int, int wr, int wc,
-                                         int8_t* l0, int8_t* l1) const {
+                                         int8_t* lds) const {
     float* p = sum + blockIdx.y * stride + n0 * nq + m0;
-    store_columns<float, BM, BN, WR, WC, FM, FN>(
-        wr, wc, l0, l1, [&](int j, int i, int e) { return acc[i][j][e]; },
+    store_columns<float, BM, BN, WR, WC, FM, FN, LDS>(
+        wr, wc, lds, [&](int j, int i, int e) { return acc[i][j][e]; },
         [&](int c, int r, const iv4& v) {
           if (r >= mr) return;
           fv4* o = reinterpret_cast<fv4*>(p + (long long)c * nq + r);
@@ -396,15 +396,15 @@ struct TokenDW {
   long long ldw;
   int n;
   static constexpr bool kLds = true;
-  template <typename T, int BM, int BN, int WR, int WC, int FM, int FN>
+  template <typename T, int BM, int BN, int WR, int WC, int FM, int FN, int LDS>
   __device__ __forceinline__ void finish(fv16 (&acc)[FM][FN], long long m0, long long n0, int, int nr, int wr, int wc,
-                                         int8_t* l0, int8_t* l1) const {
+                                         int8_t* lds) const {
     constexpr int E = 16 / (int)sizeof(OT);
     const int scale = -meta->scale;
     const int left = n - (int)m0;
     OT* p = dW + n0 * ldw + m0;
-    store_columns<OT, BM, BN, WR, WC, FM, FN>(
-        wr, wc, l0, l1,
+    store_columns<OT, BM, BN, WR, WC, FM, FN, LDS>(
+        wr, wc, lds,
         [&](int j, int i, int e) { return (OT)(__is_same(OT, _Float16) ? ldexpf(acc[i][j][e], scale) : acc[i][j][e]); },
         [&](int c, int r, const iv4& v) {
           if (c >= nr || r >= left) return;
@@ -646,14 +646,14 @@ static hipError_t token_product(const TokenPlan& P, FOperand A, long long M, FOp
   const int* c = &meta->count;
   switch (P.shape) {
     case 0:
-      if constexpr (sizeof(T) == 4) return ftile_launch<T, 64, 32, 2, 1, AX, false, kRowsOfB>(A, M, B, N, K, parts, c, epi, st);
+      if constexpr (sizeof(T) == 4) return ftile_launch<T, 64, 32, 2, 1, 128, 2, AX, false, kRowsOfB>(A, M, B, N, K, parts, c, epi, st);
       else return hipErrorInvalidValue;
     case 1:
-      if constexpr (sizeof(T) == 2) return ftile_launch<T, 128, 32, 4, 1, AX, false, kRowsOfB>(A, M, B, N, K, parts, c, epi, st);
+      if constexpr (sizeof(T) == 2) return ftile_launch<T, 128, 32, 4, 1, 128, 2, AX, false, kRowsOfB>(A, M, B, N, K, parts, c, epi, st);
       else return hipErrorInvalidValue;
-    case 2: return ftile_launch<T, 128, 64, 2, 2, AX, false, kRowsOfB>(A, M, B, N, K, parts, c, epi, st);
-    case 3: return ftile_launch<T, 128, 128, 2, 2, AX, false, kRowsOfB>(A, M, B, N, K, parts, c, epi, st);
-    default: return ftile_launch<T, 256, 256, 2, 4, AX, false, kRowsOfB>(A, M, B, N, K, parts, c, epi, st);
+    case 2: return ftile_launch<T, 128, 64, 2, 2, 128, 2, AX, false, kRowsOfB>(A, M, B, N, K, parts, c, epi, st);
+    case 3: return ftile_launch<T, 128, 128, 2, 2, 128, 2, AX, false, kRowsOfB>(A, M, B, N, K, parts, c, epi, st);
+    default: return ftile_launch<T, 256, 256, 2, 4, 128, 2, AX, false, kRowsOfB>(A, M, B, N, K, parts, c, epi, st);
   }
 }
 
@@ -662,8 +662,8 @@ template <typename T>
 static hipError_t token_dw(int rows, FOperand A, long long M, FOperand B, long long N, long long K, const TokenMeta* meta,
                            const TokenDW<T>& epi, hipStream_t st) {
   const int* c = &meta->count;
-  if (rows <= 512) return ftile_launch<T, 128, 128, 2, 2, true, true, kLength>(A, M, B, N, K, 1, c, epi, st);
-  return ftile_launch<T, 256, 256, 2, 4, true, true, kLength>(A, M, B, N, K, 1, c, epi, st);
+  if (rows <= 512) return ftile_launch<T, 128, 128, 2, 2, 128, 2, true, true, kLength>(A, M, B, N, K, 1, c, epi, st);
+  return ftile_launch<T, 256, 128, 2, 2, 64, 3, true, true, kLength>(A, M, B, N, K, 1, c, epi, st);
 }
 
 // Blocks of a row beside `count` rows: a launch holds below 2^32 threads, the kernels go on from there.
