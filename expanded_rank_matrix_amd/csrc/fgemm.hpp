@@ -38,7 +38,7 @@ struct FOperand {
 static __device__ const int kFZeros[4] = {0, 0, 0, 0};  // what a direct load reads behind an operand's end
 
 // What the product's sizes may be cut to by a count that only the device knows.
-enum FCount { kAll, kRowsOfA, kRowsOfB, kLength };
+enum FCount { kRowsOfB, kLength };
 
 // Scheduling groups that spread a step's reads of LDS evenly over its products.
 template <int READS, int MULS, int SLOTS>
@@ -72,9 +72,10 @@ constexpr int kFGroup = 4;
 template <typename T, int ROWS, bool ACROSS, int KB>
 struct FStage {  // where an operand's pieces lie in a stage
   static constexpr int PPR = ACROSS ? ROWS * (int)sizeof(T) / 16 : KB / 16;  // pieces of a row in LDS
+  static_assert(ACROSS || KB == 128, "64 bytes of a row are half a cache line: slower where k runs along rows");
   // what row r's pieces are moved by (xor)
   __device__ __forceinline__ static int place(int r) {
-    if (!ACROSS) return KB == 128 ? (r >> 1) & 7 : (r >> 2) & 3;
+    if (!ACROSS) return (r >> 1) & 7;
     if (sizeof(T) == 4) return PPR >= 16 ? ((r >> 2) & 1) << 3 : 0;
     return PPR >= 16 ? (r & 3) << 2 : PPR == 8 ? ((r >> 1) & 1) << 2 : 0;
   }
@@ -99,12 +100,9 @@ __global__ void __launch_bounds__(64 * WR * WC, WR * WC >= 8 ? 1 : 2) ftile_kern
   const int grp = tile / (kFGroup * ntn), g0 = grp * kFGroup, gs = ntm - g0 < kFGroup ? ntm - g0 : kFGroup;
   const int in = tile - g0 * ntn;
   const long long m0 = (long long)(g0 + in % gs) * BM, n0 = (long long)(in / gs) * BN;
-  if (CUT != kAll) {
-    const int c = *count;
-    if (CUT == kRowsOfA && m0 >= c) return;
-    if (CUT == kRowsOfB && n0 >= c) return;
-    if (CUT == kLength) Kall = (c + 31) / 32 * 32;  // rows behind the count are zeros up to there
-  }
+  const int counted = *count;
+  if (CUT == kRowsOfB && n0 >= counted) return;
+  if (CUT == kLength) Kall = (counted + 31) / 32 * 32;  // rows behind the count are zeros up to there
   const int kbeg = blockIdx.y * kper;
   const int K = Kall - kbeg < kper ? Kall - kbeg : kper;
   fv16 acc[FM][FN];

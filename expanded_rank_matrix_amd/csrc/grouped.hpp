@@ -170,14 +170,16 @@ __device__ __forceinline__ void spread(float v, float (&o)[128 / GROUP]) {
 // the transposition gives each product 32 consecutive ones, so that groups of 32 need nothing else.  The waves' partial
 // sums add in LDS in their order.
 
-template <typename XT, int NT, int CT, int WAVES, int GROUP, int SB>
-__global__ void __launch_bounds__(64 * WAVES) grouped_few_kernel(GroupedLaunch L) {
+constexpr int kGroupedWaves = 8;
+
+template <typename XT, int NT, int CT, int GROUP, int SB>
+__global__ void __launch_bounds__(64 * kGroupedWaves) grouped_few_kernel(GroupedLaunch L) {
   using T = typename Pieces<XT>::type;
   constexpr int NP = Pieces<XT>::count, G = 128 / GROUP;
   // chunks whose loads are in flight together, the tokens' among them where those fit the registers
   constexpr int U = NT == 1 && sizeof(XT) == 2 ? 3 : 2;
   constexpr bool EARLY = NT == 1;
-  __shared__ float red[WAVES][CT * NT * 256];
+  __shared__ float red[kGroupedWaves][CT * NT * 256];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lr = lane & 15, lg = lane >> 4;
   const int r0 = blockIdx.x * (16 * CT), n = L.n;
   const long long t0 = (long long)blockIdx.y * (16 * NT);
@@ -269,12 +271,12 @@ __global__ void __launch_bounds__(64 * WAVES) grouped_few_kernel(GroupedLaunch L
     }
   };
   const int full = n / 128;
-  for (int c = wv; c < full; c += U * WAVES) {
+  for (int c = wv; c < full; c += U * kGroupedWaves) {
     Chunk d[U];
     iv4 raw[EARLY ? U : 1][4][words8<XT>()];
     // the first chunk again where there are fewer: loads that depend on no branch
 #pragma unroll
-    for (int u = 0; u < U; ++u) d[u] = load(c + u * WAVES < full ? c + u * WAVES : c);
+    for (int u = 0; u < U; ++u) d[u] = load(c + u * kGroupedWaves < full ? c + u * kGroupedWaves : c);
     if constexpr (EARLY) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -282,11 +284,11 @@ __global__ void __launch_bounds__(64 * WAVES) grouped_few_kernel(GroupedLaunch L
         for (int k = 0; k < 4; ++k)
 #pragma unroll
           for (int h = 0; h < words8<XT>(); ++h)
-            raw[u][k][h] = word8(x[0] + 128 * (c + u * WAVES < full ? c + u * WAVES : c) + 32 * k, h);
+            raw[u][k][h] = word8(x[0] + 128 * (c + u * kGroupedWaves < full ? c + u * kGroupedWaves : c) + 32 * k, h);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int at = c + u * WAVES;
+      const int at = c + u * kGroupedWaves;
       if (at < full)
         chunk(d[u], [&](int k, int t, iv4 (&p)[NP]) {
           if constexpr (EARLY) whole8<XT>(raw[u][k], p);
@@ -294,7 +296,7 @@ __global__ void __launch_bounds__(64 * WAVES) grouped_few_kernel(GroupedLaunch L
         });
     }
   }
-  if (full % WAVES == wv && n % 128 != 0)  // the rows' end: one wave
+  if (full % kGroupedWaves == wv && n % 128 != 0)  // the rows' end: one wave
     chunk(load(full), [&](int k, int t, iv4 (&p)[NP]) { token8<true>(x[t], 128 * full + 32 * k, n - 8 * lg, p); });
 #pragma unroll
   for (int i = 0; i < CT; ++i)
@@ -303,30 +305,30 @@ __global__ void __launch_bounds__(64 * WAVES) grouped_few_kernel(GroupedLaunch L
 #pragma unroll
       for (int e = 0; e < 4; ++e) red[wv][(16 * t + 4 * lg + e) * (16 * CT) + 16 * i + lr] = acc[i][t][e];
   __syncthreads();
-  for (int i = threadIdx.x; i < CT * NT * 256; i += 64 * WAVES) {
+  for (int i = threadIdx.x; i < CT * NT * 256; i += 64 * kGroupedWaves) {
     const long long t = t0 + i / (16 * CT);
     const int o = r0 + i % (16 * CT);
     if (t < L.tokens && o < L.m) {
       float v = 0.0f;
 #pragma unroll
-      for (int w = 0; w < WAVES; ++w) v += red[w][i];
+      for (int w = 0; w < kGroupedWaves; ++w) v += red[w][i];
       put_scale(L.Y, L.y_type, t * L.ldy + o, v);
     }
   }
 }
 
-template <typename XT, int NT, int CT, int WAVES, int GROUP, int SB>
+template <typename XT, int NT, int CT, int GROUP, int SB>
 static hipError_t few_launch(const GroupedLaunch& all, hipStream_t st) {
   GroupedLaunch L = all;
   // runs of tokens whose threads a launch holds
-  const long long wide = (all.m + 16ll * CT - 1) / (16 * CT), most = (1ll << 21) / wide;
+  const long long wide = (all.m + 16ll * CT - 1) / (16 * CT), most = (1ll << 22) / wide;
   const long long step = (most < 1 ? 1 : most < 65535 ? most : 65535) * 16 * NT;
   for (long long t = 0; t < all.tokens; t += step) {
     L.tokens = all.tokens - t < step ? all.tokens - t : step;
     L.X = static_cast<const XT*>(all.X) + t * L.ldx;
     L.Y = static_cast<char*>(all.Y) + t * L.ldy * (L.y_type == 0 ? 4 : 2);
-    hipLaunchKernelGGL((grouped_few_kernel<XT, NT, CT, WAVES, GROUP, SB>), dim3((unsigned)wide, (unsigned)((L.tokens + 16 * NT - 1) / (16 * NT))),
-                       dim3(64 * WAVES), 0, st, L);
+    hipLaunchKernelGGL((grouped_few_kernel<XT, NT, CT, GROUP, SB>), dim3((unsigned)wide, (unsigned)((L.tokens + 16 * NT - 1) / (16 * NT))),
+                       dim3(64 * kGroupedWaves), 0, st, L);
   }
   return hipGetLastError();
 }
@@ -704,7 +706,9 @@ template <typename XT>
 static GroupedPlan grouped_plan(long long tokens, int n, int m, int group) {
   constexpr int NP = Pieces<XT>::count;
   GroupedPlan P{};
-  // and matrices whose offsets in a tile, or number of tiles, pass 32 bits take the kernel for few tokens, whatever their number
+  // Few: up to 64 tokens (9728 channels x 2560: 64 bf16 tokens 26 us, 100 in tiles 28, 128 25; 2560 x 2560: 64 12 us, 100 in
+  // tiles 19).  Matrices whose offsets in a tile, or number of tiles, pass 32 bits take the kernel for
+  // few tokens, whatever their number.
   const long long scales = (n + 127ll) / 128 * 128 / group * ((m + 127ll) / 128 * 128) * 4;
   P.few = tokens <= 64 || scales >= 1ll << 32 || m > 1 << 22;
   if (P.few) return P;
@@ -777,13 +781,14 @@ static hipError_t grouped_tiles(const GroupedLaunch& L, const GroupedPlan& P, hi
 
 template <typename XT, int GROUP, int SB>
 static hipError_t grouped_few(const GroupedLaunch& L, hipStream_t st) {
-  const bool wide = L.m >= 6144;  // 32 channels a workgroup still fill the card
-  // sixteen waves where long rows would take eight more than two turns
-  if (L.tokens <= 16)
-    return wide ? few_launch<XT, 1, 2, 8, GROUP, SB>(L, st)
-                : L.n > 4096 ? few_launch<XT, 1, 1, 16, GROUP, SB>(L, st) : few_launch<XT, 1, 1, 8, GROUP, SB>(L, st);
-  if (L.tokens <= 32) return wide ? few_launch<XT, 2, 2, 8, GROUP, SB>(L, st) : few_launch<XT, 2, 1, 8, GROUP, SB>(L, st);
-  return wide ? few_launch<XT, 4, 2, 8, GROUP, SB>(L, st) : few_launch<XT, 4, 1, 8, GROUP, SB>(L, st);
+  // 32 channels a workgroup read the tokens half as often, where enough workgroups are left and the tokens are many enough.
+  // Measured, 16 / 32 channels, us: 9728 x 2560, 4 tokens 8.1 / 9.0, 16 12.4 / 11.6, 32 19.6 / 16.7, 64 31.8 / 26.0; 2560 x 2560, 1 3.7 /
+  // 4.8, 64 12.1 / 13.4; 2560 x 9728, 1 8.4 / 11.5, 64 38 / 42.  (Sixteen waves instead of eight: 2560 x 9728, 1 8.4 against 8.0, 16 16.0
+  // against 14.6.)
+  const bool wide = L.m >= 6144 && L.tokens > 8;
+  if (L.tokens <= 16) return wide ? few_launch<XT, 1, 2, GROUP, SB>(L, st) : few_launch<XT, 1, 1, GROUP, SB>(L, st);
+  if (L.tokens <= 32) return wide ? few_launch<XT, 2, 2, GROUP, SB>(L, st) : few_launch<XT, 2, 1, GROUP, SB>(L, st);
+  return wide ? few_launch<XT, 4, 2, GROUP, SB>(L, st) : few_launch<XT, 4, 1, GROUP, SB>(L, st);
 }
 
 template <typename XT, int GROUP, int SB>
