@@ -67,7 +67,11 @@ __device__ __forceinline__ void interleave() {
 //           apart, and the chunks of 128 bytes change places with k / 4.
 // The fragments of the next step are read under the products of this one, and the barrier that hands a
 // stage over comes before the last of its steps.
-constexpr int kFGroup = 4;
+// Measured (bf16, K = 2560): 256 x 256, eight waves, stages of 128 bytes, 4096 x 131072: 1.21 10^15 operations a second, a
+// library product 1.28; the matrix cores are busy 54 to 58% of the time at 2.0 GHz, LDS as long as they would be if
+// fed (reads of the fragments and the loads' writes).  Both operands across, 256 x 128, four waves, two workgroups a CU,
+// three stages of 64 bytes: 1.11 10^15, 0.97 for 256 x 256 in two stages; along rows, 64 bytes are half a cache line and lost 25%.
+constexpr int kFGroup = 4;  // 2, 8 and 16 measured the same
 
 template <typename T, int ROWS, bool ACROSS, int KB>
 struct FStage {  // where an operand's pieces lie in a stage

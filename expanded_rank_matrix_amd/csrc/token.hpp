@@ -18,6 +18,9 @@
 // result's own rounding, and the largest of a row, the target's, is put back into dX.  fp16 P carries a power of two that brings the largest |g| to 2^14 .. 2^15, taken out of
 // the sums in fp32, so that small probabilities stay above fp16's smallest numbers.
 //
+// Measured (bf16, 2048 x 2560, us a piece of 32768 words): logits and P 314, dX 303, dW 309; the loss alone 4096 x 2560 x 131072 2274;
+// one row, 1024 x 32768: 13.6 (W at 4.9 TB/s) and 8 of the launches around.
+//
 // Rows that do not count (target outside the vocabulary, g = 0) are left out: the others' rows are gathered
 // at the start, their number stays on the device and cuts the products.
 #pragma once
@@ -657,7 +660,7 @@ static hipError_t token_product(const TokenPlan& P, FOperand A, long long M, FOp
   }
 }
 
-// dW: few tokens make short products, whose stores two workgroups a CU cover
+// dW: few tokens make short products, mostly stores, in smaller tiles (65 x 777 x 10007 fp32: 23 us, 27 in 256 x 256)
 template <typename T>
 static hipError_t token_dw(int rows, FOperand A, long long M, FOperand B, long long N, long long K, const TokenMeta* meta,
                            const TokenDW<T>& epi, hipStream_t st) {
