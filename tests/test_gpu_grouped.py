@@ -149,6 +149,24 @@ def test_products_of_whole_numbers_are_exact(tokens, n, m, xd, sd, offsets, grou
     assert torch.equal(y.cpu().double(), product(c, s, o, x, group)[0])
 
 
+@pytest.mark.parametrize("xd", TYPES)
+@pytest.mark.parametrize("tokens,n,m", [(1, 9728, 20), (9, 4200, 17), (16, 5000, 33), (40, 4230, 20)])
+def test_long_rows_are_exact(tokens, n, m, xd):
+    """Rows of several turns of the workgroup's waves."""
+    c, s, o, x = exact_inputs(tokens, n, m, 32, xd, "f16", True)
+    y = erm.apply_grouped(packed(c, 32).cuda(), s.cuda(), x.cuda(), offset=o.cuda(), group=32, out_dtype=torch.float32)
+    assert torch.equal(y.cpu().double(), product(c, s, o, x, 32)[0])
+
+
+@pytest.mark.parametrize("xd", TYPES)
+@pytest.mark.parametrize("tokens", [4, 9, 20, 50])
+def test_many_channels_are_exact(tokens, xd):
+    c, s, o, x = exact_inputs(tokens, 300, 6200, 64, xd, "bf16", True)
+    y = erm.apply_grouped(packed(c, 64).cuda(), s.cuda(), x.cuda(), offset=o.cuda(), group=64, out_dtype=torch.float32)
+    w = (c.cuda().double() * spread(s.cuda(), 64, 300) + spread(o.cuda(), 64, 300)).t().contiguous()
+    assert torch.equal(y.double(), x.cuda().double() @ w)
+
+
 def check(tokens, n, m, group, xd, yd, offsets, seed=0, scale=1.0):
     g = gen(tokens, n, m, group, seed)
     c = torch.randint(-8, 8, (m, n), generator=g)
