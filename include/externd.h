@@ -379,7 +379,8 @@ int64_t externd_apply_grouped_workspace(int x_type, int64_t tokens, int64_t n, i
  *   workspace  externd_token_workspace(x_type, rows, n, vocab, W, ldw, 1, dX != NULL, dW != NULL) bytes, 16-byte
  *            aligned, used by this call alone until it has run
  * Products are summed in fp32, the losses in fp64.  P is rounded to x_type before the two products
- * that take it (for fp16 times a power of two that the result is divided by again).  A NaN or an infinity in a counted row
+ * that take it (for fp16 times a power of two that the result is divided by again; what the target's
+ * rounding took is put back into dX).  A NaN or an infinity in a counted row
  * gives NaN in that row's outputs and throughout dW; in W, everywhere.  exp(z - largest) and P below
  * 2^-126 count as 0.  Deterministic.
  * 0 <= rows <= 2^20, 1 <= n <= 2^17, 1 <= vocab <= 2^24. */
