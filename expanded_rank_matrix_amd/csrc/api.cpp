@@ -774,9 +774,11 @@ static int token_entry(const void* X, int x_type, int64_t rows, int64_t n, int64
   const Rows out[] = {{dX, rows, n * es, lddx * es}, {dW, vocab, n * es, lddw * es}, dense(loss, forward ? rows * 4 : 0),
                       dense(stats, forward ? rows * 8 : 0)};
   if (dX && dX == X && lddx != ldx) return fail(EXTERND_EINVAL, "a gradient in X's place needs lddx = ldx");
+  // Only X itself, whose rows are gathered before dX is written, may lie where dX does: another input that begins there
+  // is read until the end.
   for (const Rows& o : out) {
     for (const Rows& i : in)
-      if (meet(o, i) && !(o.p == dX && i.p == X && dX == X)) return fail(EXTERND_EINVAL, "outputs must not overlap the inputs");
+      if (meet(o, i) && !(&o == &out[0] && &i == &in[0] && dX == X)) return fail(EXTERND_EINVAL, "outputs must not overlap the inputs");
     for (const Rows& p : out)
       if (&p != &o && meet(o, p)) return fail(EXTERND_EINVAL, "outputs must not overlap each other");
   }
