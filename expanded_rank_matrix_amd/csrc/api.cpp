@@ -664,7 +664,7 @@ int externd_apply_factors_grad(const uint32_t* B_packed, const uint32_t* C_packe
   const Rows gx = dense(dX, batch * n * 4), gd = dense(dD, k * 4);
   const bool over_x = dX && dX == X, over_dy = dX && dX == dY && m == n;
   for (const Rows& s : in)
-    if (meet(gd, s) || (meet(gx, s) && !(over_x && s.p == X) && !(over_dy && s.p == dY)))
+    if (meet(gd, s) || (meet(gx, s) && !(over_x && &s == &in[3]) && !(over_dy && &s == &in[4])))
       return fail(EXTERND_EINVAL, "dX and dD must not overlap the inputs");
   if (meet(gx, gd)) return fail(EXTERND_EINVAL, "dX and dD must not overlap");
   HIP_OR_FAIL(grad_run(B_packed, C_packed, D, (int)k, (int)m, (int)n, X, dY, batch, dX, dD, workspace,
