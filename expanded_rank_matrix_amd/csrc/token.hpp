@@ -560,23 +560,27 @@ constexpr TokenShape kTokenShapes[] = {{64, 32, 512}, {128, 32, 1024}, {128, 64,
 // 16 bits: up to 128 tokens the narrowest tiles that hold them in one column (reading W is what counts there); more by
 // rounds of 128 x 128 (512 at a time, 0.62 of a 256 x 256 round's time; a round of at most 256 of them 0.38) against
 // 256 x 256.  fp32, whose products are sixteen times slower, by the work of the busiest CU.
-static inline int token_shape(int es, long long rows, int V) {
-  auto tiles = [&](int s) {
-    return (V + kTokenShapes[s].bm - 1ll) / kTokenShapes[s].bm * ((rows + kTokenShapes[s].bn - 1) / kTokenShapes[s].bn);
+// A shape of which dX's product (elements of a hidden row by tokens) would need more tiles than a launch holds is left out;
+// 256 x 256, 2^21 at the most, never is.
+static inline int token_shape(int es, long long rows, int nq, int V) {
+  auto count = [&](long long m, int s) {
+    return (m + kTokenShapes[s].bm - 1) / kTokenShapes[s].bm * ((rows + kTokenShapes[s].bn - 1) / kTokenShapes[s].bn);
   };
+  auto tiles = [&](int s) { return count(V, s); };
+  auto held = [&](int s) { return count(nq, s) < kFTiles; };
   if (es == 2) {
     if (rows <= 32) return 1;
     if (rows <= 64) return 2;
     if (rows <= 128) return 3;
     const long long t3 = tiles(3), rest = t3 % 512;
     const double c3 = 0.62 * (double)(t3 / 512) + (rest == 0 ? 0.0 : rest <= 256 ? 0.38 : 0.62), c4 = (double)((tiles(4) + 255) / 256);
-    return c3 < c4 ? 3 : 4;
+    return c3 < c4 && held(3) ? 3 : 4;
   }
   int best = 4;
   double least = 1e300;
   for (int s : {4, 3, 2, 0}) {
     const double per = s == 0 ? 512 : 256, c = (double)((tiles(s) + (long long)per - 1) / (long long)per) * kTokenShapes[s].bm * kTokenShapes[s].bn * (256 / per);
-    if (c < least) {
+    if (c < least && held(s)) {
       least = c;
       best = s;
     }
@@ -586,11 +590,11 @@ static inline int token_shape(int es, long long rows, int V) {
 
 static inline TokenPlan token_plan(int es, long long rows, int n, int V, bool aligned, bool loss, bool dX, bool dW) {
   TokenPlan P{};
-  P.shape = token_shape(es, rows, V);
-  P.bm = kTokenShapes[P.shape].bm;
-  P.bn = kTokenShapes[P.shape].bn;
   const int q = 16 / es;
   P.nq = (n + q - 1) / q * q;
+  P.shape = token_shape(es, rows, P.nq, V);
+  P.bm = kTokenShapes[P.shape].bm;
+  P.bn = kTokenShapes[P.shape].bn;
   P.padded = (rows + P.bn - 1) / P.bn * P.bn;
   P.copy = !aligned;
   const bool grad = dX || dW;
