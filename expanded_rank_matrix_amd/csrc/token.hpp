@@ -559,7 +559,12 @@ constexpr TokenShape kTokenShapes[] = {{64, 32, 512}, {128, 32, 1024}, {128, 64,
 
 // 16 bits: up to 128 tokens the narrowest tiles that hold them in one column (reading W is what counts there); more by
 // rounds of 128 x 128 (512 at a time, 0.62 of a 256 x 256 round's time; a round of at most 256 of them 0.38) against
-// 256 x 256.  fp32, whose products are sixteen times slower, by the work of the busiest CU.
+// 256 x 256.  fp32, whose products are sixteen times slower, by the work of the busiest CU, of which 64 x 32 tiles do 15%
+// more slowly.  Measured, us of the loss and its dX in tiles of 64 x 32, 128 x 64, 128 x 128, 256 x 256 (n 2560):
+//   65 x 32768     518   491   504  1502        600 x 32768    2934  2474  2280  3309
+//   128 x 32768    740   516   509  1499       1024 x 32768    4067  4384  3643  3647
+//   300 x 32768   1842  1180  1471  1842       2048 x 32768    8180  7668  8570  7283
+// Over 28 sizes (rows 20 to 2048, 2051 to 50021 words) the loss is within 12% of the best shape's, and with dX within 16%.
 // A shape of which dX's product (elements of a hidden row by tokens) would need more tiles than a launch holds is left out;
 // 256 x 256, 2^21 at the most, never is.
 static inline int token_shape(int es, long long rows, int nq, int V) {
@@ -579,7 +584,9 @@ static inline int token_shape(int es, long long rows, int nq, int V) {
   int best = 4;
   double least = 1e300;
   for (int s : {4, 3, 2, 0}) {
-    const double per = s == 0 ? 512 : 256, c = (double)((tiles(s) + (long long)per - 1) / (long long)per) * kTokenShapes[s].bm * kTokenShapes[s].bn * (256 / per);
+    // rounds of tiles (64 x 32: two a CU at a time), times what a CU has of each
+    const long long per = s == 0 ? 512 : 256, rounds = (tiles(s) + per - 1) / per;
+    const double c = (s == 0 ? 1.15 : 1.0) * (double)(rounds * (per / 256) * kTokenShapes[s].bm * kTokenShapes[s].bn);
     if (c < least && held(s)) {
       least = c;
       best = s;

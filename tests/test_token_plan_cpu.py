@@ -39,3 +39,11 @@ def test_every_product_fits_a_launch(t, rows, n, vocab):
     """dX's tiles: elements of a hidden row by tokens, below 2^22."""
     for bm, bn in tiles(t, rows, n, vocab):
         assert up(n, bm) * up(rows, bn) < 1 << 22
+
+
+@pytest.mark.parametrize("t,rows,vocab,shape", [
+    (F32, 65, 10007, (64, 32)), (F32, 257, 32768, (128, 64)), (F32, 600, 32768, (128, 128)), (F32, 2048, 32768, (256, 256)),
+    (BF16, 32, 32768, (128, 32)), (BF16, 33, 32768, (128, 64)), (BF16, 65, 32768, (128, 128)), (F16, 300, 50021, (128, 128)),
+    (BF16, 2049, 32768, (256, 256))])
+def test_every_shape_serves_some_size(t, rows, vocab, shape):
+    assert shape in tiles(t, rows, 64, vocab)
