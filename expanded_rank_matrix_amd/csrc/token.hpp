@@ -476,7 +476,8 @@ __global__ void __launch_bounds__(1024) token_join_kernel(const float2* __restri
   for (int d = 16; d < 64; d <<= 1) add(__shfl_xor(m, d), __shfl_xor(s, d));
   if (k != 0 || c >= M.count) return;
   loss[r] = (float)((double)k0.g * ((double)m - (double)target + log(s)));
-  stats[2ll * r] = s == 0.0 ? -__builtin_inff() : m;
+  // the maxima pass over a NaN, the sum holds it
+  stats[2ll * r] = s != s ? __builtin_nanf("") : s == 0.0 ? -__builtin_inff() : m;
   stats[2ll * r + 1] = (float)s;
   if (GRAD) {
     const float g = ldexpf(k0.g, M.scale);

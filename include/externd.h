@@ -380,9 +380,13 @@ int64_t externd_apply_grouped_workspace(int x_type, int64_t tokens, int64_t n, i
  *            aligned, used by this call alone until it has run
  * Products are summed in fp32, the losses in fp64.  P is rounded to x_type before the two products
  * that take it (for fp16 times a power of two that the result is divided by again; what the target's
- * rounding took is put back into dX).  A NaN or an infinity in a counted row
- * gives NaN in that row's outputs and throughout dW; in W, everywhere.  exp(z - largest) and P below
- * 2^-126 count as 0.  Deterministic.
+ * rounding took is put back into dX).  exp(z - largest) and P below 2^-126 count as 0.  Deterministic.
+ * A row with a logit of +infinity or NaN has loss, statistics and dX NaN, and makes dW NaN throughout: so does
+ * a NaN in a counted row, or an infinity there (but statistics are -infinity and 0 where all logits are
+ * -infinity).  A NaN in W does that to every row.  An infinity in W acts by the logits that it gives: a row
+ * whose logit it makes -infinity takes that word's probability for 0 (loss +infinity where it is the target);
+ * but that word's row of dW, and the infinity's column of dX, are NaN or infinite wherever the arithmetic
+ * of products says so, 0 times infinity among them.
  * 0 <= rows <= 2^20, 1 <= n <= 2^17, 1 <= vocab <= 2^24. */
 int externd_token_loss(const void* X, int x_type, int64_t rows, int64_t n, int64_t ldx, const void* W, int64_t vocab,
                        int64_t ldw, const void* target, int target_bytes, const float* weight, float* loss,
