@@ -52,6 +52,10 @@ __device__ __forceinline__ float exp_neg(float d) {
   return __builtin_amdgcn_exp2f(fmaf(d, hi, d * lo));
 }
 
+// |g| for the power of two that P carries: of the numbers among the weights, so that an infinity (whose row is lost in any
+// case) leaves the other rows' P where it was
+__device__ __forceinline__ float finite_size(float g) { return fabsf(g) <= __FLT_MAX__ ? fabsf(g) : 0.0f; }
+
 // A row gathered into an aligned copy by `threads` threads: row r of X (zeros where that is -1), n elements and zeros up to nq.
 template <typename T>
 __device__ __forceinline__ void gather_row(const T* __restrict__ X, long long ldx, int n, long long r, T* __restrict__ out, int nq,
@@ -109,7 +113,7 @@ __global__ void __launch_bounds__(kTokenScan) token_rows_kernel(const TI* __rest
     if (counts) {
       list[at] = r;
       coef[at] = TokenCoef{0.0f, 0.0f, g, (int)tg};
-      top = fmaxf(top, fabsf(g));
+      top = fmaxf(top, finite_size(g));
     }
     if (r < rows) {
       place[r] = counts ? at : -1;
@@ -133,7 +137,7 @@ __global__ void __launch_bounds__(kTokenScan) token_rows_kernel(const TI* __rest
   if (threadIdx.x == 0) {
     for (int w = 0; w < kTokenScan / 64; ++w) top = fmaxf(top, tops[w]);
     int e = 0;
-    if (scaled && top > 0.0f && top <= __FLT_MAX__) e = 14 - ilogbf(top);
+    if (scaled && top > 0.0f) e = 14 - ilogbf(top);
     *meta = TokenMeta{base, e};
   }
 }
@@ -163,7 +167,7 @@ __global__ void __launch_bounds__(256) token_start_kernel(const TI* __restrict__
   for (int e = 0; e < 4; ++e) {
     counts[e] = tg[e] >= 0 && tg[e] < V && g[e] != 0.0f;
     n4 += counts[e];
-    top = fmaxf(top, counts[e] ? fabsf(g[e]) : 0.0f);
+    top = fmaxf(top, counts[e] ? finite_size(g[e]) : 0.0f);
   }
   int before = n4;  // the sum over the lanes up to this one
 #pragma unroll
@@ -206,7 +210,7 @@ __global__ void __launch_bounds__(256) token_start_kernel(const TI* __restrict__
       list[i] = -1;
       coef[i] = TokenCoef{0.0f, 0.0f, 0.0f, -1};
     }
-    if (threadIdx.x == 0) *meta = TokenMeta{count, scaled && top > 0.0f && top <= __FLT_MAX__ ? 14 - ilogbf(top) : 0};
+    if (threadIdx.x == 0) *meta = TokenMeta{count, scaled && top > 0.0f ? 14 - ilogbf(top) : 0};
   }
   __syncthreads();
   gather_row(X, ldx, n, mine, out + blockIdx.x * (long long)nq, nq, (int)threadIdx.x, 256);

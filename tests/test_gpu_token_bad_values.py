@@ -72,3 +72,25 @@ def test_logits_of_minus_infinity_alone():
     x[1] = 1.0
     loss, stats = erm.token_loss(x, w, torch.tensor([3, 4], device="cuda"))
     assert torch.isnan(loss[0]) and stats[0].tolist() == [-INF, 0.0] and stats[1].tolist() == [8.0, 30.0]
+
+
+@pytest.mark.parametrize("value", [NAN, INF, -INF])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows", [50, 1100])
+def test_a_bad_weight_leaves_the_other_rows_gradient(rows, dtype, value):
+    """Weights of 2^-18: a P of fp16 that carries no power of two falls under its smallest number, 2^-24, for most words,
+    while dX, of words 256 times as large, stays far above it."""
+    x, w, target, weight = inputs(rows, 64, 400, TYPES[dtype])
+    x, w = x / 256, w * 256
+    weight *= 2.0**-18
+    at = rows // 2
+    bad = weight.clone()
+    bad[at] = value
+    loss, _, dX, dW = erm.token_loss(x, w, target, weight=bad, grad=True)
+    assert not torch.isfinite(loss[at]) and not torch.isfinite(dX[at]).any() and not torch.isfinite(dW).any()
+    # every sum of P and dX itself are carried by the largest weight but the bad one
+    weight[at] = 0
+    want, tol = definition(x, w, target, weight)
+    rest = torch.arange(rows, device="cuda") != at
+    near(loss[rest], want[0][rest], tol[0][rest], "loss")
+    near(dX[rest], want[2][rest], tol[2][rest], "dX")
