@@ -26,8 +26,9 @@ __device__ __forceinline__ void put(T* p, float v) {
 // A code enters the matrix cores as the number c + 8: its four bits, the sign turned, are an e4m3 number of 2^-9 (c + 8) as
 // they are (the smallest exponents of e4m3 are one straight line), and one conversion widens two of them.  So eight
 // codes cost nine instructions, and for each group
-//   y += s sum (c + 8) x + (o - 8 s) sum x
-// with sum x from the same x by products with ones.  The excess costs the sums one to two of fp32's bits.
+//   y += s sum (c + 8) x + (o / 8 - s) sum 8 x
+// with sum 8 x from the same x by products with eights (8 s would leave fp32 for the largest scales).  The excess costs the
+// sums one to two of fp32's bits.
 template <typename T>
 __device__ __forceinline__ iv4 widen_pairs(unsigned a, unsigned b) {  // four bytes each
   iv4 r;
@@ -204,8 +205,8 @@ __global__ void __launch_bounds__(64 * kGroupedWaves) grouped_few_kernel(Grouped
   for (int i = 0; i < CT; ++i)
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[i][t] = fv4{0, 0, 0, 0};
-  const int one = __is_same(T, _Float16) ? 0x3C003C00 : 0x3F803F80;
-  const iv4 ones = {one, one, one, one};
+  const int eight = __is_same(T, _Float16) ? 0x48004800 : 0x41004100;
+  const iv4 eights = {eight, eight, eight, eight};
   struct Chunk {
     iv4 w[CT];
     unsigned s[CT], o[CT];
@@ -227,7 +228,7 @@ __global__ void __launch_bounds__(64 * kGroupedWaves) grouped_few_kernel(Grouped
 #pragma unroll
     for (int i = 0; i < CT; ++i) {
       d.w[i] = transpose4(d.w[i] ^ (int)kSignTurn);
-      const float sv = scale_value<SB>(d.s[i], half), bv = scale_value<SB>(d.o[i], half) - 8.0f * sv;
+      const float sv = scale_value<SB>(d.s[i], half), bv = fmaf(0.125f, scale_value<SB>(d.o[i], half), -sv);
       spread<GROUP>(sv, s[i]);
       spread<GROUP>(bv, b[i]);
     }
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(64 * kGroupedWaves) grouped_few_kernel(Grouped
           for (int h = 0; h < NP; ++h) {
 #pragma unroll
             for (int i = 0; i < CT; ++i) part[i][t] = gmul(T{}, p[h], wide[i], part[i][t]);
-            sum[t] = gmul(T{}, p[h], ones, sum[t]);
+            sum[t] = gmul(T{}, p[h], eights, sum[t]);
           }
         }
       }

@@ -348,9 +348,12 @@ int externd_quantize_groups(const void* W, int w_type, int64_t rows, int64_t n, 
  *           (EXTERND_EINVAL)
  *   workspace  externd_apply_grouped_workspace(x_type, tokens, n, m, group) bytes, 16-byte aligned (NULL where
  *           that is 0), used by this call alone until it has run
- * Codes and X enter the products exactly; they are summed in fp32, as c + 8 and less 8 X (so sums of 15 |X| over
- * a group have to stay in fp32's range), and the result is rounded once to y_type.  A NaN or an infinity in a token
- * gives NaN in its row, a NaN in a scale or an offset NaN in its channel.  Deterministic.  0 <= tokens < 2^31, 1 <= m <= 2^26, 1 <= n <= 2^20. */
+ * Codes and X enter the products exactly (of fp32 X, bits of 2^-133 and above); sums are fp32, of (c + 8) X and
+ * less 8 X, so that they are rounded as sums of terms up to (23 |scale| + |offset|) |X| are, and sums of 15 |X| over
+ * a group, and scale and offset times them, have to stay in fp32's range.  The result is rounded once to y_type.
+ * A NaN or an infinity in a token gives NaN in its row, a NaN in a scale or an offset NaN in its channel, an
+ * infinity there infinities or NaN in its channel.  Deterministic.
+ * 0 <= tokens < 2^31, 1 <= m <= 2^26, 1 <= n <= 2^20. */
 int externd_apply_grouped(const uint32_t* Q, const void* scale, const void* offset, int s_type, int64_t group, int64_t m,
                           int64_t n, int64_t ldq, const void* X, int x_type, int64_t tokens, int64_t ldx, void* Y,
                           int y_type, int64_t ldy, void* workspace, void* stream);
