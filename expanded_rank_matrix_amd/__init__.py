@@ -780,7 +780,8 @@ def _apply_grouped(Q, scale, offset, group, m, n, ldq, X, x_type, tokens, ldx, y
     else:
         Y = out.unsqueeze(0) if single and out.dim() == 1 else out
         ldy = _rows(Y, _FLOAT, "out", shape=(tokens, m), device=dev)
-    size = lib.externd_apply_grouped_workspace(x_type, tokens, n, m, group)
+    # codes with rows this far apart need none
+    size = lib.externd_apply_grouped_workspace(x_type, tokens, n, m, group) if ldq <= 1 << 22 else 0
     ws = torch.empty(size, dtype=torch.uint8, device=dev) if size > 0 else None
     _check(lib.externd_apply_grouped(
         Q.data_ptr(), scale.data_ptr(), None if offset is None else offset.data_ptr(), _TYPE[scale.dtype], group, m, n, ldq,

@@ -722,7 +722,7 @@ int externd_apply_grouped(const uint32_t* Q, const void* scale, const void* offs
     return fail(EXTERND_EINVAL, "ldq must be at least ceil(n / group) group / 8, ldx n and ldy m (and at most 2^40)");
   if (tokens == 0) return EXTERND_OK;
   if (!Q || !scale || !X || !Y) return fail(EXTERND_EINVAL, "null pointer argument");
-  if (grouped_workspace_bytes(x_type, tokens, (int)n, (int)m, (int)group) > 0 &&
+  if (ldq * 4 <= kGroupedPitch && grouped_workspace_bytes(x_type, tokens, (int)n, (int)m, (int)group) > 0 &&
       (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15)))
     return fail(EXTERND_EINVAL, "workspace of externd_apply_grouped_workspace() bytes, 16-byte aligned, is needed");
   const int64_t xs = x_type == EXTERND_F32 ? 4 : 2, ys = y_type == EXTERND_F32 ? 4 : 2, ss = s_type == EXTERND_F32 ? 4 : 2;

@@ -141,6 +141,9 @@ struct GroupedLaunch {
   long long ldq, tokens, ldx, ldy;
   int m, n, group, s_type, x_type, y_type;
 };
+// Bytes between rows of codes up to which a tile's offsets fit 32 bits; rows farther apart take the kernel for few tokens,
+// which needs no workspace.
+constexpr long long kGroupedPitch = 1 << 24;
 size_t grouped_workspace_bytes(int x_type, long long tokens, int n, int m, int group);
 hipError_t grouped_run(const GroupedLaunch& L, hipStream_t st);
 hipError_t grouped_run_f16(const GroupedLaunch& L, hipStream_t st);

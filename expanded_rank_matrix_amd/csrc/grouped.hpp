@@ -704,7 +704,6 @@ struct GroupedPlan {
   size_t sums, scale, offset, partial, bytes;  // offsets in the workspace, and its size
 };
 constexpr long long kGroupedRun = 1 << 14;    // tokens of one run, so that the group sums' offsets fit 32 bits
-constexpr long long kGroupedPitch = 1 << 24;  // bytes between rows of codes, so that a tile's offsets fit 32 bits
 
 template <typename XT>
 static GroupedPlan grouped_plan(long long tokens, int n, int m, int group) {

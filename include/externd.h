@@ -347,7 +347,7 @@ int externd_quantize_groups(const void* W, int w_type, int64_t rows, int64_t n, 
  *   Y       tokens x m of y_type (one of the same), row distance ldy; must not overlap the inputs
  *           (EXTERND_EINVAL)
  *   workspace  externd_apply_grouped_workspace(x_type, tokens, n, m, group) bytes, 16-byte aligned (NULL where
- *           that is 0), used by this call alone until it has run
+ *           that is 0, or where ldq is above 2^22), used by this call alone until it has run
  * Codes and X enter the products exactly (of fp32 X, bits of 2^-133 and above); sums are fp32, of (c + 8) X and
  * less 8 X, so that they are rounded as sums of terms up to (23 |scale| + |offset|) |X| are, and sums of 15 |X| over
  * a group, and scale and offset times them, have to stay in fp32's range.  The result is rounded once to y_type.
