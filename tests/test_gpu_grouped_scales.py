@@ -48,3 +48,45 @@ def test_an_infinite_scale_stays_in_its_channel(tokens, where):
     assert torch.equal(y[:, rest].double(), want[:, rest])
     if where == "offset":  # sum x is above 0
         assert (y[:, 7] == float("inf")).all()
+
+
+def lone(tokens, n, group, values):
+    """Tokens with one element that is not zero each, in groups and places that change from token to token."""
+    x = torch.zeros((tokens, n))
+    t = torch.arange(tokens)
+    x[t, (t * 37 + t // 5) % n] = values
+    return x
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("tokens", TOKENS)
+def test_every_bit_of_fp32_tokens_enters(tokens, group):
+    """Odd whole numbers of 20 bits: three pieces of 8.  (c + 8) x is below 2^24, and scales are powers of two: exact."""
+    n, m = 300, 50
+    g = gen(tokens, n, group)
+    c = torch.randint(-8, 8, (m, n), generator=g)
+    s = 2.0 ** torch.randint(-3, 4, (m, (n + group - 1) // group), generator=g).float()
+    v = (2 * torch.randint(2**18, 2**19, (tokens,), generator=g) + 1).float() * torch.where(torch.rand(tokens, generator=g) < 0.5, -1.0, 1.0)
+    x = lone(tokens, n, group, v)
+    y = erm.apply_grouped(packed(c, group).cuda(), s.cuda(), x.cuda(), group=group)
+    assert torch.equal(y.cpu().double(), product(c, s, None, x, group)[0])
+
+
+@pytest.mark.parametrize("xd", TYPES)
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("tokens", TOKENS)
+def test_every_bit_of_fp32_scales_and_offsets_enters(tokens, group, xd):
+    """x a power of two.  Offsets alone: the product with one is exact.  Scales: s (c + 8) x and 8 s x, or their difference,
+    round at most three times, each of at most 23 |s x|; a scale rounded to 16 bits would be off by up to 2^-12 |s c x| (fp16)."""
+    n, m = 300, 50
+    g = gen(tokens, m, group)
+    groups = (n + group - 1) // group
+    c = torch.randint(-8, 8, (m, n), generator=g)
+    s, o = torch.rand((m, groups), generator=g) + 0.5, torch.randn((m, groups), generator=g)
+    x = lone(tokens, n, group, 2.0 ** torch.randint(-4, 5, (tokens,), generator=g).float())
+    Q, X = packed(c, group).cuda(), x.to(TYPES[xd]).cuda()
+    y = erm.apply_grouped(Q, torch.zeros_like(s).cuda(), X, offset=o.cuda(), group=group, out_dtype=torch.float32)
+    assert torch.equal(y.cpu().double(), product(c, torch.zeros_like(s), o, x, group)[0])
+    y = erm.apply_grouped(Q, s.cuda(), X, group=group, out_dtype=torch.float32)
+    size = x.double().abs() @ s.double().repeat_interleave(group, 1)[:, :n].t()
+    assert ((y.cpu().double() - product(c, s, None, x, group)[0]).abs() <= 3 * 23 * 2.0**-24 * size).all()
