@@ -676,13 +676,15 @@ static hipError_t token_product(const TokenPlan& P, FOperand A, long long M, FOp
   }
 }
 
-// dW: few tokens make short products, mostly stores, in smaller tiles (65 x 777 x 10007 fp32: 23 us, 27 in 256 x 256)
+// dW.  Measured, us of dW alone with its P, in tiles of 128 x 128 / 256 x 128 (n x words): bf16, 32 rows, 2560 x 32768 95 / 90, 512
+// rows 207 / 187, 2048 rows 640 / 615, 776 x 10007 117 / 112; fp32, 65 rows, 776 x 10007 62 / 66, 512 rows 179 / 208, 2048 rows
+// 633 / 757, 512 rows, 2560 x 32768 1241 / 1229.  So by the type alone, over 32 to 2048 rows.
 template <typename T>
-static hipError_t token_dw(int rows, FOperand A, long long M, FOperand B, long long N, long long K, const TokenMeta* meta,
+static hipError_t token_dw(FOperand A, long long M, FOperand B, long long N, long long K, const TokenMeta* meta,
                            const TokenDW<T>& epi, hipStream_t st) {
   const int* c = &meta->count;
-  if (rows <= 512) return ftile_launch<T, 128, 128, 2, 2, 128, 2, true, true, kLength>(A, M, B, N, K, 1, c, epi, st);
-  return ftile_launch<T, 256, 128, 2, 2, 64, 3, true, true, kLength>(A, M, B, N, K, 1, c, epi, st);
+  if constexpr (sizeof(T) == 4) return ftile_launch<T, 128, 128, 2, 2, 128, 2, true, true, kLength>(A, M, B, N, K, 1, c, epi, st);
+  else return ftile_launch<T, 256, 128, 2, 2, 64, 3, true, true, kLength>(A, M, B, N, K, 1, c, epi, st);
 }
 
 // Blocks of a row beside `count` rows: a launch holds below 2^32 threads, the kernels go on from there.
@@ -769,7 +771,7 @@ static hipError_t token_typed(const TokenLaunch& L, hipStream_t st) {
       if (L.dX)
         TOKEN_TRY((token_product<T, true>(P, w, nq, pp, P.padded, c, P.parts, meta, TokenDX{dx, stride, nq, v == 0}, st)));
       if (L.dW)
-        TOKEN_TRY((token_dw<T>(rows, X, nq, pp, c, P.padded, meta, TokenDW<T>{meta, static_cast<T*>(L.dW) + v * L.lddw, L.lddw, n}, st)));
+        TOKEN_TRY((token_dw<T>(X, nq, pp, c, P.padded, meta, TokenDW<T>{meta, static_cast<T*>(L.dW) + v * L.lddw, L.lddw, n}, st)));
     }
     if (L.dX) {
       hipLaunchKernelGGL((token_dx_kernel<T>), dim3((unsigned)rows, token_blocks(rows, (nq + 1023) / 1024)), dim3(256), 0, st, dx, P.parts, stride, nq,
