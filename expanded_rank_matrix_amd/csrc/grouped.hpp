@@ -784,11 +784,13 @@ static hipError_t grouped_tiles(const GroupedLaunch& L, const GroupedPlan& P, hi
 
 template <typename XT, int GROUP, int SB>
 static hipError_t grouped_few(const GroupedLaunch& L, hipStream_t st) {
-  // 32 channels a workgroup read the tokens half as often, where enough workgroups are left and the tokens are many enough.
-  // Measured, 16 / 32 channels, us: 9728 x 2560, 4 tokens 8.1 / 9.0, 16 12.4 / 11.6, 32 19.6 / 16.7, 64 31.8 / 26.0; 2560 x 2560, 1 3.7 /
-  // 4.8, 64 12.1 / 13.4; 2560 x 9728, 1 8.4 / 11.5, 64 38 / 42.  (Sixteen waves instead of eight: 2560 x 9728, 1 8.4 against 8.0, 16 16.0
-  // against 14.6.)
-  const bool wide = L.m >= 6144 && L.tokens > 8;
+  // 32 channels a workgroup read the tokens half as often, but make half as many workgroups: taken where the busiest of the
+  // 256 CUs has fewer of them by more than each costs more.  Measured, 16 / 32 channels, us (n x m, groups of 128): 2560 x 2560, 1 token 4.3 /
+  // 5.4, 64 12.9 / 14.0; 2560 x 5120, 1 5.7 / 5.5, 64 22.6 / 14.1; 2560 x 9728, 1 7.2 / 8.7, 8 10.1 / 10.4, 16 12.9 / 12.3, 64
+  // 31.9 / 26.3; 9728 x 5120, 1 14.0 / 12.2, 64 75 / 45; 9728 x 16384, 8 37 / 30; 2560 x 16400, 1 9.9 / 11.5, 16 19.7 / 16.6.  (Sixteen
+  // waves instead of eight: 9728 x 2560, 1 token 8.4 against 8.0, 16 16.0 against 14.6.)
+  const long long narrow = (L.m + 4095ll) / 4096, half = (L.m + 8191ll) / 8192;  // workgroups of the busiest CU
+  const bool wide = L.tokens > 8 ? narrow > half : 4 * narrow > 7 * half;
   if (L.tokens <= 16) return wide ? few_launch<XT, 1, 2, GROUP, SB>(L, st) : few_launch<XT, 1, 1, GROUP, SB>(L, st);
   if (L.tokens <= 32) return wide ? few_launch<XT, 2, 2, GROUP, SB>(L, st) : few_launch<XT, 2, 1, GROUP, SB>(L, st);
   return wide ? few_launch<XT, 4, 2, GROUP, SB>(L, st) : few_launch<XT, 4, 1, GROUP, SB>(L, st);

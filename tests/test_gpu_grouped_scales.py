@@ -10,7 +10,7 @@ import torch
 
 import expanded_rank_matrix_amd as erm
 
-from .test_gpu_grouped import TYPES, gen, packed, product
+from .test_gpu_grouped import TYPES, exact_inputs, gen, packed, product, spread
 
 pytestmark = pytest.mark.gpu
 
@@ -90,3 +90,13 @@ def test_every_bit_of_fp32_scales_and_offsets_enters(tokens, group, xd):
     y = erm.apply_grouped(Q, s.cuda(), X, group=group, out_dtype=torch.float32)
     size = x.double().abs() @ s.double().repeat_interleave(group, 1)[:, :n].t()
     assert ((y.cpu().double() - product(c, s, None, x, group)[0]).abs() <= 3 * 23 * 2.0**-24 * size).all()
+
+
+@pytest.mark.parametrize("xd", TYPES)
+@pytest.mark.parametrize("tokens,m", [(1, 4100), (8, 8190), (8, 8200), (9, 4100), (20, 8200), (50, 4100), (3, 12300), (1, 33000)])
+def test_channels_around_whole_rounds_are_exact(tokens, m, xd):
+    """Either width of the kernel for few tokens, at sizes where it changes: whole numbers, so that no order of sums rounds."""
+    c, s, o, x = exact_inputs(tokens, 300, m, 32, xd, "bf16", True)
+    y = erm.apply_grouped(packed(c, 32).cuda(), s.cuda(), x.cuda(), offset=o.cuda(), group=32, out_dtype=torch.float32)
+    w = (c.cuda().double() * spread(s.cuda(), 32, 300) + spread(o.cuda(), 32, 300)).t().contiguous()
+    assert torch.equal(y.double(), x.cuda().double() @ w)
