@@ -709,11 +709,14 @@ template <typename XT>
 static GroupedPlan grouped_plan(long long tokens, int n, int m, int group) {
   constexpr int NP = Pieces<XT>::count;
   GroupedPlan P{};
-  // Few: up to 64 tokens (9728 channels x 2560: 64 bf16 tokens 26 us, 100 in tiles 28, 128 25; 2560 x 2560: 64 12 us, 100 in
-  // tiles 19).  Matrices whose offsets in a tile, or number of tiles, pass 32 bits take the kernel for
-  // few tokens, whatever their number.
+  // Few: up to 64 tokens of 16 bits, 32 of fp32, whose three pieces the kernel for few tokens makes again for each 16 or 32
+  // channels.  Measured, few / tiles, us (n x m, groups of 128): bf16 2560 x 2560, 64 tokens 12.6 / 17.6, 65 15.7 / 17.6; 2560 x 9728,
+  // 48 23.2 / 22.4, 65 26.0 / 23.1; 9728 x 2560, 32 21.8 / 25.6, 64 38.4 / 27.1; fp32 2560 x 2560, 32 12.8 / 16.0, 48 19.4 / 17.1; 2560 x
+  // 9728, 32 24.2 / 23.5, 48 39.8 / 24.7; 9728 x 2560, 16 22.4 / 27.5, 32 39.1 / 30.0, 64 74.4 / 31.3; 1021 x 2051, 48 9.2 / 13.3.
+  // Over 118 sizes, 12 to 160 tokens, that costs 5 to 6% over the better of the two, the worst on the longest rows.
+  // Matrices whose offsets in a tile, or number of tiles, pass 32 bits take the kernel for few tokens, whatever their number.
   const long long scales = (n + 127ll) / 128 * 128 / group * ((m + 127ll) / 128 * 128) * 4;
-  P.few = tokens <= 64 || scales >= 1ll << 32 || m > 1 << 22;
+  P.few = tokens <= (NP == 3 ? 32 : 64) || scales >= 1ll << 32 || m > 1 << 22;
   if (P.few) return P;
   P.np = (n + 127) / 128 * 128;
   P.padded = (tokens + 255) / 256 * 256;

@@ -100,3 +100,13 @@ def test_channels_around_whole_rounds_are_exact(tokens, m, xd):
     y = erm.apply_grouped(packed(c, 32).cuda(), s.cuda(), x.cuda(), offset=o.cuda(), group=32, out_dtype=torch.float32)
     w = (c.cuda().double() * spread(s.cuda(), 32, 300) + spread(o.cuda(), 32, 300)).t().contiguous()
     assert torch.equal(y.double(), x.cuda().double() @ w)
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("tokens", [32, 33, 40, 63, 64, 65])
+@pytest.mark.parametrize("n,m", [(70, 33), (1100, 150), (300, 4200)])
+def test_fp32_tokens_around_the_border_between_the_kernels(n, m, tokens, group):
+    c, s, o, x = exact_inputs(tokens, n, m, group, "f32", "f32", True)
+    y = erm.apply_grouped(packed(c, group).cuda(), s.cuda(), x.cuda(), offset=o.cuda(), group=group)
+    w = (c.cuda().double() * spread(s.cuda(), group, n) + spread(o.cuda(), group, n)).t().contiguous()
+    assert torch.equal(y.double(), x.cuda().double() @ w)
