@@ -171,7 +171,7 @@ __device__ __forceinline__ void spread(float v, float (&o)[128 / GROUP]) {
 // the transposition gives each product 32 consecutive ones, so that groups of 32 need nothing else.  The waves' partial
 // sums add in LDS in their order.
 
-constexpr int kGroupedWaves = 8;  // 2560 x 2560, one token: 3.7 us; 2560 x 9728, sixteen: 11.6 (1.1 TB/s of codes)
+constexpr int kGroupedWaves = 8;  // 2560 x 2560, one token: 4.1 us; 2560 x 9728, sixteen: 11.7 (1.1 TB/s of codes)
 
 template <typename XT, int NT, int CT, int GROUP, int SB>
 __global__ void __launch_bounds__(64 * kGroupedWaves) grouped_few_kernel(GroupedLaunch L) {
@@ -453,7 +453,7 @@ struct Buffer {
 // Every wave widens its own fragments of codes (the waves down the tile repeat that: vector work under the others'
 // products), one step ahead of the products that take them, and the barrier that hands a stage over comes before
 // the last of its four steps.
-// Measured (2048 x 2560 x 9728, groups of 128): 127 us; per wave and stage 16 products (512 cycles) beside about 130 vector
+// Measured (2048 x 2560 x 9728, groups of 128): 120 us; per wave and stage 16 products (512 cycles) beside about 130 vector
 // instructions, of which 56 widen and 32 scale.  128 x 128 and two stages two workgroups a CU; 256 x 128 in one workgroup took 170 us
 // with four waves and 177 with eight.
 // MFMA D(32 x 32) += A(32 x 16) B(16 x 32): A row = token l % 32, B column = channel l % 32, both with the eight

@@ -18,8 +18,8 @@
 // result's own rounding, and the largest of a row, the target's, is put back into dX.  fp16 P carries a power of two that brings the largest |g| to 2^14 .. 2^15, taken out of
 // the sums in fp32, so that small probabilities stay above fp16's smallest numbers.
 //
-// Measured (bf16, 2048 x 2560, us a piece of 32768 words): logits and P 314, dX 303, dW 309; the loss alone 4096 x 2560 x 131072 2274;
-// one row, 1024 x 32768: 13.6 (W at 4.9 TB/s) and 8 of the launches around.
+// Measured (bf16, 2048 x 2560, us a piece of 32768 words): logits and P 310, dX 301, dW 312; the loss alone 4096 x 2560 x 131072 2250;
+// one row, 1024 x 32768: 14.5 (W at 4.6 TB/s) and 7 of the launches around.
 //
 // Rows that do not count (target outside the vocabulary, g = 0) are left out: the others' rows are gathered
 // at the start, their number stays on the device and cuts the products.
@@ -611,7 +611,8 @@ static inline TokenPlan token_plan(int es, long long rows, int n, int V, bool al
   P.copy = !aligned;
   const bool grad = dX || dW;
   const long long vr = (V + 255ll) / 256 * 256;
-  // P of a piece, or its copied rows, at most 128 MiB: they are written and read again within the Infinity Cache's 256
+  // P of a piece, or its copied rows, at most 128 MiB (but 256 words at least: 1 GiB of P for 2^20 rows of fp32): they are
+  // written and read again within the Infinity Cache's 256
   const long long row = (grad ? P.padded * es : 0) > (P.copy ? (long long)P.nq * es : 0) ? P.padded * es : (long long)P.nq * es;
   long long most = !grad && !P.copy ? vr : (128ll << 20) / row / 256 * 256;
   if (most < 256) most = 256;
