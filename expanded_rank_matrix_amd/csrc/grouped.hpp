@@ -445,8 +445,8 @@ struct Buffer {
 };
 
 // Workgroup: BM tokens and 32 FN WC channels, WR waves down and WC across, two workgroups a CU, whose barriers leave each
-// other's waves alone.  Tokens, codes, group sums and scales go through LDS in stages of 64 elements of a row, NB in turn, all by direct
-// loads, so that NB - 1 stages are on their way while one is used.
+// other's waves alone.  Tokens, codes, group sums and scales go through LDS in stages of 64 elements of a row, NB in turn,
+// all by direct loads, so that NB - 1 stages are on their way while one is used.
 //   tokens: row r is 128 bytes, its 16-byte piece c at c ^ r / 2 % 8 (16 rows' pieces of one column in different banks)
 //   codes:  loaded a word a lane, so that any order costs nothing: a channel's eight words lie as the wave's halves take
 //           them, 0 2 4 6 and 1 3 5 7
@@ -454,8 +454,8 @@ struct Buffer {
 // products), one step ahead of the products that take them, and the barrier that hands a stage over comes before
 // the last of its four steps.
 // Measured (2048 x 2560 x 9728, groups of 128): 120 us; per wave and stage 16 products (512 cycles) beside about 130 vector
-// instructions, of which 56 widen and 32 scale.  128 x 128 and two stages two workgroups a CU; 256 x 128 in one workgroup took 170 us
-// with four waves and 177 with eight.
+// instructions, of which 56 widen and 32 scale.  128 x 128 and two stages two workgroups a CU; 256 x 128 in one workgroup
+// took 170 us with four waves and 177 with eight.
 // MFMA D(32 x 32) += A(32 x 16) B(16 x 32): A row = token l % 32, B column = channel l % 32, both with the eight
 // elements at 8 (l / 32) of the step.
 template <typename XT, int BM, int WR, int WC, int FN, int NB, int GROUP>
@@ -710,11 +710,12 @@ static GroupedPlan grouped_plan(long long tokens, int n, int m, int group) {
   constexpr int NP = Pieces<XT>::count;
   GroupedPlan P{};
   // Few: up to 64 tokens of 16 bits, 32 of fp32, whose three pieces the kernel for few tokens makes again for each 16 or 32
-  // channels.  Measured, few / tiles, us (n x m, groups of 128): bf16 2560 x 2560, 64 tokens 12.6 / 17.6, 65 15.7 / 17.6; 2560 x 9728,
-  // 48 23.2 / 22.4, 65 26.0 / 23.1; 9728 x 2560, 32 21.8 / 25.6, 64 38.4 / 27.1; fp32 2560 x 2560, 32 12.8 / 16.0, 48 19.4 / 17.1; 2560 x
-  // 9728, 32 24.2 / 23.5, 48 39.8 / 24.7; 9728 x 2560, 16 22.4 / 27.5, 32 39.1 / 30.0, 64 74.4 / 31.3; 1021 x 2051, 48 9.2 / 13.3.
-  // Over 118 sizes, 12 to 160 tokens, that costs 5 to 6% over the better of the two, the worst on the longest rows.
-  // Matrices whose offsets in a tile, or number of tiles, pass 32 bits take the kernel for few tokens, whatever their number.
+  // channels.  Measured, few / tiles, us (n x m, groups of 128): bf16 2560 x 2560, 64 tokens 12.6 / 17.6, 65 15.7 / 17.6;
+  // 2560 x 9728, 48 23.2 / 22.4, 65 26.0 / 23.1; 9728 x 2560, 32 21.8 / 25.6, 64 38.4 / 27.1; fp32 2560 x 2560, 32 12.8 /
+  // 16.0, 48 19.4 / 17.1; 2560 x 9728, 32 24.2 / 23.5, 48 39.8 / 24.7; 9728 x 2560, 16 22.4 / 27.5, 32 39.1 / 30.0, 64 74.4 /
+  // 31.3; 1021 x 2051, 48 9.2 / 13.3.  Over 118 sizes, 12 to 160 tokens, that costs 5 to 6% over the better of the two, the
+  // worst on the longest rows.  Matrices whose offsets in a tile, or number of tiles, pass 32 bits take the kernel for few
+  // tokens, whatever their number.
   const long long scales = (n + 127ll) / 128 * 128 / group * ((m + 127ll) / 128 * 128) * 4;
   P.few = tokens <= (NP == 3 ? 32 : 64) || scales >= 1ll << 32 || m > 1 << 22;
   if (P.few) return P;
@@ -788,10 +789,11 @@ static hipError_t grouped_tiles(const GroupedLaunch& L, const GroupedPlan& P, hi
 template <typename XT, int GROUP, int SB>
 static hipError_t grouped_few(const GroupedLaunch& L, hipStream_t st) {
   // 32 channels a workgroup read the tokens half as often, but make half as many workgroups: taken where the busiest of the
-  // 256 CUs has fewer of them by more than each costs more.  Measured, 16 / 32 channels, us (n x m, groups of 128): 2560 x 2560, 1 token 4.3 /
-  // 5.4, 64 12.9 / 14.0; 2560 x 5120, 1 5.7 / 5.5, 64 22.6 / 14.1; 2560 x 9728, 1 7.2 / 8.7, 8 10.1 / 10.4, 16 12.9 / 12.3, 64
-  // 31.9 / 26.3; 9728 x 5120, 1 14.0 / 12.2, 64 75 / 45; 9728 x 16384, 8 37 / 30; 2560 x 16400, 1 9.9 / 11.5, 16 19.7 / 16.6.  (Sixteen
-  // waves instead of eight: 9728 x 2560, 1 token 8.4 against 8.0, 16 16.0 against 14.6.)
+  // 256 CUs has fewer of them by more than each costs more.  Measured, 16 / 32 channels, us (n x m, groups of 128): 2560 x
+  // 2560, 1 token 4.3 / 5.4, 64 12.9 / 14.0; 2560 x 5120, 1 5.7 / 5.5, 64 22.6 / 14.1; 2560 x 9728, 1 7.2 / 8.7, 8 10.1 /
+  // 10.4, 16 12.9 / 12.3, 64 31.9 / 26.3; 9728 x 5120, 1 14.0 / 12.2, 64 75 / 45; 9728 x 16384, 8 37 / 30; 2560 x 16400, 1
+  // 9.9 / 11.5, 16 19.7 / 16.6.  (Sixteen waves instead of eight: 9728 x 2560, 1 token 8.4 against 8.0, 16 16.0 against
+  // 14.6.)
   const long long narrow = (L.m + 4095ll) / 4096, half = (L.m + 8191ll) / 8192;  // workgroups of the busiest CU
   const bool wide = L.tokens > 8 ? narrow > half : 4 * narrow > 7 * half;
   if (L.tokens <= 16) return wide ? few_launch<XT, 1, 2, GROUP, SB>(L, st) : few_launch<XT, 1, 1, GROUP, SB>(L, st);

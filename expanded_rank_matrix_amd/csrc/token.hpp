@@ -7,19 +7,20 @@
 //   dX = P W,   dW = P^T X
 //
 // The loss is one product whose tiles (columns: tokens, rows: words) reduce their logits to a maximum and a
-// sum of exponentials for each token; a second launch joins the tiles.  The gradient takes the vocabulary in pieces: a piece's logits
-// are formed again and leave as P, in X's type, which two products then read while it is in the
-// cache.  dX is summed over the pieces in fp32.  So the work is four products for loss and both gradients,
-// and the matrix cores bound it but for few tokens, where reading W does.
+// sum of exponentials for each token; a second launch joins the tiles.  The gradient takes the vocabulary in pieces: a
+// piece's logits are formed again and leave as P, in X's type, which two products then read while it is in the cache.  dX is
+// summed over the pieces in fp32.  So the work is four products for loss and both gradients, and the matrix cores bound it
+// but for few tokens, where reading W does.
 //
 // Roundings: sums of products, exponentials and a tile's sum of them are fp32, the sums over tiles, log S and
 // the loss fp64.  P is rounded once to X's type for the products that follow (as a gradient of logits held in that
 // type would be); its errors are independent and each at most half a step, like those of the
-// result's own rounding, and the largest of a row, the target's, is put back into dX.  fp16 P carries a power of two that brings the largest |g| to 2^14 .. 2^15, taken out of
-// the sums in fp32, so that small probabilities stay above fp16's smallest numbers.
+// result's own rounding, and the largest of a row, the target's, is put back into dX.  fp16 P carries a power of two that
+// brings the largest |g| to 2^14 .. 2^15, taken out of the sums in fp32, so that small probabilities stay above fp16's
+// smallest numbers.
 //
-// Measured (bf16, 2048 x 2560, us a piece of 32768 words): logits and P 310, dX 301, dW 312; the loss alone 4096 x 2560 x 131072 2250;
-// one row, 1024 x 32768: 14.5 (W at 4.6 TB/s) and 7 of the launches around.
+// Measured (bf16, 2048 x 2560, us a piece of 32768 words): logits and P 310, dX 301, dW 312; the loss alone 4096 x 2560 x
+// 131072 2250; one row, 1024 x 32768: 14.5 (W at 4.6 TB/s) and 7 of the launches around.
 //
 // Rows that do not count (target outside the vocabulary, g = 0) are left out: the others' rows are gathered
 // at the start, their number stays on the device and cuts the products.
