@@ -37,7 +37,8 @@ struct FOperand {
 
 static __device__ const int kFZeros[4] = {0, 0, 0, 0};  // what a direct load reads behind an operand's end
 
-constexpr long long kFTiles = 1ll << 22;  // fewer tiles than this in a launch
+// Whether a launch holds so many tiles of so many threads.
+static inline bool ftile_fits(long long tiles, int threads) { return tiles * threads < 1ll << 32; }
 
 // What the product's sizes may be cut to by a count that only the device knows.
 enum FCount { kRowsOfB, kLength };
@@ -282,7 +283,7 @@ template <typename T, int BM, int BN, int WR, int WC, int KB, int NB, bool AX, b
 static hipError_t ftile_launch(FOperand A, long long M, FOperand B, long long N, long long K, int parts, const int* count,
                                const EPI& epi, hipStream_t st) {
   const long long ntm = (M + BM - 1) / BM, ntn = (N + BN - 1) / BN;
-  if (ntm * ntn >= kFTiles || M >= (1ll << 31) - 256 || N >= (1ll << 31) - 256 || K >= (1ll << 30)) return hipErrorInvalidValue;
+  if (!ftile_fits(ntm * ntn * parts, 64 * WR * WC) || M >= (1ll << 31) - 256 || N >= (1ll << 31) - 256 || K >= (1ll << 30)) return hipErrorInvalidValue;
   constexpr int KS = KB / (int)sizeof(T);
   const long long kper = ((K + KS - 1) / KS + parts - 1) / parts * KS;
   hipLaunchKernelGGL((ftile_kernel<T, BM, BN, WR, WC, KB, NB, AX, BX, CUT, EPI>), dim3((unsigned)(ntm * ntn), (unsigned)parts),

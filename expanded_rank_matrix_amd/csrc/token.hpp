@@ -557,43 +557,50 @@ struct TokenPlan {
   size_t meta, list, place, coef, zt, lost, tiles, x, w, p, dx, bytes;  // offsets in the workspace, and its size
 };
 
-// Tile shapes, and how many workgroups of each the card runs at a time with a product's rate.
+// Tile shapes, how many workgroups of each the card runs at a time with a product's rate, and their threads.
 struct TokenShape {
-  int bm, bn, slots;
+  int bm, bn, slots, threads;
 };
-constexpr TokenShape kTokenShapes[] = {{64, 32, 512}, {128, 32, 1024}, {128, 64, 512}, {128, 128, 512}, {256, 256, 256}};
+constexpr TokenShape kTokenShapes[] = {{64, 32, 512, 128}, {128, 32, 1024, 256}, {128, 64, 512, 256}, {128, 128, 512, 256}, {256, 256, 256, 512}};
+
+// Parts of the length of dX's product, so that its few tiles fill the card; at least eight stages each.
+static inline long long token_parts(const TokenShape& s, long long tiles, long long words, int es) {
+  const long long parts = s.slots / tiles, longest = (words * es + 1023) / 1024;
+  return parts > longest ? longest : parts < 1 ? 1 : parts;
+}
 
 // 16 bits: up to 128 tokens the narrowest tiles that hold them in one column (reading W is what counts there); more by
 // rounds of 128 x 128 (512 at a time, 0.62 of a 256 x 256 round's time; a round of at most 256 of them 0.38) against
-// 256 x 256.  fp32, whose products are sixteen times slower, by the work of the busiest CU, of which 64 x 32 tiles do 15%
-// more slowly.  Measured, us of the loss and its dX in tiles of 64 x 32, 128 x 64, 128 x 128, 256 x 256 (n 2560):
+// 256 x 256.
+// fp32, whose products are sixteen times slower, by the work of the busiest CU in the products with the words and, half as
+// often, in dX's (rounds of tiles, 64 x 32 two a CU at a time, times what a CU has of each), of which 64 x 32 tiles do
+// 15% more slowly.  Measured, us of the loss and its dX in tiles of 64 x 32, 128 x 64, 128 x 128, 256 x 256 (n 2560):
 //   65 x 32768     518   491   504  1502        600 x 32768    2934  2474  2280  3309
 //   128 x 32768    740   516   509  1499       1024 x 32768    4067  4384  3643  3647
 //   300 x 32768   1842  1180  1471  1842       2048 x 32768    8180  7668  8570  7283
-// Over 28 sizes (rows 20 to 2048, 2051 to 50021 words) the loss is within 12% of the best shape's, and with dX within 16%.
-// A shape of which dX's product (elements of a hidden row by tokens) would need more tiles than a launch holds is left out;
-// 256 x 256, 2^21 at the most, never is.
+// Over 92 sizes (20 to 4096 rows of 64 to 4096, 1451 to 131072 words) the loss with dX is within 16% of the best shape's, 1% in
+// the mean (64 x 32 throughout: 64%, 11%), without 256 x 256, which gained 5% at one size.
+// A shape of which dX's product would not fit a launch is left out; 128 x 128 always does.
 static inline int token_shape(int es, long long rows, int nq, int V) {
-  auto count = [&](long long m, int s) {
+  auto tiles = [&](long long m, int s) {
     return (m + kTokenShapes[s].bm - 1) / kTokenShapes[s].bm * ((rows + kTokenShapes[s].bn - 1) / kTokenShapes[s].bn);
   };
-  auto tiles = [&](int s) { return count(V, s); };
-  auto held = [&](int s) { return count(nq, s) < kFTiles; };
   if (es == 2) {
     if (rows <= 32) return 1;
     if (rows <= 64) return 2;
     if (rows <= 128) return 3;
-    const long long t3 = tiles(3), rest = t3 % 512;
-    const double c3 = 0.62 * (double)(t3 / 512) + (rest == 0 ? 0.0 : rest <= 256 ? 0.38 : 0.62), c4 = (double)((tiles(4) + 255) / 256);
-    return c3 < c4 && held(3) ? 3 : 4;
+    const long long t3 = tiles(V, 3), rest = t3 % 512;
+    const double c3 = 0.62 * (double)(t3 / 512) + (rest == 0 ? 0.0 : rest <= 256 ? 0.38 : 0.62), c4 = (double)((tiles(V, 4) + 255) / 256);
+    return c3 < c4 ? 3 : 4;
   }
-  int best = 4;
+  int best = 3;
   double least = 1e300;
-  for (int s : {4, 3, 2, 0}) {
-    // rounds of tiles (64 x 32: two a CU at a time), times what a CU has of each
-    const long long per = s == 0 ? 512 : 256, rounds = (tiles(s) + per - 1) / per;
-    const double c = (s == 0 ? 1.15 : 1.0) * (double)(rounds * (per / 256) * kTokenShapes[s].bm * kTokenShapes[s].bn);
-    if (c < least && held(s)) {
+  for (int s : {3, 2, 0}) {
+    const long long each = s == 0 ? 2 : 1, dx = tiles(nq, s), parts = token_parts(kTokenShapes[s], dx, V, es);
+    auto rounds = [&](long long t) { return (double)((t + 256 * each - 1) / (256 * each) * each); };
+    const double c = (s == 0 ? 1.15 : 1.0) * kTokenShapes[s].bm * kTokenShapes[s].bn *
+                     (1.5 * rounds(tiles(V, s)) * nq + 0.5 * rounds(dx * parts) * V / (double)parts);
+    if (c < least && ftile_fits(dx, kTokenShapes[s].threads)) {
       least = c;
       best = s;
     }
@@ -623,12 +630,7 @@ static inline TokenPlan token_plan(int es, long long rows, int n, int V, bool al
   if (most > wide) most = wide;
   if (most > 1 << 20) most = 1 << 20;
   P.piece = (int)(most < vr ? most : vr);
-  // parts of the length, so that dX's few tiles fill the card
-  const long long tiles = (P.nq + P.bm - 1) / P.bm * (P.padded / P.bn);
-  long long parts = kTokenShapes[P.shape].slots / tiles;
-  const long long longest = (P.piece * es + 1023) / 1024;  // at least eight stages each
-  if (parts > longest) parts = longest;
-  P.parts = (int)(parts < 1 ? 1 : parts);
+  P.parts = (int)token_parts(kTokenShapes[P.shape], (P.nq + P.bm - 1) / P.bm * (P.padded / P.bn), P.piece, es);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t a = at;
@@ -674,7 +676,9 @@ static hipError_t token_product(const TokenPlan& P, FOperand A, long long M, FOp
       else return hipErrorInvalidValue;
     case 2: return ftile_launch<T, 128, 64, 2, 2, 128, 2, AX, false, kRowsOfB>(A, M, B, N, K, parts, c, epi, st);
     case 3: return ftile_launch<T, 128, 128, 2, 2, 128, 2, AX, false, kRowsOfB>(A, M, B, N, K, parts, c, epi, st);
-    default: return ftile_launch<T, 256, 256, 2, 4, 128, 2, AX, false, kRowsOfB>(A, M, B, N, K, parts, c, epi, st);
+    default:
+      if constexpr (sizeof(T) == 2) return ftile_launch<T, 256, 256, 2, 4, 128, 2, AX, false, kRowsOfB>(A, M, B, N, K, parts, c, epi, st);
+      else return hipErrorInvalidValue;
   }
 }
 
