@@ -75,6 +75,9 @@ __device__ __forceinline__ void interleave() {
 // fed (reads of the fragments and the loads' writes).  Both operands across, 256 x 128, four waves, two workgroups a CU,
 // three stages of 64 bytes: 1.11 10^15, 0.97 for 256 x 256 in two stages; along rows, 64 bytes are half a cache line and lost 25%.
 constexpr int kFGroup = 4;  // 2, 8 and 16 measured the same
+// Stages of a run of fp32 sums.  300 x 2560 x 32768, loss and dX: S 4.3e-6 off without runs, 5.8e-7 with, dX 1.7e-6 and 2.7e-7, for
+// 2% more time (1181 and 1203 us; 65 x 777 x 10007 109 and 112).
+constexpr int kFRun = 4;
 
 template <typename T, int ROWS, bool ACROSS, int KB>
 struct FStage {  // where an operand's pieces lie in a stage
@@ -250,8 +253,27 @@ __global__ void __launch_bounds__(64 * WR * WC, WR * WC >= 8 ? 1 : 2) ftile_kern
     asm volatile("s_barrier" ::: "memory");
     read(0, lds, 0);
     __builtin_amdgcn_sched_barrier(0);
+    // fp32 operands hold what fp32 sums lose: these go in runs of kFRun stages (128 k), added up apart, so that a sum of K
+    // terms rounds like one of 128 + K / 128.
+    constexpr bool kRuns = ES == 4;
+    fv16 runs[kRuns ? FM : 1][kRuns ? FN : 1];
+    auto run = [&](bool first) {
+      if constexpr (kRuns) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              runs[i][j][e] = first ? 0.0f : runs[i][j][e] + acc[i][j][e];
+              acc[i][j][e] = 0.0f;
+            }
+      }
+    };
+    run(true);
     int here = 0;  // of the stage's place
     for (int t = 0; t < nk - 1; ++t) {
+      if (kRuns && t > 0 && t % kFRun == 0) run(false);
       int8_t* l = lds + here;
       here = here == (NB - 1) * kStage ? 0 : here + kStage;
 #pragma unroll
@@ -272,6 +294,14 @@ __global__ void __launch_bounds__(64 * WR * WC, WR * WC >= 8 ? 1 : 2) ftile_kern
       if (k < S - 1) read((k + 1) & 1, lds + here, k + 1);
       mul(k & 1);
       if (k < S - 1) spread();
+    }
+    if constexpr (kRuns) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) acc[i][j][e] += runs[i][j][e];
     }
     if (EPI::kLds) __syncthreads();  // the stages are read: LDS is free
   }

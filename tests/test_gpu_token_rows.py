@@ -118,3 +118,25 @@ def test_rows_far_apart(dtype):
     got = erm.token_loss(xs, ws, target, weight=weight, out=(dx, dw))
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("rows,vocab", [(1, 300), (65, 10007), (300, 32768), (600, 32768)])
+def test_long_fp32_sums_keep_small_terms(rows, vocab):
+    """Logits of 4096 terms of 1 + 2^-14: 4096.25, which fp32 holds, but a sum past 2048 that takes the terms one after the other
+    loses the small part of each.  In runs of 128 every partial sum is exact (a run 128 + 2^-7, steps of 2^-16)."""
+    n = 4096
+    x = torch.ones((rows, n), device="cuda")
+    w = torch.full((vocab, n), 1 + 2.0**-14, device="cuda")
+    loss, stats = erm.token_loss(x, w, torch.zeros(rows, dtype=torch.int64, device="cuda"))
+    assert (stats[:, 0] == 4096.25).all() and (stats[:, 1] == vocab).all()
+    # the logarithm in fp64, rounded once
+    assert ((loss.double() - torch.tensor(float(vocab)).double().log().cuda()).abs() <= 2.0**-23 * 16).all()
+
+
+def test_long_fp32_sums_over_rows_keep_small_terms():
+    """Words of zeros: P is 1 / vocab, and dW of a word that is no target the mean of its rows times their number."""
+    rows, n, vocab = 4096, 40, 64
+    x = torch.full((rows, n), 1 + 2.0**-14, device="cuda")
+    w = torch.zeros((vocab, n), device="cuda")
+    _, _, dX, dW = erm.token_loss(x, w, torch.zeros(rows, dtype=torch.int64, device="cuda"), grad=True)
+    assert not dX.any() and (dW[1:] == 4096.25 / vocab).all()
