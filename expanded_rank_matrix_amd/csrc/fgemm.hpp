@@ -75,9 +75,9 @@ __device__ __forceinline__ void interleave() {
 // fed (reads of the fragments and the loads' writes).  Both operands across, 256 x 128, four waves, two workgroups a CU,
 // three stages of 64 bytes: 1.11 10^15, 0.97 for 256 x 256 in two stages; along rows, 64 bytes are half a cache line and lost 25%.
 constexpr int kFGroup = 4;  // 2, 8 and 16 measured the same
-// Stages of a run of fp32 sums.  300 x 2560 x 32768, loss and dX: S 4.3e-6 off without runs, 5.8e-7 with, dX 1.7e-6 and 2.7e-7, for
-// 2% more time (1181 and 1203 us; 65 x 777 x 10007 109 and 112).
-constexpr int kFRun = 4;
+// Stages of a run of fp32 sums.  300 x 2560 x 32768, loss and dX: S 4.3e-6 off without runs, 7.0e-7 with, dX 1.7e-6 and 3.3e-7, for
+// 1% more time (1181 and 1190 us; 65 x 777 x 10007 109 and 111); runs of four 5.8e-7, 2.7e-7 and 1203 us.
+constexpr int kFRun = 8;
 
 template <typename T, int ROWS, bool ACROSS, int KB>
 struct FStage {  // where an operand's pieces lie in a stage
@@ -253,8 +253,8 @@ __global__ void __launch_bounds__(64 * WR * WC, WR * WC >= 8 ? 1 : 2) ftile_kern
     asm volatile("s_barrier" ::: "memory");
     read(0, lds, 0);
     __builtin_amdgcn_sched_barrier(0);
-    // fp32 operands hold what fp32 sums lose: these go in runs of kFRun stages (128 k), added up apart, so that a sum of K
-    // terms rounds like one of 128 + K / 128.
+    // fp32 operands hold what fp32 sums lose: these go in runs of kFRun stages (256 k), added up apart, so that a sum of K
+    // terms rounds like one of 256 + K / 256.
     constexpr bool kRuns = ES == 4;
     fv16 runs[kRuns ? FM : 1][kRuns ? FN : 1];
     auto run = [&](bool first) {

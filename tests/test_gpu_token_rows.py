@@ -123,7 +123,7 @@ def test_rows_far_apart(dtype):
 @pytest.mark.parametrize("rows,vocab", [(1, 300), (65, 10007), (300, 32768), (600, 32768)])
 def test_long_fp32_sums_keep_small_terms(rows, vocab):
     """Logits of 4096 terms of 1 + 2^-14: 4096.25, which fp32 holds, but a sum past 2048 that takes the terms one after the other
-    loses the small part of each.  In runs of 128 every partial sum is exact (a run 128 + 2^-7, steps of 2^-16)."""
+    loses the small part of each.  In runs of up to 256 every partial sum is exact (a run 256 + 2^-6, steps of 2^-15)."""
     n = 4096
     x = torch.ones((rows, n), device="cuda")
     w = torch.full((vocab, n), 1 + 2.0**-14, device="cuda")
