@@ -12,7 +12,7 @@
 // summed over the pieces in fp32.  So the work is four products for loss and both gradients, and the matrix cores bound it
 // but for few tokens, where reading W does.
 //
-// Roundings: sums of products, exponentials and a tile's sum of them are fp32, the sums over tiles, log S and
+// Roundings: sums of products (fp32's in runs), exponentials and a tile's sum of them are fp32, the sums over tiles, log S and
 // the loss fp64.  P is rounded once to X's type for the products that follow (as a gradient of logits held in that
 // type would be); its errors are independent and each at most half a step, like those of the
 // result's own rounding, and the largest of a row, the target's, is put back into dX.  fp16 P carries a power of two that

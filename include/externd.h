@@ -382,8 +382,9 @@ int64_t externd_apply_grouped_workspace(int x_type, int64_t tokens, int64_t n, i
  *   workspace  externd_token_workspace(x_type, rows, n, vocab, W, ldw, 1, dX != NULL, dW != NULL) bytes, 16-byte
  *            aligned, used by this call alone until it has run
  * Products are summed in fp32 (those of fp32 X in runs of up to 256 terms, added up apart), the losses in
- * fp64.  P is rounded to x_type before the two products that take it (for fp16 times a power of two that the result is divided by again; what the target's
- * rounding took is put back into dX).  exp(z - largest) and P below 2^-126 count as 0.  Deterministic.
+ * fp64.  P is rounded to x_type before the two products that take it (for fp16 times a power of two that the
+ * result is divided by again; what the target's rounding took is put back into dX).  exp(z - largest) and P
+ * below 2^-126 count as 0.  Deterministic.
  * A row with a logit of +infinity or NaN has loss, statistics and dX NaN, and makes dW NaN throughout: so does
  * a NaN in a counted row, or an infinity there (but statistics are -infinity and 0 where all logits are
  * -infinity).  A NaN in W does that to every row.  An infinity in W acts by the logits that it gives: a row
